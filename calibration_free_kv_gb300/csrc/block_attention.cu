@@ -1,0 +1,1296 @@
+// Attention of a block of new tokens per sequence over the packed cache (sm_103a): the drafted
+// tokens of a tree, each seeing the whole cache and its own ancestors, or a chunk of a prompt under
+// a sliding window with a few first tokens that stay visible.
+//
+// Math (rotated basis, R = H_d / sqrt(d)): a sealed page's logit of query row r and token t is
+//   tau r_t ( sum_j code_tj (q~_rj s'_j) + sum_j q~_rj z'_j ),  o~ = sum_t p_t V~_t,
+//   V~_tj = c_j ( code_tj s'_t + z'_t )
+// [vatt §四個步驟: the rotation keeps q.k unchanged; hotdry §非对称量化与尺度折叠: the folded scales
+//  are multiplied back at read].  Three kernels:
+//  block_raw_kernel    the open tile's raw tokens and the new tokens themselves, masked, on
+//                      mma.sync: one partial (m, l, o) per query row, original basis;
+//  block_cache_kernel  the sealed pages on tcgen05: partials in the rotated basis;
+//  block_merge_kernel  joins the partials, undoes the rotation, rounds once to fp16.
+//
+// block_cache_kernel.  The G * block query rows of one (sequence, kv head) are cut into row tiles of
+// NR = 16, 32 or 64 rows.  The (row tile, visible page) pairs lie on a line that is cut into equal
+// ranges, one per CTA and one CTA per SM.  Tokens sit on the MMA's M axis (a page is exactly its
+// 128 rows) and query rows on N, so that the MMA time follows the rows a tile has.  Per page:
+//  QK  S[t][r] = sum_j A_K[t][j] B[j][r]; A_K = the codes in tensor memory as exact fp16 subnormals
+//      (one AND per two codes), B = q~ . s' as fp16 hi, then lo (2 x D/16 MMAs into one
+//      accumulator).  hi + lo because keys with outlier channels give logits in the hundreds, and
+//      one fp16 rounding of q~ s' (2^-11 relative) would move them by 0.1;
+//  PV  O[c][r] += sum_t A_V[c][t] P[t][r]; A_V = V~ rounded twice to fp16 (once per product),
+//      P = exp2 rounded once to fp16.  Both roundings move the output like its own fp16 rounding.
+// Softmax: a thread owns a token and all NR rows; each row's reference maximum is kept from page to
+// page and moved only when a logit passes it by 2^8 (then O and l are rescaled), so no maximum is
+// exchanged on the usual page; P stays below 2^8 and l is fp32.
+// Warps: 0-3 softmax (and the rescale and the row tile's partial at its end), 4-7 K codes and B and
+// q~ . z', 8-11 V, 12 page records (1-D bulk copies into a ring), 13 / 14 QK of even / odd pages,
+// 15 PV.  Operand and score buffers are double; every hand-off is an mbarrier, every wait bounded.
+#include "common.cuh"
+#include "decode_util.cuh"
+#include "params.cuh"
+#include "tcgen05.cuh"
+
+namespace kvarn {
+namespace blk {
+
+using namespace tc5;
+
+constexpr int kThreads = 512;
+constexpr int kKWarp = 4, kVWarp = 8, kLoadWarp = 12, kQkWarp = 13, kPvWarp = 15;
+constexpr int kMaxSlots = 8;
+constexpr int kRoleBar = 1, kSmBar = 2;  // named barriers: all warps but the loader, the softmax warps
+constexpr int kRoleThreads = kThreads - 32;
+constexpr int kFixUnits = 6;  // units of the line ahead of a row tile's pages: a segment's fixed work
+constexpr int kMinUnits = 10;  // smallest range
+constexpr float kSlack = 8.0f;  // log2 units a logit may pass its row's reference by
+constexpr int kSmemMax = 232448 - 1024;
+
+template <int D, int NR>
+struct Shape {
+  static constexpr int kSteps = D / 16;           // K steps of QK
+  static constexpr int kHalves = D > 128 ? 2 : 1; // 128-channel blocks of PV
+  static constexpr int kVStages = D > 128 ? 1 : 2;
+  static constexpr int kStep = NR * 32;           // bytes of one K step of a B operand
+  static constexpr int kBHalf = NR * D * 2;       // q~ s' hi (or lo) of one page
+  static constexpr int kPBytes = NR * kTile * 2;
+  // shared memory: B (two stages, hi + lo), P (two stages), q~ hi + lo, small state, records
+  static constexpr int kBOff = 0;
+  static constexpr int kPOff = 2 * 2 * kBHalf;
+  static constexpr int kQOff = kPOff + 2 * kPBytes;
+  static constexpr int kSmallOff = kQOff + 2 * kBHalf;
+  // floats: qz [2][NR], -reference, row maximum, shift, rescale, row limit [NR] each, per warp [4][NR]
+  static constexpr int kSmallFloats = (2 + 5 + 4) * NR;
+  static constexpr int kBarOff = kSmallOff + kSmallFloats * 4;
+  static constexpr int kNumBars = 2 * kMaxSlots + 6 * 2;
+  static constexpr int kRecOff = (kBarOff + kNumBars * 8 + 127) & ~127;
+  // tensor memory columns
+  static constexpr uint32_t kColK = 0, kColV = 2 * (D / 2);
+  static constexpr uint32_t kColS = kColV + kVStages * 64 * kHalves;
+  static constexpr uint32_t kColO = kColS + 2 * NR;
+  static_assert(kColO + kHalves * NR <= 512, "fits tensor memory");
+};
+
+// kind::f16, f32 accumulate, f16 A and B, M = 128, N = NR; B K-major (QK) or MN-major (PV).
+template <int NR>
+constexpr uint32_t kIdescQK = (1u << 4) | ((uint32_t)(NR >> 3) << 17) | ((128u >> 4) << 24);
+template <int NR>
+constexpr uint32_t kIdescPV = kIdescQK<NR> | (1u << 16);
+
+// Factors on q~ for channels 0..7 and 8..15 of every 16, whose 4- / 2-bit codes sit 4 / 2 bits
+// apart in their subnormals (the same lifts as the decode kernels' operands).
+__device__ __forceinline__ float lift0(int kb) { return kb == 8 ? 256.0f : (kb == 4 ? 16.0f : 4.0f); }
+__device__ __forceinline__ float lift1(int kb) { return kb == 8 ? 256.0f : 1.0f; }
+
+// Barrier of `threads` threads; returns whether any of them passed `flag`.
+__device__ __forceinline__ bool bar_any(int id, int threads, bool flag) {
+  uint32_t out;
+  asm volatile(
+      "{\n\t.reg .pred pi, po;\n\tsetp.ne.u32 pi, %1, 0;\n\t"
+      "bar.red.or.pred po, %2, %3, pi;\n\tselp.u32 %0, 1, 0, po;\n\t}"
+      : "=r"(out)
+      : "r"((uint32_t)flag), "r"(id), "r"(threads)
+      : "memory");
+  return out != 0;
+}
+
+__device__ __forceinline__ int cached_len(const BlockParams& p, int b) {
+  const int cap = p.max_pages * kTile + (kTile - 1);
+  const int len = p.seq_lens[b];
+  return len < 0 ? 0 : (len > cap ? cap : len);
+}
+__device__ __forceinline__ int new_len(const BlockParams& p, int b) {
+  if (p.new_lens == nullptr) return p.block;
+  const int n = p.new_lens[b];
+  return n < 0 ? 0 : (n > p.block ? p.block : n);
+}
+
+// The sealed pages row tile t of sequence b sees: 0 .. sinks - 1, then first ..; count in all.
+struct Span {
+  int sinks, first, count;
+  __device__ __forceinline__ int page(int i) const { return i < sinks ? i : first + (i - sinks); }
+};
+__device__ __forceinline__ Span tile_span(const BlockParams& p, int len, int nl, int t) {
+  const int n = len / kTile;
+  const int c0 = t * p.tile_rows / p.group;  // the tile's first new token
+  if (c0 >= nl) return {0, 0, 0};
+  if (p.window <= 0) return {0, 0, n};
+  const int start = max(0, len + c0 + 1 - p.window);
+  const int first = min(start / kTile, n);
+  const int sinks = min((p.sink + kTile - 1) / kTile, first);
+  return {sinks, first, sinks + n - first};
+}
+__device__ __forceinline__ int tile_units(const Span& s) { return s.count > 0 ? s.count + kFixUnits : 0; }
+// units of all row tiles of one kv head of sequence b
+__device__ __forceinline__ int64_t head_units(const BlockParams& p, int b) {
+  const int len = cached_len(p, b), nl = new_len(p, b);
+  const int live = (nl * p.group + p.tile_rows - 1) / p.tile_rows;
+  if (p.window <= 0) return (int64_t)live * (len / kTile > 0 ? len / kTile + kFixUnits : 0);
+  int64_t u = 0;
+  for (int t = 0; t < live; ++t) u += tile_units(tile_span(p, len, nl, t));
+  return u;
+}
+
+// A CTA's range of the line, as segments: runs of pages of one row tile.
+struct TileWalk {
+  int b, h, t, j;   // row tile t of (sequence b, kv head h), first visible page of the segment
+  int len, nl;      // sequence b's cached and new tokens
+  Span span;
+  int64_t left;     // units of the range from page j on (0: nothing left)
+  int64_t row0;     // unit at which the row tile starts
+  __device__ int count() const { return (int)min((int64_t)(span.count - j), left); }
+  __device__ int64_t row(const BlockParams& p) const { return ((int64_t)b * p.num_kv_heads + h) * p.tiles + t; }
+  __device__ void next(const BlockParams& p) {
+    left -= count();
+    if (left <= 0) return;
+    j = 0;
+    row0 += tile_units(span);
+    for (;;) {
+      if (++t >= p.tiles) {
+        t = 0;
+        if (++h == p.num_kv_heads) {
+          h = 0;
+          if (++b >= p.batch) {  // unreachable while the lengths stay as they were
+            left = 0;
+            return;
+          }
+          len = cached_len(p, b);
+          nl = new_len(p, b);
+        }
+      }
+      span = tile_span(p, len, nl, t);
+      if (span.count > 0) {
+        left -= kFixUnits;  // the range may end inside the row tile's fixed units
+        if (left < 0) left = 0;
+        return;
+      }
+    }
+  }
+};
+
+// Warp-collective: the partition and this CTA's walk.
+__device__ __forceinline__ TileWalk range_walk(const BlockParams& p, int64_t cta, int lane, PagePartition& pp) {
+  TileWalk w = {};
+  long long total = 0;
+  for (int b = lane; b < p.batch; b += 32) total += head_units(p, b);
+#pragma unroll
+  for (int m = 16; m > 0; m >>= 1) total += __shfl_xor_sync(0xffffffffu, total, m);
+  pp.total = total * p.num_kv_heads;
+  const int64_t c = pp.total / kMinUnits;
+  pp.ctas = pp.total > 0 ? (c < 1 ? 1 : (c > kBlockCtas ? kBlockCtas : c)) : 0;
+  if (cta >= pp.ctas) return w;
+  const int64_t x0 = range_start(pp, cta), x1 = range_start(pp, cta + 1);
+  long long cum = 0;
+  for (int b0 = 0; b0 < p.batch; b0 += 32) {
+    const int bb = b0 + lane;
+    const long long hu = bb < p.batch ? head_units(p, bb) : 0;
+    long long incl = hu * p.num_kv_heads;
+#pragma unroll
+    for (int m = 1; m < 32; m <<= 1) {
+      const long long o = __shfl_up_sync(0xffffffffu, incl, m);
+      if (lane >= m) incl += o;
+    }
+    const unsigned hit = __ballot_sync(0xffffffffu, cum + incl > x0);
+    if (hit != 0u) {
+      const int l = __ffs(hit) - 1;
+      const long long u = __shfl_sync(0xffffffffu, hu, l);
+      long long at = cum + __shfl_sync(0xffffffffu, incl, l) - u * p.num_kv_heads;  // start of sequence b
+      w.b = b0 + l;
+      w.len = cached_len(p, w.b);
+      w.nl = new_len(p, w.b);
+      w.h = (int)((x0 - at) / u);
+      at += (long long)w.h * u;
+      for (w.t = 0;; ++w.t) {  // the row tile that holds x0
+        w.span = tile_span(p, w.len, w.nl, w.t);
+        const int tu = tile_units(w.span);
+        if (x0 < at + tu || w.t + 1 >= p.tiles) break;
+        at += tu;
+      }
+      w.row0 = at;
+      const int64_t first = at + kFixUnits;  // unit of the row tile's first page
+      w.j = x0 < first ? 0 : (int)(x0 - first);
+      w.left = x1 - (first + w.j);
+      if (w.left < 0) w.left = 0;  // the range ends inside the fixed units
+      return w;
+    }
+    cum += __shfl_sync(0xffffffffu, incl, 31);
+  }
+  return w;
+}
+
+}  // namespace blk
+
+// ---- the sealed pages ----------------------------------------------------------------------
+template <int D, int NR>
+__global__ void __launch_bounds__(blk::kThreads, 1) block_cache_kernel(BlockParams p, int slots) {
+  using namespace blk;
+  using S = Shape<D, NR>;
+  extern __shared__ __align__(1024) uint8_t sm[];
+  __shared__ TileWalk walk_s;
+  __shared__ PagePartition part_s;
+  __shared__ uint32_t tslot;
+  __shared__ int abort_flag;
+  const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
+  const RecordLayout RL = record_layout(D, p.kb, p.vb);
+  const int rec = RL.bytes;
+  uint64_t* rec_full = reinterpret_cast<uint64_t*>(sm + S::kBarOff);
+  uint64_t* rec_empty = rec_full + kMaxSlots;
+  uint64_t* ops_k = rec_empty + kMaxSlots;  // per stage: K codes, B and q~ . z' written
+  uint64_t* qk_full = ops_k + 2;            // QK done: K codes and B are free
+  uint64_t* s_free = qk_full + 2;           // S and q~ . z' read
+  uint64_t* ops_v = s_free + 2;             // V written
+  uint64_t* p_full = ops_v + 2;             // P written, O rescaled
+  uint64_t* pv_done = p_full + 2;           // PV done: V and P are free, O is up to date
+  float* qz_s = reinterpret_cast<float*>(sm + S::kSmallOff);  // [2][NR]
+  float* nref_s = qz_s + 2 * NR;   // minus the row's reference
+  float* max_s = nref_s + NR;      // the row's maximum when the reference was set (-inf: none yet)
+  float* shift_s = max_s + NR;     // old reference - new reference
+  float* alpha_s = shift_s + NR;   // rescale of l and O
+  int* lim_s = reinterpret_cast<int*>(alpha_s + NR);  // position from which the row's window sees
+  float* warp_s = reinterpret_cast<float*>(lim_s + NR);  // [4][NR]
+  uint8_t* recs = sm + S::kRecOff;
+  uint8_t* q_hi = sm + S::kQOff;
+  uint8_t* q_lo = q_hi + S::kBHalf;
+
+  // The kernel before this one (block_raw_kernel) waited for everything ahead of it before it let
+  // this grid start, so the inputs are complete; its own partials are read by the merge only.
+  if (warp == 1) {
+    PagePartition pp;
+    const TileWalk w = range_walk(p, blockIdx.x, lane, pp);
+    if (lane == 0) {
+      walk_s = w;
+      part_s = pp;
+    }
+  }
+  if (threadIdx.x == 0) {
+    for (int i = 0; i < kMaxSlots; ++i) {
+      mbar_init(&rec_full[i], 1);
+      mbar_init(&rec_empty[i], 12);
+    }
+    for (int s = 0; s < 2; ++s) {
+      mbar_init(&ops_k[s], 4);
+      mbar_init(&qk_full[s], 1);
+      mbar_init(&s_free[s], 4);
+      mbar_init(&ops_v[s], 4);
+      mbar_init(&p_full[s], 4);
+      mbar_init(&pv_done[s], 1);
+    }
+    abort_flag = 0;
+    fence_mbar_init();
+  }
+  __syncthreads();
+  grid_launch_dependents();
+  int64_t total = 0;  // pages of this CTA's range
+  for (TileWalk w = walk_s; w.left > 0; w.next(p)) total += w.count();
+  if (total <= 0) {
+    grid_dependency_wait();  // block_raw_kernel has finished when this grid has
+    return;
+  }
+  if (warp == 0) {
+    asm volatile("tcgen05.alloc.cta_group::1.sync.aligned.shared::cta.b32 [%0], 512;" ::"r"(smem_u32(&tslot)));
+    asm volatile("tcgen05.relinquish_alloc_permit.cta_group::1.sync.aligned;");
+  }
+  fence_before();
+  __syncthreads();
+  fence_after();
+  const uint32_t tmem = tslot;
+  const TileWalk w0 = walk_s;
+  volatile int* abort_v = &abort_flag;
+  auto fail = [&]() {
+    *abort_v = 1;
+    flag_error(p.status, KVARN_DEV_WAIT_TIMEOUT);
+  };
+  // q~ of a segment's rows, hi + lo, in the order and layout of the QK operand; every warp but the
+  // loader's takes part.  Returns true when the CTA gives up (all warps alike).
+  auto stage_queries = [&](const TileWalk& w, bool bad) -> bool {
+    if (bar_any(kRoleBar, kRoleThreads, bad || *abort_v != 0)) return true;
+    const int wi = warp < kLoadWarp ? warp : warp - 1;
+    const float sc = p.qscale * inv_sqrt_d<D>();
+    const float h0 = lift0(p.kb), h1 = lift1(p.kb);
+    const bool q4 = (reinterpret_cast<uintptr_t>(p.q) & 3u) == 0u;
+    for (int n = wi; n < NR; n += kRoleThreads / 32) {
+      const int r = w.t * NR + n, c = r / p.group;
+      const bool live = c < w.nl;
+      float v[D / 32];
+      const __half* src =
+          p.q + (((int64_t)w.b * p.block + (live ? c : 0)) * p.num_q_heads + w.h * p.group + (r - c * p.group)) * p.d0;
+#pragma unroll
+      for (int e = 0; e < D / 32; e += 2) {
+        const int j = lane * (D / 32) + e;
+        float2 f = make_float2(0.0f, 0.0f);
+        if (live && j < p.d0)
+          f = q4 ? __half22float2(*reinterpret_cast<const __half2*>(src + j))
+                 : make_float2(__half2float(src[j]), __half2float(src[j + 1]));
+        v[e] = f.x;
+        v[e + 1] = f.y;
+      }
+      warp_fwht<D>(v, lane);
+#pragma unroll
+      for (int e = 0; e < D / 32; e += 2) {
+        const int j = lane * (D / 32) + e, c16 = j & 15;
+        const float f = sc * (c16 < 8 ? h0 : h1);
+        const float x = v[e] * f, y = v[e + 1] * f;
+        const __half2 hi = __floats2half2_rn(x, y);
+        const float2 hf = __half22float2(hi);
+        const int kpos = 4 * ((c16 & 7) >> 1) + 2 * (c16 >> 3);
+        const int at = (j >> 4) * S::kStep + (n >> 3) * 256 + (kpos >> 3) * 128 + (n & 7) * 16 + (kpos & 7) * 2;
+        *reinterpret_cast<__half2*>(q_hi + at) = hi;
+        *reinterpret_cast<__half2*>(q_lo + at) = __floats2half2_rn(x - hf.x, y - hf.y);
+      }
+      // padding rows see everything: they get a reference on the first page
+      if (lane == 0) lim_s[n] = live ? w.len + c + 1 - p.window : INT32_MIN;
+    }
+    return bar_any(kRoleBar, kRoleThreads, false);
+  };
+
+  // The softmax warpgroup holds a token's NR logits and NR sums: 208 registers there and 96 in the
+  // other three, 63,488 of the 65,536 the CTA is launched with.
+  if (warp < 4) {
+    asm volatile("setmaxnreg.inc.sync.aligned.u32 208;");
+  } else {
+    asm volatile("setmaxnreg.dec.sync.aligned.u32 96;");
+  }
+  if (warp < 4) {
+    // ---- softmax (thread = token), rescale and the segment's partial (thread = channel) ----
+    const int u = threadIdx.x;
+    const uint32_t lanes = (uint32_t)(32 * warp) << 16;
+    const int kpos = 4 * ((u >> 1) & 3) + 2 * ((u >> 3) & 1) + (u & 1);
+    const int poff = (u >> 4) * S::kStep + (kpos >> 3) * (NR * 16) + (kpos & 7) * 16;
+    const float cf = kTwo24 / lift0(p.kb) * (p.kb == 2 && ((u >> 4) & 1) ? 0.0625f : 1.0f);
+    int64_t g = 0;
+    int r = 0;
+    uint32_t rph = 0;
+    bool bad = false, stop = false;
+    for (TileWalk w = w0; w.left > 0; w.next(p)) {
+      if (stage_queries(w, bad)) break;
+      const int cnt = w.count();
+      const int64_t row = w.row(p);
+      const int c1 = min((w.t * NR + NR - 1) / p.group, w.nl - 1);  // the tile's last new token
+      const int sure = w.len + c1 + 1 - p.window;  // from here on every row's window sees
+      float2 l[NR / 2];
+#pragma unroll
+      for (int i = 0; i < NR / 2; ++i) l[i] = make_float2(0.0f, 0.0f);
+      if (u < NR) {
+        nref_s[u] = 0.0f;
+        max_s[u] = -INFINITY;
+      }
+      bar_any(kSmBar, 128, false);
+      bool unset = true;  // some row has no reference yet
+      for (int i = 0; i < cnt; ++i, ++g) {
+        const int s = (int)(g & 1);
+        const uint32_t par = (uint32_t)((g >> 1) & 1);
+        const bool ok = !bad && wait_all(&qk_full[s], par) && wait_all(&ops_k[s], par) && wait_all(&rec_full[r], rph);
+        float x[NR];
+        if (ok) {
+          fence_after();
+          const float rt = __half2float(reinterpret_cast<const __half*>(recs + r * rec + RL.kfactor)[u]);
+          ld_cols<NR>(tmem + S::kColS + (uint32_t)(s * NR) + lanes, x);
+          const float at = rt * cf;
+          const float* qz = qz_s + s * NR;
+#pragma unroll
+          for (int n = 0; n < NR; n += 4) {
+            const float4 z = *reinterpret_cast<const float4*>(qz + n), m = *reinterpret_cast<const float4*>(nref_s + n);
+            const float2 a = fma2(make_float2(at, at), make_float2(x[n], x[n + 1]),
+                                  fma2(make_float2(rt, rt), make_float2(z.x, z.y), make_float2(m.x, m.y)));
+            const float2 c = fma2(make_float2(at, at), make_float2(x[n + 2], x[n + 3]),
+                                  fma2(make_float2(rt, rt), make_float2(z.z, z.w), make_float2(m.z, m.w)));
+            x[n] = a.x;
+            x[n + 1] = a.y;
+            x[n + 2] = c.x;
+            x[n + 3] = c.y;
+          }
+          fence_before();
+          __syncwarp();
+          if (lane == 0) {
+            mbar_arrive(&s_free[s]);
+            mbar_arrive(&rec_empty[r]);
+          }
+          if (p.window > 0) {
+            const int at0 = w.span.page(w.j + i) * kTile;
+            if (at0 + kTile > p.sink && at0 < sure) {  // an edge page of the window or of the first tokens
+              const int pos = at0 + u;
+#pragma unroll
+              for (int n = 0; n < NR; ++n)
+                if (pos >= p.sink && pos < lim_s[n]) x[n] = -INFINITY;
+            }
+          }
+        } else {
+          if (!bad) fail();
+          bad = true;
+#pragma unroll
+          for (int n = 0; n < NR; ++n) x[n] = 0.0f;
+        }
+        if (++r == slots) {
+          r = 0;
+          rph ^= 1u;
+        }
+        float mx = -INFINITY;
+#pragma unroll
+        for (int n = 0; n < NR; n += 2) mx = fmax3(mx, x[n], x[n + 1]);
+        if (bar_any(kSmBar, 128, bad || unset || mx > kSlack)) {
+          stop = bar_any(kSmBar, 128, bad);
+          if (stop) break;
+          // move the references to the rows' maxima
+#pragma unroll
+          for (int n = 0; n < NR; ++n) {
+            const float v = warp_max(x[n]);
+            if (lane == (n & 31)) warp_s[warp * NR + n] = v;
+          }
+          bar_any(kSmBar, 128, false);
+          bool none = false;
+          if (u < NR) {
+            const float old = max_s[u], ref = -nref_s[u];
+            const float pm = fmaxf(fmaxf(warp_s[u], warp_s[NR + u]), fmaxf(warp_s[2 * NR + u], warp_s[3 * NR + u])) + ref;
+            const float mn = fmaxf(old, pm);
+            none = mn == -INFINITY;
+            const float to = none ? 0.0f : mn;
+            max_s[u] = mn;
+            nref_s[u] = -to;
+            shift_s[u] = ref - to;
+            alpha_s[u] = old == -INFINITY ? 0.0f : ex2_approx(old - mn);
+          }
+          unset = bar_any(kSmBar, 128, none);
+#pragma unroll
+          for (int n = 0; n < NR; n += 2) {
+            x[n] += shift_s[n];
+            x[n + 1] += shift_s[n + 1];
+            l[n / 2] = mul2(l[n / 2], make_float2(alpha_s[n], alpha_s[n + 1]));
+          }
+          if (i > 0) {  // O of the pages before this one
+            if (!wait_all(&pv_done[(g - 1) & 1], (uint32_t)(((g - 1) >> 1) & 1))) {
+              fail();
+              bad = true;
+            } else {
+              fence_after();
+#pragma unroll
+              for (int hf = 0; hf < S::kHalves; ++hf)
+#pragma unroll
+                for (int n0 = 0; n0 < NR; n0 += 16) {
+                  float o[16];
+                  const uint32_t ta = tmem + S::kColO + (uint32_t)(hf * NR + n0) + lanes;
+                  ld_cols<16>(ta, o);
+#pragma unroll
+                  for (int n = 0; n < 16; ++n) o[n] *= alpha_s[n0 + n];
+                  st_32x32b_x16(ta, o);
+                }
+              wait_st();
+            }
+          }
+        }
+        // P of the stage, once PV of the page before the last has read it
+        if (!bad && !wait_all(&pv_done[s], par ^ 1u)) {
+          fail();
+          bad = true;
+        }
+        uint8_t* pb = sm + S::kPOff + s * S::kPBytes + poff;
+#pragma unroll
+        for (int n = 0; n < NR; n += 8) {
+          uint32_t h[4];
+#pragma unroll
+          for (int e = 0; e < 4; ++e) {
+            const float2 v = make_float2(ex2_approx(x[n + 2 * e]), ex2_approx(x[n + 2 * e + 1]));
+            l[n / 2 + e] = add2(l[n / 2 + e], v);
+            h[e] = h2u(__floats2half2_rn(v.x, v.y));
+          }
+          *reinterpret_cast<uint4*>(pb + 16 * n) = make_uint4(h[0], h[1], h[2], h[3]);
+        }
+        fence_proxy_async_smem();
+        fence_before();
+        __syncwarp();
+        if (lane == 0 && !bad) mbar_arrive(&p_full[s]);
+      }
+      if (bar_any(kSmBar, 128, bad || stop)) {
+        bad = true;
+        continue;  // the next stage_queries() ends the loop for every warp
+      }
+      // the segment's partial: l over the tokens, O once its last PV is done
+#pragma unroll
+      for (int n = 0; n < NR; ++n) {
+        float v = (n & 1) ? l[n / 2].y : l[n / 2].x;
+#pragma unroll
+        for (int m = 16; m > 0; m >>= 1) v += __shfl_xor_sync(0xffffffffu, v, m);
+        if (lane == (n & 31)) warp_s[warp * NR + n] = v;
+      }
+      bar_any(kSmBar, 128, false);
+      const int live = min(NR, w.nl * p.group - w.t * NR);  // rows of the tile that exist
+      float* dst = p.part + ((int64_t)blockIdx.x + row) * NR * (D + 4);
+      if (u < live) {
+        float* d = dst + (int64_t)u * (D + 4);
+        d[0] = max_s[u] == -INFINITY ? -INFINITY : -nref_s[u];
+        d[1] = (warp_s[u] + warp_s[NR + u]) + (warp_s[2 * NR + u] + warp_s[3 * NR + u]);
+      }
+      if (w.j == 0 && u == 0) {
+        const int64_t last = owner_cta(part_s, w.row0 + kFixUnits + w.span.count - 1);
+        p.row_info[row] = make_int2((int)((int64_t)blockIdx.x + row), (int)(last - blockIdx.x + 1));
+      }
+      if (!wait_all(&pv_done[(g - 1) & 1], (uint32_t)(((g - 1) >> 1) & 1))) {
+        fail();
+        bad = true;
+      } else {
+        fence_after();
+#pragma unroll
+        for (int hf = 0; hf < S::kHalves; ++hf) {
+#pragma unroll
+          for (int n0 = 0; n0 < NR; n0 += 16) {
+            float o[16];
+            ld_cols<16>(tmem + S::kColO + (uint32_t)(hf * NR + n0) + lanes, o);
+            if (D >= 128 || u < D) {
+#pragma unroll
+              for (int n = 0; n < 16; ++n)
+                if (n0 + n < live) dst[(int64_t)(n0 + n) * (D + 4) + 4 + hf * 128 + u] = o[n];
+            }
+          }
+        }
+        fence_before();
+      }
+    }
+  } else if (warp < kVWarp) {
+    // ---- K codes -> tensor memory, B = q~ s' (hi + lo), q~ . z' ----
+    const int t = threadIdx.x - 32 * kKWarp, q = warp - kKWarp;
+    const int grp = t >> 3, nl = t & 7;
+    const int gq = lane >> 2, tq = lane & 3;
+    const float i0 = 1.0f / lift0(p.kb), i1 = 1.0f / lift1(p.kb);
+    int64_t g = 0;
+    int r = 0;
+    uint32_t rph = 0;
+    bool bad = false;
+    for (TileWalk w = w0; w.left > 0; w.next(p)) {
+      if (stage_queries(w, bad)) break;
+      const int cnt = w.count();
+      for (int i = 0; i < cnt; ++i, ++g) {
+        const int s = (int)(g & 1);
+        const uint32_t par = (uint32_t)((g >> 1) & 1);
+        // QK of the page before the last has read the codes and B, the softmax its q~ . z'
+        if (!wait_all(&rec_full[r], rph) || !wait_all(&qk_full[s], par ^ 1u) || !wait_all(&s_free[s], par ^ 1u) ||
+            *abort_v != 0) {
+          bad = true;
+          fail();
+          break;
+        }
+        fence_after();
+        const uint8_t* R = recs + r * rec;
+        // fragment (o, i) of 16 tokens x 16 channels is lanes 16o.., columns 8i..8i+7; column
+        // 2tq + h holds channels 16i + 8h + 2tq, +1 of its tokens g and g + 8
+        const uint32_t ta = tmem + S::kColK + (uint32_t)(s * (D / 2)) + ((uint32_t)(32 * q) << 16);
+        const uint4* kc = reinterpret_cast<const uint4*>(R + RL.kcodes);
+        if (p.kb == 4) {
+#pragma unroll
+          for (int oo = 0; oo < 2; ++oo)
+#pragma unroll
+            for (int kq = 0; kq < D / 64; ++kq) {
+              const uint4 w4 = kc[((2 * q + oo) * (D / 64) + kq) * 32 + lane];
+              const uint32_t ws[4] = {w4.x, w4.y, w4.z, w4.w};
+              uint32_t rr[16];
+#pragma unroll
+              for (int e = 0; e < 4; ++e) {
+                const uint32_t x = ws[e], y = x >> 8;
+                rr[4 * e] = x & 0x000F000Fu;
+                rr[4 * e + 1] = x & 0x00F000F0u;
+                rr[4 * e + 2] = y & 0x000F000Fu;
+                rr[4 * e + 3] = y & 0x00F000F0u;
+              }
+              st_16x256b_x4(ta + ((uint32_t)(16 * oo) << 16) + 32 * kq, rr);
+            }
+        } else if (p.kb == 8) {
+#pragma unroll
+          for (int oo = 0; oo < 2; ++oo)
+#pragma unroll
+            for (int kp = 0; kp < D / 32; ++kp) {
+              const uint4 w4 = kc[((2 * q + oo) * (D / 32) + kp) * 32 + lane];
+              uint32_t rr[8], a[4];
+              unpack_k8(w4.x, w4.y, a);
+              rr[0] = a[0];
+              rr[1] = a[2];
+              rr[2] = a[1];
+              rr[3] = a[3];
+              unpack_k8(w4.z, w4.w, a);
+              rr[4] = a[0];
+              rr[5] = a[2];
+              rr[6] = a[1];
+              rr[7] = a[3];
+              st_16x256b_x2(ta + ((uint32_t)(16 * oo) << 16) + 16 * kp, rr);
+            }
+        } else {  // 2-bit: a word holds token blocks 2q and 2q + 1, the odd one's codes 4 bits higher
+#pragma unroll
+          for (int kq = 0; kq < D / 64; ++kq) {
+            const uint4 w4 = kc[(q * (D / 64) + kq) * 32 + lane];
+            const uint32_t ws[4] = {w4.x, w4.y, w4.z, w4.w};
+#pragma unroll
+            for (int oo = 0; oo < 2; ++oo) {
+              uint32_t rr[16];
+#pragma unroll
+              for (int e = 0; e < 4; ++e) {
+                const uint32_t x = ws[e], y = x >> 8;
+                rr[4 * e] = x & (0x00030003u << (4 * oo));
+                rr[4 * e + 1] = x & (0x000C000Cu << (4 * oo));
+                rr[4 * e + 2] = y & (0x00030003u << (4 * oo));
+                rr[4 * e + 3] = y & (0x000C000Cu << (4 * oo));
+              }
+              st_16x256b_x4(ta + ((uint32_t)(16 * oo) << 16) + 32 * kq, rr);
+            }
+          }
+        }
+        // B rows n = 8 rg + nl over K indexes 8kb..8kb+7 of step kk (channels cb + {0, 1, 8, 9, 2,
+        // 3, 10, 11}): 16 thread groups of 8 over the D / 8 (kk, kb) pairs
+        uint8_t* bs = sm + S::kBOff + s * 2 * S::kBHalf;
+#pragma unroll
+        for (int c2 = 0; c2 < (D > 128 ? 2 : 1); ++c2) {
+          const int oc = D == 64 ? (grp & 7) : grp + 16 * c2;
+          const int kk = oc >> 1, kb = oc & 1, cb = 16 * kk + 4 * kb;
+          const uint2 sa = *reinterpret_cast<const uint2*>(R + RL.kscale + 2 * cb);
+          const uint2 sb = *reinterpret_cast<const uint2*>(R + RL.kscale + 2 * (cb + 8));
+          const __half2 sv[4] = {u2h2(sa.x), u2h2(sb.x), u2h2(sa.y), u2h2(sb.y)};
+#pragma unroll
+          for (int rg = 0; rg < NR / 8; ++rg) {
+            if (D == 64 && (rg & 1) != (grp >> 3)) continue;
+            const int at = kk * S::kStep + rg * 256 + kb * 128 + nl * 16;
+            const uint4 h4 = *reinterpret_cast<const uint4*>(q_hi + at);
+            const uint4 l4 = *reinterpret_cast<const uint4*>(q_lo + at);
+            const __half2 qh[4] = {u2h2(h4.x), u2h2(h4.y), u2h2(h4.z), u2h2(h4.w)};
+            const __half2 ql[4] = {u2h2(l4.x), u2h2(l4.y), u2h2(l4.z), u2h2(l4.w)};
+            uint32_t hi[4], lo[4];
+#pragma unroll
+            for (int e = 0; e < 4; ++e) {
+              const __half2 hv = __hmul2(qh[e], sv[e]);
+              hi[e] = h2u(hv);
+              lo[e] = h2u(__hfma2(ql[e], sv[e], __hfma2(qh[e], sv[e], __hneg2(hv))));
+            }
+            *reinterpret_cast<uint4*>(bs + at) = make_uint4(hi[0], hi[1], hi[2], hi[3]);
+            *reinterpret_cast<uint4*>(bs + S::kBHalf + at) = make_uint4(lo[0], lo[1], lo[2], lo[3]);
+          }
+        }
+        // q~ . z' of rows 16q..16q+15 on mma.sync: B column 0 holds z' of channels 0..7 of every
+        // 16, column 1 of channels 8..15, whose q~ carry different lifts
+        if (16 * q < NR) {
+          float acc[4] = {0.0f, 0.0f, 0.0f, 0.0f};
+          const int m = lane >> 3;
+          const uint32_t qa = smem_u32(q_hi) + (2 * q + (m & 1)) * 256 + (m >> 1) * 128 + (lane & 7) * 16;
+          const bool mine = gq < 2 && (tq & 1) == gq;
+          const uint8_t* zc = R + RL.kzero + 2 * (8 * (tq & 1) + 2 * (tq >> 1));
+#pragma unroll
+          for (int kk = 0; kk < S::kSteps; ++kk) {
+            const uint32_t b0 = mine ? *reinterpret_cast<const uint32_t*>(zc + 32 * kk) : 0u;
+            const uint32_t b1 = mine ? *reinterpret_cast<const uint32_t*>(zc + 32 * kk + 8) : 0u;
+            uint32_t a[4];
+            ldsm_x4(qa + kk * S::kStep, a);
+            mma16816(acc, a, b0, b1);
+            ldsm_x4(qa + S::kBHalf + kk * S::kStep, a);
+            mma16816(acc, a, b0, b1);
+          }
+          if (tq == 0) {
+            float* qz = qz_s + s * NR + 16 * q + gq;
+            qz[0] = acc[0] * i0 + acc[1] * i1;
+            qz[8] = acc[2] * i0 + acc[3] * i1;
+          }
+        }
+        wait_st();
+        fence_proxy_async_smem();
+        fence_before();
+        __syncwarp();
+        if (lane == 0) {
+          mbar_arrive(&ops_k[s]);
+          mbar_arrive(&rec_empty[r]);
+        }
+        if (++r == slots) {
+          r = 0;
+          rph ^= 1u;
+        }
+      }
+    }
+  } else if (warp < kLoadWarp) {
+    // ---- V~ -> tensor memory: channels on the lanes, tokens along K ----
+    const int q = warp - kVWarp;
+    const int gq = lane >> 2, tq = lane & 3;
+    int64_t g = 0;
+    int r = 0;
+    uint32_t rph = 0;
+    bool bad = false;
+    for (TileWalk w = w0; w.left > 0; w.next(p)) {
+      if (stage_queries(w, bad)) break;
+      const int cnt = w.count();
+      for (int i = 0; i < cnt; ++i, ++g) {
+        const int s = (int)(g & 1);
+        const int vs = S::kVStages == 2 ? s : 0;
+        // PV of the page that last used this buffer
+        const int64_t gp = g - S::kVStages;
+        if (!wait_all(&rec_full[r], rph) ||
+            (gp >= 0 && !wait_all(&pv_done[gp & 1], (uint32_t)((gp >> 1) & 1))) || *abort_v != 0) {
+          bad = true;
+          fail();
+          break;
+        }
+        fence_after();
+        const uint8_t* R = recs + r * rec;
+        const __half2* vsc = reinterpret_cast<const __half2*>(R + RL.vscale);
+        const __half2* vzr = reinterpret_cast<const __half2*>(R + RL.vzero);
+        const __half* vch = reinterpret_cast<const __half*>(R + RL.vfactor);
+        const uint2* vc = reinterpret_cast<const uint2*>(R + RL.vcodes);
+        const uint32_t ta = tmem + S::kColV + (uint32_t)(vs * 64 * S::kHalves) + ((uint32_t)(32 * q) << 16);
+        if (D >= 128 || q < D / 32) {
+          __half2 cv[S::kHalves][2][2];  // channel factors of rows g, g + 8 of the two blocks
+#pragma unroll
+          for (int hf = 0; hf < S::kHalves; ++hf)
+#pragma unroll
+            for (int ii = 0; ii < 2; ++ii)
+#pragma unroll
+              for (int rho = 0; rho < 2; ++rho)
+                cv[hf][ii][rho] = __half2half2(vch[16 * (8 * hf + 2 * q + ii) + gq + 8 * rho]);
+#pragma unroll
+          for (int o2 = 0; o2 < 4; ++o2) {
+            __half2 s2[2][2], z2[2][2];  // [token block of the pair][token half]
+#pragma unroll
+            for (int f = 0; f < 2; ++f)
+#pragma unroll
+              for (int h = 0; h < 2; ++h) {
+                s2[f][h] = vsc[8 * (2 * o2 + f) + 4 * h + tq];
+                z2[f][h] = vzr[8 * (2 * o2 + f) + 4 * h + tq];
+              }
+#pragma unroll
+            for (int hf = 0; hf < S::kHalves; ++hf) {
+              const int cb = 8 * hf + 2 * q;  // channel blocks cb, cb + 1: adjacent words
+              uint32_t x[2][2];               // [channel block][word of token block f]
+              if (p.vb == 2) {
+                const uint2 a = vc[(((o2 * (D / 64) + (cb >> 2)) * 32 + lane) * 4 + (cb & 3)) >> 1];
+                x[0][0] = x[0][1] = a.x;
+                x[1][0] = x[1][1] = a.y;
+              } else {
+#pragma unroll
+                for (int f = 0; f < 2; ++f) {
+                  const uint2 a = vc[((((2 * o2 + f) * (D / 64) + (cb >> 2)) * 32 + lane) * 4 + (cb & 3)) >> 1];
+                  x[0][f] = a.x;
+                  x[1][f] = a.y;
+                }
+              }
+#pragma unroll
+              for (int ii = 0; ii < 2; ++ii) {
+                uint32_t rr[8];
+#pragma unroll
+                for (int f = 0; f < 2; ++f)
+#pragma unroll
+                  for (int rho = 0; rho < 2; ++rho) {
+                    const uint32_t y = rho ? x[ii][f] >> 8 : x[ii][f];
+#pragma unroll
+                    for (int h = 0; h < 2; ++h) {
+                      // the code's bits under an exponent that makes them base + code, minus base
+                      const int k2 = 4 * f + 2 * h, k4 = 4 * h;
+                      uint32_t cu;
+                      if (p.vb == 2)
+                        cu = h2u(__hsub2(u2h2((y & (0x00030003u << k2)) | (0x64006400u - (uint32_t)k2 * 0x04000400u)),
+                                         u2h2(0x64006400u - (uint32_t)k2 * 0x04000400u)));
+                      else
+                        cu = h2u(__hsub2(u2h2((y & (0x000F000Fu << k4)) | (0x64006400u - (uint32_t)k4 * 0x04000400u)),
+                                         u2h2(0x64006400u - (uint32_t)k4 * 0x04000400u)));
+                      rr[4 * f + 2 * rho + h] = h2u(__hmul2(__hfma2(u2h2(cu), s2[f][h], z2[f][h]), cv[hf][ii][rho]));
+                    }
+                  }
+                st_16x256b_x2(ta + ((uint32_t)(16 * ii) << 16) + 64 * hf + 16 * o2, rr);
+              }
+            }
+          }
+        }
+        wait_st();
+        fence_before();
+        __syncwarp();
+        if (lane == 0) {
+          mbar_arrive(&ops_v[s]);
+          mbar_arrive(&rec_empty[r]);
+        }
+        if (++r == slots) {
+          r = 0;
+          rph ^= 1u;
+        }
+      }
+    }
+  } else if (warp == kLoadWarp) {
+    // ---- page records -> the ring ----
+    if (lane == 0) {
+      int64_t g = 0;
+      int r = 0;
+      uint32_t rph = 0;
+      bool bad = false;
+      for (TileWalk w = w0; w.left > 0 && !bad; w.next(p)) {
+        const int cnt = w.count();
+        const int32_t* bt = p.block_table + (int64_t)w.b * p.max_pages;
+        for (int i = 0; i < cnt; ++i, ++g) {
+          int64_t id = bt[w.span.page(w.j + i)];
+          if (id < 0 || id >= p.num_pool_pages) {
+            flag_error(p.status, KVARN_DEV_BAD_PAGE_ID);
+            id = 0;
+          }
+          if (!mbar_wait(&rec_empty[r], rph ^ 1u) || *abort_v != 0) {
+            fail();
+            bad = true;
+            break;
+          }
+          fence_proxy_async_smem();
+          mbar_expect_tx(&rec_full[r], (uint32_t)rec);
+          bulk_copy_g2s(recs + r * rec, p.pool + (id * p.num_kv_heads + w.h) * (int64_t)rec, (uint32_t)rec, &rec_full[r]);
+          if (++r == slots) {
+            r = 0;
+            rph ^= 1u;
+          }
+        }
+      }
+      // copies still in flight land before the CTA may leave
+      for (int64_t k = g > slots ? g - slots : 0; k < g; ++k)
+        mbar_wait(&rec_full[k % slots], (uint32_t)((k / slots) & 1));
+    }
+    __syncwarp();
+  } else {
+    // ---- MMA issue: one lane; QK of even and of odd pages on two warps, PV on a third ----
+    const bool is_pv = warp == kPvWarp;
+    int64_t g = 0;
+    bool bad = false;
+    uint64_t* last = nullptr;
+    uint32_t last_par = 0;
+    for (TileWalk w = w0; w.left > 0; w.next(p)) {
+      if (stage_queries(w, __any_sync(0xffffffffu, bad))) break;
+      const int cnt = w.count();
+      if (lane == 0) {
+        for (int i = 0; i < cnt; ++i) {
+          const int64_t gi = g + i;
+          const int s = (int)(gi & 1);
+          const uint32_t par = (uint32_t)((gi >> 1) & 1);
+          if (!is_pv && s != warp - kQkWarp) continue;
+          const bool ok = is_pv ? mbar_wait(&ops_v[s], par) && mbar_wait(&p_full[s], par)
+                                : mbar_wait(&ops_k[s], par) && mbar_wait(&s_free[s], par ^ 1u);
+          if (!ok || *abort_v != 0) {
+            fail();
+            bad = true;
+            break;
+          }
+          fence_after();
+          if (is_pv) {
+            const uint32_t pb = smem_u32(sm + S::kPOff + s * S::kPBytes);
+            const uint32_t av = tmem + S::kColV + (S::kVStages == 2 ? (uint32_t)(s * 64 * S::kHalves) : 0u);
+#pragma unroll
+            for (int hf = 0; hf < S::kHalves; ++hf)
+#pragma unroll
+              for (int o = 0; o < 8; ++o)
+                mma_ts(tmem + S::kColO + hf * NR, av + 64 * hf + 8 * o, smem_desc(pb + o * S::kStep, NR * 16, 128),
+                       kIdescPV<NR>, (uint32_t)(i > 0 || o > 0));
+            mma_commit(&pv_done[s]);
+            last = &pv_done[s];
+          } else {
+            const uint32_t bb = smem_u32(sm + S::kBOff + s * 2 * S::kBHalf);
+            const uint32_t ak = tmem + S::kColK + (uint32_t)(s * (D / 2));
+#pragma unroll
+            for (int kk = 0; kk < 2 * S::kSteps; ++kk)  // hi, then lo
+              mma_ts(tmem + S::kColS + (uint32_t)(s * NR), ak + 8 * (kk % S::kSteps),
+                     smem_desc(bb + kk * S::kStep, 128, 256), kIdescQK<NR>, (uint32_t)(kk > 0));
+            mma_commit(&qk_full[s]);
+            last = &qk_full[s];
+          }
+          last_par = par;
+        }
+      }
+      g += cnt;
+      __syncwarp();
+    }
+    if (last != nullptr) mbar_wait(last, last_par);  // this lane's MMAs have completed
+    __syncwarp();
+  }
+
+  // ---- tear-down: every role is past its last wait ----
+  fence_before();
+  __syncthreads();
+  if (warp == 0) {
+    fence_after();
+    asm volatile("tcgen05.dealloc.cta_group::1.sync.aligned.b32 %0, 512;" ::"r"(tmem));
+  }
+  grid_dependency_wait();  // block_raw_kernel has finished when this grid has
+}
+
+// ---- the open tile's raw tokens and the new tokens -------------------------------------------
+// One CTA of 8 warps per (128 query rows, kv head, sequence), warp w taking rows 16w..16w+15; K and
+// V rows stream through shared memory 64 tokens at a time (cp.async into swizzled fp16 rows, two
+// stages), the open tile's first, then the new tokens'.  mma.sync m16n8k16: A = the fp16 queries
+// (exact products; the scale applied to the fp32 sums), B = K rows by ldmatrix; online softmax in
+// the log2 domain; PV with the probabilities as fp16 hi + lo.  A row that sees nothing leaves
+// m = -inf, l = 0, o = 0.
+template <int D>
+__global__ void __launch_bounds__(256, 1) block_raw_kernel(BlockParams p) {
+  constexpr int NB = 64;      // tokens per stage
+  constexpr int NN = D / 8;   // channel n-tiles
+  constexpr int KK = D / 16;  // channel k-steps
+  constexpr uint32_t kStage = 2 * NB * 2 * D;  // K rows then V rows, fp16
+  extern __shared__ __align__(128) uint8_t cs[];
+  const int lane = threadIdx.x & 31, wi = threadIdx.x >> 5;
+  const int g = lane >> 2, tq = lane & 3;
+  const int b = blockIdx.z, h = blockIdx.y;
+  const int G = p.group;
+  grid_dependency_wait();    // lengths, tiles and tokens may come from the previous kernel
+  grid_launch_dependents();  // block_cache_kernel reads nothing of this one
+  const int raw_len = p.seq_lens[b], len = blk::cached_len(p, b), nl = blk::new_len(p, b);
+  int n_part = len % kTile;
+  if (blockIdx.x == 0 && h == 0 && threadIdx.x == 0) {
+    if (raw_len != len || (p.new_lens != nullptr && p.new_lens[b] != nl)) flag_error(p.status, KVARN_DEV_SEQ_TOO_LONG);
+    if (n_part > 0 && p.partial_k == nullptr) flag_error(p.status, KVARN_DEV_NO_PARTIAL);
+  }
+  if (p.partial_k == nullptr) n_part = 0;
+  const int part0 = len - len % kTile;  // position of the open tile's first token
+  const int rows = nl * G;
+  const int rbase = blockIdx.x * 128;
+  if (rbase >= rows) return;
+  const int r0 = rbase + 16 * wi;  // this warp's first query row
+  const bool warp_live = r0 < rows;
+  const int c_first = rbase / G, c_last = min(rbase + 127, rows - 1) / G;  // the CTA's new tokens
+  const int ra = r0 + g, rb = r0 + g + 8;
+  const int ca = ra < rows ? ra / G : -1, cb = rb < rows ? rb / G : -1;  // -1: padding row
+  const uint32_t sbase = smem_u32(cs);
+  const int64_t rstride = (int64_t)p.num_kv_heads * p.d0;
+  const int64_t nbase = ((int64_t)b * p.block * p.num_kv_heads + h) * p.d0;
+  const int64_t pbase = ((int64_t)b * p.num_kv_heads + h) * kTile * p.d0;
+  const int dch = p.d0 / 8;  // 16-byte chunks of a row (d0 % 8 == 0)
+  // stages: `pblk` of the open tile, then those of the new tokens any row of the CTA may see
+  const int pblk = (n_part + NB - 1) / NB;
+  const int n_new = p.mask != nullptr ? nl : c_last + 1;
+  const int nblk = pblk + (n_new + NB - 1) / NB;
+  // whether no row of the CTA sees a token of stage `blk` (windows only)
+  auto skipped = [&](int blk) {
+    if (p.window <= 0) return false;
+    const int at = blk < pblk ? part0 + blk * NB : len + (blk - pblk) * NB;  // position of its first token
+    return at >= p.sink && at + NB <= len + c_first + 1 - p.window;
+  };
+  auto next_blk = [&](int blk) {
+    do ++blk;
+    while (blk < nblk && skipped(blk));
+    return blk;
+  };
+  auto stage = [&](int blk, int buf) {
+    const uint32_t base = sbase + (uint32_t)buf * kStage;
+    const bool part = blk < pblk;
+    const int t0 = part ? blk * NB : (blk - pblk) * NB;
+    const int n = part ? n_part : n_new;
+    const __half* kg = part ? p.partial_k + pbase : p.new_k + nbase;
+    const __half* vg = part ? p.partial_v + pbase : p.new_v + nbase;
+    const int64_t stride = part ? p.d0 : rstride;
+    for (int qi = threadIdx.x; qi < 2 * NB * (D / 8); qi += blockDim.x) {
+      const int r = qi / (D / 8), c = qi - r * (D / 8);
+      const int t = t0 + (r < NB ? r : r - NB);
+      const bool in = t < n && c < dch;
+      const __half* src = (r < NB ? kg : vg) + (int64_t)t * stride + 8 * c;
+      cp_async_16(base + swz_row<D>(r, c), in ? src : p.new_k, in ? 16u : 0u);
+    }
+    cp_async_commit_all();
+  };
+  int blk = next_blk(-1);
+  if (blk < nblk) stage(blk, 0);
+  auto qrow = [&](int r) {
+    const int c = r / G, j = r - c * G;
+    return p.q + (((int64_t)b * p.block + c) * p.num_q_heads + h * G + j) * p.d0;
+  };
+  const __half* qa = qrow(ca >= 0 ? ra : 0);
+  const __half* qb = qrow(cb >= 0 ? rb : 0);
+  const bool q4 = (reinterpret_cast<uintptr_t>(p.q) & 3u) == 0u;
+  auto pair = [&](const __half* row, bool ok, int ch) -> uint32_t {
+    if (!(ok && ch < p.d0)) return 0u;
+    return q4 ? *reinterpret_cast<const uint32_t*>(row + ch) : h2u(__halves2half2(row[ch], row[ch + 1]));
+  };
+  // A fragment of channels 16kk..: rows g (ra) and g + 8 (rb)
+  auto afrag = [&](int kk, uint32_t (&a)[4]) {
+    const int ch = 16 * kk + 2 * tq;
+    a[0] = pair(qa, ca >= 0, ch);
+    a[1] = pair(qb, cb >= 0, ch);
+    a[2] = pair(qa, ca >= 0, ch + 8);
+    a[3] = pair(qb, cb >= 0, ch + 8);
+  };
+  constexpr bool kKeepQ = D <= 128;  // head_dim 256 reads the fragments again for every stage
+  uint32_t aq[kKeepQ ? KK : 1][4];
+  if constexpr (kKeepQ) {
+#pragma unroll
+    for (int kk = 0; kk < KK; ++kk) afrag(kk, aq[kk]);
+  }
+  float ma = -INFINITY, mb = -INFINITY, la = 0.0f, lb = 0.0f;  // l: this lane's share
+  float o[NN][4];
+#pragma unroll
+  for (int n = 0; n < NN; ++n) o[n][0] = o[n][1] = o[n][2] = o[n][3] = 0.0f;
+  for (int buf = 0; blk < nblk; buf ^= 1) {
+    const int nxt = next_blk(blk);
+    if (nxt < nblk) {
+      stage(nxt, buf ^ 1);  // its buffer was released by the barrier closing the stage before
+      cp_async_wait_prev();
+    } else {
+      cp_async_wait_all();
+    }
+    __syncthreads();
+    const bool part = blk < pblk;
+    const int t0 = part ? blk * NB : (blk - pblk) * NB;
+    const int n = part ? n_part : n_new;
+    // bit 8nt + 2tq + e of va / vb: row ra / rb sees token t0 + 8nt + 2tq + e
+    uint64_t va = 0, vb = 0;
+    if (warp_live) {
+      if (!part && p.mask != nullptr) {
+        auto bits = [&](int c) -> uint64_t {
+          if (c < 0) return 0;
+          const uint32_t* m = p.mask + ((int64_t)b * p.block + c) * p.mask_words;
+          const int w = t0 / 32;
+          return (uint64_t)m[w] | ((uint64_t)(w + 1 < p.mask_words ? m[w + 1] : 0u) << 32);
+        };
+        va = bits(ca);
+        vb = bits(cb);
+      } else {
+        const int at = part ? part0 + t0 : len + t0;  // position of the stage's first token
+        auto bits = [&](int c) -> uint64_t {
+          if (c < 0) return 0;
+          const int upto = len + c + 1 - at;                            // tokens up to the query's own
+          uint64_t v = upto >= 64 ? ~0ull : (upto <= 0 ? 0ull : (1ull << upto) - 1ull);
+          if (p.window > 0) {
+            const int drop = upto - p.window, keep = p.sink - at;       // tokens before the window / sinks
+            const uint64_t old = drop >= 64 ? ~0ull : (drop <= 0 ? 0ull : (1ull << drop) - 1ull);
+            const uint64_t snk = keep >= 64 ? ~0ull : (keep <= 0 ? 0ull : (1ull << keep) - 1ull);
+            v &= ~old | snk;
+          }
+          return v;
+        };
+        va = bits(ca);
+        vb = bits(cb);
+      }
+      const uint64_t in = n - t0 >= 64 ? ~0ull : (1ull << (n - t0)) - 1ull;
+      va &= in;
+      vb &= in;
+    }
+    if (__any_sync(0xffffffffu, (va | vb) != 0ull)) {
+      const uint32_t base = sbase + (uint32_t)buf * kStage;
+      float s[NB / 8][4];
+#pragma unroll
+      for (int nt = 0; nt < NB / 8; ++nt) s[nt][0] = s[nt][1] = s[nt][2] = s[nt][3] = 0.0f;
+#pragma unroll
+      for (int kk = 0; kk < KK; ++kk) {
+        uint32_t a[4];
+        if constexpr (kKeepQ) {
+#pragma unroll
+          for (int e = 0; e < 4; ++e) a[e] = aq[kk][e];
+        } else {
+          afrag(kk, a);
+        }
+#pragma unroll
+        for (int np = 0; np < NB / 16; ++np) {  // token n-tiles 2np, 2np + 1
+          uint32_t bk[4];
+          ldsm_x4(base + swz_row<D>(16 * np + (lane & 7) + 8 * (lane >> 4), 2 * kk + ((lane >> 3) & 1)), bk);
+          mma16816(s[2 * np], a, bk[0], bk[1]);
+          mma16816(s[2 * np + 1], a, bk[2], bk[3]);
+        }
+      }
+      float mxa = -INFINITY, mxb = -INFINITY;
+#pragma unroll
+      for (int nt = 0; nt < NB / 8; ++nt) {
+#pragma unroll
+        for (int e = 0; e < 2; ++e) {
+          const int t = 8 * nt + 2 * tq + e;
+          s[nt][e] = ((va >> t) & 1u) ? s[nt][e] * p.qscale : -INFINITY;
+          s[nt][2 + e] = ((vb >> t) & 1u) ? s[nt][2 + e] * p.qscale : -INFINITY;
+          mxa = fmaxf(mxa, s[nt][e]);
+          mxb = fmaxf(mxb, s[nt][2 + e]);
+        }
+      }
+      mxa = fmaxf(mxa, __shfl_xor_sync(0xffffffffu, mxa, 1));
+      mxa = fmaxf(mxa, __shfl_xor_sync(0xffffffffu, mxa, 2));
+      mxb = fmaxf(mxb, __shfl_xor_sync(0xffffffffu, mxb, 1));
+      mxb = fmaxf(mxb, __shfl_xor_sync(0xffffffffu, mxb, 2));
+      const float na = fmaxf(ma, mxa), nb = fmaxf(mb, mxb);
+      const float sa = na == -INFINITY ? 0.0f : na, sb = nb == -INFINITY ? 0.0f : nb;
+      const float aa = ma == -INFINITY ? 0.0f : exp2f(ma - na);
+      const float ab = mb == -INFINITY ? 0.0f : exp2f(mb - nb);
+      ma = na;
+      mb = nb;
+      float pa = 0.0f, pb = 0.0f;
+#pragma unroll
+      for (int nt = 0; nt < NB / 8; ++nt) {
+        s[nt][0] = exp2f(s[nt][0] - sa);
+        s[nt][1] = exp2f(s[nt][1] - sa);
+        s[nt][2] = exp2f(s[nt][2] - sb);
+        s[nt][3] = exp2f(s[nt][3] - sb);
+        pa += s[nt][0] + s[nt][1];
+        pb += s[nt][2] + s[nt][3];
+      }
+      la = fmaf(la, aa, pa);
+      lb = fmaf(lb, ab, pb);
+#pragma unroll
+      for (int n2 = 0; n2 < NN; ++n2) {
+        o[n2][0] *= aa;
+        o[n2][1] *= aa;
+        o[n2][2] *= ab;
+        o[n2][3] *= ab;
+      }
+#pragma unroll
+      for (int ks = 0; ks < NB / 16; ++ks) {
+        if (t0 + 16 * ks >= n) break;  // past the tokens (warp-uniform)
+        // A = p of tokens t0 + 16ks..: n-tiles 2ks (k 0..7) and 2ks + 1 (k 8..15), hi + lo
+        uint32_t ah[4], al[4];
+#pragma unroll
+        for (int i = 0; i < 4; ++i) {
+          const float x = s[2 * ks + (i >> 1)][2 * (i & 1)], y = s[2 * ks + (i >> 1)][2 * (i & 1) + 1];
+          const __half2 hi = __floats2half2_rn(x, y);
+          const float2 hf = __half22float2(hi);
+          ah[i] = h2u(hi);
+          al[i] = h2u(__floats2half2_rn(x - hf.x, y - hf.y));
+        }
+#pragma unroll
+        for (int np = 0; np < NN / 2; ++np) {  // channel n-tiles 2np, 2np + 1
+          uint32_t bv[4];
+          ldsm_x4_trans(base + swz_row<D>(NB + 16 * ks + (lane & 7) + 8 * ((lane >> 3) & 1), 2 * np + (lane >> 4)), bv);
+          mma16816(o[2 * np], ah, bv[0], bv[1]);
+          mma16816(o[2 * np], al, bv[0], bv[1]);
+          mma16816(o[2 * np + 1], ah, bv[2], bv[3]);
+          mma16816(o[2 * np + 1], al, bv[2], bv[3]);
+        }
+      }
+    }
+    __syncthreads();  // the stage buffer is refilled two stages on
+    blk = nxt;
+  }
+  if (!warp_live) return;
+  la += __shfl_xor_sync(0xffffffffu, la, 1);
+  la += __shfl_xor_sync(0xffffffffu, la, 2);
+  lb += __shfl_xor_sync(0xffffffffu, lb, 1);
+  lb += __shfl_xor_sync(0xffffffffu, lb, 2);
+  const int64_t row0 = ((int64_t)b * p.num_kv_heads + h) * p.tiles * p.tile_rows;
+  auto store = [&](int r, int hf, float m, float l) {  // hf: o[.][2 hf..2 hf + 1]
+    float* dst = p.raw_part + (row0 + r) * (D + 4);
+#pragma unroll
+    for (int n = 0; n < NN; ++n)
+      *reinterpret_cast<float2*>(dst + 4 + 8 * n + 2 * tq) = make_float2(o[n][2 * hf], o[n][2 * hf + 1]);
+    if (tq == 0) *reinterpret_cast<float2*>(dst) = make_float2(m, l);
+  };
+  if (ca >= 0) store(ra, 0, ma, la);
+  if (cb >= 0) store(rb, 1, mb, lb);
+}
+
+// ---- the merge -------------------------------------------------------------------------------
+// One warp per (sequence, new token, query head): the cache partials of the row's tile are summed
+// with their weights and rotated back [R is orthonormal and symmetric], the raw partial joins in the
+// original basis.  Rows past a sequence's new tokens are not written.
+template <int D>
+__global__ void __launch_bounds__(128) block_merge_kernel(BlockParams p) {
+  constexpr int E = D / 32;
+  const int lane = threadIdx.x & 31;
+  const int64_t gw = (int64_t)blockIdx.x * 4 + (threadIdx.x >> 5);
+  grid_dependency_wait();
+  grid_launch_dependents();
+  if (gw >= (int64_t)p.batch * p.block * p.num_q_heads) return;
+  const int hq = (int)(gw % p.num_q_heads);
+  const int64_t bc = gw / p.num_q_heads;
+  const int b = (int)(bc / p.block), c = (int)(bc - (int64_t)b * p.block);
+  const int len = blk::cached_len(p, b), nl = blk::new_len(p, b);
+  if (c >= nl) return;
+  const int h = hq / p.group;
+  const int r = c * p.group + (hq - h * p.group);
+  const int t = r / p.tile_rows;
+  const int64_t row = ((int64_t)b * p.num_kv_heads + h) * p.tiles + t;
+  const int in_tile = r - t * p.tile_rows;
+  const float* raw = p.raw_part + (row * p.tile_rows + in_tile) * (D + 4);
+  const float2 rml = *reinterpret_cast<const float2*>(raw);
+  float ro[E];
+  load_f32<E>(raw + 4 + lane * E, ro);
+  float M = rml.x, lsum = 0.0f;
+  float v[E];
+#pragma unroll
+  for (int e = 0; e < E; ++e) v[e] = 0.0f;
+  const bool cache = blk::tile_span(p, len, nl, t).count > 0;
+  if (cache) {
+    const int2 info = p.row_info[row];
+    const int64_t step = (int64_t)p.tile_rows * (D + 4);
+    const float* base = p.part + (int64_t)info.x * step + (int64_t)in_tile * (D + 4);
+    for (int s = lane; s < info.y; s += 32) M = fmaxf(M, base[s * step]);
+#pragma unroll
+    for (int m = 16; m > 0; m >>= 1) M = fmaxf(M, __shfl_xor_sync(0xffffffffu, M, m));
+    const float ref = M == -INFINITY ? 0.0f : M;
+    for (int s0 = 0; s0 < info.y; s0 += 32) {
+      const int s = s0 + lane;
+      float2 ml = make_float2(-INFINITY, 0.0f);
+      if (s < info.y) ml = *reinterpret_cast<const float2*>(base + s * step);
+      const float wt = exp2f(ml.x - ref);
+      float lw = wt * ml.y;
+#pragma unroll
+      for (int m = 16; m > 0; m >>= 1) lw += __shfl_xor_sync(0xffffffffu, lw, m);
+      lsum += lw;
+      const int cnt = min(32, info.y - s0);
+#pragma unroll 4
+      for (int i = 0; i < cnt; ++i) {
+        const float wi = __shfl_sync(0xffffffffu, wt, i);
+        float o[E];
+        load_f32<E>(base + (s0 + i) * step + 4 + lane * E, o);
+#pragma unroll
+        for (int e = 0; e < E; ++e) v[e] = fmaf(wi, o[e], v[e]);
+      }
+    }
+    warp_fwht<D>(v, lane);
+  }
+  const float wr = rml.x == -INFINITY ? 0.0f : exp2f(rml.x - M);
+  lsum = fmaf(wr, rml.y, lsum);
+  const float inv = lsum > 0.0f ? 1.0f / lsum : 0.0f;
+  __half* dst = p.out + gw * p.d0;
+#pragma unroll
+  for (int e = 0; e < E; ++e) {
+    const int j = lane * E + e;
+    if (j < p.d0) dst[j] = __float2half_rn(fmaf(v[e], inv_sqrt_d<D>(), wr * ro[e]) * inv);
+  }
+}
+
+// ---- launches --------------------------------------------------------------------------------
+template <int D, int NR>
+static int launch_block_t(const BlockParams& p, cudaStream_t stream) {
+  using S = blk::Shape<D, NR>;
+  cudaLaunchAttribute attr[1];
+  attr[0].id = cudaLaunchAttributeProgrammaticStreamSerialization;
+  attr[0].val.programmaticStreamSerializationAllowed = 1;
+  cudaLaunchConfig_t cfg = {};
+  cfg.stream = stream;
+  cfg.attrs = attr;
+  cfg.numAttrs = 1;
+  {
+    constexpr int kSmem = 2 * 2 * 64 * 2 * D;
+    static PerDeviceOnce once;
+    const void* fn = reinterpret_cast<const void*>(block_raw_kernel<D>);
+    if (const int st = set_smem_limit(once, fn, kSmem); st != KVARN_OK) return st;
+    cfg.gridDim = dim3((unsigned)(((int64_t)p.block * p.group + 127) / 128), p.num_kv_heads, p.batch);
+    cfg.blockDim = dim3(256);
+    cfg.dynamicSmemBytes = kSmem;
+    if (cudaLaunchKernelEx(&cfg, block_raw_kernel<D>, p) != cudaSuccess) return KVARN_ERR_CUDA;
+  }
+  {
+    const int rec = record_layout(D, p.kb, p.vb).bytes;
+    int slots = (blk::kSmemMax - S::kRecOff) / rec;
+    slots = slots > blk::kMaxSlots ? blk::kMaxSlots : slots;
+    if (slots < 2) return KVARN_ERR_UNSUPPORTED;
+    static PerDeviceOnce once;
+    const void* fn = reinterpret_cast<const void*>(block_cache_kernel<D, NR>);
+    if (const int st = set_smem_limit(once, fn, blk::kSmemMax); st != KVARN_OK) return st;
+    cfg.gridDim = dim3(kBlockCtas);
+    cfg.blockDim = dim3(blk::kThreads);
+    cfg.dynamicSmemBytes = S::kRecOff + slots * rec;
+    if (cudaLaunchKernelEx(&cfg, block_cache_kernel<D, NR>, p, slots) != cudaSuccess) return KVARN_ERR_CUDA;
+  }
+  const int64_t warps = (int64_t)p.batch * p.block * p.num_q_heads;
+  cfg.gridDim = dim3((unsigned)((warps + 3) / 4));
+  cfg.blockDim = dim3(128);
+  cfg.dynamicSmemBytes = 0;
+  return cudaLaunchKernelEx(&cfg, block_merge_kernel<D>, p) == cudaSuccess ? KVARN_OK : KVARN_ERR_CUDA;
+}
+
+int block_tile_rows(int d, int64_t rows) {
+  if (rows <= 16) return 16;
+  if (rows <= 32 || d > 128) return 32;
+  return 64;
+}
+
+int launch_block_attention(int d, const BlockParams& p, cudaStream_t stream) {
+  if (d == 64) {
+    if (p.tile_rows == 16) return launch_block_t<64, 16>(p, stream);
+    if (p.tile_rows == 32) return launch_block_t<64, 32>(p, stream);
+    if (p.tile_rows == 64) return launch_block_t<64, 64>(p, stream);
+  } else if (d == 128) {
+    if (p.tile_rows == 16) return launch_block_t<128, 16>(p, stream);
+    if (p.tile_rows == 32) return launch_block_t<128, 32>(p, stream);
+    if (p.tile_rows == 64) return launch_block_t<128, 64>(p, stream);
+  } else if (d == 256) {
+    if (p.tile_rows == 16) return launch_block_t<256, 16>(p, stream);
+    if (p.tile_rows == 32) return launch_block_t<256, 32>(p, stream);
+  }
+  return KVARN_ERR_UNSUPPORTED;
+}
+
+}  // namespace kvarn

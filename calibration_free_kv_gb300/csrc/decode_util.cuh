@@ -163,20 +163,36 @@ __device__ __forceinline__ float inv_sqrt_d() {
 // line of virtual pages where every row with sealed pages first takes kSegPages units for the
 // fixed work of a segment (its queries, its first page's latency, the CTA merge), then one unit
 // per page.  The line is cut into `ctas` contiguous ranges of floor or ceil(total / ctas) units,
-// one per CTA, with ctas no larger than total / 32: every range holds at least 32 units, so a
-// row's pages (n consecutive units) fall in row_segments <= ceil(n / 32) + 1 ranges, and the
+// one per CTA, with ctas no larger than total / p.min_range (32 for a whole cache): every range
+// holds at least that many units, so a row's pages (n consecutive units) fall in row_segments <=
+// ceil(n / p.min_range) + 1 ranges, and the
 // segment whose first page sits at unit x writes split owner_cta(x) - owner_cta(the row's first
 // page).  A range may hold only the fixed units of a row (no page): that CTA has no work.  Every
 // kernel of the launch derives the same partition from seq_lens.
-constexpr int kMinRangePages = 32;
 constexpr int kSegPages = 8;  // virtual pages of a segment's fixed work
 
-__device__ __forceinline__ int sealed_pages(const DecodeParams& p, int b) {
+// The sealed pages a query of sequence b sees.  Whole cache (p.window == 0): all of them.  Windowed
+// decode (the query is the last of `len` tokens): the pages of its first p.sink tokens and those
+// from its first window token on, each once, in order; the pages in between are never looked up.
+struct PageSpan {
+  int sinks;  // pages 0 .. sinks - 1, then
+  int first;  // pages first ..
+  int count;  // in all
+  int start;  // position of the first window token
+  __device__ __forceinline__ int page(int i) const { return i < sinks ? i : first + (i - sinks); }
+};
+__device__ __forceinline__ PageSpan page_span(const DecodeParams& p, int b) {
   const int cap = p.max_pages * kTile + (kTile - 1);
   int len = p.seq_lens[b];
   len = len < 0 ? 0 : (len > cap ? cap : len);
-  return len / kTile;
+  const int n = len / kTile;
+  if (p.window <= 0) return {0, 0, n, 0};
+  const int start = max(0, len - p.window);
+  const int first = min(start / kTile, n);
+  const int sinks = min((p.sink + kTile - 1) / kTile, first);
+  return {sinks, first, sinks + n - first, start};
 }
+__device__ __forceinline__ int sealed_pages(const DecodeParams& p, int b) { return page_span(p, b).count; }
 
 // Virtual length of one row of n sealed pages.
 __device__ __forceinline__ int row_units(int n) { return n > 0 ? n + kSegPages : 0; }
@@ -199,7 +215,7 @@ struct PagePartition {
 __device__ __forceinline__ PagePartition page_partition(const DecodeParams& p, int lane) {
   PagePartition pp;
   pp.total = units_prefix(p, p.batch, lane) * p.num_kv_heads;
-  int64_t c = pp.total / kMinRangePages;
+  int64_t c = pp.total / p.min_range;
   c = c < 1 ? 1 : (c > p.part_ctas ? p.part_ctas : c);
   pp.ctas = pp.total > 0 ? c : 0;
   return pp;

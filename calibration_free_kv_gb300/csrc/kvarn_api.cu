@@ -275,6 +275,7 @@ static int decode_phases(const kvarn_desc* desc, int batch, int num_q_heads, con
                                          (int64_t)batch * desc->num_kv_heads, max_pages);
   p.chunk = 1;
   p.vgroups = 1;
+  p.min_range = kDecodeMinRange;
   p.status = dev_status;
   p.partial_in_merge = decode_env("KVARN_DECODE_OPEN_TILES", "split") ? 0 : 1;
   if (decode_tc_requested() && decode_tc_serves(desc->head_dim_padded, nt, desc->k_bits, desc->v_bits, p)) {
@@ -382,6 +383,7 @@ int kvarn_prefill_attention(const kvarn_desc* desc, int batch, int num_q_heads, 
   p.pages_per_split = decode_split_pages(desc->head_dim_padded, nt, desc->k_bits, desc->v_bits,
                                          (int64_t)batch * desc->num_kv_heads * vgroups, max_pages);
   p.chunk = chunk_len;
+  p.min_range = kDecodeMinRange;
   p.vgroups = (int)vgroups;
   p.chunk_k = static_cast<const __half*>(chunk_k);
   p.chunk_v = static_cast<const __half*>(chunk_v);
@@ -391,6 +393,212 @@ int kvarn_prefill_attention(const kvarn_desc* desc, int batch, int num_q_heads, 
   st = launch_chunk_any(desc->head_dim_padded, p, s);
   if (st != KVARN_OK) return st;
   return launch_decode_any(desc->head_dim_padded, nt, desc->k_bits, desc->v_bits, p, s);
+}
+
+// ---- windowed decode, tree attention, windowed prefill ---------------------------------------
+
+// Block tables up to 2^23 pages, so that positions stay within int32.
+static constexpr int kMaxTablePages = 1 << 23;
+
+static int window_check(const kvarn_desc* desc, int max_pages, int sink_tokens, int window) {
+  const int st = check_desc(desc);
+  if (st != KVARN_OK) return st;
+  if (max_pages < 1 || sink_tokens < 0 || window < 1) return KVARN_ERR_INVALID_ARG;
+  return max_pages > kMaxTablePages ? KVARN_ERR_UNSUPPORTED : KVARN_OK;
+}
+
+// Splits a row of a windowed decode may fill: the pages it sees are at most those of the first
+// tokens, those the window covers and one more (both ends partly), in ranges of kWindowMinRange.
+static int64_t window_splits(int max_pages, int sink_tokens, int window) {
+  int64_t vis = ((int64_t)sink_tokens + kTile - 1) / kTile + ((int64_t)window + kTile - 1) / kTile + 1;
+  if (vis > max_pages) vis = max_pages;
+  return (vis + kWindowMinRange - 1) / kWindowMinRange + 1;
+}
+
+size_t kvarn_window_decode_workspace_bytes(const kvarn_desc* desc, int batch, int num_q_heads,
+                                           int max_pages, int sink_tokens, int window) {
+  if (window_check(desc, max_pages, sink_tokens, window) != KVARN_OK || batch < 0 || num_q_heads < 1) return 0;
+  return (size_t)batch * num_q_heads * window_splits(max_pages, sink_tokens, window) *
+         (desc->head_dim_padded + 4) * sizeof(float);
+}
+
+int kvarn_window_decode_attention(const kvarn_desc* desc, int batch, int num_q_heads, const void* q,
+                                  const void* page_pool, int64_t num_pool_pages,
+                                  const int32_t* block_table, int max_pages, const int32_t* seq_lens,
+                                  const void* partial_k, const void* partial_v, int sink_tokens,
+                                  int window, float softmax_scale, void* out, void* workspace,
+                                  size_t workspace_bytes, int32_t* dev_status, void* stream) {
+  int st = decode_args_check(desc, batch, num_q_heads, q, page_pool, num_pool_pages, block_table,
+                             max_pages, seq_lens, partial_k, partial_v, softmax_scale, out);
+  if (st < 0) return st;
+  if (const int ws = window_check(desc, max_pages, sink_tokens, window); ws != KVARN_OK) return ws;
+  if (st == kDecodeNothingToDo) return KVARN_OK;
+  if (workspace == nullptr || !aligned16(workspace)) return KVARN_ERR_INVALID_ARG;
+  if (workspace_bytes <
+      kvarn_window_decode_workspace_bytes(desc, batch, num_q_heads, max_pages, sink_tokens, window))
+    return KVARN_ERR_WORKSPACE_TOO_SMALL;
+  const int group = num_q_heads / desc->num_kv_heads;
+  const int nt = group <= 4 ? 1 : 2;
+  const int cap = max_pages * kTile + kTile;  // no sequence is longer
+  DecodeParams p{};
+  p.q = static_cast<const __half*>(q);
+  p.pool = static_cast<const uint8_t*>(page_pool);
+  p.num_pool_pages = num_pool_pages;
+  p.block_table = block_table;
+  p.max_pages = max_pages;
+  p.seq_lens = seq_lens;
+  p.partial_k = static_cast<const __half*>(partial_k);
+  p.partial_v = static_cast<const __half*>(partial_v);
+  p.qscale = softmax_scale * kLog2e;
+  p.out = static_cast<__half*>(out);
+  p.part = static_cast<float*>(workspace);
+  p.batch = batch;
+  p.num_kv_heads = desc->num_kv_heads;
+  p.num_q_heads = num_q_heads;
+  p.group = group;
+  p.d0 = desc->head_dim;
+  p.max_splits = (int)window_splits(max_pages, sink_tokens, window);
+  p.chunk = 1;
+  p.vgroups = 1;
+  p.status = dev_status;
+  p.partial_in_merge = 1;
+  p.part_mode = 1;
+  p.part_ctas = decode_persistent_ctas(desc->head_dim_padded, nt, desc->k_bits, desc->v_bits);
+  if (p.part_ctas < 1) return KVARN_ERR_CUDA;
+  p.min_range = kWindowMinRange;
+  p.window = window < cap ? window : cap;
+  p.sink = sink_tokens < cap ? sink_tokens : cap;
+  return launch_window_decode(desc->head_dim_padded, nt, desc->k_bits, desc->v_bits, p,
+                              static_cast<cudaStream_t>(stream));
+}
+
+// Row tiles of a block-attention call and its workspace: the cache partials (one slot per CTA and
+// row tile in all), the raw tokens' partials, one (slot, slots) pair per row tile.
+struct BlockLayout {
+  int64_t tile_rows, tiles, row_tiles, slot_floats;
+  size_t part_bytes, raw_bytes, info_bytes;
+  size_t bytes() const { return part_bytes + raw_bytes + info_bytes; }
+};
+static BlockLayout block_layout(const kvarn_desc* desc, int batch, int num_q_heads, int block_len) {
+  BlockLayout L;
+  const int64_t rows = (int64_t)block_len * (num_q_heads / desc->num_kv_heads);
+  L.tile_rows = block_tile_rows(desc->head_dim_padded, rows);
+  L.tiles = (rows + L.tile_rows - 1) / L.tile_rows;
+  L.row_tiles = (int64_t)batch * desc->num_kv_heads * L.tiles;
+  L.slot_floats = L.tile_rows * (desc->head_dim_padded + 4);
+  L.part_bytes = (size_t)(kBlockCtas + L.row_tiles) * L.slot_floats * sizeof(float);
+  L.raw_bytes = (size_t)L.row_tiles * L.slot_floats * sizeof(float);
+  L.info_bytes = ((size_t)L.row_tiles * sizeof(int2) + 15) / 16 * 16;
+  return L;
+}
+
+// Host-side checks shared by the two block-attention calls and their workspace sizes.
+static int block_shape_check(const kvarn_desc* desc, int batch, int num_q_heads, int block_len, int max_pages) {
+  const int st = check_desc(desc);
+  if (st != KVARN_OK) return st;
+  if (batch < 0 || num_q_heads < 1 || max_pages < 1 || block_len < 1) return KVARN_ERR_INVALID_ARG;
+  if (num_q_heads % desc->num_kv_heads != 0) return KVARN_ERR_UNSUPPORTED;
+  const int group = num_q_heads / desc->num_kv_heads;
+  if (!(group == 1 || group == 2 || group == 4 || group == 8)) return KVARN_ERR_UNSUPPORTED;
+  // grid limits; rows and row tiles within int32
+  if (batch > 65535 || desc->num_kv_heads > 65535 || max_pages > kMaxTablePages) return KVARN_ERR_UNSUPPORTED;
+  if ((int64_t)block_len * group > (1 << 22)) return KVARN_ERR_UNSUPPORTED;
+  const int64_t row_tiles = batch > 0 ? block_layout(desc, batch, num_q_heads, block_len).row_tiles : 0;
+  if (row_tiles > (1 << 28) || (int64_t)batch * block_len * num_q_heads > 0x7fffffffLL) return KVARN_ERR_UNSUPPORTED;
+  return KVARN_OK;
+}
+
+static int block_attention(const kvarn_desc* desc, int batch, int num_q_heads, int block_len, const void* q,
+                           const void* new_k, const void* new_v, const uint32_t* mask, const int32_t* new_lens,
+                           const void* page_pool, int64_t num_pool_pages, const int32_t* block_table,
+                           int max_pages, const int32_t* cache_lens, const void* partial_k,
+                           const void* partial_v, int sink_tokens, int window, float softmax_scale, void* out,
+                           void* workspace, size_t workspace_bytes, int32_t* dev_status, void* stream) {
+  if (const int st = block_shape_check(desc, batch, num_q_heads, block_len, max_pages); st != KVARN_OK) return st;
+  if (batch == 0) return KVARN_OK;
+  if (q == nullptr || new_k == nullptr || new_v == nullptr || page_pool == nullptr || block_table == nullptr ||
+      cache_lens == nullptr || out == nullptr || workspace == nullptr)
+    return KVARN_ERR_INVALID_ARG;
+  if ((partial_k == nullptr) != (partial_v == nullptr)) return KVARN_ERR_INVALID_ARG;
+  if (!aligned16(new_k) || !aligned16(new_v) || !aligned16(page_pool) || !aligned16(workspace) ||
+      !aligned16(partial_k) || !aligned16(partial_v))
+    return KVARN_ERR_INVALID_ARG;
+  if (num_pool_pages < 1 || !(softmax_scale > 0.0f)) return KVARN_ERR_INVALID_ARG;
+  const BlockLayout L = block_layout(desc, batch, num_q_heads, block_len);
+  if (workspace_bytes < L.bytes()) return KVARN_ERR_WORKSPACE_TOO_SMALL;
+  const int cap = max_pages * kTile + kTile + block_len;  // no position is beyond it
+  BlockParams p{};
+  p.q = static_cast<const __half*>(q);
+  p.new_k = static_cast<const __half*>(new_k);
+  p.new_v = static_cast<const __half*>(new_v);
+  p.mask = mask;
+  p.mask_words = (block_len + 31) / 32;
+  p.new_lens = new_lens;
+  p.pool = static_cast<const uint8_t*>(page_pool);
+  p.num_pool_pages = num_pool_pages;
+  p.block_table = block_table;
+  p.max_pages = max_pages;
+  p.seq_lens = cache_lens;
+  p.partial_k = static_cast<const __half*>(partial_k);
+  p.partial_v = static_cast<const __half*>(partial_v);
+  p.window = window < cap ? window : cap;
+  p.sink = sink_tokens < cap ? sink_tokens : cap;
+  p.qscale = softmax_scale * kLog2e;
+  p.out = static_cast<__half*>(out);
+  uint8_t* ws = static_cast<uint8_t*>(workspace);
+  p.part = reinterpret_cast<float*>(ws);
+  p.raw_part = reinterpret_cast<float*>(ws + L.part_bytes);
+  p.row_info = reinterpret_cast<int2*>(ws + L.part_bytes + L.raw_bytes);
+  p.batch = batch;
+  p.block = block_len;
+  p.num_kv_heads = desc->num_kv_heads;
+  p.num_q_heads = num_q_heads;
+  p.group = num_q_heads / desc->num_kv_heads;
+  p.d0 = desc->head_dim;
+  p.tile_rows = (int)L.tile_rows;
+  p.tiles = (int)L.tiles;
+  p.kb = desc->k_bits;
+  p.vb = desc->v_bits;
+  p.status = dev_status;
+  return launch_block_attention(desc->head_dim_padded, p, static_cast<cudaStream_t>(stream));
+}
+
+size_t kvarn_tree_workspace_bytes(const kvarn_desc* desc, int batch, int num_q_heads, int tree_len,
+                                  int max_pages) {
+  if (block_shape_check(desc, batch, num_q_heads, tree_len, max_pages) != KVARN_OK) return 0;
+  return block_layout(desc, batch, num_q_heads, tree_len).bytes();
+}
+
+int kvarn_tree_attention(const kvarn_desc* desc, int batch, int num_q_heads, int tree_len, const void* q,
+                         const void* tree_k, const void* tree_v, const uint32_t* tree_mask,
+                         const int32_t* tree_lens, const void* page_pool, int64_t num_pool_pages,
+                         const int32_t* block_table, int max_pages, const int32_t* cache_lens,
+                         const void* partial_k, const void* partial_v, float softmax_scale, void* out,
+                         void* workspace, size_t workspace_bytes, int32_t* dev_status, void* stream) {
+  return block_attention(desc, batch, num_q_heads, tree_len, q, tree_k, tree_v, tree_mask, tree_lens, page_pool,
+                         num_pool_pages, block_table, max_pages, cache_lens, partial_k, partial_v, 0, 0,
+                         softmax_scale, out, workspace, workspace_bytes, dev_status, stream);
+}
+
+size_t kvarn_window_prefill_workspace_bytes(const kvarn_desc* desc, int batch, int num_q_heads, int chunk_len,
+                                            int max_pages, int sink_tokens, int window) {
+  if (block_shape_check(desc, batch, num_q_heads, chunk_len, max_pages) != KVARN_OK ||
+      window_check(desc, max_pages, sink_tokens, window) != KVARN_OK)
+    return 0;
+  return block_layout(desc, batch, num_q_heads, chunk_len).bytes();
+}
+
+int kvarn_window_prefill_attention(const kvarn_desc* desc, int batch, int num_q_heads, int chunk_len,
+                                   const void* q, const void* chunk_k, const void* chunk_v,
+                                   const int32_t* chunk_lens, const void* page_pool, int64_t num_pool_pages,
+                                   const int32_t* block_table, int max_pages, const int32_t* cache_lens,
+                                   const void* partial_k, const void* partial_v, int sink_tokens, int window,
+                                   float softmax_scale, void* out, void* workspace, size_t workspace_bytes,
+                                   int32_t* dev_status, void* stream) {
+  if (const int st = window_check(desc, max_pages, sink_tokens, window); st != KVARN_OK) return st;
+  return block_attention(desc, batch, num_q_heads, chunk_len, q, chunk_k, chunk_v, nullptr, chunk_lens, page_pool,
+                         num_pool_pages, block_table, max_pages, cache_lens, partial_k, partial_v, sink_tokens,
+                         window, softmax_scale, out, workspace, workspace_bytes, dev_status, stream);
 }
 
 int kvarn_dequantize_tiles(const kvarn_desc* desc, const void* page_pool, int64_t num_pool_pages,
@@ -452,7 +660,7 @@ const char* kvarn_status_string(int status) {
     case KVARN_OK: return "ok";
     case KVARN_ERR_INVALID_ARG: return "invalid argument (null pointer, size, stride or alignment)";
     case KVARN_ERR_UNSUPPORTED: return "unsupported configuration (preset, head_dim, bits or GQA group)";
-    case KVARN_ERR_WORKSPACE_TOO_SMALL: return "decode workspace smaller than kvarn_decode_workspace_bytes";
+    case KVARN_ERR_WORKSPACE_TOO_SMALL: return "workspace smaller than the call's kvarn_*_workspace_bytes";
     case KVARN_ERR_CUDA: return "CUDA launch or attribute call failed";
     default: return "unknown status";
   }

@@ -73,6 +73,39 @@ struct DecodeParams {
   int part_mode;  // 0: one CTA per split (grid splits x Hkv*vgroups x batch); 1: persistent
                   // CTAs over the partition's sealed pages; 2: partial tiles only; 3: the
                   // tcgen05 kernel over the sealed pages
+  int min_range;  // smallest range of the partition, in units (32: the decode workspace's layout)
+  // Windowed decode: 0, or the tokens (the query's own included) at the end that are seen, beside
+  // the first `sink` ones
+  int window, sink;
+};
+
+// Attention of a block of new tokens per sequence (block_attention.cu): the drafted nodes of a tree
+// (mask != null) or a chunk under a sliding window (window > 0).
+struct BlockParams {
+  const __half* q;      // [batch][block][Hq][d0]
+  const __half* new_k;  // [batch][block][Hkv][d0]
+  const __half* new_v;
+  const uint32_t* mask;  // [batch][block][mask_words]: bit j of row i = new token i sees new token j
+  int mask_words;
+  const int32_t* new_lens;  // new tokens of each sequence, or null: all `block`
+  const uint8_t* pool;
+  int64_t num_pool_pages;
+  const int32_t* block_table;
+  int max_pages;
+  const int32_t* seq_lens;  // cached tokens
+  const __half* partial_k;
+  const __half* partial_v;
+  int window, sink;
+  float qscale;  // softmax_scale * log2(e)
+  __half* out;   // [batch][block][Hq][d0]
+  // workspace: row tiles of `tile_rows` query rows, rows of D + 4 floats (m, l, -, -, o[D])
+  float* part;      // [kBlockCtas + row tiles][tile_rows]: cache partials, rotated basis
+  float* raw_part;  // [row tiles][tile_rows]: the raw tokens' partial, original basis
+  int2* row_info;   // [row tiles]: first slot and number of slots of `part`
+  int batch, block, num_kv_heads, num_q_heads, group, d0;
+  int tile_rows, tiles;  // rows of a row tile; row tiles of one (sequence, kv head)
+  int kb, vb;            // code bits
+  int32_t* status;
 };
 
 struct DequantParams {
@@ -121,6 +154,15 @@ int launch_decode_partial_tiles(const DecodeParams& p, cudaStream_t stream);
 // CTAs of the persistent mma.sync decode for this shape (SMs x CTAs per SM), 0 on error.
 int decode_persistent_ctas(int d, int nt, int kb, int vb);
 int launch_decode_combine(int d, const DecodeParams& p, cudaStream_t stream);
+int launch_window_decode(int d, int nt, int kb, int vb, const DecodeParams& p, cudaStream_t stream);
+// Smallest ranges of the decode partition, in units: whole cache / windowed decode.
+constexpr int kDecodeMinRange = 32, kWindowMinRange = 16;
+// Block attention: the CTAs its page line is cut for (a GB300's SMs; the workspace's layout, not a
+// requirement on the device), the query rows of a row tile for `rows` rows of one (sequence, kv
+// head), and the launch of its three kernels.
+constexpr int kBlockCtas = 152;
+int block_tile_rows(int d, int64_t rows);
+int launch_block_attention(int d, const BlockParams& p, cudaStream_t stream);
 int launch_dequant_any(int d, int kb, int vb, const DequantParams& p, int num_pages, cudaStream_t stream);
 
 }  // namespace kvarn

@@ -46,6 +46,12 @@ EXPORTED_SYMBOLS = (
     "kvarn_quantization_error",
     "kvarn_decode_partials",
     "kvarn_decode_combine",
+    "kvarn_window_decode_workspace_bytes",
+    "kvarn_window_decode_attention",
+    "kvarn_window_prefill_workspace_bytes",
+    "kvarn_window_prefill_attention",
+    "kvarn_tree_workspace_bytes",
+    "kvarn_tree_attention",
 )
 
 # Size of the library's fixed decode scratch (KVARN_DECODE_NOALLOC_SCRATCH_BYTES in kvarn.h).
@@ -107,6 +113,18 @@ def _load():
         "kvarn_decode_combine": (i32, [D, i32, i32, P, P, i64, P, i32, P, P, P, ctypes.c_float,
                                        P, P, ctypes.c_size_t, P, P]),
     }
+    F, Z = ctypes.c_float, ctypes.c_size_t
+    sig.update({
+        "kvarn_window_decode_workspace_bytes": (Z, [D, i32, i32, i32, i32, i32]),
+        "kvarn_window_decode_attention": (i32, [D, i32, i32, P, P, i64, P, i32, P, P, P, i32, i32, F,
+                                                P, P, Z, P, P]),
+        "kvarn_window_prefill_workspace_bytes": (Z, [D, i32, i32, i32, i32, i32, i32]),
+        "kvarn_window_prefill_attention": (i32, [D, i32, i32, i32, P, P, P, P, P, i64, P, i32, P, P, P,
+                                                 i32, i32, F, P, P, Z, P, P]),
+        "kvarn_tree_workspace_bytes": (Z, [D, i32, i32, i32, i32]),
+        "kvarn_tree_attention": (i32, [D, i32, i32, i32, P, P, P, P, P, P, i64, P, i32, P, P, P, F,
+                                       P, P, Z, P, P]),
+    })
     for name, (res, args) in sig.items():
         fn = getattr(lib, name)
         fn.restype = res
@@ -271,6 +289,148 @@ def prefill_attention(desc: KvarnDesc, q, chunk_k, chunk_v, pool, block_table, c
                                         _ptr(partial_v), float(softmax_scale), _ptr(out),
                                         _ptr(workspace), workspace.numel() * workspace.element_size(),
                                         _ptr(status), _stream(stream)), "kvarn_prefill_attention")
+
+
+def _tensors(device, **named):
+    """Checks of the tensors of one call: on `device`, of their dtype and shape, contiguous.  Each
+    name gives (tensor or None, dtypes, shape or None); shape entries of None are free."""
+    for name, (t, dtypes, shape) in named.items():
+        if t is None:
+            continue
+        _ptr(t)
+        if t.device != device:
+            raise ValueError("%s is on %s, q on %s" % (name, t.device, device))
+        if t.dtype not in dtypes:
+            raise ValueError("%s must be %s" % (name, " or ".join(str(d) for d in dtypes)))
+        if not t.is_contiguous():
+            raise ValueError("%s must be contiguous" % name)
+        if shape is not None and (t.dim() != len(shape) or
+                                  any(w is not None and n != w for n, w in zip(t.shape, shape))):
+            raise ValueError("%s must be %s, got %s" % (name, list(shape), list(t.shape)))
+
+
+def _cache_tensors(desc, q, batch, pool, block_table, lens, partial_k, partial_v, workspace, status):
+    half, i32 = (torch.float16,), (torch.int32,)
+    tile = (batch, desc.num_kv_heads, 128, desc.head_dim)
+    _ptr(q)
+    _tensors(q.device, pool=(pool, (torch.uint8,), (None, desc.num_kv_heads, desc.page_record_bytes)),
+             block_table=(block_table, i32, (batch, None)), lens=(lens, i32, (batch,)),
+             partial_k=(partial_k, half, tile), partial_v=(partial_v, half, tile),
+             workspace=(workspace, (workspace.dtype,), None), status=(status, i32, None))
+
+
+def _stream_on(device, stream):
+    return _stream(torch.cuda.current_stream(device) if stream is None else stream)
+
+
+def _alloc_bytes(n: int, what: str, device):
+    if n <= 0:
+        raise ValueError("%s: invalid shape" % what)
+    return torch.empty((n + 15) // 16 * 4, dtype=torch.float32, device=device)
+
+
+def window_decode_workspace_bytes(desc: KvarnDesc, batch: int, num_q_heads: int, max_pages: int,
+                                  sink_tokens: int, window: int) -> int:
+    return int(_lib.kvarn_window_decode_workspace_bytes(ctypes.byref(desc), batch, num_q_heads, max_pages,
+                                                        sink_tokens, window))
+
+
+def alloc_window_decode_workspace(desc: KvarnDesc, batch: int, num_q_heads: int, max_pages: int,
+                                  sink_tokens: int, window: int, device="cuda"):
+    return _alloc_bytes(window_decode_workspace_bytes(desc, max(batch, 1), num_q_heads, max_pages, sink_tokens,
+                                                      window), "window_decode_workspace", device)
+
+
+def window_decode_attention(desc: KvarnDesc, q, pool, block_table, seq_lens, out, workspace, sink_tokens: int,
+                            window: int, partial_k=None, partial_v=None, softmax_scale=None, status=None,
+                            stream=None):
+    """decode_attention of queries that see the first `sink_tokens` tokens and the last `window`
+    ones (their own, token seq_lens[b] - 1, included).  q, out: fp16 [batch, Hq, d0].  Block-table
+    entries of pages between the two are not read."""
+    batch, hq, d0 = q.shape
+    _cache_tensors(desc, q, batch, pool, block_table, seq_lens, partial_k, partial_v, workspace, status)
+    rows = (batch, hq, desc.head_dim)
+    _tensors(q.device, q=(q, (torch.float16,), rows), out=(out, (torch.float16,), rows))
+    if softmax_scale is None:
+        softmax_scale = 1.0 / math.sqrt(d0)
+    with torch.cuda.device(q.device):
+        _check(_lib.kvarn_window_decode_attention(
+            ctypes.byref(desc), batch, hq, _ptr(q), _ptr(pool), pool.shape[0], _ptr(block_table),
+            block_table.shape[1], _ptr(seq_lens), _ptr(partial_k), _ptr(partial_v), int(sink_tokens), int(window),
+            float(softmax_scale), _ptr(out), _ptr(workspace), workspace.numel() * workspace.element_size(),
+            _ptr(status), _stream_on(q.device, stream)), "kvarn_window_decode_attention")
+
+
+def window_prefill_workspace_bytes(desc: KvarnDesc, batch: int, num_q_heads: int, chunk_len: int, max_pages: int,
+                                   sink_tokens: int, window: int) -> int:
+    return int(_lib.kvarn_window_prefill_workspace_bytes(ctypes.byref(desc), batch, num_q_heads, chunk_len,
+                                                         max_pages, sink_tokens, window))
+
+
+def alloc_window_prefill_workspace(desc: KvarnDesc, batch: int, num_q_heads: int, chunk_len: int, max_pages: int,
+                                   sink_tokens: int, window: int, device="cuda"):
+    return _alloc_bytes(window_prefill_workspace_bytes(desc, max(batch, 1), num_q_heads, chunk_len, max_pages,
+                                                       sink_tokens, window), "window_prefill_workspace", device)
+
+
+def _block_tensors(desc, q, new_k, new_v, out, new_lens, what):
+    batch, block, hq, _ = q.shape
+    half, rows = (torch.float16,), (batch, block, hq, desc.head_dim)
+    kv = (batch, block, desc.num_kv_heads, desc.head_dim)
+    _tensors(q.device, **{"q": (q, half, rows), "out": (out, half, rows), what + "_k": (new_k, half, kv),
+                          what + "_v": (new_v, half, kv), what + "_lens": (new_lens, (torch.int32,), (batch,))})
+
+
+def window_prefill_attention(desc: KvarnDesc, q, chunk_k, chunk_v, pool, block_table, cache_lens, out, workspace,
+                             sink_tokens: int, window: int, chunk_lens=None, partial_k=None, partial_v=None,
+                             softmax_scale=None, status=None, stream=None):
+    """prefill_attention of queries that see the first `sink_tokens` tokens and the last `window`
+    ones up to their own.  q, out: fp16 [batch, chunk, Hq, d0]; chunk_k/v: fp16 [batch, chunk, Hkv,
+    d0]; chunk_lens: int32 [batch] or None, tokens of each sequence's chunk (rows of out past them
+    stay as they were).  Block-table entries of pages that no query sees are not read."""
+    batch, chunk, hq, d0 = q.shape
+    _cache_tensors(desc, q, batch, pool, block_table, cache_lens, partial_k, partial_v, workspace, status)
+    _block_tensors(desc, q, chunk_k, chunk_v, out, chunk_lens, "chunk")
+    if softmax_scale is None:
+        softmax_scale = 1.0 / math.sqrt(d0)
+    with torch.cuda.device(q.device):
+        _check(_lib.kvarn_window_prefill_attention(
+            ctypes.byref(desc), batch, hq, chunk, _ptr(q), _ptr(chunk_k), _ptr(chunk_v), _ptr(chunk_lens), _ptr(pool),
+            pool.shape[0], _ptr(block_table), block_table.shape[1], _ptr(cache_lens), _ptr(partial_k),
+            _ptr(partial_v), int(sink_tokens), int(window), float(softmax_scale), _ptr(out), _ptr(workspace),
+            workspace.numel() * workspace.element_size(), _ptr(status), _stream_on(q.device, stream)),
+            "kvarn_window_prefill_attention")
+
+
+def tree_workspace_bytes(desc: KvarnDesc, batch: int, num_q_heads: int, tree_len: int, max_pages: int) -> int:
+    return int(_lib.kvarn_tree_workspace_bytes(ctypes.byref(desc), batch, num_q_heads, tree_len, max_pages))
+
+
+def alloc_tree_workspace(desc: KvarnDesc, batch: int, num_q_heads: int, tree_len: int, max_pages: int,
+                         device="cuda"):
+    return _alloc_bytes(tree_workspace_bytes(desc, max(batch, 1), num_q_heads, tree_len, max_pages),
+                        "tree_workspace", device)
+
+
+def tree_attention(desc: KvarnDesc, q, tree_k, tree_v, tree_mask, pool, block_table, cache_lens, out, workspace,
+                   tree_lens=None, partial_k=None, partial_v=None, softmax_scale=None, status=None, stream=None):
+    """Drafted tokens of a tree over the cache: q, out fp16 [batch, nodes, Hq, d0]; tree_k/v fp16
+    [batch, nodes, Hkv, d0]; tree_mask int32 (or uint32) [batch, nodes, ceil(nodes / 32)], bit j % 32
+    of word j / 32 of row i set when node i sees node j, or None for a chain; tree_lens: int32
+    [batch] or None, nodes of each sequence (rows of out past them stay as they were)."""
+    batch, nodes, hq, d0 = q.shape
+    _cache_tensors(desc, q, batch, pool, block_table, cache_lens, partial_k, partial_v, workspace, status)
+    _block_tensors(desc, q, tree_k, tree_v, out, tree_lens, "tree")
+    _tensors(q.device, tree_mask=(tree_mask, (torch.int32, torch.uint32), (batch, nodes, (nodes + 31) // 32)))
+    if softmax_scale is None:
+        softmax_scale = 1.0 / math.sqrt(d0)
+    with torch.cuda.device(q.device):
+        _check(_lib.kvarn_tree_attention(
+            ctypes.byref(desc), batch, hq, nodes, _ptr(q), _ptr(tree_k), _ptr(tree_v), _ptr(tree_mask), _ptr(tree_lens),
+            _ptr(pool), pool.shape[0], _ptr(block_table), block_table.shape[1], _ptr(cache_lens), _ptr(partial_k),
+            _ptr(partial_v), float(softmax_scale), _ptr(out), _ptr(workspace),
+            workspace.numel() * workspace.element_size(), _ptr(status), _stream_on(q.device, stream)),
+            "kvarn_tree_attention")
 
 
 def decode_attention_noalloc(desc: KvarnDesc, q, pool, block_table, seq_lens, out, partial_k=None,

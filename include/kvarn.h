@@ -235,6 +235,73 @@ int kvarn_prefill_attention(const kvarn_desc* desc, int batch, int num_q_heads, 
                             void* out, void* workspace, size_t workspace_bytes,
                             int32_t* dev_status, void* stream);
 
+/* ---- Attention under a sliding window with visible first tokens ----
+ * A query at position p sees token j <= p when j < sink_tokens (the first tokens, which stay
+ * visible) or j > p - window (the last `window` tokens, its own included).  Pages that no query
+ * of the call sees are never looked up: their block-table entries may hold anything (the pages
+ * may have been given to another sequence), as long as the entries of visible pages hold.
+ * sink_tokens >= 0 and window >= 1 (else INVALID_ARG); either may exceed the sequence.
+ * max_pages up to 2^23 (else UNSUPPORTED). */
+
+/* Workspace bytes of kvarn_window_decode_attention (host only; 0 if invalid).  It does not grow
+ * with the sequences once they are longer than the window. */
+size_t kvarn_window_decode_workspace_bytes(const kvarn_desc* desc, int batch, int num_q_heads,
+                                           int max_pages, int sink_tokens, int window);
+
+/* kvarn_decode_attention under the window: the query of sequence b is its token seq_lens[b] - 1
+ * (already appended).  Other arguments, results and errors as kvarn_decode_attention. */
+int kvarn_window_decode_attention(const kvarn_desc* desc, int batch, int num_q_heads, const void* q,
+                                  const void* page_pool, int64_t num_pool_pages,
+                                  const int32_t* block_table, int max_pages, const int32_t* seq_lens,
+                                  const void* partial_k, const void* partial_v, int sink_tokens,
+                                  int window, float softmax_scale, void* out, void* workspace,
+                                  size_t workspace_bytes, int32_t* dev_status, void* stream);
+
+/* Workspace bytes of kvarn_window_prefill_attention (host only; 0 if invalid). */
+size_t kvarn_window_prefill_workspace_bytes(const kvarn_desc* desc, int batch, int num_q_heads,
+                                            int chunk_len, int max_pages, int sink_tokens, int window);
+
+/* kvarn_prefill_attention under the window: chunk token c of sequence b is at position
+ * cache_lens[b] + c.
+ *  chunk_lens   device int32 [batch] or NULL (all chunk_len): tokens of each sequence's chunk,
+ *               0..chunk_len (else clamped, KVARN_DEV_SEQ_TOO_LONG).  Rows of q, chunk_k and
+ *               chunk_v from chunk_lens[b] on are not used, and those of out stay as they were.
+ *  Other arguments as kvarn_prefill_attention (chunk_k / chunk_v 16-byte aligned).
+ *  UNSUPPORTED if batch or Hkv exceeds 65535 or chunk_len * G exceeds 2^22. */
+int kvarn_window_prefill_attention(const kvarn_desc* desc, int batch, int num_q_heads, int chunk_len,
+                                   const void* q, const void* chunk_k, const void* chunk_v,
+                                   const int32_t* chunk_lens, const void* page_pool,
+                                   int64_t num_pool_pages, const int32_t* block_table, int max_pages,
+                                   const int32_t* cache_lens, const void* partial_k,
+                                   const void* partial_v, int sink_tokens, int window,
+                                   float softmax_scale, void* out, void* workspace,
+                                   size_t workspace_bytes, int32_t* dev_status, void* stream);
+
+/* Workspace bytes of kvarn_tree_attention (host only; 0 if invalid). */
+size_t kvarn_tree_workspace_bytes(const kvarn_desc* desc, int batch, int num_q_heads, int tree_len,
+                                  int max_pages);
+
+/* Attention of a tree of drafted tokens over the cache (the verification step of speculative
+ * decoding).  Node i of sequence b attends to all cache_lens[b] cached tokens (sealed pages + raw
+ * partial tile) and to the nodes its mask row names.
+ *  q            fp16 [batch][tree_len][Hq][d0];  out fp16 [batch][tree_len][Hq][d0].
+ *  tree_k/v     fp16 [batch][tree_len][Hkv][d0], 16-byte aligned: the nodes' own keys and values.
+ *  tree_mask    device uint32 [batch][tree_len][ceil(tree_len / 32)]: bit j % 32 of word j / 32 of
+ *               row i is set when node i sees node j (usually its ancestors and itself; any pattern
+ *               is taken).  NULL: node i sees nodes 0..i (a chain).  Bits of absent nodes are ignored.
+ *  tree_lens    device int32 [batch] or NULL (all tree_len): nodes of each sequence, 0..tree_len
+ *               (else clamped, KVARN_DEV_SEQ_TOO_LONG).  Rows of absent nodes are not used, and
+ *               those of out stay as they were.
+ *  A node that sees nothing (no cached token, an empty mask row) gives zeros.
+ *  Other arguments as kvarn_prefill_attention; limits as kvarn_window_prefill_attention. */
+int kvarn_tree_attention(const kvarn_desc* desc, int batch, int num_q_heads, int tree_len,
+                         const void* q, const void* tree_k, const void* tree_v,
+                         const uint32_t* tree_mask, const int32_t* tree_lens, const void* page_pool,
+                         int64_t num_pool_pages, const int32_t* block_table, int max_pages,
+                         const int32_t* cache_lens, const void* partial_k, const void* partial_v,
+                         float softmax_scale, void* out, void* workspace, size_t workspace_bytes,
+                         int32_t* dev_status, void* stream);
+
 /* kvarn_decode_attention without a workspace argument, for callers that cannot allocate
  * device memory: plugins in engines that plan and own all device memory in advance, code
  * that must not call cudaMalloc on the decode path (it may synchronise the device), and
