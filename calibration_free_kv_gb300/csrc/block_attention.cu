@@ -96,6 +96,27 @@ __device__ __forceinline__ bool bar_any(int id, int threads, bool flag) {
   return out != 0;
 }
 
+// Bounded wait in a few instructions: the roles' code together has to stay in the SM's instruction
+// cache.  A poll suspends for up to about a microsecond, so the limit is some two seconds.
+__device__ __forceinline__ bool wait_one(uint64_t* bar, uint32_t parity) {
+  const uint32_t at = smem_u32(bar);
+  for (uint32_t n = 0; n < (1u << 21); ++n) {
+    uint32_t ok;
+    asm volatile(
+        "{\n\t.reg .pred p;\n\t"
+        "mbarrier.try_wait.parity.shared::cta.b64 p, [%1], %2, %3;\n\t"
+        "selp.u32 %0, 1, 0, p;\n\t}"
+        : "=r"(ok)
+        : "r"(at), "r"(parity), "r"(1000u)
+        : "memory");
+    if (ok) return true;
+  }
+  return false;
+}
+__device__ __forceinline__ bool wait_warp(uint64_t* bar, uint32_t parity) {
+  return __all_sync(0xffffffffu, wait_one(bar, parity));
+}
+
 __device__ __forceinline__ int cached_len(const BlockParams& p, int b) {
   const int cap = p.max_pages * kTile + (kTile - 1);
   const int len = p.seq_lens[b];
@@ -381,7 +402,7 @@ __global__ void __launch_bounds__(blk::kThreads, 1) block_cache_kernel(BlockPara
       for (int i = 0; i < cnt; ++i, ++g) {
         const int s = (int)(g & 1);
         const uint32_t par = (uint32_t)((g >> 1) & 1);
-        const bool ok = !bad && wait_all(&qk_full[s], par) && wait_all(&ops_k[s], par) && wait_all(&rec_full[r], rph);
+        const bool ok = !bad && wait_warp(&qk_full[s], par) && wait_warp(&ops_k[s], par) && wait_warp(&rec_full[r], rph);
         float x[NR];
         if (ok) {
           fence_after();
@@ -459,7 +480,7 @@ __global__ void __launch_bounds__(blk::kThreads, 1) block_cache_kernel(BlockPara
             l[n / 2] = mul2(l[n / 2], make_float2(alpha_s[n], alpha_s[n + 1]));
           }
           if (i > 0) {  // O of the pages before this one
-            if (!wait_all(&pv_done[(g - 1) & 1], (uint32_t)(((g - 1) >> 1) & 1))) {
+            if (!wait_warp(&pv_done[(g - 1) & 1], (uint32_t)(((g - 1) >> 1) & 1))) {
               fail();
               bad = true;
             } else {
@@ -480,7 +501,7 @@ __global__ void __launch_bounds__(blk::kThreads, 1) block_cache_kernel(BlockPara
           }
         }
         // P of the stage, once PV of the page before the last has read it
-        if (!bad && !wait_all(&pv_done[s], par ^ 1u)) {
+        if (!bad && !wait_warp(&pv_done[s], par ^ 1u)) {
           fail();
           bad = true;
         }
@@ -525,7 +546,7 @@ __global__ void __launch_bounds__(blk::kThreads, 1) block_cache_kernel(BlockPara
         const int64_t last = owner_cta(part_s, w.row0 + kFixUnits + w.span.count - 1);
         p.row_info[row] = make_int2((int)((int64_t)blockIdx.x + row), (int)(last - blockIdx.x + 1));
       }
-      if (!wait_all(&pv_done[(g - 1) & 1], (uint32_t)(((g - 1) >> 1) & 1))) {
+      if (!wait_warp(&pv_done[(g - 1) & 1], (uint32_t)(((g - 1) >> 1) & 1))) {
         fail();
         bad = true;
       } else {
@@ -546,263 +567,6 @@ __global__ void __launch_bounds__(blk::kThreads, 1) block_cache_kernel(BlockPara
         fence_before();
       }
     }
-  } else if (warp < kVWarp) {
-    // ---- K codes -> tensor memory, B = q~ s' (hi + lo), q~ . z' ----
-    const int t = threadIdx.x - 32 * kKWarp, q = warp - kKWarp;
-    const int grp = t >> 3, nl = t & 7;
-    const int gq = lane >> 2, tq = lane & 3;
-    const float i0 = 1.0f / lift0(p.kb), i1 = 1.0f / lift1(p.kb);
-    int64_t g = 0;
-    int r = 0;
-    uint32_t rph = 0;
-    bool bad = false;
-    for (TileWalk w = w0; w.left > 0; w.next(p)) {
-      if (stage_queries(w, bad)) break;
-      const int cnt = w.count();
-      for (int i = 0; i < cnt; ++i, ++g) {
-        const int s = (int)(g & 1);
-        const uint32_t par = (uint32_t)((g >> 1) & 1);
-        // QK of the page before the last has read the codes and B, the softmax its q~ . z'
-        if (!wait_all(&rec_full[r], rph) || !wait_all(&qk_full[s], par ^ 1u) || !wait_all(&s_free[s], par ^ 1u) ||
-            *abort_v != 0) {
-          bad = true;
-          fail();
-          break;
-        }
-        fence_after();
-        const uint8_t* R = recs + r * rec;
-        // fragment (o, i) of 16 tokens x 16 channels is lanes 16o.., columns 8i..8i+7; column
-        // 2tq + h holds channels 16i + 8h + 2tq, +1 of its tokens g and g + 8
-        const uint32_t ta = tmem + S::kColK + (uint32_t)(s * (D / 2)) + ((uint32_t)(32 * q) << 16);
-        const uint4* kc = reinterpret_cast<const uint4*>(R + RL.kcodes);
-        if (p.kb == 4) {
-#pragma unroll
-          for (int oo = 0; oo < 2; ++oo)
-#pragma unroll
-            for (int kq = 0; kq < D / 64; ++kq) {
-              const uint4 w4 = kc[((2 * q + oo) * (D / 64) + kq) * 32 + lane];
-              const uint32_t ws[4] = {w4.x, w4.y, w4.z, w4.w};
-              uint32_t rr[16];
-#pragma unroll
-              for (int e = 0; e < 4; ++e) {
-                const uint32_t x = ws[e], y = x >> 8;
-                rr[4 * e] = x & 0x000F000Fu;
-                rr[4 * e + 1] = x & 0x00F000F0u;
-                rr[4 * e + 2] = y & 0x000F000Fu;
-                rr[4 * e + 3] = y & 0x00F000F0u;
-              }
-              st_16x256b_x4(ta + ((uint32_t)(16 * oo) << 16) + 32 * kq, rr);
-            }
-        } else if (p.kb == 8) {
-#pragma unroll
-          for (int oo = 0; oo < 2; ++oo)
-#pragma unroll
-            for (int kp = 0; kp < D / 32; ++kp) {
-              const uint4 w4 = kc[((2 * q + oo) * (D / 32) + kp) * 32 + lane];
-              uint32_t rr[8], a[4];
-              unpack_k8(w4.x, w4.y, a);
-              rr[0] = a[0];
-              rr[1] = a[2];
-              rr[2] = a[1];
-              rr[3] = a[3];
-              unpack_k8(w4.z, w4.w, a);
-              rr[4] = a[0];
-              rr[5] = a[2];
-              rr[6] = a[1];
-              rr[7] = a[3];
-              st_16x256b_x2(ta + ((uint32_t)(16 * oo) << 16) + 16 * kp, rr);
-            }
-        } else {  // 2-bit: a word holds token blocks 2q and 2q + 1, the odd one's codes 4 bits higher
-#pragma unroll
-          for (int kq = 0; kq < D / 64; ++kq) {
-            const uint4 w4 = kc[(q * (D / 64) + kq) * 32 + lane];
-            const uint32_t ws[4] = {w4.x, w4.y, w4.z, w4.w};
-#pragma unroll
-            for (int oo = 0; oo < 2; ++oo) {
-              uint32_t rr[16];
-#pragma unroll
-              for (int e = 0; e < 4; ++e) {
-                const uint32_t x = ws[e], y = x >> 8;
-                rr[4 * e] = x & (0x00030003u << (4 * oo));
-                rr[4 * e + 1] = x & (0x000C000Cu << (4 * oo));
-                rr[4 * e + 2] = y & (0x00030003u << (4 * oo));
-                rr[4 * e + 3] = y & (0x000C000Cu << (4 * oo));
-              }
-              st_16x256b_x4(ta + ((uint32_t)(16 * oo) << 16) + 32 * kq, rr);
-            }
-          }
-        }
-        // B rows n = 8 rg + nl over K indexes 8kb..8kb+7 of step kk (channels cb + {0, 1, 8, 9, 2,
-        // 3, 10, 11}): 16 thread groups of 8 over the D / 8 (kk, kb) pairs
-        uint8_t* bs = sm + S::kBOff + s * 2 * S::kBHalf;
-#pragma unroll
-        for (int c2 = 0; c2 < (D > 128 ? 2 : 1); ++c2) {
-          const int oc = D == 64 ? (grp & 7) : grp + 16 * c2;
-          const int kk = oc >> 1, kb = oc & 1, cb = 16 * kk + 4 * kb;
-          const uint2 sa = *reinterpret_cast<const uint2*>(R + RL.kscale + 2 * cb);
-          const uint2 sb = *reinterpret_cast<const uint2*>(R + RL.kscale + 2 * (cb + 8));
-          const __half2 sv[4] = {u2h2(sa.x), u2h2(sb.x), u2h2(sa.y), u2h2(sb.y)};
-#pragma unroll
-          for (int rg = 0; rg < NR / 8; ++rg) {
-            if (D == 64 && (rg & 1) != (grp >> 3)) continue;
-            const int at = kk * S::kStep + rg * 256 + kb * 128 + nl * 16;
-            const uint4 h4 = *reinterpret_cast<const uint4*>(q_hi + at);
-            const uint4 l4 = *reinterpret_cast<const uint4*>(q_lo + at);
-            const __half2 qh[4] = {u2h2(h4.x), u2h2(h4.y), u2h2(h4.z), u2h2(h4.w)};
-            const __half2 ql[4] = {u2h2(l4.x), u2h2(l4.y), u2h2(l4.z), u2h2(l4.w)};
-            uint32_t hi[4], lo[4];
-#pragma unroll
-            for (int e = 0; e < 4; ++e) {
-              const __half2 hv = __hmul2(qh[e], sv[e]);
-              hi[e] = h2u(hv);
-              lo[e] = h2u(__hfma2(ql[e], sv[e], __hfma2(qh[e], sv[e], __hneg2(hv))));
-            }
-            *reinterpret_cast<uint4*>(bs + at) = make_uint4(hi[0], hi[1], hi[2], hi[3]);
-            *reinterpret_cast<uint4*>(bs + S::kBHalf + at) = make_uint4(lo[0], lo[1], lo[2], lo[3]);
-          }
-        }
-        // q~ . z' of rows 16q..16q+15 on mma.sync: B column 0 holds z' of channels 0..7 of every
-        // 16, column 1 of channels 8..15, whose q~ carry different lifts
-        if (16 * q < NR) {
-          float acc[4] = {0.0f, 0.0f, 0.0f, 0.0f};
-          const int m = lane >> 3;
-          const uint32_t qa = smem_u32(q_hi) + (2 * q + (m & 1)) * 256 + (m >> 1) * 128 + (lane & 7) * 16;
-          const bool mine = gq < 2 && (tq & 1) == gq;
-          const uint8_t* zc = R + RL.kzero + 2 * (8 * (tq & 1) + 2 * (tq >> 1));
-#pragma unroll
-          for (int kk = 0; kk < S::kSteps; ++kk) {
-            const uint32_t b0 = mine ? *reinterpret_cast<const uint32_t*>(zc + 32 * kk) : 0u;
-            const uint32_t b1 = mine ? *reinterpret_cast<const uint32_t*>(zc + 32 * kk + 8) : 0u;
-            uint32_t a[4];
-            ldsm_x4(qa + kk * S::kStep, a);
-            mma16816(acc, a, b0, b1);
-            ldsm_x4(qa + S::kBHalf + kk * S::kStep, a);
-            mma16816(acc, a, b0, b1);
-          }
-          if (tq == 0) {
-            float* qz = qz_s + s * NR + 16 * q + gq;
-            qz[0] = acc[0] * i0 + acc[1] * i1;
-            qz[8] = acc[2] * i0 + acc[3] * i1;
-          }
-        }
-        wait_st();
-        fence_proxy_async_smem();
-        fence_before();
-        __syncwarp();
-        if (lane == 0) {
-          mbar_arrive(&ops_k[s]);
-          mbar_arrive(&rec_empty[r]);
-        }
-        if (++r == slots) {
-          r = 0;
-          rph ^= 1u;
-        }
-      }
-    }
-  } else if (warp < kLoadWarp) {
-    // ---- V~ -> tensor memory: channels on the lanes, tokens along K ----
-    const int q = warp - kVWarp;
-    const int gq = lane >> 2, tq = lane & 3;
-    int64_t g = 0;
-    int r = 0;
-    uint32_t rph = 0;
-    bool bad = false;
-    for (TileWalk w = w0; w.left > 0; w.next(p)) {
-      if (stage_queries(w, bad)) break;
-      const int cnt = w.count();
-      for (int i = 0; i < cnt; ++i, ++g) {
-        const int s = (int)(g & 1);
-        const int vs = S::kVStages == 2 ? s : 0;
-        // PV of the page that last used this buffer
-        const int64_t gp = g - S::kVStages;
-        if (!wait_all(&rec_full[r], rph) ||
-            (gp >= 0 && !wait_all(&pv_done[gp & 1], (uint32_t)((gp >> 1) & 1))) || *abort_v != 0) {
-          bad = true;
-          fail();
-          break;
-        }
-        fence_after();
-        const uint8_t* R = recs + r * rec;
-        const __half2* vsc = reinterpret_cast<const __half2*>(R + RL.vscale);
-        const __half2* vzr = reinterpret_cast<const __half2*>(R + RL.vzero);
-        const __half* vch = reinterpret_cast<const __half*>(R + RL.vfactor);
-        const uint2* vc = reinterpret_cast<const uint2*>(R + RL.vcodes);
-        const uint32_t ta = tmem + S::kColV + (uint32_t)(vs * 64 * S::kHalves) + ((uint32_t)(32 * q) << 16);
-        if (D >= 128 || q < D / 32) {
-          __half2 cv[S::kHalves][2][2];  // channel factors of rows g, g + 8 of the two blocks
-#pragma unroll
-          for (int hf = 0; hf < S::kHalves; ++hf)
-#pragma unroll
-            for (int ii = 0; ii < 2; ++ii)
-#pragma unroll
-              for (int rho = 0; rho < 2; ++rho)
-                cv[hf][ii][rho] = __half2half2(vch[16 * (8 * hf + 2 * q + ii) + gq + 8 * rho]);
-#pragma unroll
-          for (int o2 = 0; o2 < 4; ++o2) {
-            __half2 s2[2][2], z2[2][2];  // [token block of the pair][token half]
-#pragma unroll
-            for (int f = 0; f < 2; ++f)
-#pragma unroll
-              for (int h = 0; h < 2; ++h) {
-                s2[f][h] = vsc[8 * (2 * o2 + f) + 4 * h + tq];
-                z2[f][h] = vzr[8 * (2 * o2 + f) + 4 * h + tq];
-              }
-#pragma unroll
-            for (int hf = 0; hf < S::kHalves; ++hf) {
-              const int cb = 8 * hf + 2 * q;  // channel blocks cb, cb + 1: adjacent words
-              uint32_t x[2][2];               // [channel block][word of token block f]
-              if (p.vb == 2) {
-                const uint2 a = vc[(((o2 * (D / 64) + (cb >> 2)) * 32 + lane) * 4 + (cb & 3)) >> 1];
-                x[0][0] = x[0][1] = a.x;
-                x[1][0] = x[1][1] = a.y;
-              } else {
-#pragma unroll
-                for (int f = 0; f < 2; ++f) {
-                  const uint2 a = vc[((((2 * o2 + f) * (D / 64) + (cb >> 2)) * 32 + lane) * 4 + (cb & 3)) >> 1];
-                  x[0][f] = a.x;
-                  x[1][f] = a.y;
-                }
-              }
-#pragma unroll
-              for (int ii = 0; ii < 2; ++ii) {
-                uint32_t rr[8];
-#pragma unroll
-                for (int f = 0; f < 2; ++f)
-#pragma unroll
-                  for (int rho = 0; rho < 2; ++rho) {
-                    const uint32_t y = rho ? x[ii][f] >> 8 : x[ii][f];
-#pragma unroll
-                    for (int h = 0; h < 2; ++h) {
-                      // the code's bits under an exponent that makes them base + code, minus base
-                      const int k2 = 4 * f + 2 * h, k4 = 4 * h;
-                      uint32_t cu;
-                      if (p.vb == 2)
-                        cu = h2u(__hsub2(u2h2((y & (0x00030003u << k2)) | (0x64006400u - (uint32_t)k2 * 0x04000400u)),
-                                         u2h2(0x64006400u - (uint32_t)k2 * 0x04000400u)));
-                      else
-                        cu = h2u(__hsub2(u2h2((y & (0x000F000Fu << k4)) | (0x64006400u - (uint32_t)k4 * 0x04000400u)),
-                                         u2h2(0x64006400u - (uint32_t)k4 * 0x04000400u)));
-                      rr[4 * f + 2 * rho + h] = h2u(__hmul2(__hfma2(u2h2(cu), s2[f][h], z2[f][h]), cv[hf][ii][rho]));
-                    }
-                  }
-                st_16x256b_x2(ta + ((uint32_t)(16 * ii) << 16) + 64 * hf + 16 * o2, rr);
-              }
-            }
-          }
-        }
-        wait_st();
-        fence_before();
-        __syncwarp();
-        if (lane == 0) {
-          mbar_arrive(&ops_v[s]);
-          mbar_arrive(&rec_empty[r]);
-        }
-        if (++r == slots) {
-          r = 0;
-          rph ^= 1u;
-        }
-      }
-    }
   } else if (warp == kLoadWarp) {
     // ---- page records -> the ring ----
     if (lane == 0) {
@@ -819,7 +583,7 @@ __global__ void __launch_bounds__(blk::kThreads, 1) block_cache_kernel(BlockPara
             flag_error(p.status, KVARN_DEV_BAD_PAGE_ID);
             id = 0;
           }
-          if (!mbar_wait(&rec_empty[r], rph ^ 1u) || *abort_v != 0) {
+          if (!wait_one(&rec_empty[r], rph ^ 1u) || *abort_v != 0) {
             fail();
             bad = true;
             break;
@@ -835,61 +599,306 @@ __global__ void __launch_bounds__(blk::kThreads, 1) block_cache_kernel(BlockPara
       }
       // copies still in flight land before the CTA may leave
       for (int64_t k = g > slots ? g - slots : 0; k < g; ++k)
-        mbar_wait(&rec_full[k % slots], (uint32_t)((k / slots) & 1));
+        wait_one(&rec_full[k % slots], (uint32_t)((k / slots) & 1));
     }
     __syncwarp();
   } else {
-    // ---- MMA issue: one lane; QK of even and of odd pages on two warps, PV on a third ----
-    const bool is_pv = warp == kPvWarp;
-    int64_t g = 0;
+    int64_t g = 0;  // pages done, and the ring slot and its phase for the roles that read records
+    int r = 0;
+    uint32_t rph = 0;
     bool bad = false;
-    uint64_t* last = nullptr;
+    uint64_t* last = nullptr;  // MMA issue: the barrier of this lane's last commit
     uint32_t last_par = 0;
     for (TileWalk w = w0; w.left > 0; w.next(p)) {
       if (stage_queries(w, __any_sync(0xffffffffu, bad))) break;
       const int cnt = w.count();
-      if (lane == 0) {
-        for (int i = 0; i < cnt; ++i) {
-          const int64_t gi = g + i;
-          const int s = (int)(gi & 1);
-          const uint32_t par = (uint32_t)((gi >> 1) & 1);
-          if (!is_pv && s != warp - kQkWarp) continue;
-          const bool ok = is_pv ? mbar_wait(&ops_v[s], par) && mbar_wait(&p_full[s], par)
-                                : mbar_wait(&ops_k[s], par) && mbar_wait(&s_free[s], par ^ 1u);
-          if (!ok || *abort_v != 0) {
-            fail();
+      if (warp < kVWarp) {
+        // ---- K codes -> tensor memory, B = q~ s' (hi + lo), q~ . z' ----
+        const int t = threadIdx.x - 32 * kKWarp, q = warp - kKWarp;
+        const int grp = t >> 3, nl = t & 7;
+        const int gq = lane >> 2, tq = lane & 3;
+        const float i0 = 1.0f / lift0(p.kb), i1 = 1.0f / lift1(p.kb);
+        for (int i = 0; i < cnt; ++i, ++g) {
+          const int s = (int)(g & 1);
+          const uint32_t par = (uint32_t)((g >> 1) & 1);
+          // QK of the page before the last has read the codes and B, the softmax its q~ . z'
+          if (!wait_warp(&rec_full[r], rph) || !wait_warp(&qk_full[s], par ^ 1u) || !wait_warp(&s_free[s], par ^ 1u) ||
+              *abort_v != 0) {
             bad = true;
+            fail();
             break;
           }
           fence_after();
-          if (is_pv) {
-            const uint32_t pb = smem_u32(sm + S::kPOff + s * S::kPBytes);
-            const uint32_t av = tmem + S::kColV + (S::kVStages == 2 ? (uint32_t)(s * 64 * S::kHalves) : 0u);
-#pragma unroll
-            for (int hf = 0; hf < S::kHalves; ++hf)
-#pragma unroll
-              for (int o = 0; o < 8; ++o)
-                mma_ts(tmem + S::kColO + hf * NR, av + 64 * hf + 8 * o, smem_desc(pb + o * S::kStep, NR * 16, 128),
-                       kIdescPV<NR>, (uint32_t)(i > 0 || o > 0));
-            mma_commit(&pv_done[s]);
-            last = &pv_done[s];
-          } else {
-            const uint32_t bb = smem_u32(sm + S::kBOff + s * 2 * S::kBHalf);
-            const uint32_t ak = tmem + S::kColK + (uint32_t)(s * (D / 2));
-#pragma unroll
-            for (int kk = 0; kk < 2 * S::kSteps; ++kk)  // hi, then lo
-              mma_ts(tmem + S::kColS + (uint32_t)(s * NR), ak + 8 * (kk % S::kSteps),
-                     smem_desc(bb + kk * S::kStep, 128, 256), kIdescQK<NR>, (uint32_t)(kk > 0));
-            mma_commit(&qk_full[s]);
-            last = &qk_full[s];
+          const uint8_t* R = recs + r * rec;
+          // fragment (o, i) of 16 tokens x 16 channels is lanes 16o.., columns 8i..8i+7; column
+          // 2tq + h holds channels 16i + 8h + 2tq, +1 of its tokens g and g + 8
+          const uint32_t ta = tmem + S::kColK + (uint32_t)(s * (D / 2)) + ((uint32_t)(32 * q) << 16);
+          const uint4* kc = reinterpret_cast<const uint4*>(R + RL.kcodes);
+          if (p.kb == 4) {
+  #pragma unroll 1
+            for (int oo = 0; oo < 2; ++oo)
+  #pragma unroll
+              for (int kq = 0; kq < D / 64; ++kq) {
+                const uint4 w4 = kc[((2 * q + oo) * (D / 64) + kq) * 32 + lane];
+                const uint32_t ws[4] = {w4.x, w4.y, w4.z, w4.w};
+                uint32_t rr[16];
+  #pragma unroll
+                for (int e = 0; e < 4; ++e) {
+                  const uint32_t x = ws[e], y = x >> 8;
+                  rr[4 * e] = x & 0x000F000Fu;
+                  rr[4 * e + 1] = x & 0x00F000F0u;
+                  rr[4 * e + 2] = y & 0x000F000Fu;
+                  rr[4 * e + 3] = y & 0x00F000F0u;
+                }
+                st_16x256b_x4(ta + ((uint32_t)(16 * oo) << 16) + 32 * kq, rr);
+              }
+          } else if (p.kb == 8) {
+  #pragma unroll 1
+            for (int oo = 0; oo < 2; ++oo)
+  #pragma unroll 2
+              for (int kp = 0; kp < D / 32; ++kp) {
+                const uint4 w4 = kc[((2 * q + oo) * (D / 32) + kp) * 32 + lane];
+                uint32_t rr[8], a[4];
+                unpack_k8(w4.x, w4.y, a);
+                rr[0] = a[0];
+                rr[1] = a[2];
+                rr[2] = a[1];
+                rr[3] = a[3];
+                unpack_k8(w4.z, w4.w, a);
+                rr[4] = a[0];
+                rr[5] = a[2];
+                rr[6] = a[1];
+                rr[7] = a[3];
+                st_16x256b_x2(ta + ((uint32_t)(16 * oo) << 16) + 16 * kp, rr);
+              }
+          } else {  // 2-bit: a word holds token blocks 2q and 2q + 1, the odd one's codes 4 bits higher
+  #pragma unroll 1
+            for (int kq = 0; kq < D / 64; ++kq) {
+              const uint4 w4 = kc[(q * (D / 64) + kq) * 32 + lane];
+              const uint32_t ws[4] = {w4.x, w4.y, w4.z, w4.w};
+  #pragma unroll
+              for (int oo = 0; oo < 2; ++oo) {
+                uint32_t rr[16];
+  #pragma unroll
+                for (int e = 0; e < 4; ++e) {
+                  const uint32_t x = ws[e], y = x >> 8;
+                  rr[4 * e] = x & (0x00030003u << (4 * oo));
+                  rr[4 * e + 1] = x & (0x000C000Cu << (4 * oo));
+                  rr[4 * e + 2] = y & (0x00030003u << (4 * oo));
+                  rr[4 * e + 3] = y & (0x000C000Cu << (4 * oo));
+                }
+                st_16x256b_x4(ta + ((uint32_t)(16 * oo) << 16) + 32 * kq, rr);
+              }
+            }
           }
-          last_par = par;
+          // B rows n = 8 rg + nl over K indexes 8kb..8kb+7 of step kk (channels cb + {0, 1, 8, 9, 2,
+          // 3, 10, 11}): 16 thread groups of 8 over the D / 8 (kk, kb) pairs
+          uint8_t* bs = sm + S::kBOff + s * 2 * S::kBHalf;
+  #pragma unroll
+          for (int c2 = 0; c2 < (D > 128 ? 2 : 1); ++c2) {
+            const int oc = D == 64 ? (grp & 7) : grp + 16 * c2;
+            const int kk = oc >> 1, kb = oc & 1, cb = 16 * kk + 4 * kb;
+            const uint2 sa = *reinterpret_cast<const uint2*>(R + RL.kscale + 2 * cb);
+            const uint2 sb = *reinterpret_cast<const uint2*>(R + RL.kscale + 2 * (cb + 8));
+            const __half2 sv[4] = {u2h2(sa.x), u2h2(sb.x), u2h2(sa.y), u2h2(sb.y)};
+  #pragma unroll 2
+            for (int rg = 0; rg < NR / 8; ++rg) {
+              if (D == 64 && (rg & 1) != (grp >> 3)) continue;
+              const int at = kk * S::kStep + rg * 256 + kb * 128 + nl * 16;
+              const uint4 h4 = *reinterpret_cast<const uint4*>(q_hi + at);
+              const uint4 l4 = *reinterpret_cast<const uint4*>(q_lo + at);
+              const __half2 qh[4] = {u2h2(h4.x), u2h2(h4.y), u2h2(h4.z), u2h2(h4.w)};
+              const __half2 ql[4] = {u2h2(l4.x), u2h2(l4.y), u2h2(l4.z), u2h2(l4.w)};
+              uint32_t hi[4], lo[4];
+  #pragma unroll
+              for (int e = 0; e < 4; ++e) {
+                const __half2 hv = __hmul2(qh[e], sv[e]);
+                hi[e] = h2u(hv);
+                lo[e] = h2u(__hfma2(ql[e], sv[e], __hfma2(qh[e], sv[e], __hneg2(hv))));
+              }
+              *reinterpret_cast<uint4*>(bs + at) = make_uint4(hi[0], hi[1], hi[2], hi[3]);
+              *reinterpret_cast<uint4*>(bs + S::kBHalf + at) = make_uint4(lo[0], lo[1], lo[2], lo[3]);
+            }
+          }
+          // q~ . z' of rows 16q..16q+15 on mma.sync: B column 0 holds z' of channels 0..7 of every
+          // 16, column 1 of channels 8..15, whose q~ carry different lifts
+          if (16 * q < NR) {
+            float acc[4] = {0.0f, 0.0f, 0.0f, 0.0f};
+            const int m = lane >> 3;
+            const uint32_t qa = smem_u32(q_hi) + (2 * q + (m & 1)) * 256 + (m >> 1) * 128 + (lane & 7) * 16;
+            const bool mine = gq < 2 && (tq & 1) == gq;
+            const uint8_t* zc = R + RL.kzero + 2 * (8 * (tq & 1) + 2 * (tq >> 1));
+  #pragma unroll 2
+            for (int kk = 0; kk < S::kSteps; ++kk) {
+              const uint32_t b0 = mine ? *reinterpret_cast<const uint32_t*>(zc + 32 * kk) : 0u;
+              const uint32_t b1 = mine ? *reinterpret_cast<const uint32_t*>(zc + 32 * kk + 8) : 0u;
+              uint32_t a[4];
+              ldsm_x4(qa + kk * S::kStep, a);
+              mma16816(acc, a, b0, b1);
+              ldsm_x4(qa + S::kBHalf + kk * S::kStep, a);
+              mma16816(acc, a, b0, b1);
+            }
+            if (tq == 0) {
+              float* qz = qz_s + s * NR + 16 * q + gq;
+              qz[0] = acc[0] * i0 + acc[1] * i1;
+              qz[8] = acc[2] * i0 + acc[3] * i1;
+            }
+          }
+          wait_st();
+          fence_proxy_async_smem();
+          fence_before();
+          __syncwarp();
+          if (lane == 0) {
+            mbar_arrive(&ops_k[s]);
+            mbar_arrive(&rec_empty[r]);
+          }
+          if (++r == slots) {
+            r = 0;
+            rph ^= 1u;
+          }
         }
+      } else if (warp < kLoadWarp) {
+        // ---- V~ -> tensor memory: channels on the lanes, tokens along K ----
+        const int q = warp - kVWarp;
+        const int gq = lane >> 2, tq = lane & 3;
+        for (int i = 0; i < cnt; ++i, ++g) {
+          const int s = (int)(g & 1);
+          const int vs = S::kVStages == 2 ? s : 0;
+          // PV of the page that last used this buffer
+          const int64_t gp = g - S::kVStages;
+          if (!wait_warp(&rec_full[r], rph) ||
+              (gp >= 0 && !wait_warp(&pv_done[gp & 1], (uint32_t)((gp >> 1) & 1))) || *abort_v != 0) {
+            bad = true;
+            fail();
+            break;
+          }
+          fence_after();
+          const uint8_t* R = recs + r * rec;
+          const __half2* vsc = reinterpret_cast<const __half2*>(R + RL.vscale);
+          const __half2* vzr = reinterpret_cast<const __half2*>(R + RL.vzero);
+          const __half* vch = reinterpret_cast<const __half*>(R + RL.vfactor);
+          const uint2* vc = reinterpret_cast<const uint2*>(R + RL.vcodes);
+          const uint32_t ta = tmem + S::kColV + (uint32_t)(vs * 64 * S::kHalves) + ((uint32_t)(32 * q) << 16);
+          if (D >= 128 || q < D / 32) {
+            __half2 cv[S::kHalves][2][2];  // channel factors of rows g, g + 8 of the two blocks
+  #pragma unroll
+            for (int hf = 0; hf < S::kHalves; ++hf)
+  #pragma unroll
+              for (int ii = 0; ii < 2; ++ii)
+  #pragma unroll
+                for (int rho = 0; rho < 2; ++rho)
+                  cv[hf][ii][rho] = __half2half2(vch[16 * (8 * hf + 2 * q + ii) + gq + 8 * rho]);
+  #pragma unroll 1
+            for (int o2 = 0; o2 < 4; ++o2) {
+              __half2 s2[2][2], z2[2][2];  // [token block of the pair][token half]
+  #pragma unroll
+              for (int f = 0; f < 2; ++f)
+  #pragma unroll
+                for (int h = 0; h < 2; ++h) {
+                  s2[f][h] = vsc[8 * (2 * o2 + f) + 4 * h + tq];
+                  z2[f][h] = vzr[8 * (2 * o2 + f) + 4 * h + tq];
+                }
+  #pragma unroll
+              for (int hf = 0; hf < S::kHalves; ++hf) {
+                const int cb = 8 * hf + 2 * q;  // channel blocks cb, cb + 1: adjacent words
+                uint32_t x[2][2];               // [channel block][word of token block f]
+                if (p.vb == 2) {
+                  const uint2 a = vc[(((o2 * (D / 64) + (cb >> 2)) * 32 + lane) * 4 + (cb & 3)) >> 1];
+                  x[0][0] = x[0][1] = a.x;
+                  x[1][0] = x[1][1] = a.y;
+                } else {
+  #pragma unroll
+                  for (int f = 0; f < 2; ++f) {
+                    const uint2 a = vc[((((2 * o2 + f) * (D / 64) + (cb >> 2)) * 32 + lane) * 4 + (cb & 3)) >> 1];
+                    x[0][f] = a.x;
+                    x[1][f] = a.y;
+                  }
+                }
+  #pragma unroll
+                for (int ii = 0; ii < 2; ++ii) {
+                  uint32_t rr[8];
+  #pragma unroll
+                  for (int f = 0; f < 2; ++f)
+  #pragma unroll
+                    for (int rho = 0; rho < 2; ++rho) {
+                      const uint32_t y = rho ? x[ii][f] >> 8 : x[ii][f];
+  #pragma unroll
+                      for (int h = 0; h < 2; ++h) {
+                        // the code's bits under an exponent that makes them base + code, minus base
+                        const int k2 = 4 * f + 2 * h, k4 = 4 * h;
+                        uint32_t cu;
+                        if (p.vb == 2)
+                          cu = h2u(__hsub2(u2h2((y & (0x00030003u << k2)) | (0x64006400u - (uint32_t)k2 * 0x04000400u)),
+                                           u2h2(0x64006400u - (uint32_t)k2 * 0x04000400u)));
+                        else
+                          cu = h2u(__hsub2(u2h2((y & (0x000F000Fu << k4)) | (0x64006400u - (uint32_t)k4 * 0x04000400u)),
+                                           u2h2(0x64006400u - (uint32_t)k4 * 0x04000400u)));
+                        rr[4 * f + 2 * rho + h] = h2u(__hmul2(__hfma2(u2h2(cu), s2[f][h], z2[f][h]), cv[hf][ii][rho]));
+                      }
+                    }
+                  st_16x256b_x2(ta + ((uint32_t)(16 * ii) << 16) + 64 * hf + 16 * o2, rr);
+                }
+              }
+            }
+          }
+          wait_st();
+          fence_before();
+          __syncwarp();
+          if (lane == 0) {
+            mbar_arrive(&ops_v[s]);
+            mbar_arrive(&rec_empty[r]);
+          }
+          if (++r == slots) {
+            r = 0;
+            rph ^= 1u;
+          }
+        }
+      } else {
+        // ---- MMA issue: one lane; QK of even and of odd pages on two warps, PV on a third ----
+        const bool is_pv = warp == kPvWarp;
+        if (lane == 0) {
+          for (int i = 0; i < cnt; ++i) {
+            const int64_t gi = g + i;
+            const int s = (int)(gi & 1);
+            const uint32_t par = (uint32_t)((gi >> 1) & 1);
+            if (!is_pv && s != warp - kQkWarp) continue;
+            const bool ok = is_pv ? wait_one(&ops_v[s], par) && wait_one(&p_full[s], par)
+                                  : wait_one(&ops_k[s], par) && wait_one(&s_free[s], par ^ 1u);
+            if (!ok || *abort_v != 0) {
+              fail();
+              bad = true;
+              break;
+            }
+            fence_after();
+            if (is_pv) {
+              const uint32_t pb = smem_u32(sm + S::kPOff + s * S::kPBytes);
+              const uint32_t av = tmem + S::kColV + (S::kVStages == 2 ? (uint32_t)(s * 64 * S::kHalves) : 0u);
+  #pragma unroll 1
+              for (int hf = 0; hf < S::kHalves; ++hf)
+  #pragma unroll 2
+                for (int o = 0; o < 8; ++o)
+                  mma_ts(tmem + S::kColO + hf * NR, av + 64 * hf + 8 * o, smem_desc(pb + o * S::kStep, NR * 16, 128),
+                         kIdescPV<NR>, (uint32_t)(i > 0 || o > 0));
+              mma_commit(&pv_done[s]);
+              last = &pv_done[s];
+            } else {
+              const uint32_t bb = smem_u32(sm + S::kBOff + s * 2 * S::kBHalf);
+              const uint32_t ak = tmem + S::kColK + (uint32_t)(s * (D / 2));
+  #pragma unroll 2
+              for (int kk = 0; kk < 2 * S::kSteps; ++kk)  // hi, then lo
+                mma_ts(tmem + S::kColS + (uint32_t)(s * NR), ak + 8 * (kk % S::kSteps),
+                       smem_desc(bb + kk * S::kStep, 128, 256), kIdescQK<NR>, (uint32_t)(kk > 0));
+              mma_commit(&qk_full[s]);
+              last = &qk_full[s];
+            }
+            last_par = par;
+          }
+        }
+        g += cnt;
+        __syncwarp();
       }
-      g += cnt;
-      __syncwarp();
     }
-    if (last != nullptr) mbar_wait(last, last_par);  // this lane's MMAs have completed
+    if (last != nullptr) wait_one(last, last_par);  // this lane's MMAs have completed
     __syncwarp();
   }
 
