@@ -635,14 +635,14 @@ __global__ void __launch_bounds__(blk::kThreads, 1) block_cache_kernel(BlockPara
           const uint32_t ta = tmem + S::kColK + (uint32_t)(s * (D / 2)) + ((uint32_t)(32 * q) << 16);
           const uint4* kc = reinterpret_cast<const uint4*>(R + RL.kcodes);
           if (p.kb == 4) {
-  #pragma unroll 1
+#pragma unroll 1
             for (int oo = 0; oo < 2; ++oo)
-  #pragma unroll
+#pragma unroll
               for (int kq = 0; kq < D / 64; ++kq) {
                 const uint4 w4 = kc[((2 * q + oo) * (D / 64) + kq) * 32 + lane];
                 const uint32_t ws[4] = {w4.x, w4.y, w4.z, w4.w};
                 uint32_t rr[16];
-  #pragma unroll
+#pragma unroll
                 for (int e = 0; e < 4; ++e) {
                   const uint32_t x = ws[e], y = x >> 8;
                   rr[4 * e] = x & 0x000F000Fu;
@@ -653,9 +653,9 @@ __global__ void __launch_bounds__(blk::kThreads, 1) block_cache_kernel(BlockPara
                 st_16x256b_x4(ta + ((uint32_t)(16 * oo) << 16) + 32 * kq, rr);
               }
           } else if (p.kb == 8) {
-  #pragma unroll 1
+#pragma unroll 1
             for (int oo = 0; oo < 2; ++oo)
-  #pragma unroll 2
+#pragma unroll 2
               for (int kp = 0; kp < D / 32; ++kp) {
                 const uint4 w4 = kc[((2 * q + oo) * (D / 32) + kp) * 32 + lane];
                 uint32_t rr[8], a[4];
@@ -672,14 +672,14 @@ __global__ void __launch_bounds__(blk::kThreads, 1) block_cache_kernel(BlockPara
                 st_16x256b_x2(ta + ((uint32_t)(16 * oo) << 16) + 16 * kp, rr);
               }
           } else {  // 2-bit: a word holds token blocks 2q and 2q + 1, the odd one's codes 4 bits higher
-  #pragma unroll 1
+#pragma unroll 1
             for (int kq = 0; kq < D / 64; ++kq) {
               const uint4 w4 = kc[(q * (D / 64) + kq) * 32 + lane];
               const uint32_t ws[4] = {w4.x, w4.y, w4.z, w4.w};
-  #pragma unroll
+#pragma unroll
               for (int oo = 0; oo < 2; ++oo) {
                 uint32_t rr[16];
-  #pragma unroll
+#pragma unroll
                 for (int e = 0; e < 4; ++e) {
                   const uint32_t x = ws[e], y = x >> 8;
                   rr[4 * e] = x & (0x00030003u << (4 * oo));
@@ -694,14 +694,14 @@ __global__ void __launch_bounds__(blk::kThreads, 1) block_cache_kernel(BlockPara
           // B rows n = 8 rg + nl over K indexes 8kb..8kb+7 of step kk (channels cb + {0, 1, 8, 9, 2,
           // 3, 10, 11}): 16 thread groups of 8 over the D / 8 (kk, kb) pairs
           uint8_t* bs = sm + S::kBOff + s * 2 * S::kBHalf;
-  #pragma unroll
+#pragma unroll
           for (int c2 = 0; c2 < (D > 128 ? 2 : 1); ++c2) {
             const int oc = D == 64 ? (grp & 7) : grp + 16 * c2;
             const int kk = oc >> 1, kb = oc & 1, cb = 16 * kk + 4 * kb;
             const uint2 sa = *reinterpret_cast<const uint2*>(R + RL.kscale + 2 * cb);
             const uint2 sb = *reinterpret_cast<const uint2*>(R + RL.kscale + 2 * (cb + 8));
             const __half2 sv[4] = {u2h2(sa.x), u2h2(sb.x), u2h2(sa.y), u2h2(sb.y)};
-  #pragma unroll 2
+#pragma unroll 2
             for (int rg = 0; rg < NR / 8; ++rg) {
               if (D == 64 && (rg & 1) != (grp >> 3)) continue;
               const int at = kk * S::kStep + rg * 256 + kb * 128 + nl * 16;
@@ -710,7 +710,7 @@ __global__ void __launch_bounds__(blk::kThreads, 1) block_cache_kernel(BlockPara
               const __half2 qh[4] = {u2h2(h4.x), u2h2(h4.y), u2h2(h4.z), u2h2(h4.w)};
               const __half2 ql[4] = {u2h2(l4.x), u2h2(l4.y), u2h2(l4.z), u2h2(l4.w)};
               uint32_t hi[4], lo[4];
-  #pragma unroll
+#pragma unroll
               for (int e = 0; e < 4; ++e) {
                 const __half2 hv = __hmul2(qh[e], sv[e]);
                 hi[e] = h2u(hv);
@@ -728,7 +728,7 @@ __global__ void __launch_bounds__(blk::kThreads, 1) block_cache_kernel(BlockPara
             const uint32_t qa = smem_u32(q_hi) + (2 * q + (m & 1)) * 256 + (m >> 1) * 128 + (lane & 7) * 16;
             const bool mine = gq < 2 && (tq & 1) == gq;
             const uint8_t* zc = R + RL.kzero + 2 * (8 * (tq & 1) + 2 * (tq >> 1));
-  #pragma unroll 2
+#pragma unroll 2
             for (int kk = 0; kk < S::kSteps; ++kk) {
               const uint32_t b0 = mine ? *reinterpret_cast<const uint32_t*>(zc + 32 * kk) : 0u;
               const uint32_t b1 = mine ? *reinterpret_cast<const uint32_t*>(zc + 32 * kk + 8) : 0u;
@@ -781,24 +781,24 @@ __global__ void __launch_bounds__(blk::kThreads, 1) block_cache_kernel(BlockPara
           const uint32_t ta = tmem + S::kColV + (uint32_t)(vs * 64 * S::kHalves) + ((uint32_t)(32 * q) << 16);
           if (D >= 128 || q < D / 32) {
             __half2 cv[S::kHalves][2][2];  // channel factors of rows g, g + 8 of the two blocks
-  #pragma unroll
+#pragma unroll
             for (int hf = 0; hf < S::kHalves; ++hf)
-  #pragma unroll
+#pragma unroll
               for (int ii = 0; ii < 2; ++ii)
-  #pragma unroll
+#pragma unroll
                 for (int rho = 0; rho < 2; ++rho)
                   cv[hf][ii][rho] = __half2half2(vch[16 * (8 * hf + 2 * q + ii) + gq + 8 * rho]);
-  #pragma unroll 1
+#pragma unroll 1
             for (int o2 = 0; o2 < 4; ++o2) {
               __half2 s2[2][2], z2[2][2];  // [token block of the pair][token half]
-  #pragma unroll
+#pragma unroll
               for (int f = 0; f < 2; ++f)
-  #pragma unroll
+#pragma unroll
                 for (int h = 0; h < 2; ++h) {
                   s2[f][h] = vsc[8 * (2 * o2 + f) + 4 * h + tq];
                   z2[f][h] = vzr[8 * (2 * o2 + f) + 4 * h + tq];
                 }
-  #pragma unroll
+#pragma unroll
               for (int hf = 0; hf < S::kHalves; ++hf) {
                 const int cb = 8 * hf + 2 * q;  // channel blocks cb, cb + 1: adjacent words
                 uint32_t x[2][2];               // [channel block][word of token block f]
@@ -807,22 +807,22 @@ __global__ void __launch_bounds__(blk::kThreads, 1) block_cache_kernel(BlockPara
                   x[0][0] = x[0][1] = a.x;
                   x[1][0] = x[1][1] = a.y;
                 } else {
-  #pragma unroll
+#pragma unroll
                   for (int f = 0; f < 2; ++f) {
                     const uint2 a = vc[((((2 * o2 + f) * (D / 64) + (cb >> 2)) * 32 + lane) * 4 + (cb & 3)) >> 1];
                     x[0][f] = a.x;
                     x[1][f] = a.y;
                   }
                 }
-  #pragma unroll
+#pragma unroll
                 for (int ii = 0; ii < 2; ++ii) {
                   uint32_t rr[8];
-  #pragma unroll
+#pragma unroll
                   for (int f = 0; f < 2; ++f)
-  #pragma unroll
+#pragma unroll
                     for (int rho = 0; rho < 2; ++rho) {
                       const uint32_t y = rho ? x[ii][f] >> 8 : x[ii][f];
-  #pragma unroll
+#pragma unroll
                       for (int h = 0; h < 2; ++h) {
                         // the code's bits under an exponent that makes them base + code, minus base
                         const int k2 = 4 * f + 2 * h, k4 = 4 * h;
@@ -873,9 +873,9 @@ __global__ void __launch_bounds__(blk::kThreads, 1) block_cache_kernel(BlockPara
             if (is_pv) {
               const uint32_t pb = smem_u32(sm + S::kPOff + s * S::kPBytes);
               const uint32_t av = tmem + S::kColV + (S::kVStages == 2 ? (uint32_t)(s * 64 * S::kHalves) : 0u);
-  #pragma unroll 1
+#pragma unroll 1
               for (int hf = 0; hf < S::kHalves; ++hf)
-  #pragma unroll 2
+#pragma unroll 2
                 for (int o = 0; o < 8; ++o)
                   mma_ts(tmem + S::kColO + hf * NR, av + 64 * hf + 8 * o, smem_desc(pb + o * S::kStep, NR * 16, 128),
                          kIdescPV<NR>, (uint32_t)(i > 0 || o > 0));
@@ -884,7 +884,7 @@ __global__ void __launch_bounds__(blk::kThreads, 1) block_cache_kernel(BlockPara
             } else {
               const uint32_t bb = smem_u32(sm + S::kBOff + s * 2 * S::kBHalf);
               const uint32_t ak = tmem + S::kColK + (uint32_t)(s * (D / 2));
-  #pragma unroll 2
+#pragma unroll 2
               for (int kk = 0; kk < 2 * S::kSteps; ++kk)  // hi, then lo
                 mma_ts(tmem + S::kColS + (uint32_t)(s * NR), ak + 8 * (kk % S::kSteps),
                        smem_desc(bb + kk * S::kStep, 128, 256), kIdescQK<NR>, (uint32_t)(kk > 0));

@@ -291,36 +291,40 @@ def prefill_attention(desc: KvarnDesc, q, chunk_k, chunk_v, pool, block_table, c
                                         _ptr(status), _stream(stream)), "kvarn_prefill_attention")
 
 
-def _tensors(device, **named):
-    """Checks of the tensors of one call: on `device`, of their dtype and shape, contiguous.  Each
-    name gives (tensor or None, dtypes, shape or None); shape entries of None are free."""
-    for name, (t, dtypes, shape) in named.items():
-        if t is None:
-            continue
+def _arg(name, t, device, dtype, shape):
+    """Device pointer of a contiguous tensor argument on `device` of the given dtype and shape."""
+    if t.dtype is not dtype or t.shape != shape or t.device != device or not t.is_contiguous():
         _ptr(t)
         if t.device != device:
             raise ValueError("%s is on %s, q on %s" % (name, t.device, device))
-        if t.dtype not in dtypes:
-            raise ValueError("%s must be %s" % (name, " or ".join(str(d) for d in dtypes)))
-        if not t.is_contiguous():
-            raise ValueError("%s must be contiguous" % name)
-        if shape is not None and (t.dim() != len(shape) or
-                                  any(w is not None and n != w for n, w in zip(t.shape, shape))):
-            raise ValueError("%s must be %s, got %s" % (name, list(shape), list(t.shape)))
+        raise ValueError("%s must be a contiguous %s tensor of shape %s, got %s of shape %s (strides %s)" %
+                         (name, dtype, list(shape), t.dtype, list(t.shape), list(t.stride())))
+    return t.data_ptr()
 
 
-def _cache_tensors(desc, q, batch, pool, block_table, lens, partial_k, partial_v, workspace, status):
-    half, i32 = (torch.float16,), (torch.int32,)
-    tile = (batch, desc.num_kv_heads, 128, desc.head_dim)
-    _ptr(q)
-    _tensors(q.device, pool=(pool, (torch.uint8,), (None, desc.num_kv_heads, desc.page_record_bytes)),
-             block_table=(block_table, i32, (batch, None)), lens=(lens, i32, (batch,)),
-             partial_k=(partial_k, half, tile), partial_v=(partial_v, half, tile),
-             workspace=(workspace, (workspace.dtype,), None), status=(status, i32, None))
+def _opt(name, t, device, dtype, shape):
+    return None if t is None else _arg(name, t, device, dtype, shape)
 
 
-def _stream_on(device, stream):
-    return _stream(torch.cuda.current_stream(device) if stream is None else stream)
+def _status_arg(status, device):
+    return None if status is None else _arg("status", status, device, torch.int32, status.shape)
+
+
+def _workspace_arg(workspace, device):
+    return (_arg("workspace", workspace, device, workspace.dtype, workspace.shape),
+            workspace.numel() * workspace.element_size())
+
+
+def _launch(fn, where, device, stream, *args):
+    """Call fn(*args, stream) with `device` current, on `stream` or the device's current stream."""
+    if stream is None:
+        stream = torch.cuda.current_stream(device)
+    if torch.cuda.current_device() == device.index:
+        status = fn(*args, stream.cuda_stream)
+    else:
+        with torch.cuda.device(device):
+            status = fn(*args, stream.cuda_stream)
+    _check(status, where)
 
 
 def _alloc_bytes(n: int, what: str, device):
@@ -348,17 +352,19 @@ def window_decode_attention(desc: KvarnDesc, q, pool, block_table, seq_lens, out
     ones (their own, token seq_lens[b] - 1, included).  q, out: fp16 [batch, Hq, d0].  Block-table
     entries of pages between the two are not read."""
     batch, hq, d0 = q.shape
-    _cache_tensors(desc, q, batch, pool, block_table, seq_lens, partial_k, partial_v, workspace, status)
-    rows = (batch, hq, desc.head_dim)
-    _tensors(q.device, q=(q, (torch.float16,), rows), out=(out, (torch.float16,), rows))
-    if softmax_scale is None:
-        softmax_scale = 1.0 / math.sqrt(d0)
-    with torch.cuda.device(q.device):
-        _check(_lib.kvarn_window_decode_attention(
-            ctypes.byref(desc), batch, hq, _ptr(q), _ptr(pool), pool.shape[0], _ptr(block_table),
-            block_table.shape[1], _ptr(seq_lens), _ptr(partial_k), _ptr(partial_v), int(sink_tokens), int(window),
-            float(softmax_scale), _ptr(out), _ptr(workspace), workspace.numel() * workspace.element_size(),
-            _ptr(status), _stream_on(q.device, stream)), "kvarn_window_decode_attention")
+    dev, hkv, half, i32 = q.device, desc.num_kv_heads, torch.float16, torch.int32
+    rows, tile = (batch, hq, desc.head_dim), (batch, hkv, 128, desc.head_dim)
+    pages, width = pool.shape[0], block_table.shape[-1]
+    ws, ws_bytes = _workspace_arg(workspace, dev)
+    _ptr(q)
+    _launch(_lib.kvarn_window_decode_attention, "kvarn_window_decode_attention", dev, stream,
+            ctypes.byref(desc), batch, hq, _arg("q", q, dev, half, rows),
+            _arg("pool", pool, dev, torch.uint8, (pages, hkv, desc.page_record_bytes)), pages,
+            _arg("block_table", block_table, dev, i32, (batch, width)), width,
+            _arg("seq_lens", seq_lens, dev, i32, (batch,)), _opt("partial_k", partial_k, dev, half, tile),
+            _opt("partial_v", partial_v, dev, half, tile), sink_tokens, window,
+            1.0 / math.sqrt(d0) if softmax_scale is None else softmax_scale, _arg("out", out, dev, half, rows),
+            ws, ws_bytes, _status_arg(status, dev))
 
 
 def window_prefill_workspace_bytes(desc: KvarnDesc, batch: int, num_q_heads: int, chunk_len: int, max_pages: int,
@@ -373,12 +379,20 @@ def alloc_window_prefill_workspace(desc: KvarnDesc, batch: int, num_q_heads: int
                                                        sink_tokens, window), "window_prefill_workspace", device)
 
 
-def _block_tensors(desc, q, new_k, new_v, out, new_lens, what):
+def _block_args(desc, what, q, new_k, new_v, new_lens, pool, block_table, cache_lens, partial_k, partial_v):
+    """Pointers of the tensors that the two block-attention calls share, in the order of their
+    parameters (the mask, which only one has, apart)."""
     batch, block, hq, _ = q.shape
-    half, rows = (torch.float16,), (batch, block, hq, desc.head_dim)
-    kv = (batch, block, desc.num_kv_heads, desc.head_dim)
-    _tensors(q.device, **{"q": (q, half, rows), "out": (out, half, rows), what + "_k": (new_k, half, kv),
-                          what + "_v": (new_v, half, kv), what + "_lens": (new_lens, (torch.int32,), (batch,))})
+    _ptr(q)
+    dev, hkv, d0, half, i32 = q.device, desc.num_kv_heads, desc.head_dim, torch.float16, torch.int32
+    kv, tile = (batch, block, hkv, d0), (batch, hkv, 128, d0)
+    pages, width = pool.shape[0], block_table.shape[-1]
+    return ((_arg("q", q, dev, half, (batch, block, hq, d0)), _arg(what + "_k", new_k, dev, half, kv),
+             _arg(what + "_v", new_v, dev, half, kv)), _opt(what + "_lens", new_lens, dev, i32, (batch,)),
+            (_arg("pool", pool, dev, torch.uint8, (pages, hkv, desc.page_record_bytes)), pages,
+             _arg("block_table", block_table, dev, i32, (batch, width)), width,
+             _arg("cache_lens", cache_lens, dev, i32, (batch,)), _opt("partial_k", partial_k, dev, half, tile),
+             _opt("partial_v", partial_v, dev, half, tile)))
 
 
 def window_prefill_attention(desc: KvarnDesc, q, chunk_k, chunk_v, pool, block_table, cache_lens, out, workspace,
@@ -389,17 +403,15 @@ def window_prefill_attention(desc: KvarnDesc, q, chunk_k, chunk_v, pool, block_t
     d0]; chunk_lens: int32 [batch] or None, tokens of each sequence's chunk (rows of out past them
     stay as they were).  Block-table entries of pages that no query sees are not read."""
     batch, chunk, hq, d0 = q.shape
-    _cache_tensors(desc, q, batch, pool, block_table, cache_lens, partial_k, partial_v, workspace, status)
-    _block_tensors(desc, q, chunk_k, chunk_v, out, chunk_lens, "chunk")
-    if softmax_scale is None:
-        softmax_scale = 1.0 / math.sqrt(d0)
-    with torch.cuda.device(q.device):
-        _check(_lib.kvarn_window_prefill_attention(
-            ctypes.byref(desc), batch, hq, chunk, _ptr(q), _ptr(chunk_k), _ptr(chunk_v), _ptr(chunk_lens), _ptr(pool),
-            pool.shape[0], _ptr(block_table), block_table.shape[1], _ptr(cache_lens), _ptr(partial_k),
-            _ptr(partial_v), int(sink_tokens), int(window), float(softmax_scale), _ptr(out), _ptr(workspace),
-            workspace.numel() * workspace.element_size(), _ptr(status), _stream_on(q.device, stream)),
-            "kvarn_window_prefill_attention")
+    new, lens, cache = _block_args(desc, "chunk", q, chunk_k, chunk_v, chunk_lens, pool, block_table, cache_lens,
+                                   partial_k, partial_v)
+    dev = q.device
+    ws, ws_bytes = _workspace_arg(workspace, dev)
+    _launch(_lib.kvarn_window_prefill_attention, "kvarn_window_prefill_attention", dev, stream,
+            ctypes.byref(desc), batch, hq, chunk, *new, lens, *cache, sink_tokens, window,
+            1.0 / math.sqrt(d0) if softmax_scale is None else softmax_scale,
+            _arg("out", out, dev, torch.float16, (batch, chunk, hq, desc.head_dim)), ws, ws_bytes,
+            _status_arg(status, dev))
 
 
 def tree_workspace_bytes(desc: KvarnDesc, batch: int, num_q_heads: int, tree_len: int, max_pages: int) -> int:
@@ -419,18 +431,18 @@ def tree_attention(desc: KvarnDesc, q, tree_k, tree_v, tree_mask, pool, block_ta
     of word j / 32 of row i set when node i sees node j, or None for a chain; tree_lens: int32
     [batch] or None, nodes of each sequence (rows of out past them stay as they were)."""
     batch, nodes, hq, d0 = q.shape
-    _cache_tensors(desc, q, batch, pool, block_table, cache_lens, partial_k, partial_v, workspace, status)
-    _block_tensors(desc, q, tree_k, tree_v, out, tree_lens, "tree")
-    _tensors(q.device, tree_mask=(tree_mask, (torch.int32, torch.uint32), (batch, nodes, (nodes + 31) // 32)))
-    if softmax_scale is None:
-        softmax_scale = 1.0 / math.sqrt(d0)
-    with torch.cuda.device(q.device):
-        _check(_lib.kvarn_tree_attention(
-            ctypes.byref(desc), batch, hq, nodes, _ptr(q), _ptr(tree_k), _ptr(tree_v), _ptr(tree_mask), _ptr(tree_lens),
-            _ptr(pool), pool.shape[0], _ptr(block_table), block_table.shape[1], _ptr(cache_lens), _ptr(partial_k),
-            _ptr(partial_v), float(softmax_scale), _ptr(out), _ptr(workspace),
-            workspace.numel() * workspace.element_size(), _ptr(status), _stream_on(q.device, stream)),
-            "kvarn_tree_attention")
+    new, lens, cache = _block_args(desc, "tree", q, tree_k, tree_v, tree_lens, pool, block_table, cache_lens,
+                                   partial_k, partial_v)
+    dev = q.device
+    ws, ws_bytes = _workspace_arg(workspace, dev)
+    if tree_mask is not None and tree_mask.dtype is torch.uint32:
+        tree_mask = tree_mask.view(torch.int32)
+    _launch(_lib.kvarn_tree_attention, "kvarn_tree_attention", dev, stream,
+            ctypes.byref(desc), batch, hq, nodes, *new,
+            _opt("tree_mask", tree_mask, dev, torch.int32, (batch, nodes, (nodes + 31) // 32)), lens, *cache,
+            1.0 / math.sqrt(d0) if softmax_scale is None else softmax_scale,
+            _arg("out", out, dev, torch.float16, (batch, nodes, hq, desc.head_dim)), ws, ws_bytes,
+            _status_arg(status, dev))
 
 
 def decode_attention_noalloc(desc: KvarnDesc, q, pool, block_table, seq_lens, out, partial_k=None,
