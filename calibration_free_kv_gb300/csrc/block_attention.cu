@@ -38,13 +38,16 @@ namespace blk {
 
 using namespace tc5;
 
-constexpr int kThreads = 512;
-constexpr int kKWarp = 4, kVWarp = 8, kLoadWarp = 12, kQkWarp = 13, kPvWarp = 15;
+constexpr int kThreads = 1024;
+// warps: 0-7 softmax (4 per column half), 8-15 K, 16-23 V, 24 loader, 25-28 QK, 29-30 PV, 31 walk
+constexpr int kKWarp = 8, kVWarp = 16, kMiscWarp = 24;
+constexpr int kLoadWarp = 24, kQkWarp = 25, kWalkWarp = 31;
 constexpr int kMaxSlots = 8;
-constexpr int kRoleBar = 1, kSmBar = 2;  // named barriers: all warps but the loader, the softmax warps
+// named barriers: all warps but the loader, the two softmax warpgroups (kSmBar, kSmBar + 1)
+constexpr int kRoleBar = 1, kSmBar = 2;
 constexpr int kRoleThreads = kThreads - 32;
-constexpr int kFixUnits = 6;  // units of the line ahead of a row tile's pages: a segment's fixed work
-constexpr int kMinUnits = 10;  // smallest range
+// Units of the line ahead of a row tile's pages for a segment's fixed work, and the smallest range.
+constexpr int kFixUnits = 4, kMinUnits = 3;
 constexpr float kSlack = 8.0f;  // log2 units a logit may pass its row's reference by
 constexpr int kSmemMax = 232448 - 1024;
 
@@ -52,6 +55,7 @@ template <int D, int NR>
 struct Shape {
   static constexpr int kSteps = D / 16;           // K steps of QK
   static constexpr int kHalves = D > 128 ? 2 : 1; // 128-channel blocks of PV
+  static constexpr int kParts = NR >= 32 ? 2 : 1; // column parts of the MMAs (N at least 16)
   static constexpr int kVStages = D > 128 ? 1 : 2;
   static constexpr int kStep = NR * 32;           // bytes of one K step of a B operand
   static constexpr int kBHalf = NR * D * 2;       // q~ s' hi (or lo) of one page
@@ -61,10 +65,10 @@ struct Shape {
   static constexpr int kPOff = 2 * 2 * kBHalf;
   static constexpr int kQOff = kPOff + 2 * kPBytes;
   static constexpr int kSmallOff = kQOff + 2 * kBHalf;
-  // floats: qz [2][NR], -reference, row maximum, shift, rescale, row limit [NR] each, per warp [4][NR]
-  static constexpr int kSmallFloats = (2 + 5 + 4) * NR;
+  // floats: qz [4][NR], -reference, row maximum, shift, rescale, row limit [NR] each, per warp [4][NR]
+  static constexpr int kSmallFloats = (4 + 5 + 4) * NR;
   static constexpr int kBarOff = kSmallOff + kSmallFloats * 4;
-  static constexpr int kNumBars = 2 * kMaxSlots + 6 * 2;
+  static constexpr int kNumBars = 2 * kMaxSlots + 3 * 2 + 3 * 4;
   static constexpr int kRecOff = (kBarOff + kNumBars * 8 + 127) & ~127;
   // tensor memory columns
   static constexpr uint32_t kColK = 0, kColV = 2 * (D / 2);
@@ -113,9 +117,21 @@ __device__ __forceinline__ bool wait_one(uint64_t* bar, uint32_t parity) {
   }
   return false;
 }
+// One lane of a converged warp.  MMAs are issued under it: the compiler then knows that a single
+// thread runs them and keeps their operands in uniform registers.
+__device__ __forceinline__ bool elect_one() {
+  uint32_t p;
+  asm volatile("{\n\t.reg .pred p;\n\telect.sync _|p, 0xffffffff;\n\tselp.u32 %0, 1, 0, p;\n\t}" : "=r"(p));
+  return p != 0;
+}
 __device__ __forceinline__ bool wait_warp(uint64_t* bar, uint32_t parity) {
   return __all_sync(0xffffffffu, wait_one(bar, parity));
 }
+
+template <int N>
+struct IntC {
+  static constexpr int value = N;
+};
 
 __device__ __forceinline__ int cached_len(const BlockParams& p, int b) {
   const int cap = p.max_pages * kTile + (kTile - 1);
@@ -143,16 +159,28 @@ __device__ __forceinline__ Span tile_span(const BlockParams& p, int len, int nl,
   const int sinks = min((p.sink + kTile - 1) / kTile, first);
   return {sinks, first, sinks + n - first};
 }
-__device__ __forceinline__ int tile_units(const Span& s) { return s.count > 0 ? s.count + kFixUnits : 0; }
-// units of all row tiles of one kv head of sequence b
-__device__ __forceinline__ int64_t head_units(const BlockParams& p, int b) {
+__device__ __forceinline__ int tile_units(const Span& s, int fix) { return s.count > 0 ? s.count + fix : 0; }
+// pages of all row tiles of one kv head of sequence b, and the tiles that have any
+__device__ __forceinline__ int64_t head_pages(const BlockParams& p, int b, int& tiles) {
   const int len = cached_len(p, b), nl = new_len(p, b);
   const int live = (nl * p.group + p.tile_rows - 1) / p.tile_rows;
-  if (p.window <= 0) return (int64_t)live * (len / kTile > 0 ? len / kTile + kFixUnits : 0);
-  int64_t u = 0;
-  for (int t = 0; t < live; ++t) u += tile_units(tile_span(p, len, nl, t));
-  return u;
+  tiles = 0;
+  if (p.window <= 0) {
+    if (len >= kTile) tiles = live;
+    return (int64_t)live * (len / kTile);
+  }
+  int64_t n = 0;
+  for (int t = 0; t < live; ++t) {
+    const Span s = tile_span(p, len, nl, t);
+    n += s.count;
+    tiles += s.count > 0 ? 1 : 0;
+  }
+  return n;
 }
+
+struct Partition : PagePartition {
+  int fix;  // units ahead of a row tile's pages
+};
 
 // A CTA's range of the line, as segments: runs of pages of one row tile.
 struct TileWalk {
@@ -163,11 +191,11 @@ struct TileWalk {
   int64_t row0;     // unit at which the row tile starts
   __device__ int count() const { return (int)min((int64_t)(span.count - j), left); }
   __device__ int64_t row(const BlockParams& p) const { return ((int64_t)b * p.num_kv_heads + h) * p.tiles + t; }
-  __device__ void next(const BlockParams& p) {
+  __device__ void next(const BlockParams& p, int fix) {
     left -= count();
     if (left <= 0) return;
     j = 0;
-    row0 += tile_units(span);
+    row0 += tile_units(span, fix);
     for (;;) {
       if (++t >= p.tiles) {
         t = 0;
@@ -183,7 +211,7 @@ struct TileWalk {
       }
       span = tile_span(p, len, nl, t);
       if (span.count > 0) {
-        left -= kFixUnits;  // the range may end inside the row tile's fixed units
+        left -= fix;  // the range may end inside the row tile's fixed units
         if (left < 0) left = 0;
         return;
       }
@@ -192,21 +220,35 @@ struct TileWalk {
 };
 
 // Warp-collective: the partition and this CTA's walk.
-__device__ __forceinline__ TileWalk range_walk(const BlockParams& p, int64_t cta, int lane, PagePartition& pp) {
+__device__ __forceinline__ TileWalk range_walk(const BlockParams& p, int64_t cta, int lane, Partition& pp) {
   TileWalk w = {};
-  long long total = 0;
-  for (int b = lane; b < p.batch; b += 32) total += head_units(p, b);
+  long long pages = 0, tiles = 0;
+  for (int b = lane; b < p.batch; b += 32) {
+    int t;
+    pages += head_pages(p, b, t);
+    tiles += t;
+  }
 #pragma unroll
-  for (int m = 16; m > 0; m >>= 1) total += __shfl_xor_sync(0xffffffffu, total, m);
-  pp.total = total * p.num_kv_heads;
-  const int64_t c = pp.total / kMinUnits;
+  for (int m = 16; m > 0; m >>= 1) {
+    pages += __shfl_xor_sync(0xffffffffu, pages, m);
+    tiles += __shfl_xor_sync(0xffffffffu, tiles, m);
+  }
+  pages *= p.num_kv_heads;
+  tiles *= p.num_kv_heads;
+  // With few pages a CTA each the pages are spread one by one (a segment's fixed work then runs on
+  // all SMs at once); with more the line charges each row tile for it.
+  pp.fix = pages <= 2 * kBlockCtas ? 0 : kFixUnits;
+  pp.total = pages + tiles * pp.fix;
+  const int64_t c = pp.fix == 0 ? pp.total : pp.total / kMinUnits;
   pp.ctas = pp.total > 0 ? (c < 1 ? 1 : (c > kBlockCtas ? kBlockCtas : c)) : 0;
   if (cta >= pp.ctas) return w;
   const int64_t x0 = range_start(pp, cta), x1 = range_start(pp, cta + 1);
   long long cum = 0;
   for (int b0 = 0; b0 < p.batch; b0 += 32) {
     const int bb = b0 + lane;
-    const long long hu = bb < p.batch ? head_units(p, bb) : 0;
+    int ht = 0;
+    long long hu = bb < p.batch ? head_pages(p, bb, ht) : 0;
+    hu += (long long)ht * pp.fix;
     long long incl = hu * p.num_kv_heads;
 #pragma unroll
     for (int m = 1; m < 32; m <<= 1) {
@@ -225,12 +267,12 @@ __device__ __forceinline__ TileWalk range_walk(const BlockParams& p, int64_t cta
       at += (long long)w.h * u;
       for (w.t = 0;; ++w.t) {  // the row tile that holds x0
         w.span = tile_span(p, w.len, w.nl, w.t);
-        const int tu = tile_units(w.span);
+        const int tu = tile_units(w.span, pp.fix);
         if (x0 < at + tu || w.t + 1 >= p.tiles) break;
         at += tu;
       }
       w.row0 = at;
-      const int64_t first = at + kFixUnits;  // unit of the row tile's first page
+      const int64_t first = at + pp.fix;  // unit of the row tile's first page
       w.j = x0 < first ? 0 : (int)(x0 - first);
       w.left = x1 - (first + w.j);
       if (w.left < 0) w.left = 0;  // the range ends inside the fixed units
@@ -248,9 +290,12 @@ template <int D, int NR>
 __global__ void __launch_bounds__(blk::kThreads, 1) block_cache_kernel(BlockParams p, int slots) {
   using namespace blk;
   using S = Shape<D, NR>;
+  constexpr int NC = NR / 2;       // rows (columns of S, P and O) of one softmax warpgroup
+  constexpr int NP = S::kParts;    // MMA column parts
+  constexpr int NM = NR / NP;      // columns of one MMA
   extern __shared__ __align__(1024) uint8_t sm[];
-  __shared__ TileWalk walk_s;
-  __shared__ PagePartition part_s;
+  __shared__ TileWalk seg_s[2];
+  __shared__ Partition part_s;
   __shared__ uint32_t tslot;
   __shared__ int abort_flag;
   const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
@@ -258,14 +303,14 @@ __global__ void __launch_bounds__(blk::kThreads, 1) block_cache_kernel(BlockPara
   const int rec = RL.bytes;
   uint64_t* rec_full = reinterpret_cast<uint64_t*>(sm + S::kBarOff);
   uint64_t* rec_empty = rec_full + kMaxSlots;
-  uint64_t* ops_k = rec_empty + kMaxSlots;  // per stage: K codes, B and q~ . z' written
-  uint64_t* qk_full = ops_k + 2;            // QK done: K codes and B are free
-  uint64_t* s_free = qk_full + 2;           // S and q~ . z' read
-  uint64_t* ops_v = s_free + 2;             // V written
-  uint64_t* p_full = ops_v + 2;             // P written, O rescaled
-  uint64_t* pv_done = p_full + 2;           // PV done: V and P are free, O is up to date
-  float* qz_s = reinterpret_cast<float*>(sm + S::kSmallOff);  // [2][NR]
-  float* nref_s = qz_s + 2 * NR;   // minus the row's reference
+  uint64_t* ops_k = rec_empty + kMaxSlots;  // [stage]: K codes, B and q~ . z' written
+  uint64_t* s_free = ops_k + 2;             // [stage]: S and q~ . z' read
+  uint64_t* ops_v = s_free + 2;             // [stage]: V written
+  uint64_t* qk_full = ops_v + 2;            // [part][stage]: QK done (K codes and B are free)
+  uint64_t* p_full = qk_full + 4;           // [part][stage]: P written, O rescaled
+  uint64_t* pv_done = p_full + 4;           // [part][stage]: PV done: V and P are free, O is up to date
+  float* qz_s = reinterpret_cast<float*>(sm + S::kSmallOff);  // [4][NR]: page g's at g % 4
+  float* nref_s = qz_s + 4 * NR;   // minus the row's reference
   float* max_s = nref_s + NR;      // the row's maximum when the reference was set (-inf: none yet)
   float* shift_s = max_s + NR;     // old reference - new reference
   float* alpha_s = shift_s + NR;   // rescale of l and O
@@ -278,60 +323,59 @@ __global__ void __launch_bounds__(blk::kThreads, 1) block_cache_kernel(BlockPara
   // The kernel before this one (block_raw_kernel) waited for everything ahead of it before it let
   // this grid start, so the inputs are complete; its own partials are read by the merge only.
   if (warp == 1) {
-    PagePartition pp;
+    Partition pp;
     const TileWalk w = range_walk(p, blockIdx.x, lane, pp);
     if (lane == 0) {
-      walk_s = w;
+      seg_s[0] = w;
       part_s = pp;
     }
   }
   if (threadIdx.x == 0) {
     for (int i = 0; i < kMaxSlots; ++i) {
       mbar_init(&rec_full[i], 1);
-      mbar_init(&rec_empty[i], 12);
+      mbar_init(&rec_empty[i], 24);
     }
     for (int s = 0; s < 2; ++s) {
-      mbar_init(&ops_k[s], 4);
-      mbar_init(&qk_full[s], 1);
-      mbar_init(&s_free[s], 4);
-      mbar_init(&ops_v[s], 4);
-      mbar_init(&p_full[s], 4);
+      mbar_init(&ops_k[s], 8);
+      mbar_init(&s_free[s], 8);
+      mbar_init(&ops_v[s], 8);
+    }
+    for (int s = 0; s < 4; ++s) {
+      mbar_init(&qk_full[s], 2);
+      mbar_init(&p_full[s], 8 / NP);
       mbar_init(&pv_done[s], 1);
     }
     abort_flag = 0;
     fence_mbar_init();
   }
-  __syncthreads();
-  grid_launch_dependents();
-  int64_t total = 0;  // pages of this CTA's range
-  for (TileWalk w = walk_s; w.left > 0; w.next(p)) total += w.count();
-  if (total <= 0) {
-    grid_dependency_wait();  // block_raw_kernel has finished when this grid has
-    return;
-  }
-  if (warp == 0) {
+  if (warp == 2) {
     asm volatile("tcgen05.alloc.cta_group::1.sync.aligned.shared::cta.b32 [%0], 512;" ::"r"(smem_u32(&tslot)));
     asm volatile("tcgen05.relinquish_alloc_permit.cta_group::1.sync.aligned;");
   }
   fence_before();
   __syncthreads();
   fence_after();
+  grid_launch_dependents();
   const uint32_t tmem = tslot;
-  const TileWalk w0 = walk_s;
   volatile int* abort_v = &abort_flag;
   auto fail = [&]() {
     *abort_v = 1;
     flag_error(p.status, KVARN_DEV_WAIT_TIMEOUT);
   };
-  // q~ of a segment's rows, hi + lo, in the order and layout of the QK operand; every warp but the
-  // loader's takes part.  Returns true when the CTA gives up (all warps alike).
-  auto stage_queries = [&](const TileWalk& w, bool bad) -> bool {
-    if (bar_any(kRoleBar, kRoleThreads, bad || *abort_v != 0)) return true;
-    const int wi = warp < kLoadWarp ? warp : warp - 1;
+  // Segment k of this CTA's range, or false at its end (or when the CTA gives up): the same for all
+  // warps but the loader's.
+  auto segment = [&](int k, bool bad) -> bool {
+    if (bar_any(kRoleBar, kRoleThreads, bad || *abort_v != 0)) return false;
+    return seg_s[k & 1].left > 0;
+  };
+  // q~ of a segment's rows, hi + lo, in the order and layout of the QK operand, by the 24 warps of
+  // the softmax, K and V roles.
+  auto stage_queries = [&](const TileWalk& w) {
     const float sc = p.qscale * inv_sqrt_d<D>();
     const float h0 = lift0(p.kb), h1 = lift1(p.kb);
     const bool q4 = (reinterpret_cast<uintptr_t>(p.q) & 3u) == 0u;
-    for (int n = wi; n < NR; n += kRoleThreads / 32) {
+#pragma unroll 1
+    for (int n = warp; n < NR; n += 24) {
       const int r = w.t * NR + n, c = r / p.group;
       const bool live = c < w.nl;
       float v[D / 32];
@@ -363,56 +407,63 @@ __global__ void __launch_bounds__(blk::kThreads, 1) block_cache_kernel(BlockPara
       // padding rows see everything: they get a reference on the first page
       if (lane == 0) lim_s[n] = live ? w.len + c + 1 - p.window : INT32_MIN;
     }
-    return bar_any(kRoleBar, kRoleThreads, false);
+  };
+  // the roles' place in the line of pages and in the ring of records
+  int g = 0;
+  int r = 0;
+  uint32_t rph = 0;
+  auto next_record = [&]() {
+    if (++r == slots) {
+      r = 0;
+      rph ^= 1u;
+    }
   };
 
-  // The softmax warpgroup holds a token's NR logits and NR sums: 208 registers there and 96 in the
-  // other three, 63,488 of the 65,536 the CTA is launched with.
-  if (warp < 4) {
-    asm volatile("setmaxnreg.inc.sync.aligned.u32 208;");
-  } else {
-    asm volatile("setmaxnreg.dec.sync.aligned.u32 96;");
-  }
-  if (warp < 4) {
-    // ---- softmax (thread = token), rescale and the segment's partial (thread = channel) ----
-    const int u = threadIdx.x;
-    const uint32_t lanes = (uint32_t)(32 * warp) << 16;
+  // Registers of the 65,536 the CTA is launched with: 104 a thread for the softmax, which holds a
+  // token's NR / 2 logits and as many sums, 56 for K and V, 40 for the rest.
+  if (warp < kKWarp) {
+    asm volatile("setmaxnreg.inc.sync.aligned.u32 104;");
+    // ---- softmax (thread = token, rows c0 ..), rescale and the segment's partial (thread = channel) ----
+    const int u = threadIdx.x & 127, wq = warp & 3;
+    const int half = warp >> 2;
+    const int c0 = half * NC;
+    const int part = NP == 2 ? half : 0;
+    const int sbar = kSmBar + half;
+    const uint32_t lanes = (uint32_t)(32 * wq) << 16;
     const int kpos = 4 * ((u >> 1) & 3) + 2 * ((u >> 3) & 1) + (u & 1);
-    const int poff = (u >> 4) * S::kStep + (kpos >> 3) * (NR * 16) + (kpos & 7) * 16;
+    const int poff = (u >> 4) * S::kStep + (kpos >> 3) * (NR * 16) + (kpos & 7) * 16 + 16 * c0;
     const float cf = kTwo24 / lift0(p.kb) * (p.kb == 2 && ((u >> 4) & 1) ? 0.0625f : 1.0f);
-    int64_t g = 0;
-    int r = 0;
-    uint32_t rph = 0;
     bool bad = false, stop = false;
-    for (TileWalk w = w0; w.left > 0; w.next(p)) {
-      if (stage_queries(w, bad)) break;
+    for (int k = 0; segment(k, bad); ++k) {
+      const TileWalk w = seg_s[k & 1];
+      stage_queries(w);
       const int cnt = w.count();
       const int64_t row = w.row(p);
       const int c1 = min((w.t * NR + NR - 1) / p.group, w.nl - 1);  // the tile's last new token
       const int sure = w.len + c1 + 1 - p.window;  // from here on every row's window sees
-      float2 l[NR / 2];
+      float2 l[NC / 2];
 #pragma unroll
-      for (int i = 0; i < NR / 2; ++i) l[i] = make_float2(0.0f, 0.0f);
-      if (u < NR) {
-        nref_s[u] = 0.0f;
-        max_s[u] = -INFINITY;
+      for (int i = 0; i < NC / 2; ++i) l[i] = make_float2(0.0f, 0.0f);
+      if (u < NC) {
+        nref_s[c0 + u] = 0.0f;
+        max_s[c0 + u] = -INFINITY;
       }
-      bar_any(kSmBar, 128, false);
+      bar_any(kRoleBar, kRoleThreads, false);
       bool unset = true;  // some row has no reference yet
       for (int i = 0; i < cnt; ++i, ++g) {
         const int s = (int)(g & 1);
         const uint32_t par = (uint32_t)((g >> 1) & 1);
-        const bool ok = !bad && wait_warp(&qk_full[s], par) && wait_warp(&ops_k[s], par) && wait_warp(&rec_full[r], rph);
-        float x[NR];
-        if (ok) {
+        float x[NC];
+        if (!bad && wait_warp(&qk_full[2 * part + s], par)) {
           fence_after();
+          ld_cols<NC>(tmem + S::kColS + (uint32_t)(s * NR + c0) + lanes, x);
           const float rt = __half2float(reinterpret_cast<const __half*>(recs + r * rec + RL.kfactor)[u]);
-          ld_cols<NR>(tmem + S::kColS + (uint32_t)(s * NR) + lanes, x);
           const float at = rt * cf;
-          const float* qz = qz_s + s * NR;
+          const float* qz = qz_s + (g & 3) * NR + c0;
 #pragma unroll
-          for (int n = 0; n < NR; n += 4) {
-            const float4 z = *reinterpret_cast<const float4*>(qz + n), m = *reinterpret_cast<const float4*>(nref_s + n);
+          for (int n = 0; n < NC; n += 4) {
+            const float4 z = *reinterpret_cast<const float4*>(qz + n);
+            const float4 m = *reinterpret_cast<const float4*>(nref_s + c0 + n);
             const float2 a = fma2(make_float2(at, at), make_float2(x[n], x[n + 1]),
                                   fma2(make_float2(rt, rt), make_float2(z.x, z.y), make_float2(m.x, m.y)));
             const float2 c = fma2(make_float2(at, at), make_float2(x[n + 2], x[n + 3]),
@@ -433,81 +484,81 @@ __global__ void __launch_bounds__(blk::kThreads, 1) block_cache_kernel(BlockPara
             if (at0 + kTile > p.sink && at0 < sure) {  // an edge page of the window or of the first tokens
               const int pos = at0 + u;
 #pragma unroll
-              for (int n = 0; n < NR; ++n)
-                if (pos >= p.sink && pos < lim_s[n]) x[n] = -INFINITY;
+              for (int n = 0; n < NC; ++n)
+                if (pos >= p.sink && pos < lim_s[c0 + n]) x[n] = -INFINITY;
             }
           }
         } else {
           if (!bad) fail();
           bad = true;
 #pragma unroll
-          for (int n = 0; n < NR; ++n) x[n] = 0.0f;
+          for (int n = 0; n < NC; ++n) x[n] = 0.0f;
         }
-        if (++r == slots) {
-          r = 0;
-          rph ^= 1u;
-        }
+        next_record();
         float mx = -INFINITY;
 #pragma unroll
-        for (int n = 0; n < NR; n += 2) mx = fmax3(mx, x[n], x[n + 1]);
-        if (bar_any(kSmBar, 128, bad || unset || mx > kSlack)) {
-          stop = bar_any(kSmBar, 128, bad);
+        for (int n = 0; n < NC; n += 2) mx = fmax3(mx, x[n], x[n + 1]);
+        if (bar_any(sbar, 128, bad || unset || mx > kSlack)) {
+          stop = bar_any(sbar, 128, bad);
           if (stop) break;
           // move the references to the rows' maxima
 #pragma unroll
-          for (int n = 0; n < NR; ++n) {
+          for (int n = 0; n < NC; ++n) {
             const float v = warp_max(x[n]);
-            if (lane == (n & 31)) warp_s[warp * NR + n] = v;
+            if (lane == n) warp_s[wq * NR + c0 + n] = v;
           }
-          bar_any(kSmBar, 128, false);
+          bar_any(sbar, 128, false);
           bool none = false;
-          if (u < NR) {
-            const float old = max_s[u], ref = -nref_s[u];
-            const float pm = fmaxf(fmaxf(warp_s[u], warp_s[NR + u]), fmaxf(warp_s[2 * NR + u], warp_s[3 * NR + u])) + ref;
+          if (u < NC) {
+            const int n = c0 + u;
+            const float old = max_s[n], ref = -nref_s[n];
+            const float pm =
+                fmaxf(fmaxf(warp_s[n], warp_s[NR + n]), fmaxf(warp_s[2 * NR + n], warp_s[3 * NR + n])) + ref;
             const float mn = fmaxf(old, pm);
             none = mn == -INFINITY;
             const float to = none ? 0.0f : mn;
-            max_s[u] = mn;
-            nref_s[u] = -to;
-            shift_s[u] = ref - to;
-            alpha_s[u] = old == -INFINITY ? 0.0f : ex2_approx(old - mn);
+            max_s[n] = mn;
+            nref_s[n] = -to;
+            shift_s[n] = ref - to;
+            alpha_s[n] = old == -INFINITY ? 0.0f : ex2_approx(old - mn);
           }
-          unset = bar_any(kSmBar, 128, none);
+          unset = bar_any(sbar, 128, none);
 #pragma unroll
-          for (int n = 0; n < NR; n += 2) {
-            x[n] += shift_s[n];
-            x[n + 1] += shift_s[n + 1];
-            l[n / 2] = mul2(l[n / 2], make_float2(alpha_s[n], alpha_s[n + 1]));
+          for (int n = 0; n < NC; n += 2) {
+            x[n] += shift_s[c0 + n];
+            x[n + 1] += shift_s[c0 + n + 1];
+            l[n / 2] = mul2(l[n / 2], make_float2(alpha_s[c0 + n], alpha_s[c0 + n + 1]));
           }
           if (i > 0) {  // O of the pages before this one
-            if (!wait_warp(&pv_done[(g - 1) & 1], (uint32_t)(((g - 1) >> 1) & 1))) {
+            if (!wait_warp(&pv_done[2 * part + ((g - 1) & 1)], (uint32_t)(((g - 1) >> 1) & 1))) {
               fail();
               bad = true;
             } else {
               fence_after();
-#pragma unroll
+#pragma unroll 1
               for (int hf = 0; hf < S::kHalves; ++hf)
+#pragma unroll 1
+                for (int n0 = 0; n0 < NC; n0 += 8) {
+                  float o[8];
+                  const uint32_t ta = tmem + S::kColO + (uint32_t)(hf * NR + c0 + n0) + lanes;
+                  ld_cols<8>(ta, o);
+                  uint32_t ob[8];
 #pragma unroll
-                for (int n0 = 0; n0 < NR; n0 += 16) {
-                  float o[16];
-                  const uint32_t ta = tmem + S::kColO + (uint32_t)(hf * NR + n0) + lanes;
-                  ld_cols<16>(ta, o);
-#pragma unroll
-                  for (int n = 0; n < 16; ++n) o[n] *= alpha_s[n0 + n];
-                  st_32x32b_x16(ta, o);
+                  for (int n = 0; n < 8; ++n) ob[n] = __float_as_uint(o[n] * alpha_s[c0 + n0 + n]);
+                  st_32x32b_x8(ta, ob);
                 }
               wait_st();
             }
           }
         }
         // P of the stage, once PV of the page before the last has read it
-        if (!bad && !wait_warp(&pv_done[s], par ^ 1u)) {
+        if (!bad && !wait_warp(&pv_done[2 * part + s], par ^ 1u)) {
           fail();
           bad = true;
         }
         uint8_t* pb = sm + S::kPOff + s * S::kPBytes + poff;
 #pragma unroll
-        for (int n = 0; n < NR; n += 8) {
+        for (int n = 0; n < NC; n += 8) {
           uint32_t h[4];
 #pragma unroll
           for (int e = 0; e < 4; ++e) {
@@ -520,46 +571,47 @@ __global__ void __launch_bounds__(blk::kThreads, 1) block_cache_kernel(BlockPara
         fence_proxy_async_smem();
         fence_before();
         __syncwarp();
-        if (lane == 0 && !bad) mbar_arrive(&p_full[s]);
+        if (lane == 0 && !bad) mbar_arrive(&p_full[2 * part + s]);
       }
-      if (bar_any(kSmBar, 128, bad || stop)) {
+      if (bar_any(sbar, 128, bad || stop)) {
         bad = true;
-        continue;  // the next stage_queries() ends the loop for every warp
+        continue;  // segment() ends the loop for every warp
       }
       // the segment's partial: l over the tokens, O once its last PV is done
 #pragma unroll
-      for (int n = 0; n < NR; ++n) {
+      for (int n = 0; n < NC; ++n) {
         float v = (n & 1) ? l[n / 2].y : l[n / 2].x;
 #pragma unroll
         for (int m = 16; m > 0; m >>= 1) v += __shfl_xor_sync(0xffffffffu, v, m);
-        if (lane == (n & 31)) warp_s[warp * NR + n] = v;
+        if (lane == n) warp_s[wq * NR + c0 + n] = v;
       }
-      bar_any(kSmBar, 128, false);
-      const int live = min(NR, w.nl * p.group - w.t * NR);  // rows of the tile that exist
-      float* dst = p.part + ((int64_t)blockIdx.x + row) * NR * (D + 4);
-      if (u < live) {
+      bar_any(sbar, 128, false);
+      const int live = min(NR, w.nl * p.group - w.t * NR) - c0;  // rows of this half that exist
+      float* dst = p.part + (((int64_t)blockIdx.x + row) * NR + c0) * (D + 4);
+      if (u < min(live, NC)) {
+        const int n = c0 + u;
         float* d = dst + (int64_t)u * (D + 4);
-        d[0] = max_s[u] == -INFINITY ? -INFINITY : -nref_s[u];
-        d[1] = (warp_s[u] + warp_s[NR + u]) + (warp_s[2 * NR + u] + warp_s[3 * NR + u]);
+        d[0] = max_s[n];
+        d[1] = (warp_s[n] + warp_s[NR + n]) + (warp_s[2 * NR + n] + warp_s[3 * NR + n]);
       }
-      if (w.j == 0 && u == 0) {
-        const int64_t last = owner_cta(part_s, w.row0 + kFixUnits + w.span.count - 1);
+      if (w.j == 0 && threadIdx.x == 0) {
+        const int64_t last = owner_cta(part_s, w.row0 + part_s.fix + w.span.count - 1);
         p.row_info[row] = make_int2((int)((int64_t)blockIdx.x + row), (int)(last - blockIdx.x + 1));
       }
-      if (!wait_warp(&pv_done[(g - 1) & 1], (uint32_t)(((g - 1) >> 1) & 1))) {
+      if (!wait_warp(&pv_done[2 * part + ((g - 1) & 1)], (uint32_t)(((g - 1) >> 1) & 1))) {
         fail();
         bad = true;
       } else {
         fence_after();
-#pragma unroll
+#pragma unroll 1
         for (int hf = 0; hf < S::kHalves; ++hf) {
-#pragma unroll
-          for (int n0 = 0; n0 < NR; n0 += 16) {
-            float o[16];
-            ld_cols<16>(tmem + S::kColO + (uint32_t)(hf * NR + n0) + lanes, o);
+#pragma unroll 1
+          for (int n0 = 0; n0 < min(NC, live); n0 += 8) {
+            float o[8];
+            ld_cols<8>(tmem + S::kColO + (uint32_t)(hf * NR + c0 + n0) + lanes, o);
             if (D >= 128 || u < D) {
 #pragma unroll
-              for (int n = 0; n < 16; ++n)
+              for (int n = 0; n < 8; ++n)
                 if (n0 + n < live) dst[(int64_t)(n0 + n) * (D + 4) + 4 + hf * 128 + u] = o[n];
             }
           }
@@ -567,77 +619,42 @@ __global__ void __launch_bounds__(blk::kThreads, 1) block_cache_kernel(BlockPara
         fence_before();
       }
     }
-  } else if (warp == kLoadWarp) {
-    // ---- page records -> the ring ----
-    if (lane == 0) {
-      int64_t g = 0;
-      int r = 0;
-      uint32_t rph = 0;
-      bool bad = false;
-      for (TileWalk w = w0; w.left > 0 && !bad; w.next(p)) {
-        const int cnt = w.count();
-        const int32_t* bt = p.block_table + (int64_t)w.b * p.max_pages;
-        for (int i = 0; i < cnt; ++i, ++g) {
-          int64_t id = bt[w.span.page(w.j + i)];
-          if (id < 0 || id >= p.num_pool_pages) {
-            flag_error(p.status, KVARN_DEV_BAD_PAGE_ID);
-            id = 0;
-          }
-          if (!wait_one(&rec_empty[r], rph ^ 1u) || *abort_v != 0) {
-            fail();
-            bad = true;
-            break;
-          }
-          fence_proxy_async_smem();
-          mbar_expect_tx(&rec_full[r], (uint32_t)rec);
-          bulk_copy_g2s(recs + r * rec, p.pool + (id * p.num_kv_heads + w.h) * (int64_t)rec, (uint32_t)rec, &rec_full[r]);
-          if (++r == slots) {
-            r = 0;
-            rph ^= 1u;
-          }
-        }
-      }
-      // copies still in flight land before the CTA may leave
-      for (int64_t k = g > slots ? g - slots : 0; k < g; ++k)
-        wait_one(&rec_full[k % slots], (uint32_t)((k / slots) & 1));
-    }
-    __syncwarp();
-  } else {
-    int64_t g = 0;  // pages done, and the ring slot and its phase for the roles that read records
-    int r = 0;
-    uint32_t rph = 0;
+  } else if (warp < kVWarp) {
+    asm volatile("setmaxnreg.dec.sync.aligned.u32 56;");
+    // ---- warps 8-11: K codes -> tensor memory; 12-15: q~ . z'; each half of the rows of B = q~ s' ----
+    const int t = threadIdx.x & 127, q = warp & 3;
+    const bool codes = warp < kKWarp + 4;
+    const int grp = t >> 3, nl = t & 7;
+    const int gq = lane >> 2, tq = lane & 3;
+    const float i0 = 1.0f / lift0(p.kb), i1 = 1.0f / lift1(p.kb);
     bool bad = false;
-    uint64_t* last = nullptr;  // MMA issue: the barrier of this lane's last commit
-    uint32_t last_par = 0;
-    for (TileWalk w = w0; w.left > 0; w.next(p)) {
-      if (stage_queries(w, __any_sync(0xffffffffu, bad))) break;
-      const int cnt = w.count();
-      if (warp < kVWarp) {
-        // ---- K codes -> tensor memory, B = q~ s' (hi + lo), q~ . z' ----
-        const int t = threadIdx.x - 32 * kKWarp, q = warp - kKWarp;
-        const int grp = t >> 3, nl = t & 7;
-        const int gq = lane >> 2, tq = lane & 3;
-        const float i0 = 1.0f / lift0(p.kb), i1 = 1.0f / lift1(p.kb);
-        for (int i = 0; i < cnt; ++i, ++g) {
-          const int s = (int)(g & 1);
-          const uint32_t par = (uint32_t)((g >> 1) & 1);
-          // QK of the page before the last has read the codes and B, the softmax its q~ . z'
-          if (!wait_warp(&rec_full[r], rph) || !wait_warp(&qk_full[s], par ^ 1u) || !wait_warp(&s_free[s], par ^ 1u) ||
-              *abort_v != 0) {
-            bad = true;
-            fail();
-            break;
-          }
-          fence_after();
-          const uint8_t* R = recs + r * rec;
+    for (int k = 0; segment(k, bad); ++k) {
+      stage_queries(seg_s[k & 1]);
+      const int cnt = seg_s[k & 1].count();
+      bar_any(kRoleBar, kRoleThreads, false);
+      for (int i = 0; i < cnt; ++i, ++g) {
+        const int s = (int)(g & 1);
+        const uint32_t par = (uint32_t)((g >> 1) & 1);
+        // QK of the page before the last has read the codes and B
+        bool ok = wait_warp(&rec_full[r], rph);
+#pragma unroll
+        for (int m = 0; m < NP; ++m) ok = ok && wait_warp(&qk_full[2 * m + s], par ^ 1u);
+        if (!ok) {
+          bad = true;
+          fail();
+          break;
+        }
+        fence_after();
+        const uint8_t* R = recs + r * rec;
+        if (codes) {
           // fragment (o, i) of 16 tokens x 16 channels is lanes 16o.., columns 8i..8i+7; column
           // 2tq + h holds channels 16i + 8h + 2tq, +1 of its tokens g and g + 8
           const uint32_t ta = tmem + S::kColK + (uint32_t)(s * (D / 2)) + ((uint32_t)(32 * q) << 16);
           const uint4* kc = reinterpret_cast<const uint4*>(R + RL.kcodes);
           if (p.kb == 4) {
-#pragma unroll 1
-            for (int oo = 0; oo < 2; ++oo)
 #pragma unroll
+            for (int oo = 0; oo < 2; ++oo)
+#pragma unroll 2
               for (int kq = 0; kq < D / 64; ++kq) {
                 const uint4 w4 = kc[((2 * q + oo) * (D / 64) + kq) * 32 + lane];
                 const uint32_t ws[4] = {w4.x, w4.y, w4.z, w4.w};
@@ -691,221 +708,262 @@ __global__ void __launch_bounds__(blk::kThreads, 1) block_cache_kernel(BlockPara
               }
             }
           }
-          // B rows n = 8 rg + nl over K indexes 8kb..8kb+7 of step kk (channels cb + {0, 1, 8, 9, 2,
-          // 3, 10, 11}): 16 thread groups of 8 over the D / 8 (kk, kb) pairs
-          uint8_t* bs = sm + S::kBOff + s * 2 * S::kBHalf;
-#pragma unroll
-          for (int c2 = 0; c2 < (D > 128 ? 2 : 1); ++c2) {
-            const int oc = D == 64 ? (grp & 7) : grp + 16 * c2;
-            const int kk = oc >> 1, kb = oc & 1, cb = 16 * kk + 4 * kb;
-            const uint2 sa = *reinterpret_cast<const uint2*>(R + RL.kscale + 2 * cb);
-            const uint2 sb = *reinterpret_cast<const uint2*>(R + RL.kscale + 2 * (cb + 8));
-            const __half2 sv[4] = {u2h2(sa.x), u2h2(sb.x), u2h2(sa.y), u2h2(sb.y)};
-#pragma unroll 2
-            for (int rg = 0; rg < NR / 8; ++rg) {
-              if (D == 64 && (rg & 1) != (grp >> 3)) continue;
-              const int at = kk * S::kStep + rg * 256 + kb * 128 + nl * 16;
-              const uint4 h4 = *reinterpret_cast<const uint4*>(q_hi + at);
-              const uint4 l4 = *reinterpret_cast<const uint4*>(q_lo + at);
-              const __half2 qh[4] = {u2h2(h4.x), u2h2(h4.y), u2h2(h4.z), u2h2(h4.w)};
-              const __half2 ql[4] = {u2h2(l4.x), u2h2(l4.y), u2h2(l4.z), u2h2(l4.w)};
-              uint32_t hi[4], lo[4];
-#pragma unroll
-              for (int e = 0; e < 4; ++e) {
-                const __half2 hv = __hmul2(qh[e], sv[e]);
-                hi[e] = h2u(hv);
-                lo[e] = h2u(__hfma2(ql[e], sv[e], __hfma2(qh[e], sv[e], __hneg2(hv))));
-              }
-              *reinterpret_cast<uint4*>(bs + at) = make_uint4(hi[0], hi[1], hi[2], hi[3]);
-              *reinterpret_cast<uint4*>(bs + S::kBHalf + at) = make_uint4(lo[0], lo[1], lo[2], lo[3]);
-            }
-          }
+        } else if (16 * q < NR) {
           // q~ . z' of rows 16q..16q+15 on mma.sync: B column 0 holds z' of channels 0..7 of every
           // 16, column 1 of channels 8..15, whose q~ carry different lifts
-          if (16 * q < NR) {
-            float acc[4] = {0.0f, 0.0f, 0.0f, 0.0f};
-            const int m = lane >> 3;
-            const uint32_t qa = smem_u32(q_hi) + (2 * q + (m & 1)) * 256 + (m >> 1) * 128 + (lane & 7) * 16;
-            const bool mine = gq < 2 && (tq & 1) == gq;
-            const uint8_t* zc = R + RL.kzero + 2 * (8 * (tq & 1) + 2 * (tq >> 1));
-#pragma unroll 2
-            for (int kk = 0; kk < S::kSteps; ++kk) {
-              const uint32_t b0 = mine ? *reinterpret_cast<const uint32_t*>(zc + 32 * kk) : 0u;
-              const uint32_t b1 = mine ? *reinterpret_cast<const uint32_t*>(zc + 32 * kk + 8) : 0u;
-              uint32_t a[4];
-              ldsm_x4(qa + kk * S::kStep, a);
-              mma16816(acc, a, b0, b1);
-              ldsm_x4(qa + S::kBHalf + kk * S::kStep, a);
-              mma16816(acc, a, b0, b1);
-            }
-            if (tq == 0) {
-              float* qz = qz_s + s * NR + 16 * q + gq;
-              qz[0] = acc[0] * i0 + acc[1] * i1;
-              qz[8] = acc[2] * i0 + acc[3] * i1;
-            }
+          float acc[2][4] = {};  // q~ hi and lo: two chains
+          const int m = lane >> 3;
+          const uint32_t qa = smem_u32(q_hi) + (2 * q + (m & 1)) * 256 + (m >> 1) * 128 + (lane & 7) * 16;
+          const bool mine = gq < 2 && (tq & 1) == gq;
+          const uint8_t* zc = R + RL.kzero + 2 * (8 * (tq & 1) + 2 * (tq >> 1));
+#pragma unroll 4
+          for (int kk = 0; kk < S::kSteps; ++kk) {
+            const uint32_t b0 = mine ? *reinterpret_cast<const uint32_t*>(zc + 32 * kk) : 0u;
+            const uint32_t b1 = mine ? *reinterpret_cast<const uint32_t*>(zc + 32 * kk + 8) : 0u;
+            uint32_t a[4];
+            ldsm_x4(qa + kk * S::kStep, a);
+            mma16816(acc[0], a, b0, b1);
+            ldsm_x4(qa + S::kBHalf + kk * S::kStep, a);
+            mma16816(acc[1], a, b0, b1);
           }
-          wait_st();
-          fence_proxy_async_smem();
-          fence_before();
-          __syncwarp();
-          if (lane == 0) {
-            mbar_arrive(&ops_k[s]);
-            mbar_arrive(&rec_empty[r]);
-          }
-          if (++r == slots) {
-            r = 0;
-            rph ^= 1u;
+          if (tq == 0) {
+            float* qz = qz_s + (g & 3) * NR + 16 * q + gq;
+            qz[0] = (acc[0][0] + acc[1][0]) * i0 + (acc[0][1] + acc[1][1]) * i1;
+            qz[8] = (acc[0][2] + acc[1][2]) * i0 + (acc[0][3] + acc[1][3]) * i1;
           }
         }
-      } else if (warp < kLoadWarp) {
-        // ---- V~ -> tensor memory: channels on the lanes, tokens along K ----
-        const int q = warp - kVWarp;
-        const int gq = lane >> 2, tq = lane & 3;
-        for (int i = 0; i < cnt; ++i, ++g) {
-          const int s = (int)(g & 1);
-          const int vs = S::kVStages == 2 ? s : 0;
-          // PV of the page that last used this buffer
-          const int64_t gp = g - S::kVStages;
-          if (!wait_warp(&rec_full[r], rph) ||
-              (gp >= 0 && !wait_warp(&pv_done[gp & 1], (uint32_t)((gp >> 1) & 1))) || *abort_v != 0) {
-            bad = true;
-            fail();
-            break;
-          }
-          fence_after();
-          const uint8_t* R = recs + r * rec;
-          const __half2* vsc = reinterpret_cast<const __half2*>(R + RL.vscale);
-          const __half2* vzr = reinterpret_cast<const __half2*>(R + RL.vzero);
-          const __half* vch = reinterpret_cast<const __half*>(R + RL.vfactor);
-          const uint2* vc = reinterpret_cast<const uint2*>(R + RL.vcodes);
-          const uint32_t ta = tmem + S::kColV + (uint32_t)(vs * 64 * S::kHalves) + ((uint32_t)(32 * q) << 16);
-          if (D >= 128 || q < D / 32) {
-            __half2 cv[S::kHalves][2][2];  // channel factors of rows g, g + 8 of the two blocks
-#pragma unroll
-            for (int hf = 0; hf < S::kHalves; ++hf)
-#pragma unroll
-              for (int ii = 0; ii < 2; ++ii)
-#pragma unroll
-                for (int rho = 0; rho < 2; ++rho)
-                  cv[hf][ii][rho] = __half2half2(vch[16 * (8 * hf + 2 * q + ii) + gq + 8 * rho]);
+        // B rows n = 8 rg + nl over K indexes 8kb..8kb+7 of step kk (channels cb + {0, 1, 8, 9, 2,
+        // 3, 10, 11}): 16 thread groups of 8 over the D / 8 (kk, kb) pairs
+        uint8_t* bs = sm + S::kBOff + s * 2 * S::kBHalf;
 #pragma unroll 1
-            for (int o2 = 0; o2 < 4; ++o2) {
-              __half2 s2[2][2], z2[2][2];  // [token block of the pair][token half]
+        for (int c2 = 0; c2 < (D > 128 ? 2 : 1); ++c2) {
+          const int oc = D == 64 ? (grp & 7) : grp + 16 * c2;
+          const int kk = oc >> 1, kb = oc & 1, cb = 16 * kk + 4 * kb;
+          const uint2 sa = *reinterpret_cast<const uint2*>(R + RL.kscale + 2 * cb);
+          const uint2 sb = *reinterpret_cast<const uint2*>(R + RL.kscale + 2 * (cb + 8));
+          const __half2 sv[4] = {u2h2(sa.x), u2h2(sb.x), u2h2(sa.y), u2h2(sb.y)};
+          const int rg0 = codes ? 0 : NR / 16;
+#pragma unroll 2
+          for (int rg = 0; rg < NR / 16; ++rg) {
+            if (D == 64 && NR > 16 && (rg & 1) != (grp >> 3)) continue;
+            if (D == 64 && NR == 16 && grp >= 8) continue;
+            const int at = kk * S::kStep + (rg0 + rg) * 256 + kb * 128 + nl * 16;
+            const uint4 h4 = *reinterpret_cast<const uint4*>(q_hi + at);
+            const uint4 l4 = *reinterpret_cast<const uint4*>(q_lo + at);
+            const __half2 qh[4] = {u2h2(h4.x), u2h2(h4.y), u2h2(h4.z), u2h2(h4.w)};
+            const __half2 ql[4] = {u2h2(l4.x), u2h2(l4.y), u2h2(l4.z), u2h2(l4.w)};
+            uint32_t hi[4], lo[4];
 #pragma unroll
-              for (int f = 0; f < 2; ++f)
+            for (int e = 0; e < 4; ++e) {
+              const __half2 hv = __hmul2(qh[e], sv[e]);
+              hi[e] = h2u(hv);
+              lo[e] = h2u(__hfma2(ql[e], sv[e], __hfma2(qh[e], sv[e], __hneg2(hv))));
+            }
+            *reinterpret_cast<uint4*>(bs + at) = make_uint4(hi[0], hi[1], hi[2], hi[3]);
+            *reinterpret_cast<uint4*>(bs + S::kBHalf + at) = make_uint4(lo[0], lo[1], lo[2], lo[3]);
+          }
+        }
+        if (codes) wait_st();
+        fence_proxy_async_smem();
+        fence_before();
+        __syncwarp();
+        if (lane == 0) {
+          mbar_arrive(&ops_k[s]);
+          mbar_arrive(&rec_empty[r]);
+        }
+        next_record();
+      }
+    }
+  } else if (warp < kMiscWarp) {
+    asm volatile("setmaxnreg.dec.sync.aligned.u32 56;");
+    // ---- V~ -> tensor memory: channels on the lanes, tokens along K; a warp takes one 16-channel
+    // block of each 128 ----
+    const int q = warp & 3, ii = (warp - kVWarp) >> 2;
+    const int gq = lane >> 2, tq = lane & 3;
+    bool bad = false;
+    for (int k = 0; segment(k, bad); ++k) {
+      stage_queries(seg_s[k & 1]);
+      const int cnt = seg_s[k & 1].count();
+      bar_any(kRoleBar, kRoleThreads, false);
+      for (int i = 0; i < cnt; ++i, ++g) {
+        const int s = (int)(g & 1);
+        const int vs = S::kVStages == 2 ? s : 0;
+        // PV of the page that last used this buffer
+        const int gp = g - S::kVStages;
+        bool ok = wait_warp(&rec_full[r], rph);
+        if (gp >= 0) {
 #pragma unroll
-                for (int h = 0; h < 2; ++h) {
-                  s2[f][h] = vsc[8 * (2 * o2 + f) + 4 * h + tq];
-                  z2[f][h] = vzr[8 * (2 * o2 + f) + 4 * h + tq];
-                }
+          for (int m = 0; m < NP; ++m)
+            ok = ok && wait_warp(&pv_done[2 * m + (gp & 1)], (uint32_t)((gp >> 1) & 1));
+        }
+        if (!ok) {
+          bad = true;
+          fail();
+          break;
+        }
+        fence_after();
+        const uint8_t* R = recs + r * rec;
+        const __half2* vsc = reinterpret_cast<const __half2*>(R + RL.vscale);
+        const __half2* vzr = reinterpret_cast<const __half2*>(R + RL.vzero);
+        const __half* vch = reinterpret_cast<const __half*>(R + RL.vfactor);
+        const uint32_t* vc = reinterpret_cast<const uint32_t*>(R + RL.vcodes);
+        const uint32_t ta =
+            tmem + S::kColV + (uint32_t)(vs * 64 * S::kHalves) + ((uint32_t)(32 * q + 16 * ii) << 16);
+        if (D >= 128 || q < D / 32) {
+#pragma unroll 1
+          for (int hf = 0; hf < S::kHalves; ++hf) {
+            const int cb = 8 * hf + 2 * q + ii;
+            const __half2 cv[2] = {__half2half2(vch[16 * cb + gq]), __half2half2(vch[16 * cb + gq + 8])};
+            const uint32_t* vw = vc + ((cb >> 2) * 32 + lane) * 4 + (cb & 3);
+            auto tile = [&](auto vbc) {
+              constexpr int VB = decltype(vbc)::value;
+#pragma unroll 2
+              for (int o2 = 0; o2 < 4; ++o2) {
+                uint32_t rr[8];
 #pragma unroll
-              for (int hf = 0; hf < S::kHalves; ++hf) {
-                const int cb = 8 * hf + 2 * q;  // channel blocks cb, cb + 1: adjacent words
-                uint32_t x[2][2];               // [channel block][word of token block f]
-                if (p.vb == 2) {
-                  const uint2 a = vc[(((o2 * (D / 64) + (cb >> 2)) * 32 + lane) * 4 + (cb & 3)) >> 1];
-                  x[0][0] = x[0][1] = a.x;
-                  x[1][0] = x[1][1] = a.y;
-                } else {
+                for (int f = 0; f < 2; ++f) {
+                  const uint32_t x = vw[(VB == 2 ? o2 : 2 * o2 + f) * (D / 64) * 128];
 #pragma unroll
-                  for (int f = 0; f < 2; ++f) {
-                    const uint2 a = vc[((((2 * o2 + f) * (D / 64) + (cb >> 2)) * 32 + lane) * 4 + (cb & 3)) >> 1];
-                    x[0][f] = a.x;
-                    x[1][f] = a.y;
-                  }
-                }
-#pragma unroll
-                for (int ii = 0; ii < 2; ++ii) {
-                  uint32_t rr[8];
-#pragma unroll
-                  for (int f = 0; f < 2; ++f)
+                  for (int h = 0; h < 2; ++h) {
+                    const __half2 s2 = vsc[8 * (2 * o2 + f) + 4 * h + tq], z2 = vzr[8 * (2 * o2 + f) + 4 * h + tq];
+                    // the code's bits under an exponent that makes them base + code, minus base
+                    constexpr uint32_t one = VB == 2 ? 0x00030003u : 0x000F000Fu;
+                    const int sh = VB == 2 ? 4 * f + 2 * h : 4 * h;
+                    const uint32_t base = 0x64006400u - (uint32_t)sh * 0x04000400u;
 #pragma unroll
                     for (int rho = 0; rho < 2; ++rho) {
-                      const uint32_t y = rho ? x[ii][f] >> 8 : x[ii][f];
-#pragma unroll
-                      for (int h = 0; h < 2; ++h) {
-                        // the code's bits under an exponent that makes them base + code, minus base
-                        const int k2 = 4 * f + 2 * h, k4 = 4 * h;
-                        uint32_t cu;
-                        if (p.vb == 2)
-                          cu = h2u(__hsub2(u2h2((y & (0x00030003u << k2)) | (0x64006400u - (uint32_t)k2 * 0x04000400u)),
-                                           u2h2(0x64006400u - (uint32_t)k2 * 0x04000400u)));
-                        else
-                          cu = h2u(__hsub2(u2h2((y & (0x000F000Fu << k4)) | (0x64006400u - (uint32_t)k4 * 0x04000400u)),
-                                           u2h2(0x64006400u - (uint32_t)k4 * 0x04000400u)));
-                        rr[4 * f + 2 * rho + h] = h2u(__hmul2(__hfma2(u2h2(cu), s2[f][h], z2[f][h]), cv[hf][ii][rho]));
-                      }
+                      const uint32_t y = rho ? x >> 8 : x;
+                      const __half2 c = __hsub2(u2h2((y & (one << sh)) | base), u2h2(base));
+                      rr[4 * f + 2 * rho + h] = h2u(__hmul2(__hfma2(c, s2, z2), cv[rho]));
                     }
-                  st_16x256b_x2(ta + ((uint32_t)(16 * ii) << 16) + 64 * hf + 16 * o2, rr);
+                  }
                 }
+                st_16x256b_x2(ta + 64 * hf + 16 * o2, rr);
               }
-            }
-          }
-          wait_st();
-          fence_before();
-          __syncwarp();
-          if (lane == 0) {
-            mbar_arrive(&ops_v[s]);
-            mbar_arrive(&rec_empty[r]);
-          }
-          if (++r == slots) {
-            r = 0;
-            rph ^= 1u;
+            };
+            if (p.vb == 2) tile(IntC<2>{});
+            else tile(IntC<4>{});
           }
         }
-      } else {
-        // ---- MMA issue: one lane; QK of even and of odd pages on two warps, PV on a third ----
-        const bool is_pv = warp == kPvWarp;
+        wait_st();
+        fence_before();
+        __syncwarp();
         if (lane == 0) {
+          mbar_arrive(&ops_v[s]);
+          mbar_arrive(&rec_empty[r]);
+        }
+        next_record();
+      }
+    }
+  } else {
+    asm volatile("setmaxnreg.dec.sync.aligned.u32 40;");
+    if (warp == kLoadWarp) {
+      // ---- page records -> the ring ----
+      if (lane == 0) {
+        bool bad = false;
+        for (TileWalk w = seg_s[0]; w.left > 0 && !bad; w.next(p, part_s.fix)) {
+          const int cnt = w.count();
+          const int32_t* bt = p.block_table + (int64_t)w.b * p.max_pages;
+          for (int i = 0; i < cnt; ++i, ++g) {
+            int64_t id = bt[w.span.page(w.j + i)];
+            if (id < 0 || id >= p.num_pool_pages) {
+              flag_error(p.status, KVARN_DEV_BAD_PAGE_ID);
+              id = 0;
+            }
+            if (!wait_one(&rec_empty[r], rph ^ 1u)) {
+              fail();
+              bad = true;
+              break;
+            }
+            fence_proxy_async_smem();
+            mbar_expect_tx(&rec_full[r], (uint32_t)rec);
+            bulk_copy_g2s(recs + r * rec, p.pool + (id * p.num_kv_heads + w.h) * (int64_t)rec, (uint32_t)rec,
+                          &rec_full[r]);
+            next_record();
+          }
+        }
+        // copies still in flight land before the CTA may leave
+        for (int k = g > slots ? g - slots : 0; k < g; ++k)
+          wait_one(&rec_full[k % slots], (uint32_t)((k / slots) & 1));
+      }
+      __syncwarp();
+    } else if (warp == kWalkWarp) {
+      // ---- the segments: the next one while the roles work on this one ----
+      for (int k = 0; segment(k, false); ++k) {
+        bar_any(kRoleBar, kRoleThreads, false);
+        if (lane == 0) {
+          TileWalk w = seg_s[k & 1];
+          w.next(p, part_s.fix);
+          seg_s[(k + 1) & 1] = w;
+        }
+        __syncwarp();
+      }
+    } else {
+      // ---- MMA issue, one lane a warp (an MMA holds its issuing warp for over 100 cycles whatever
+      // its N): QK of even and of odd pages and PV, each by column parts ----
+      const int role = warp - kQkWarp;            // 0..3: QK (part, page parity), 4..5: PV (part)
+      const bool is_pv = role >= 4;
+      const int part = is_pv ? role - 4 : role >> 1;
+      const int parity = role & 1;
+      bool bad = false;
+      uint64_t* last = nullptr;  // the barrier of this warp's last commit
+      uint32_t last_par = 0;
+      for (int k = 0; segment(k, bad); ++k) {
+        const int cnt = seg_s[k & 1].count();
+        bar_any(kRoleBar, kRoleThreads, false);
+        if (part < NP) {
           for (int i = 0; i < cnt; ++i) {
-            const int64_t gi = g + i;
+            const int gi = g + i;
             const int s = (int)(gi & 1);
             const uint32_t par = (uint32_t)((gi >> 1) & 1);
-            if (!is_pv && s != warp - kQkWarp) continue;
-            const bool ok = is_pv ? wait_one(&ops_v[s], par) && wait_one(&p_full[s], par)
-                                  : wait_one(&ops_k[s], par) && wait_one(&s_free[s], par ^ 1u);
-            if (!ok || *abort_v != 0) {
+            if (!is_pv && s != parity) continue;
+            const bool ok = is_pv ? wait_warp(&ops_v[s], par) && wait_warp(&p_full[2 * part + s], par)
+                                  : wait_warp(&ops_k[s], par) && wait_warp(&s_free[s], par ^ 1u);
+            if (!ok) {
               fail();
               bad = true;
               break;
             }
             fence_after();
+            last = is_pv ? &pv_done[2 * part + s] : &qk_full[2 * part + s];
+            last_par = par;
+            if (!elect_one()) continue;
             if (is_pv) {
-              const uint32_t pb = smem_u32(sm + S::kPOff + s * S::kPBytes);
+              const uint64_t pd = smem_desc(smem_u32(sm + S::kPOff + s * S::kPBytes) + part * NR * 8, NR * 16, 128);
               const uint32_t av = tmem + S::kColV + (S::kVStages == 2 ? (uint32_t)(s * 64 * S::kHalves) : 0u);
 #pragma unroll 1
               for (int hf = 0; hf < S::kHalves; ++hf)
-#pragma unroll 2
+#pragma unroll
                 for (int o = 0; o < 8; ++o)
-                  mma_ts(tmem + S::kColO + hf * NR, av + 64 * hf + 8 * o, smem_desc(pb + o * S::kStep, NR * 16, 128),
-                         kIdescPV<NR>, (uint32_t)(i > 0 || o > 0));
-              mma_commit(&pv_done[s]);
-              last = &pv_done[s];
+                  mma_ts(tmem + S::kColO + hf * NR + part * NM, av + 64 * hf + 8 * o, pd + o * (S::kStep >> 4),
+                         kIdescPV<NM>, (uint32_t)(i > 0 || o > 0));
             } else {
-              const uint32_t bb = smem_u32(sm + S::kBOff + s * 2 * S::kBHalf);
+                const uint64_t bd = smem_desc(smem_u32(sm + S::kBOff + s * 2 * S::kBHalf) + part * NR * 16, 128, 256);
               const uint32_t ak = tmem + S::kColK + (uint32_t)(s * (D / 2));
-#pragma unroll 2
-              for (int kk = 0; kk < 2 * S::kSteps; ++kk)  // hi, then lo
-                mma_ts(tmem + S::kColS + (uint32_t)(s * NR), ak + 8 * (kk % S::kSteps),
-                       smem_desc(bb + kk * S::kStep, 128, 256), kIdescQK<NR>, (uint32_t)(kk > 0));
-              mma_commit(&qk_full[s]);
-              last = &qk_full[s];
+#pragma unroll 1
+              for (int lo = 0; lo < 2; ++lo)
+#pragma unroll 8
+                for (int kk = 0; kk < S::kSteps; ++kk)
+                  mma_ts(tmem + S::kColS + (uint32_t)(s * NR + part * NM), ak + 8 * kk,
+                         bd + (lo * S::kSteps + kk) * (S::kStep >> 4), kIdescQK<NM>, (uint32_t)(lo + kk > 0));
             }
-            last_par = par;
+            mma_commit(last);
+            // QK: this thread has seen the K warps' writes (q~ . z') and passes them on to the softmax
+            if (!is_pv) mbar_arrive(last);
           }
         }
         g += cnt;
         __syncwarp();
       }
+      if (last != nullptr) wait_warp(last, last_par);  // this warp's MMAs have completed
+      __syncwarp();
     }
-    if (last != nullptr) wait_one(last, last_par);  // this lane's MMAs have completed
-    __syncwarp();
   }
 
   // ---- tear-down: every role is past its last wait ----
   fence_before();
   __syncthreads();
-  if (warp == 0) {
+  if (warp == 2) {
     fence_after();
     asm volatile("tcgen05.dealloc.cta_group::1.sync.aligned.b32 %0, 512;" ::"r"(tmem));
   }
@@ -1198,9 +1256,11 @@ __global__ void __launch_bounds__(128) block_merge_kernel(BlockParams p) {
   float v[E];
 #pragma unroll
   for (int e = 0; e < E; ++e) v[e] = 0.0f;
-  const bool cache = blk::tile_span(p, len, nl, t).count > 0;
-  if (cache) {
-    const int2 info = p.row_info[row];
+  // the row tile's slots; a CTA of the cache kernel whose waits ran out leaves its entries unwritten
+  int2 info = make_int2(0, 0);
+  if (blk::tile_span(p, len, nl, t).count > 0) info = p.row_info[row];
+  const int64_t all_slots = kBlockCtas + (int64_t)p.batch * p.num_kv_heads * p.tiles;
+  if (info.y > 0 && info.x >= 0 && (int64_t)info.x + info.y <= all_slots) {
     const int64_t step = (int64_t)p.tile_rows * (D + 4);
     const float* base = p.part + (int64_t)info.x * step + (int64_t)in_tile * (D + 4);
     for (int s = lane; s < info.y; s += 32) M = fmaxf(M, base[s * step]);

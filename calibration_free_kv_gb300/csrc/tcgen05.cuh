@@ -66,6 +66,19 @@ __device__ __forceinline__ void st_32x32b_x16(uint32_t taddr, const float* f) {
 }
 // N columns of this warp's lane quarter.  The waits name the loaded registers as operands, so that
 // nothing that reads them is moved ahead of the wait.
+__device__ __forceinline__ void ld_32x32b_x8_async(uint32_t taddr, float* f) {
+  asm volatile(
+      "tcgen05.ld.sync.aligned.32x32b.x8.b32 {%0, %1, %2, %3, %4, %5, %6, %7}, [%8];"
+      : "=f"(f[0]), "=f"(f[1]), "=f"(f[2]), "=f"(f[3]), "=f"(f[4]), "=f"(f[5]), "=f"(f[6]), "=f"(f[7])
+      : "r"(taddr)
+      : "memory");
+}
+__device__ __forceinline__ void wait_ld_x8(float* f) {
+  asm volatile("tcgen05.wait::ld.sync.aligned;"
+               : "+f"(f[0]), "+f"(f[1]), "+f"(f[2]), "+f"(f[3]), "+f"(f[4]), "+f"(f[5]), "+f"(f[6]), "+f"(f[7])
+               :
+               : "memory");
+}
 __device__ __forceinline__ void ld_32x32b_x16_async(uint32_t taddr, float* f) {
   asm volatile(
       "tcgen05.ld.sync.aligned.32x32b.x16.b32 {%0, %1, %2, %3, %4, %5, %6, %7, %8, %9, %10, %11, %12, %13, %14, %15}, [%16];"
@@ -88,15 +101,16 @@ __device__ __forceinline__ void wait_ld_x32(float* f) {
 }
 template <int N>
 __device__ __forceinline__ void ld_cols(uint32_t taddr, float (&f)[N]) {
-  static_assert(N == 16 || N == 32 || N == 64, "16, 32 or 64 columns");
-  if constexpr (N == 16) {
+  static_assert(N == 8 || N == 16 || N == 32, "8, 16 or 32 columns");
+  if constexpr (N == 8) {
+    ld_32x32b_x8_async(taddr, f);
+    wait_ld_x8(f);
+  } else if constexpr (N == 16) {
     ld_32x32b_x16_async(taddr, f);
     wait_ld_x16(f);
   } else {
-#pragma unroll
-    for (int i = 0; i < N; i += 32) ld_32x32b_x32_async(taddr + i, f + i);
-#pragma unroll
-    for (int i = 0; i < N; i += 32) wait_ld_x32(f + i);
+    ld_32x32b_x32_async(taddr, f);
+    wait_ld_x32(f);
   }
 }
 __device__ __forceinline__ void wait_st() { asm volatile("tcgen05.wait::st.sync.aligned;" ::: "memory"); }
