@@ -43,8 +43,10 @@ constexpr int kThreads = 1024;
 constexpr int kKWarp = 8, kVWarp = 16, kMiscWarp = 24;
 constexpr int kLoadWarp = 24, kQkWarp = 25, kWalkWarp = 31;
 constexpr int kMaxSlots = 8;
-// named barriers: all warps but the loader, the two softmax warpgroups (kSmBar, kSmBar + 1)
-constexpr int kRoleBar = 1, kSmBar = 2;
+// named barriers: all warps but the loader; the two warpgroups of the softmax, K and V roles.  One
+// warp of a group polls the mbarriers for it and a named barrier passes that on: waiting there
+// issues nothing, while polls by every warp took a third of the kernel's instructions.
+constexpr int kRoleBar = 1, kSmBar = 2, kKBar = 4, kVBar = 6;
 constexpr int kRoleThreads = kThreads - 32;
 // Units of the line ahead of a row tile's pages for a segment's fixed work, and the smallest range.
 constexpr int kFixUnits = 4, kMinUnits = 3;
@@ -433,7 +435,7 @@ __global__ void __launch_bounds__(blk::kThreads, 1) block_cache_kernel(BlockPara
     const int kpos = 4 * ((u >> 1) & 3) + 2 * ((u >> 3) & 1) + (u & 1);
     const int poff = (u >> 4) * S::kStep + (kpos >> 3) * (NR * 16) + (kpos & 7) * 16 + 16 * c0;
     const float cf = kTwo24 / lift0(p.kb) * (p.kb == 2 && ((u >> 4) & 1) ? 0.0625f : 1.0f);
-    bool bad = false, stop = false;
+    bool bad = false, late = false;  // the group gave up; this warp's wait for O ran out
     for (int k = 0; segment(k, bad); ++k) {
       const TileWalk w = seg_s[k & 1];
       stage_queries(w);
@@ -454,7 +456,15 @@ __global__ void __launch_bounds__(blk::kThreads, 1) block_cache_kernel(BlockPara
         const int s = (int)(g & 1);
         const uint32_t par = (uint32_t)((g >> 1) & 1);
         float x[NC];
-        if (!bad && wait_warp(&qk_full[2 * part + s], par)) {
+        // S of the page, and PV of the page before the last, which has read this stage's P
+        bool ok = true;
+        if (wq == 0) ok = wait_warp(&qk_full[2 * part + s], par) && wait_warp(&pv_done[2 * part + s], par ^ 1u);
+        if (bar_any(sbar, 128, !ok || late)) {
+          bad = true;
+          fail();
+          break;
+        }
+        {
           fence_after();
           ld_cols<NC>(tmem + S::kColS + (uint32_t)(s * NR + c0) + lanes, x);
           const float rt = __half2float(reinterpret_cast<const __half*>(recs + r * rec + RL.kfactor)[u]);
@@ -488,19 +498,12 @@ __global__ void __launch_bounds__(blk::kThreads, 1) block_cache_kernel(BlockPara
                 if (pos >= p.sink && pos < lim_s[c0 + n]) x[n] = -INFINITY;
             }
           }
-        } else {
-          if (!bad) fail();
-          bad = true;
-#pragma unroll
-          for (int n = 0; n < NC; ++n) x[n] = 0.0f;
         }
         next_record();
         float mx = -INFINITY;
 #pragma unroll
         for (int n = 0; n < NC; n += 2) mx = fmax3(mx, x[n], x[n + 1]);
-        if (bar_any(sbar, 128, bad || unset || mx > kSlack)) {
-          stop = bar_any(sbar, 128, bad);
-          if (stop) break;
+        if (bar_any(sbar, 128, unset || mx > kSlack)) {
           // move the references to the rows' maxima
 #pragma unroll
           for (int n = 0; n < NC; ++n) {
@@ -531,8 +534,7 @@ __global__ void __launch_bounds__(blk::kThreads, 1) block_cache_kernel(BlockPara
           }
           if (i > 0) {  // O of the pages before this one
             if (!wait_warp(&pv_done[2 * part + ((g - 1) & 1)], (uint32_t)(((g - 1) >> 1) & 1))) {
-              fail();
-              bad = true;
+              late = true;  // the group learns of it at its next wait
             } else {
               fence_after();
 #pragma unroll 1
@@ -551,11 +553,6 @@ __global__ void __launch_bounds__(blk::kThreads, 1) block_cache_kernel(BlockPara
             }
           }
         }
-        // P of the stage, once PV of the page before the last has read it
-        if (!bad && !wait_warp(&pv_done[2 * part + s], par ^ 1u)) {
-          fail();
-          bad = true;
-        }
         uint8_t* pb = sm + S::kPOff + s * S::kPBytes + poff;
 #pragma unroll
         for (int n = 0; n < NC; n += 8) {
@@ -571,9 +568,10 @@ __global__ void __launch_bounds__(blk::kThreads, 1) block_cache_kernel(BlockPara
         fence_proxy_async_smem();
         fence_before();
         __syncwarp();
-        if (lane == 0 && !bad) mbar_arrive(&p_full[2 * part + s]);
+        if (lane == 0 && !late) mbar_arrive(&p_full[2 * part + s]);
       }
-      if (bar_any(sbar, 128, bad || stop)) {
+      if (bar_any(sbar, 128, bad || late)) {
+        if (!bad) fail();
         bad = true;
         continue;  // segment() ends the loop for every warp
       }
@@ -636,10 +634,13 @@ __global__ void __launch_bounds__(blk::kThreads, 1) block_cache_kernel(BlockPara
         const int s = (int)(g & 1);
         const uint32_t par = (uint32_t)((g >> 1) & 1);
         // QK of the page before the last has read the codes and B
-        bool ok = wait_warp(&rec_full[r], rph);
+        bool ok = true;
+        if (q == 0) {
+          ok = wait_warp(&rec_full[r], rph);
 #pragma unroll
-        for (int m = 0; m < NP; ++m) ok = ok && wait_warp(&qk_full[2 * m + s], par ^ 1u);
-        if (!ok) {
+          for (int m = 0; m < NP; ++m) ok = ok && wait_warp(&qk_full[2 * m + s], par ^ 1u);
+        }
+        if (bar_any(codes ? kKBar : kKBar + 1, 128, !ok)) {
           bad = true;
           fail();
           break;
@@ -790,13 +791,16 @@ __global__ void __launch_bounds__(blk::kThreads, 1) block_cache_kernel(BlockPara
         const int vs = S::kVStages == 2 ? s : 0;
         // PV of the page that last used this buffer
         const int gp = g - S::kVStages;
-        bool ok = wait_warp(&rec_full[r], rph);
-        if (gp >= 0) {
+        bool ok = true;
+        if (q == 0) {
+          ok = wait_warp(&rec_full[r], rph);
+          if (gp >= 0) {
 #pragma unroll
-          for (int m = 0; m < NP; ++m)
-            ok = ok && wait_warp(&pv_done[2 * m + (gp & 1)], (uint32_t)((gp >> 1) & 1));
+            for (int m = 0; m < NP; ++m)
+              ok = ok && wait_warp(&pv_done[2 * m + (gp & 1)], (uint32_t)((gp >> 1) & 1));
+          }
         }
-        if (!ok) {
+        if (bar_any(kVBar + ii, 128, !ok)) {
           bad = true;
           fail();
           break;
