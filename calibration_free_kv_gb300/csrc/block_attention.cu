@@ -39,14 +39,18 @@ namespace blk {
 using namespace tc5;
 
 constexpr int kThreads = 1024;
-// warps: 0-7 softmax (4 per column half), 8-15 K, 16-23 V, 24 loader, 25-28 QK, 29-30 PV, 31 walk
+// warps: 0-7 softmax (4 per row half), 8-15 K, 16-23 V, 24 loader, 25-26 QK, 27-28 PV, 29 walk, 30-31 idle
 constexpr int kKWarp = 8, kVWarp = 16, kMiscWarp = 24;
-constexpr int kLoadWarp = 24, kQkWarp = 25, kWalkWarp = 31;
+constexpr int kLoadWarp = 24, kQkWarp = 25, kPvWarp = 27, kWalkWarp = 29;
 constexpr int kMaxSlots = 8;
-// named barriers: all warps but the loader; the two warpgroups of the softmax, K and V roles.  One
-// warp of a group polls the mbarriers for it and a named barrier passes that on: waiting there
-// issues nothing, while polls by every warp took a third of the kernel's instructions.
-constexpr int kRoleBar = 1, kSmBar = 2, kKBar = 4, kVBar = 6;
+// Named barriers.  Warps hand work to each other through them: a warp waiting at one issues nothing,
+// while polls of mbarriers by 13 warps (one every ~23 cycles each) kept the arrivals of the others
+// waiting and cost more than the work itself.  mbarriers remain where the hardware signals (bulk
+// copies, MMA completion), polled by one warp of a role, which then meets the others.
+//   0 the CTA; kRoleBar all warps but the loader; kSmBar + half the softmax warps of a row half;
+//   kKBar, kVBar the K and V warps; per stage kOpsK (K warps -> QK), kSFree (softmax -> QK),
+//   kOpsV (V warps -> PV); kPFull + 2 part + stage (softmax -> PV).
+constexpr int kRoleBar = 1, kSmBar = 2, kKBar = 4, kVBar = 5, kOpsK = 6, kSFree = 8, kOpsV = 10, kPFull = 12;
 constexpr int kRoleThreads = kThreads - 32;
 // Units of the line ahead of a row tile's pages for a segment's fixed work, and the smallest range.
 constexpr int kFixUnits = 4, kMinUnits = 3;
@@ -70,7 +74,7 @@ struct Shape {
   // floats: qz [4][NR], -reference, row maximum, shift, rescale, row limit [NR] each, per warp [4][NR]
   static constexpr int kSmallFloats = (4 + 5 + 4) * NR;
   static constexpr int kBarOff = kSmallOff + kSmallFloats * 4;
-  static constexpr int kNumBars = 2 * kMaxSlots + 3 * 2 + 3 * 4;
+  static constexpr int kNumBars = 2 * kMaxSlots + 2 * 4;
   static constexpr int kRecOff = (kBarOff + kNumBars * 8 + 127) & ~127;
   // tensor memory columns
   static constexpr uint32_t kColK = 0, kColV = 2 * (D / 2);
@@ -90,6 +94,12 @@ constexpr uint32_t kIdescPV = kIdescQK<NR> | (1u << 16);
 __device__ __forceinline__ float lift0(int kb) { return kb == 8 ? 256.0f : (kb == 4 ? 16.0f : 4.0f); }
 __device__ __forceinline__ float lift1(int kb) { return kb == 8 ? 256.0f : 1.0f; }
 
+__device__ __forceinline__ void bar_sync(int id, int threads) {
+  asm volatile("bar.sync %0, %1;" ::"r"(id), "r"(threads) : "memory");
+}
+__device__ __forceinline__ void bar_arrive(int id, int threads) {
+  asm volatile("bar.arrive %0, %1;" ::"r"(id), "r"(threads) : "memory");
+}
 // Barrier of `threads` threads; returns whether any of them passed `flag`.
 __device__ __forceinline__ bool bar_any(int id, int threads, bool flag) {
   uint32_t out;
@@ -102,11 +112,15 @@ __device__ __forceinline__ bool bar_any(int id, int threads, bool flag) {
   return out != 0;
 }
 
-// Bounded wait in a few instructions: the roles' code together has to stay in the SM's instruction
-// cache.  A poll suspends for up to about a microsecond, so the limit is some two seconds.
-__device__ __forceinline__ bool wait_one(uint64_t* bar, uint32_t parity) {
+// Bounded wait (about two seconds) on an mbarrier.  When one runs out, *abort_flag is set and the
+// role goes on all the same: every role runs through all its pages, so that no named barrier is left
+// waiting, and the call's results are flagged.  From then on a wait ends once the MMA warp it waits
+// for has issued page `need` - 1 (*issued >= need; null: at once), which keeps the roles within two
+// pages of each other as the completed MMAs would.
+__device__ __forceinline__ void wait_one(uint64_t* bar, uint32_t parity, volatile int* abort_flag,
+                                         const volatile int* issued, int need) {
   const uint32_t at = smem_u32(bar);
-  for (uint32_t n = 0; n < (1u << 21); ++n) {
+  for (uint32_t n = 0; n < (1u << 22); ++n) {
     uint32_t ok;
     asm volatile(
         "{\n\t.reg .pred p;\n\t"
@@ -115,9 +129,13 @@ __device__ __forceinline__ bool wait_one(uint64_t* bar, uint32_t parity) {
         : "=r"(ok)
         : "r"(at), "r"(parity), "r"(1000u)
         : "memory");
-    if (ok) return true;
+    if (ok) return;
+    if ((n & 63u) == 63u) {
+      if (n >= (1u << 21)) *abort_flag = 1;
+      if (*abort_flag != 0 && (issued == nullptr || *issued >= need)) return;
+    }
   }
-  return false;
+  *abort_flag = 1;
 }
 // One lane of a converged warp.  MMAs are issued under it: the compiler then knows that a single
 // thread runs them and keeps their operands in uniform registers.
@@ -126,10 +144,6 @@ __device__ __forceinline__ bool elect_one() {
   asm volatile("{\n\t.reg .pred p;\n\telect.sync _|p, 0xffffffff;\n\tselp.u32 %0, 1, 0, p;\n\t}" : "=r"(p));
   return p != 0;
 }
-__device__ __forceinline__ bool wait_warp(uint64_t* bar, uint32_t parity) {
-  return __all_sync(0xffffffffu, wait_one(bar, parity));
-}
-
 template <int N>
 struct IntC {
   static constexpr int value = N;
@@ -300,17 +314,16 @@ __global__ void __launch_bounds__(blk::kThreads, 1) block_cache_kernel(BlockPara
   __shared__ Partition part_s;
   __shared__ uint32_t tslot;
   __shared__ int abort_flag;
+  __shared__ int issued_s[4];  // pages whose QK (parts 0, 1) and PV (parts 0, 1) are issued
   const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
   const RecordLayout RL = record_layout(D, p.kb, p.vb);
   const int rec = RL.bytes;
   uint64_t* rec_full = reinterpret_cast<uint64_t*>(sm + S::kBarOff);
   uint64_t* rec_empty = rec_full + kMaxSlots;
-  uint64_t* ops_k = rec_empty + kMaxSlots;  // [stage]: K codes, B and q~ . z' written
-  uint64_t* s_free = ops_k + 2;             // [stage]: S and q~ . z' read
-  uint64_t* ops_v = s_free + 2;             // [stage]: V written
-  uint64_t* qk_full = ops_v + 2;            // [part][stage]: QK done (K codes and B are free)
-  uint64_t* p_full = qk_full + 4;           // [part][stage]: P written, O rescaled
-  uint64_t* pv_done = p_full + 4;           // [part][stage]: PV done: V and P are free, O is up to date
+  uint64_t* qk_full = rec_empty + kMaxSlots;  // [part][stage]: QK done (K codes and B are free)
+  uint64_t* pv_done = qk_full + 4;            // [part][stage]: PV done: V and P are free, O is up to date
+  constexpr int kOpsThreads = 256 + 32 * NP;           // kOpsK, kSFree, kOpsV
+  constexpr int kPThreads = 256 / NP + 32;             // kPFull
   float* qz_s = reinterpret_cast<float*>(sm + S::kSmallOff);  // [4][NR]: page g's at g % 4
   float* nref_s = qz_s + 4 * NR;   // minus the row's reference
   float* max_s = nref_s + NR;      // the row's maximum when the reference was set (-inf: none yet)
@@ -335,19 +348,14 @@ __global__ void __launch_bounds__(blk::kThreads, 1) block_cache_kernel(BlockPara
   if (threadIdx.x == 0) {
     for (int i = 0; i < kMaxSlots; ++i) {
       mbar_init(&rec_full[i], 1);
-      mbar_init(&rec_empty[i], 24);
-    }
-    for (int s = 0; s < 2; ++s) {
-      mbar_init(&ops_k[s], 8);
-      mbar_init(&s_free[s], 8);
-      mbar_init(&ops_v[s], 8);
+      mbar_init(&rec_empty[i], 4);  // the K and V roles and the two row halves of the softmax
     }
     for (int s = 0; s < 4; ++s) {
       mbar_init(&qk_full[s], 2);
-      mbar_init(&p_full[s], 8 / NP);
       mbar_init(&pv_done[s], 1);
     }
     abort_flag = 0;
+    for (int i = 0; i < 4; ++i) issued_s[i] = 0;
     fence_mbar_init();
   }
   if (warp == 2) {
@@ -360,14 +368,18 @@ __global__ void __launch_bounds__(blk::kThreads, 1) block_cache_kernel(BlockPara
   grid_launch_dependents();
   const uint32_t tmem = tslot;
   volatile int* abort_v = &abort_flag;
-  auto fail = [&]() {
-    *abort_v = 1;
-    flag_error(p.status, KVARN_DEV_WAIT_TIMEOUT);
+  volatile int* issued = issued_s;
+  auto wait = [&](uint64_t* bar, uint32_t parity) { wait_one(bar, parity, abort_v, nullptr, 0); };
+  // QK / PV of page j (j < 0: none) by the warp of column part m
+  auto wait_qk = [&](int m, int j) {
+    if (j >= 0) wait_one(&qk_full[2 * m + (j & 1)], (uint32_t)((j >> 1) & 1), abort_v, issued + m, j + 1);
   };
-  // Segment k of this CTA's range, or false at its end (or when the CTA gives up): the same for all
-  // warps but the loader's.
-  auto segment = [&](int k, bool bad) -> bool {
-    if (bar_any(kRoleBar, kRoleThreads, bad || *abort_v != 0)) return false;
+  auto wait_pv = [&](int m, int j) {
+    if (j >= 0) wait_one(&pv_done[2 * m + (j & 1)], (uint32_t)((j >> 1) & 1), abort_v, issued + 2 + m, j + 1);
+  };
+  // Segment k of this CTA's range, or false at its end: the same for all warps but the loader's.
+  auto segment = [&](int k) -> bool {
+    bar_sync(kRoleBar, kRoleThreads);
     return seg_s[k & 1].left > 0;
   };
   // q~ of a segment's rows, hi + lo, in the order and layout of the QK operand, by the 24 warps of
@@ -435,8 +447,7 @@ __global__ void __launch_bounds__(blk::kThreads, 1) block_cache_kernel(BlockPara
     const int kpos = 4 * ((u >> 1) & 3) + 2 * ((u >> 3) & 1) + (u & 1);
     const int poff = (u >> 4) * S::kStep + (kpos >> 3) * (NR * 16) + (kpos & 7) * 16 + 16 * c0;
     const float cf = kTwo24 / lift0(p.kb) * (p.kb == 2 && ((u >> 4) & 1) ? 0.0625f : 1.0f);
-    bool bad = false, late = false;  // the group gave up; this warp's wait for O ran out
-    for (int k = 0; segment(k, bad); ++k) {
+    for (int k = 0; segment(k); ++k) {
       const TileWalk w = seg_s[k & 1];
       stage_queries(w);
       const int cnt = w.count();
@@ -450,20 +461,18 @@ __global__ void __launch_bounds__(blk::kThreads, 1) block_cache_kernel(BlockPara
         nref_s[c0 + u] = 0.0f;
         max_s[c0 + u] = -INFINITY;
       }
-      bar_any(kRoleBar, kRoleThreads, false);
+      bar_sync(kRoleBar, kRoleThreads);
       bool unset = true;  // some row has no reference yet
       for (int i = 0; i < cnt; ++i, ++g) {
         const int s = (int)(g & 1);
-        const uint32_t par = (uint32_t)((g >> 1) & 1);
         float x[NC];
         // S of the page, and PV of the page before the last, which has read this stage's P
-        bool ok = true;
-        if (wq == 0) ok = wait_warp(&qk_full[2 * part + s], par) && wait_warp(&pv_done[2 * part + s], par ^ 1u);
-        if (bar_any(sbar, 128, !ok || late)) {
-          bad = true;
-          fail();
-          break;
+        if (wq == 0) {
+          wait_qk(part, g);
+          wait_pv(part, g - 2);
         }
+        bar_sync(sbar, 128);
+        if (g > 0 && u == 0) mbar_arrive(&rec_empty[r == 0 ? slots - 1 : r - 1]);  // all warps are past the last page
         {
           fence_after();
           ld_cols<NC>(tmem + S::kColS + (uint32_t)(s * NR + c0) + lanes, x);
@@ -484,11 +493,7 @@ __global__ void __launch_bounds__(blk::kThreads, 1) block_cache_kernel(BlockPara
             x[n + 3] = c.y;
           }
           fence_before();
-          __syncwarp();
-          if (lane == 0) {
-            mbar_arrive(&s_free[s]);
-            mbar_arrive(&rec_empty[r]);
-          }
+          bar_arrive(kSFree + s, kOpsThreads);
           if (p.window > 0) {
             const int at0 = w.span.page(w.j + i) * kTile;
             if (at0 + kTile > p.sink && at0 < sure) {  // an edge page of the window or of the first tokens
@@ -510,7 +515,7 @@ __global__ void __launch_bounds__(blk::kThreads, 1) block_cache_kernel(BlockPara
             const float v = warp_max(x[n]);
             if (lane == n) warp_s[wq * NR + c0 + n] = v;
           }
-          bar_any(sbar, 128, false);
+          bar_sync(sbar, 128);
           bool none = false;
           if (u < NC) {
             const int n = c0 + u;
@@ -533,24 +538,22 @@ __global__ void __launch_bounds__(blk::kThreads, 1) block_cache_kernel(BlockPara
             l[n / 2] = mul2(l[n / 2], make_float2(alpha_s[c0 + n], alpha_s[c0 + n + 1]));
           }
           if (i > 0) {  // O of the pages before this one
-            if (!wait_warp(&pv_done[2 * part + ((g - 1) & 1)], (uint32_t)(((g - 1) >> 1) & 1))) {
-              late = true;  // the group learns of it at its next wait
-            } else {
-              fence_after();
+            wait_pv(part, g - 1);
+            __syncwarp();
+            fence_after();
 #pragma unroll 1
-              for (int hf = 0; hf < S::kHalves; ++hf)
+            for (int hf = 0; hf < S::kHalves; ++hf)
 #pragma unroll 1
-                for (int n0 = 0; n0 < NC; n0 += 8) {
-                  float o[8];
-                  const uint32_t ta = tmem + S::kColO + (uint32_t)(hf * NR + c0 + n0) + lanes;
-                  ld_cols<8>(ta, o);
-                  uint32_t ob[8];
+              for (int n0 = 0; n0 < NC; n0 += 8) {
+                float o[8];
+                const uint32_t ta = tmem + S::kColO + (uint32_t)(hf * NR + c0 + n0) + lanes;
+                ld_cols<8>(ta, o);
+                uint32_t ob[8];
 #pragma unroll
-                  for (int n = 0; n < 8; ++n) ob[n] = __float_as_uint(o[n] * alpha_s[c0 + n0 + n]);
-                  st_32x32b_x8(ta, ob);
-                }
-              wait_st();
-            }
+                for (int n = 0; n < 8; ++n) ob[n] = __float_as_uint(o[n] * alpha_s[c0 + n0 + n]);
+                st_32x32b_x8(ta, ob);
+              }
+            wait_st();
           }
         }
         uint8_t* pb = sm + S::kPOff + s * S::kPBytes + poff;
@@ -567,13 +570,7 @@ __global__ void __launch_bounds__(blk::kThreads, 1) block_cache_kernel(BlockPara
         }
         fence_proxy_async_smem();
         fence_before();
-        __syncwarp();
-        if (lane == 0 && !late) mbar_arrive(&p_full[2 * part + s]);
-      }
-      if (bar_any(sbar, 128, bad || late)) {
-        if (!bad) fail();
-        bad = true;
-        continue;  // segment() ends the loop for every warp
+        bar_arrive(kPFull + 2 * part + s, kPThreads);
       }
       // the segment's partial: l over the tokens, O once its last PV is done
 #pragma unroll
@@ -583,7 +580,7 @@ __global__ void __launch_bounds__(blk::kThreads, 1) block_cache_kernel(BlockPara
         for (int m = 16; m > 0; m >>= 1) v += __shfl_xor_sync(0xffffffffu, v, m);
         if (lane == n) warp_s[wq * NR + c0 + n] = v;
       }
-      bar_any(sbar, 128, false);
+      bar_sync(sbar, 128);
       const int live = min(NR, w.nl * p.group - w.t * NR) - c0;  // rows of this half that exist
       float* dst = p.part + (((int64_t)blockIdx.x + row) * NR + c0) * (D + 4);
       if (u < min(live, NC)) {
@@ -596,26 +593,23 @@ __global__ void __launch_bounds__(blk::kThreads, 1) block_cache_kernel(BlockPara
         const int64_t last = owner_cta(part_s, w.row0 + part_s.fix + w.span.count - 1);
         p.row_info[row] = make_int2((int)((int64_t)blockIdx.x + row), (int)(last - blockIdx.x + 1));
       }
-      if (!wait_warp(&pv_done[2 * part + ((g - 1) & 1)], (uint32_t)(((g - 1) >> 1) & 1))) {
-        fail();
-        bad = true;
-      } else {
-        fence_after();
+      wait_pv(part, g - 1);
+      __syncwarp();
+      fence_after();
 #pragma unroll 1
-        for (int hf = 0; hf < S::kHalves; ++hf) {
+      for (int hf = 0; hf < S::kHalves; ++hf) {
 #pragma unroll 1
-          for (int n0 = 0; n0 < min(NC, live); n0 += 8) {
-            float o[8];
-            ld_cols<8>(tmem + S::kColO + (uint32_t)(hf * NR + c0 + n0) + lanes, o);
-            if (D >= 128 || u < D) {
+        for (int n0 = 0; n0 < min(NC, live); n0 += 8) {
+          float o[8];
+          ld_cols<8>(tmem + S::kColO + (uint32_t)(hf * NR + c0 + n0) + lanes, o);
+          if (D >= 128 || u < D) {
 #pragma unroll
-              for (int n = 0; n < 8; ++n)
-                if (n0 + n < live) dst[(int64_t)(n0 + n) * (D + 4) + 4 + hf * 128 + u] = o[n];
-            }
+            for (int n = 0; n < 8; ++n)
+              if (n0 + n < live) dst[(int64_t)(n0 + n) * (D + 4) + 4 + hf * 128 + u] = o[n];
           }
         }
-        fence_before();
       }
+      fence_before();
     }
   } else if (warp < kVWarp) {
     asm volatile("setmaxnreg.dec.sync.aligned.u32 56;");
@@ -625,26 +619,20 @@ __global__ void __launch_bounds__(blk::kThreads, 1) block_cache_kernel(BlockPara
     const int grp = t >> 3, nl = t & 7;
     const int gq = lane >> 2, tq = lane & 3;
     const float i0 = 1.0f / lift0(p.kb), i1 = 1.0f / lift1(p.kb);
-    bool bad = false;
-    for (int k = 0; segment(k, bad); ++k) {
+    for (int k = 0; segment(k); ++k) {
       stage_queries(seg_s[k & 1]);
       const int cnt = seg_s[k & 1].count();
-      bar_any(kRoleBar, kRoleThreads, false);
+      bar_sync(kRoleBar, kRoleThreads);
       for (int i = 0; i < cnt; ++i, ++g) {
         const int s = (int)(g & 1);
-        const uint32_t par = (uint32_t)((g >> 1) & 1);
         // QK of the page before the last has read the codes and B
-        bool ok = true;
-        if (q == 0) {
-          ok = wait_warp(&rec_full[r], rph);
+        if (warp == kKWarp) {
+          wait(&rec_full[r], rph);
 #pragma unroll
-          for (int m = 0; m < NP; ++m) ok = ok && wait_warp(&qk_full[2 * m + s], par ^ 1u);
+          for (int m = 0; m < NP; ++m) wait_qk(m, g - 2);
         }
-        if (bar_any(codes ? kKBar : kKBar + 1, 128, !ok)) {
-          bad = true;
-          fail();
-          break;
-        }
+        bar_sync(kKBar, 256);
+        if (g > 0 && t == 0 && codes) mbar_arrive(&rec_empty[r == 0 ? slots - 1 : r - 1]);
         fence_after();
         const uint8_t* R = recs + r * rec;
         if (codes) {
@@ -767,11 +755,7 @@ __global__ void __launch_bounds__(blk::kThreads, 1) block_cache_kernel(BlockPara
         if (codes) wait_st();
         fence_proxy_async_smem();
         fence_before();
-        __syncwarp();
-        if (lane == 0) {
-          mbar_arrive(&ops_k[s]);
-          mbar_arrive(&rec_empty[r]);
-        }
+        bar_arrive(kOpsK + s, kOpsThreads);
         next_record();
       }
     }
@@ -781,30 +765,21 @@ __global__ void __launch_bounds__(blk::kThreads, 1) block_cache_kernel(BlockPara
     // block of each 128 ----
     const int q = warp & 3, ii = (warp - kVWarp) >> 2;
     const int gq = lane >> 2, tq = lane & 3;
-    bool bad = false;
-    for (int k = 0; segment(k, bad); ++k) {
+    for (int k = 0; segment(k); ++k) {
       stage_queries(seg_s[k & 1]);
       const int cnt = seg_s[k & 1].count();
-      bar_any(kRoleBar, kRoleThreads, false);
+      bar_sync(kRoleBar, kRoleThreads);
       for (int i = 0; i < cnt; ++i, ++g) {
         const int s = (int)(g & 1);
         const int vs = S::kVStages == 2 ? s : 0;
         // PV of the page that last used this buffer
-        const int gp = g - S::kVStages;
-        bool ok = true;
-        if (q == 0) {
-          ok = wait_warp(&rec_full[r], rph);
-          if (gp >= 0) {
+        if (warp == kVWarp) {
+          wait(&rec_full[r], rph);
 #pragma unroll
-            for (int m = 0; m < NP; ++m)
-              ok = ok && wait_warp(&pv_done[2 * m + (gp & 1)], (uint32_t)((gp >> 1) & 1));
-          }
+          for (int m = 0; m < NP; ++m) wait_pv(m, g - S::kVStages);
         }
-        if (bar_any(kVBar + ii, 128, !ok)) {
-          bad = true;
-          fail();
-          break;
-        }
+        bar_sync(kVBar, 256);
+        if (g > 0 && warp == kVWarp && lane == 0) mbar_arrive(&rec_empty[r == 0 ? slots - 1 : r - 1]);
         fence_after();
         const uint8_t* R = recs + r * rec;
         const __half2* vsc = reinterpret_cast<const __half2*>(R + RL.vscale);
@@ -851,11 +826,7 @@ __global__ void __launch_bounds__(blk::kThreads, 1) block_cache_kernel(BlockPara
         }
         wait_st();
         fence_before();
-        __syncwarp();
-        if (lane == 0) {
-          mbar_arrive(&ops_v[s]);
-          mbar_arrive(&rec_empty[r]);
-        }
+        bar_arrive(kOpsV + s, kOpsThreads);
         next_record();
       }
     }
@@ -864,8 +835,7 @@ __global__ void __launch_bounds__(blk::kThreads, 1) block_cache_kernel(BlockPara
     if (warp == kLoadWarp) {
       // ---- page records -> the ring ----
       if (lane == 0) {
-        bool bad = false;
-        for (TileWalk w = seg_s[0]; w.left > 0 && !bad; w.next(p, part_s.fix)) {
+        for (TileWalk w = seg_s[0]; w.left > 0; w.next(p, part_s.fix)) {
           const int cnt = w.count();
           const int32_t* bt = p.block_table + (int64_t)w.b * p.max_pages;
           for (int i = 0; i < cnt; ++i, ++g) {
@@ -874,11 +844,8 @@ __global__ void __launch_bounds__(blk::kThreads, 1) block_cache_kernel(BlockPara
               flag_error(p.status, KVARN_DEV_BAD_PAGE_ID);
               id = 0;
             }
-            if (!wait_one(&rec_empty[r], rph ^ 1u)) {
-              fail();
-              bad = true;
-              break;
-            }
+            wait(&rec_empty[r], rph ^ 1u);
+            if (*abort_v != 0) continue;  // nobody waits for the copies any more
             fence_proxy_async_smem();
             mbar_expect_tx(&rec_full[r], (uint32_t)rec);
             bulk_copy_g2s(recs + r * rec, p.pool + (id * p.num_kv_heads + w.h) * (int64_t)rec, (uint32_t)rec,
@@ -888,13 +855,13 @@ __global__ void __launch_bounds__(blk::kThreads, 1) block_cache_kernel(BlockPara
         }
         // copies still in flight land before the CTA may leave
         for (int k = g > slots ? g - slots : 0; k < g; ++k)
-          wait_one(&rec_full[k % slots], (uint32_t)((k / slots) & 1));
+          wait(&rec_full[k % slots], (uint32_t)((k / slots) & 1));
       }
       __syncwarp();
     } else if (warp == kWalkWarp) {
       // ---- the segments: the next one while the roles work on this one ----
-      for (int k = 0; segment(k, false); ++k) {
-        bar_any(kRoleBar, kRoleThreads, false);
+      for (int k = 0; segment(k); ++k) {
+        bar_sync(kRoleBar, kRoleThreads);
         if (lane == 0) {
           TileWalk w = seg_s[k & 1];
           w.next(p, part_s.fix);
@@ -902,71 +869,69 @@ __global__ void __launch_bounds__(blk::kThreads, 1) block_cache_kernel(BlockPara
         }
         __syncwarp();
       }
-    } else {
-      // ---- MMA issue, one lane a warp (an MMA holds its issuing warp for over 100 cycles whatever
-      // its N): QK of even and of odd pages and PV, each by column parts ----
-      const int role = warp - kQkWarp;            // 0..3: QK (part, page parity), 4..5: PV (part)
-      const bool is_pv = role >= 4;
-      const int part = is_pv ? role - 4 : role >> 1;
-      const int parity = role & 1;
-      bool bad = false;
-      uint64_t* last = nullptr;  // the barrier of this warp's last commit
-      uint32_t last_par = 0;
-      for (int k = 0; segment(k, bad); ++k) {
+    } else if (warp < kWalkWarp) {
+      // ---- MMA issue: QK and PV, a warp for each row half ----
+      const bool is_pv = warp >= kPvWarp;
+      const int part = is_pv ? warp - kPvWarp : warp - kQkWarp;
+      for (int k = 0; segment(k); ++k) {
         const int cnt = seg_s[k & 1].count();
-        bar_any(kRoleBar, kRoleThreads, false);
-        if (part < NP) {
-          for (int i = 0; i < cnt; ++i) {
-            const int gi = g + i;
-            const int s = (int)(gi & 1);
-            const uint32_t par = (uint32_t)((gi >> 1) & 1);
-            if (!is_pv && s != parity) continue;
-            const bool ok = is_pv ? wait_warp(&ops_v[s], par) && wait_warp(&p_full[2 * part + s], par)
-                                  : wait_warp(&ops_k[s], par) && wait_warp(&s_free[s], par ^ 1u);
-            if (!ok) {
-              fail();
-              bad = true;
-              break;
-            }
-            fence_after();
-            last = is_pv ? &pv_done[2 * part + s] : &qk_full[2 * part + s];
-            last_par = par;
-            if (!elect_one()) continue;
-            if (is_pv) {
-              const uint64_t pd = smem_desc(smem_u32(sm + S::kPOff + s * S::kPBytes) + part * NR * 8, NR * 16, 128);
-              const uint32_t av = tmem + S::kColV + (S::kVStages == 2 ? (uint32_t)(s * 64 * S::kHalves) : 0u);
+        bar_sync(kRoleBar, kRoleThreads);
+        if (part >= NP) continue;
+        for (int i = 0; i < cnt; ++i, ++g) {
+          const int s = g & 1;
+          if (is_pv) {
+            bar_sync(kOpsV + s, kOpsThreads);
+            bar_sync(kPFull + 2 * part + s, kPThreads);
+          } else {
+            bar_sync(kOpsK + s, kOpsThreads);
+            if (g >= 2) bar_sync(kSFree + s, kOpsThreads);  // S of the page before the last is read
+          }
+          fence_after();
+          if (!elect_one()) continue;
+          if (is_pv) {
+            const uint64_t pd = smem_desc(smem_u32(sm + S::kPOff + s * S::kPBytes) + part * NR * 8, NR * 16, 128);
+            const uint32_t av = tmem + S::kColV + (S::kVStages == 2 ? (uint32_t)(s * 64 * S::kHalves) : 0u);
 #pragma unroll 1
-              for (int hf = 0; hf < S::kHalves; ++hf)
+            for (int hf = 0; hf < S::kHalves; ++hf)
 #pragma unroll
-                for (int o = 0; o < 8; ++o)
-                  mma_ts(tmem + S::kColO + hf * NR + part * NM, av + 64 * hf + 8 * o, pd + o * (S::kStep >> 4),
-                         kIdescPV<NM>, (uint32_t)(i > 0 || o > 0));
-            } else {
-                const uint64_t bd = smem_desc(smem_u32(sm + S::kBOff + s * 2 * S::kBHalf) + part * NR * 16, 128, 256);
-              const uint32_t ak = tmem + S::kColK + (uint32_t)(s * (D / 2));
+              for (int o = 0; o < 8; ++o)
+                mma_ts(tmem + S::kColO + hf * NR + part * NM, av + 64 * hf + 8 * o, pd + o * (S::kStep >> 4),
+                       kIdescPV<NM>, (uint32_t)(i > 0 || o > 0));
+            mma_commit(&pv_done[2 * part + s]);
+            issued[2 + part] = g + 1;
+          } else {
+            const uint64_t bd = smem_desc(smem_u32(sm + S::kBOff + s * 2 * S::kBHalf) + part * NR * 16, 128, 256);
+            const uint32_t ak = tmem + S::kColK + (uint32_t)(s * (D / 2));
 #pragma unroll 1
-              for (int lo = 0; lo < 2; ++lo)
+            for (int lo = 0; lo < 2; ++lo)
 #pragma unroll 8
-                for (int kk = 0; kk < S::kSteps; ++kk)
-                  mma_ts(tmem + S::kColS + (uint32_t)(s * NR + part * NM), ak + 8 * kk,
-                         bd + (lo * S::kSteps + kk) * (S::kStep >> 4), kIdescQK<NM>, (uint32_t)(lo + kk > 0));
-            }
-            mma_commit(last);
-            // QK: this thread has seen the K warps' writes (q~ . z') and passes them on to the softmax
-            if (!is_pv) mbar_arrive(last);
+              for (int kk = 0; kk < S::kSteps; ++kk)
+                mma_ts(tmem + S::kColS + (uint32_t)(s * NR + part * NM), ak + 8 * kk,
+                       bd + (lo * S::kSteps + kk) * (S::kStep >> 4), kIdescQK<NM>, (uint32_t)(lo + kk > 0));
+            mma_commit(&qk_full[2 * part + s]);
+            // this thread has seen the K warps' writes (q~ . z') and passes them on to the softmax
+            mbar_arrive(&qk_full[2 * part + s]);
+            issued[part] = g + 1;
           }
         }
-        g += cnt;
-        __syncwarp();
       }
-      if (last != nullptr) wait_warp(last, last_par);  // this warp's MMAs have completed
+      if (g > 0 && part < NP) {
+        // the last MMAs have completed; the arrivals for pages that do not follow are taken
+        if (is_pv) wait_pv(part, g - 1);
+        else wait_qk(part, g - 1);
+        if (!is_pv)
+          for (int i = g > 1 ? g - 2 : 0; i < g; ++i) bar_sync(kSFree + (i & 1), kOpsThreads);
+      }
       __syncwarp();
+    } else {
+      for (int k = 0; segment(k); ++k) bar_sync(kRoleBar, kRoleThreads);
     }
   }
 
   // ---- tear-down: every role is past its last wait ----
   fence_before();
   __syncthreads();
+  if (threadIdx.x == 0 && abort_flag != 0) flag_error(p.status, KVARN_DEV_WAIT_TIMEOUT);
   if (warp == 2) {
     fence_after();
     asm volatile("tcgen05.dealloc.cta_group::1.sync.aligned.b32 %0, 512;" ::"r"(tmem));
