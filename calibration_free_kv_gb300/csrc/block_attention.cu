@@ -112,26 +112,17 @@ __device__ __forceinline__ bool bar_any(int id, int threads, bool flag) {
   return out != 0;
 }
 
-// Bounded wait (about two seconds) on an mbarrier.  When one runs out, *abort_flag is set and the
+// Bounded wait (2^25 polls, about a second) on an mbarrier.  When one runs out, *abort_flag is set and the
 // role goes on all the same: every role runs through all its pages, so that no named barrier is left
 // waiting, and the call's results are flagged.  From then on a wait ends once the MMA warp it waits
 // for has issued page `need` - 1 (*issued >= need; null: at once), which keeps the roles within two
 // pages of each other as the completed MMAs would.
 __device__ __forceinline__ void wait_one(uint64_t* bar, uint32_t parity, volatile int* abort_flag,
                                          const volatile int* issued, int need) {
-  const uint32_t at = smem_u32(bar);
-  for (uint32_t n = 0; n < (1u << 22); ++n) {
-    uint32_t ok;
-    asm volatile(
-        "{\n\t.reg .pred p;\n\t"
-        "mbarrier.try_wait.parity.shared::cta.b64 p, [%1], %2, %3;\n\t"
-        "selp.u32 %0, 1, 0, p;\n\t}"
-        : "=r"(ok)
-        : "r"(at), "r"(parity), "r"(1000u)
-        : "memory");
-    if (ok) return;
-    if ((n & 63u) == 63u) {
-      if (n >= (1u << 21)) *abort_flag = 1;
+  for (uint32_t n = 0; n < (1u << 26); ++n) {
+    if (mbar_try_wait(bar, parity)) return;
+    if ((n & 255u) == 255u) {
+      if (n >= (1u << 25)) *abort_flag = 1;
       if (*abort_flag != 0 && (issued == nullptr || *issued >= need)) return;
     }
   }
@@ -144,6 +135,12 @@ __device__ __forceinline__ bool elect_one() {
   asm volatile("{\n\t.reg .pred p;\n\telect.sync _|p, 0xffffffff;\n\tselp.u32 %0, 1, 0, p;\n\t}" : "=r"(p));
   return p != 0;
 }
+__device__ __forceinline__ uint32_t and_or(uint32_t a, uint32_t b, uint32_t c) {  // (a & b) | c
+  uint32_t d;
+  asm("lop3.b32 %0, %1, %2, %3, 0xEA;" : "=r"(d) : "r"(a), "r"(b), "r"(c));
+  return d;
+}
+
 template <int N>
 struct IntC {
   static constexpr int value = N;
@@ -705,7 +702,7 @@ __global__ void __launch_bounds__(blk::kThreads, 1) block_cache_kernel(BlockPara
           const uint32_t qa = smem_u32(q_hi) + (2 * q + (m & 1)) * 256 + (m >> 1) * 128 + (lane & 7) * 16;
           const bool mine = gq < 2 && (tq & 1) == gq;
           const uint8_t* zc = R + RL.kzero + 2 * (8 * (tq & 1) + 2 * (tq >> 1));
-#pragma unroll 4
+#pragma unroll 8
           for (int kk = 0; kk < S::kSteps; ++kk) {
             const uint32_t b0 = mine ? *reinterpret_cast<const uint32_t*>(zc + 32 * kk) : 0u;
             const uint32_t b1 = mine ? *reinterpret_cast<const uint32_t*>(zc + 32 * kk + 8) : 0u;
@@ -732,7 +729,7 @@ __global__ void __launch_bounds__(blk::kThreads, 1) block_cache_kernel(BlockPara
           const uint2 sb = *reinterpret_cast<const uint2*>(R + RL.kscale + 2 * (cb + 8));
           const __half2 sv[4] = {u2h2(sa.x), u2h2(sb.x), u2h2(sa.y), u2h2(sb.y)};
           const int rg0 = codes ? 0 : NR / 16;
-#pragma unroll 2
+#pragma unroll
           for (int rg = 0; rg < NR / 16; ++rg) {
             if (D == 64 && NR > 16 && (rg & 1) != (grp >> 3)) continue;
             if (D == 64 && NR == 16 && grp >= 8) continue;
@@ -764,7 +761,7 @@ __global__ void __launch_bounds__(blk::kThreads, 1) block_cache_kernel(BlockPara
     // ---- V~ -> tensor memory: channels on the lanes, tokens along K; a warp takes one 16-channel
     // block of each 128 ----
     const int q = warp & 3, ii = (warp - kVWarp) >> 2;
-    const int gq = lane >> 2, tq = lane & 3;
+    const int gq = lane >> 2;
     for (int k = 0; segment(k); ++k) {
       stage_queries(seg_s[k & 1]);
       const int cnt = seg_s[k & 1].count();
@@ -782,8 +779,7 @@ __global__ void __launch_bounds__(blk::kThreads, 1) block_cache_kernel(BlockPara
         if (g > 0 && warp == kVWarp && lane == 0) mbar_arrive(&rec_empty[r == 0 ? slots - 1 : r - 1]);
         fence_after();
         const uint8_t* R = recs + r * rec;
-        const __half2* vsc = reinterpret_cast<const __half2*>(R + RL.vscale);
-        const __half2* vzr = reinterpret_cast<const __half2*>(R + RL.vzero);
+        const uint32_t sz = smem_u32(R + RL.vscale) + 16 * (lane >> 3);  // group lane / 8 of a pair's four
         const __half* vch = reinterpret_cast<const __half*>(R + RL.vfactor);
         const uint32_t* vc = reinterpret_cast<const uint32_t*>(R + RL.vcodes);
         const uint32_t ta =
@@ -796,24 +792,35 @@ __global__ void __launch_bounds__(blk::kThreads, 1) block_cache_kernel(BlockPara
             const uint32_t* vw = vc + ((cb >> 2) * 32 + lane) * 4 + (cb & 3);
             auto tile = [&](auto vbc) {
               constexpr int VB = decltype(vbc)::value;
-#pragma unroll 2
+              constexpr int kMasks = VB == 2 ? 4 : 2;  // bit offsets of a code: 2-bit 0, 2, 4, 6, 4-bit 0, 4
+              uint32_t mask[kMasks];
+#pragma unroll
+              for (int e = 0; e < kMasks; ++e) {
+                mask[e] = VB == 2 ? 0x00030003u << (2 * e) : 0x000F000Fu << (4 * e);
+                asm("" : "+r"(mask[e]));  // kept in registers: a LOP3 takes one immediate
+              }
+#pragma unroll
               for (int o2 = 0; o2 < 4; ++o2) {
+                // token scales and zeros of the pair's four 8-token groups: rows of one ldmatrix all
+                // at the same 16 bytes leave lane (g, tq) tokens 2tq, 2tq + 1 of each group
+                uint32_t s2[4], z2[4];
+                ldsm_x4(sz + 64 * o2, s2);
+                ldsm_x4(sz + 2 * kTile + 64 * o2, z2);
                 uint32_t rr[8];
 #pragma unroll
                 for (int f = 0; f < 2; ++f) {
                   const uint32_t x = vw[(VB == 2 ? o2 : 2 * o2 + f) * (D / 64) * 128];
+                  const uint32_t y = x >> 8;
 #pragma unroll
                   for (int h = 0; h < 2; ++h) {
-                    const __half2 s2 = vsc[8 * (2 * o2 + f) + 4 * h + tq], z2 = vzr[8 * (2 * o2 + f) + 4 * h + tq];
                     // the code's bits under an exponent that makes them base + code, minus base
-                    constexpr uint32_t one = VB == 2 ? 0x00030003u : 0x000F000Fu;
-                    const int sh = VB == 2 ? 4 * f + 2 * h : 4 * h;
-                    const uint32_t base = 0x64006400u - (uint32_t)sh * 0x04000400u;
+                    const int e = VB == 2 ? 2 * f + h : h;
+                    const uint32_t base = 0x64006400u - (uint32_t)(VB == 2 ? 2 * e : 4 * e) * 0x04000400u;
 #pragma unroll
                     for (int rho = 0; rho < 2; ++rho) {
-                      const uint32_t y = rho ? x >> 8 : x;
-                      const __half2 c = __hsub2(u2h2((y & (one << sh)) | base), u2h2(base));
-                      rr[4 * f + 2 * rho + h] = h2u(__hmul2(__hfma2(c, s2, z2), cv[rho]));
+                      const __half2 c = __hsub2(u2h2(and_or(rho ? y : x, mask[e], base)), u2h2(base));
+                      rr[4 * f + 2 * rho + h] =
+                          h2u(__hmul2(__hfma2(c, u2h2(s2[2 * f + h]), u2h2(z2[2 * f + h])), cv[rho]));
                     }
                   }
                 }
