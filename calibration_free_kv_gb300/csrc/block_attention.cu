@@ -65,7 +65,10 @@ struct Shape {
   static constexpr int kVStages = D > 128 ? 1 : 2;
   static constexpr int kStep = NR * 32;           // bytes of one K step of a B operand
   static constexpr int kBHalf = NR * D * 2;       // q~ s' hi (or lo) of one page
-  static constexpr int kPBytes = NR * kTile * 2;
+  // P, MN-major: per 16 tokens two groups of 8 rows (tokens) of 16 bytes per 8 columns; the second
+  // group is 32 bytes off so that the 8 lanes of a store phase, two groups of four, miss each other
+  static constexpr int kPGroup = NR * 16 + 32, kPStep = 2 * kPGroup;
+  static constexpr int kPBytes = 8 * kPStep;
   // shared memory: B (two stages, hi + lo), P (two stages), q~ hi + lo, small state, records
   static constexpr int kBOff = 0;
   static constexpr int kPOff = 2 * 2 * kBHalf;
@@ -431,7 +434,7 @@ __global__ void __launch_bounds__(blk::kThreads, 1) block_cache_kernel(BlockPara
   };
 
   // Registers of the 65,536 the CTA is launched with: 104 a thread for the softmax, which holds a
-  // token's NR / 2 logits and as many sums, 56 for K and V, 40 for the rest.
+  // token's NR / 2 logits and as many sums, 72 for K, which holds its share of q~, 48 for V, 32 for the rest.
   if (warp < kKWarp) {
     asm volatile("setmaxnreg.inc.sync.aligned.u32 104;");
     // ---- softmax (thread = token, rows c0 ..), rescale and the segment's partial (thread = channel) ----
@@ -442,7 +445,7 @@ __global__ void __launch_bounds__(blk::kThreads, 1) block_cache_kernel(BlockPara
     const int sbar = kSmBar + half;
     const uint32_t lanes = (uint32_t)(32 * wq) << 16;
     const int kpos = 4 * ((u >> 1) & 3) + 2 * ((u >> 3) & 1) + (u & 1);
-    const int poff = (u >> 4) * S::kStep + (kpos >> 3) * (NR * 16) + (kpos & 7) * 16 + 16 * c0;
+    const int poff = (u >> 4) * S::kPStep + (kpos >> 3) * S::kPGroup + (kpos & 7) * 16 + 16 * c0;
     const float cf = kTwo24 / lift0(p.kb) * (p.kb == 2 && ((u >> 4) & 1) ? 0.0625f : 1.0f);
     for (int k = 0; segment(k); ++k) {
       const TileWalk w = seg_s[k & 1];
@@ -609,17 +612,37 @@ __global__ void __launch_bounds__(blk::kThreads, 1) block_cache_kernel(BlockPara
       fence_before();
     }
   } else if (warp < kVWarp) {
-    asm volatile("setmaxnreg.dec.sync.aligned.u32 56;");
+    asm volatile("setmaxnreg.inc.sync.aligned.u32 72;");
     // ---- warps 8-11: K codes -> tensor memory; 12-15: q~ . z'; each half of the rows of B = q~ s' ----
     const int t = threadIdx.x & 127, q = warp & 3;
     const bool codes = warp < kKWarp + 4;
     const int grp = t >> 3, nl = t & 7;
     const int gq = lane >> 2, tq = lane & 3;
     const float i0 = 1.0f / lift0(p.kb), i1 = 1.0f / lift1(p.kb);
+    // B rows n = 8 rg + nl over K indexes 8kb..8kb+7 of step kk (channels cb + {0, 1, 8, 9, 2, 3, 10,
+    // 11}): the 16 thread groups of 8 take the D / 8 (kk, kb) pairs and, each warpgroup, half the rows.
+    // A thread's q~ stay in registers for the segment.
+    constexpr int kPairs = D > 128 ? 2 : 1;
+    constexpr int kRows = D == 64 ? (NR > 16 ? NR / 32 : 1) : NR / 16;
+    const bool builds = !(D == 64 && NR == 16 && grp >= 8);
+    auto pair_of = [&](int c2) { return D == 64 ? (grp & 7) : grp + 16 * c2; };
+    auto b_at = [&](int c2, int e) {
+      const int oc = pair_of(c2);
+      const int rg = (codes ? 0 : NR / 16) + (D == 64 && NR > 16 ? 2 * e + (grp >> 3) : e);
+      return (oc >> 1) * S::kStep + rg * 256 + (oc & 1) * 128 + nl * 16;
+    };
     for (int k = 0; segment(k); ++k) {
       stage_queries(seg_s[k & 1]);
       const int cnt = seg_s[k & 1].count();
       bar_sync(kRoleBar, kRoleThreads);
+      uint4 qh[kPairs][kRows], ql[kPairs][kRows];
+#pragma unroll
+      for (int c2 = 0; c2 < kPairs; ++c2)
+#pragma unroll
+        for (int e = 0; e < kRows; ++e) {
+          qh[c2][e] = *reinterpret_cast<const uint4*>(q_hi + b_at(c2, e));
+          ql[c2][e] = *reinterpret_cast<const uint4*>(q_lo + b_at(c2, e));
+        }
       for (int i = 0; i < cnt; ++i, ++g) {
         const int s = (int)(g & 1);
         // QK of the page before the last has read the codes and B
@@ -718,35 +741,28 @@ __global__ void __launch_bounds__(blk::kThreads, 1) block_cache_kernel(BlockPara
             qz[8] = (acc[0][2] + acc[1][2]) * i0 + (acc[0][3] + acc[1][3]) * i1;
           }
         }
-        // B rows n = 8 rg + nl over K indexes 8kb..8kb+7 of step kk (channels cb + {0, 1, 8, 9, 2,
-        // 3, 10, 11}): 16 thread groups of 8 over the D / 8 (kk, kb) pairs
         uint8_t* bs = sm + S::kBOff + s * 2 * S::kBHalf;
-#pragma unroll 1
-        for (int c2 = 0; c2 < (D > 128 ? 2 : 1); ++c2) {
-          const int oc = D == 64 ? (grp & 7) : grp + 16 * c2;
-          const int kk = oc >> 1, kb = oc & 1, cb = 16 * kk + 4 * kb;
-          const uint2 sa = *reinterpret_cast<const uint2*>(R + RL.kscale + 2 * cb);
-          const uint2 sb = *reinterpret_cast<const uint2*>(R + RL.kscale + 2 * (cb + 8));
-          const __half2 sv[4] = {u2h2(sa.x), u2h2(sb.x), u2h2(sa.y), u2h2(sb.y)};
-          const int rg0 = codes ? 0 : NR / 16;
+        if (builds) {
 #pragma unroll
-          for (int rg = 0; rg < NR / 16; ++rg) {
-            if (D == 64 && NR > 16 && (rg & 1) != (grp >> 3)) continue;
-            if (D == 64 && NR == 16 && grp >= 8) continue;
-            const int at = kk * S::kStep + (rg0 + rg) * 256 + kb * 128 + nl * 16;
-            const uint4 h4 = *reinterpret_cast<const uint4*>(q_hi + at);
-            const uint4 l4 = *reinterpret_cast<const uint4*>(q_lo + at);
-            const __half2 qh[4] = {u2h2(h4.x), u2h2(h4.y), u2h2(h4.z), u2h2(h4.w)};
-            const __half2 ql[4] = {u2h2(l4.x), u2h2(l4.y), u2h2(l4.z), u2h2(l4.w)};
-            uint32_t hi[4], lo[4];
+          for (int c2 = 0; c2 < kPairs; ++c2) {
+            const int oc = pair_of(c2), cb = 16 * (oc >> 1) + 4 * (oc & 1);
+            const uint2 sa = *reinterpret_cast<const uint2*>(R + RL.kscale + 2 * cb);
+            const uint2 sb = *reinterpret_cast<const uint2*>(R + RL.kscale + 2 * (cb + 8));
+            const __half2 sv[4] = {u2h2(sa.x), u2h2(sb.x), u2h2(sa.y), u2h2(sb.y)};
 #pragma unroll
-            for (int e = 0; e < 4; ++e) {
-              const __half2 hv = __hmul2(qh[e], sv[e]);
-              hi[e] = h2u(hv);
-              lo[e] = h2u(__hfma2(ql[e], sv[e], __hfma2(qh[e], sv[e], __hneg2(hv))));
+            for (int e = 0; e < kRows; ++e) {
+              const __half2 h4[4] = {u2h2(qh[c2][e].x), u2h2(qh[c2][e].y), u2h2(qh[c2][e].z), u2h2(qh[c2][e].w)};
+              const __half2 l4[4] = {u2h2(ql[c2][e].x), u2h2(ql[c2][e].y), u2h2(ql[c2][e].z), u2h2(ql[c2][e].w)};
+              uint32_t hi[4], lo[4];
+#pragma unroll
+              for (int j = 0; j < 4; ++j) {
+                const __half2 hv = __hmul2(h4[j], sv[j]);
+                hi[j] = h2u(hv);
+                lo[j] = h2u(__hfma2(l4[j], sv[j], __hfma2(h4[j], sv[j], __hneg2(hv))));
+              }
+              *reinterpret_cast<uint4*>(bs + b_at(c2, e)) = make_uint4(hi[0], hi[1], hi[2], hi[3]);
+              *reinterpret_cast<uint4*>(bs + S::kBHalf + b_at(c2, e)) = make_uint4(lo[0], lo[1], lo[2], lo[3]);
             }
-            *reinterpret_cast<uint4*>(bs + at) = make_uint4(hi[0], hi[1], hi[2], hi[3]);
-            *reinterpret_cast<uint4*>(bs + S::kBHalf + at) = make_uint4(lo[0], lo[1], lo[2], lo[3]);
           }
         }
         if (codes) wait_st();
@@ -757,10 +773,10 @@ __global__ void __launch_bounds__(blk::kThreads, 1) block_cache_kernel(BlockPara
       }
     }
   } else if (warp < kMiscWarp) {
-    asm volatile("setmaxnreg.dec.sync.aligned.u32 56;");
-    // ---- V~ -> tensor memory: channels on the lanes, tokens along K; a warp takes one 16-channel
-    // block of each 128 ----
-    const int q = warp & 3, ii = (warp - kVWarp) >> 2;
+    asm volatile("setmaxnreg.dec.sync.aligned.u32 48;");
+    // ---- V~ -> tensor memory: channels on the lanes, tokens along K; a warp takes its quarter's
+    // 32 channels of each 128 and half the tokens ----
+    const int q = warp & 3, th = (warp - kVWarp) >> 2;
     const int gq = lane >> 2;
     for (int k = 0; segment(k); ++k) {
       stage_queries(seg_s[k & 1]);
@@ -783,12 +799,16 @@ __global__ void __launch_bounds__(blk::kThreads, 1) block_cache_kernel(BlockPara
         const __half* vch = reinterpret_cast<const __half*>(R + RL.vfactor);
         const uint32_t* vc = reinterpret_cast<const uint32_t*>(R + RL.vcodes);
         const uint32_t ta =
-            tmem + S::kColV + (uint32_t)(vs * 64 * S::kHalves) + ((uint32_t)(32 * q + 16 * ii) << 16);
+            tmem + S::kColV + (uint32_t)(vs * 64 * S::kHalves) + ((uint32_t)(32 * q) << 16);
         if (D >= 128 || q < D / 32) {
 #pragma unroll 1
           for (int hf = 0; hf < S::kHalves; ++hf) {
-            const int cb = 8 * hf + 2 * q + ii;
-            const __half2 cv[2] = {__half2half2(vch[16 * cb + gq]), __half2half2(vch[16 * cb + gq + 8])};
+            const int cb = 8 * hf + 2 * q;  // channel blocks cb and cb + 1: adjacent words
+            __half2 cv[2][2];
+#pragma unroll
+            for (int ii = 0; ii < 2; ++ii)
+#pragma unroll
+              for (int rho = 0; rho < 2; ++rho) cv[ii][rho] = __half2half2(vch[16 * (cb + ii) + gq + 8 * rho]);
             const uint32_t* vw = vc + ((cb >> 2) * 32 + lane) * 4 + (cb & 3);
             auto tile = [&](auto vbc) {
               constexpr int VB = decltype(vbc)::value;
@@ -800,31 +820,38 @@ __global__ void __launch_bounds__(blk::kThreads, 1) block_cache_kernel(BlockPara
                 asm("" : "+r"(mask[e]));  // kept in registers: a LOP3 takes one immediate
               }
 #pragma unroll
-              for (int o2 = 0; o2 < 4; ++o2) {
+              for (int oo = 0; oo < 2; ++oo) {
+                const int o2 = 2 * th + oo;  // pair of 16-token blocks
                 // token scales and zeros of the pair's four 8-token groups: rows of one ldmatrix all
                 // at the same 16 bytes leave lane (g, tq) tokens 2tq, 2tq + 1 of each group
                 uint32_t s2[4], z2[4];
                 ldsm_x4(sz + 64 * o2, s2);
                 ldsm_x4(sz + 2 * kTile + 64 * o2, z2);
-                uint32_t rr[8];
+                uint2 x[2];  // words of blocks cb, cb + 1 (2-bit: both token blocks share one)
+                x[0] = *reinterpret_cast<const uint2*>(vw + (VB == 2 ? o2 : 2 * o2) * (D / 64) * 128);
+                if (VB == 4) x[1] = *reinterpret_cast<const uint2*>(vw + (2 * o2 + 1) * (D / 64) * 128);
 #pragma unroll
-                for (int f = 0; f < 2; ++f) {
-                  const uint32_t x = vw[(VB == 2 ? o2 : 2 * o2 + f) * (D / 64) * 128];
-                  const uint32_t y = x >> 8;
+                for (int ii = 0; ii < 2; ++ii) {
+                  uint32_t rr[8];
 #pragma unroll
-                  for (int h = 0; h < 2; ++h) {
-                    // the code's bits under an exponent that makes them base + code, minus base
-                    const int e = VB == 2 ? 2 * f + h : h;
-                    const uint32_t base = 0x64006400u - (uint32_t)(VB == 2 ? 2 * e : 4 * e) * 0x04000400u;
+                  for (int f = 0; f < 2; ++f) {
+                    const uint2 w2 = x[VB == 2 ? 0 : f];
+                    const uint32_t lo = ii ? w2.y : w2.x, hi = lo >> 8;
 #pragma unroll
-                    for (int rho = 0; rho < 2; ++rho) {
-                      const __half2 c = __hsub2(u2h2(and_or(rho ? y : x, mask[e], base)), u2h2(base));
-                      rr[4 * f + 2 * rho + h] =
-                          h2u(__hmul2(__hfma2(c, u2h2(s2[2 * f + h]), u2h2(z2[2 * f + h])), cv[rho]));
+                    for (int h = 0; h < 2; ++h) {
+                      // the code's bits under an exponent that makes them base + code, minus base
+                      const int e = VB == 2 ? 2 * f + h : h;
+                      const uint32_t base = 0x64006400u - (uint32_t)(VB == 2 ? 2 * e : 4 * e) * 0x04000400u;
+#pragma unroll
+                      for (int rho = 0; rho < 2; ++rho) {
+                        const __half2 c = __hsub2(u2h2(and_or(rho ? hi : lo, mask[e], base)), u2h2(base));
+                        rr[4 * f + 2 * rho + h] =
+                            h2u(__hmul2(__hfma2(c, u2h2(s2[2 * f + h]), u2h2(z2[2 * f + h])), cv[ii][rho]));
+                      }
                     }
                   }
+                  st_16x256b_x2(ta + ((uint32_t)(16 * ii) << 16) + 64 * hf + 16 * o2, rr);
                 }
-                st_16x256b_x2(ta + 64 * hf + 16 * o2, rr);
               }
             };
             if (p.vb == 2) tile(IntC<2>{});
@@ -838,7 +865,7 @@ __global__ void __launch_bounds__(blk::kThreads, 1) block_cache_kernel(BlockPara
       }
     }
   } else {
-    asm volatile("setmaxnreg.dec.sync.aligned.u32 40;");
+    asm volatile("setmaxnreg.dec.sync.aligned.u32 32;");
     if (warp == kLoadWarp) {
       // ---- page records -> the ring ----
       if (lane == 0) {
@@ -896,13 +923,13 @@ __global__ void __launch_bounds__(blk::kThreads, 1) block_cache_kernel(BlockPara
           fence_after();
           if (!elect_one()) continue;
           if (is_pv) {
-            const uint64_t pd = smem_desc(smem_u32(sm + S::kPOff + s * S::kPBytes) + part * NR * 8, NR * 16, 128);
+            const uint64_t pd = smem_desc(smem_u32(sm + S::kPOff + s * S::kPBytes) + part * NR * 8, S::kPGroup, 128);
             const uint32_t av = tmem + S::kColV + (S::kVStages == 2 ? (uint32_t)(s * 64 * S::kHalves) : 0u);
 #pragma unroll 1
             for (int hf = 0; hf < S::kHalves; ++hf)
 #pragma unroll
               for (int o = 0; o < 8; ++o)
-                mma_ts(tmem + S::kColO + hf * NR + part * NM, av + 64 * hf + 8 * o, pd + o * (S::kStep >> 4),
+                mma_ts(tmem + S::kColO + hf * NR + part * NM, av + 64 * hf + 8 * o, pd + o * (S::kPStep >> 4),
                        kIdescPV<NM>, (uint32_t)(i > 0 || o > 0));
             mma_commit(&pv_done[2 * part + s]);
             issued[2 + part] = g + 1;
