@@ -39,21 +39,20 @@ namespace blk {
 using namespace tc5;
 
 constexpr int kThreads = 1024;
-// warps: 0-7 softmax (4 per row half), 8-15 K, 16-23 V, 24 loader, 25-26 QK, 27-28 PV, 29 walk, 30-31 idle
+// warps: 0-7 softmax (4 per row half), 8-15 K, 16-23 V, 24 loader, 25-26 QK, 27-28 PV, 29-31 queries
 constexpr int kKWarp = 8, kVWarp = 16, kMiscWarp = 24;
-constexpr int kLoadWarp = 24, kQkWarp = 25, kPvWarp = 27, kWalkWarp = 29;
+constexpr int kLoadWarp = 24, kQkWarp = 25, kPvWarp = 27, kQueryWarp = 29;
 constexpr int kMaxSlots = 8;
 // Named barriers.  Warps hand work to each other through them: a warp waiting at one issues nothing,
 // while polls of mbarriers by 13 warps (one every ~23 cycles each) kept the arrivals of the others
 // waiting and cost more than the work itself.  mbarriers remain where the hardware signals (bulk
 // copies, MMA completion), polled by one warp of a role, which then meets the others.
-//   0 the CTA; kRoleBar all warps but the loader; kSmBar + half the softmax warps of a row half;
+//   0 the CTA; kQueryBar the query warps; kSmBar + half the softmax warps of a row half;
 //   kKBar, kVBar the K and V warps; per stage kOpsK (K warps -> QK), kSFree (softmax -> QK),
 //   kOpsV (V warps -> PV); kPFull + 2 part + stage (softmax -> PV).
-constexpr int kRoleBar = 1, kSmBar = 2, kKBar = 4, kVBar = 5, kOpsK = 6, kSFree = 8, kOpsV = 10, kPFull = 12;
-constexpr int kRoleThreads = kThreads - 32;
+constexpr int kQueryBar = 1, kSmBar = 2, kKBar = 4, kVBar = 5, kOpsK = 6, kSFree = 8, kOpsV = 10, kPFull = 12;
 // Units of the line ahead of a row tile's pages for a segment's fixed work, and the smallest range.
-constexpr int kFixUnits = 4, kMinUnits = 3;
+constexpr int kFixUnits = 3, kMinUnits = 3;
 constexpr float kSlack = 8.0f;  // log2 units a logit may pass its row's reference by
 constexpr int kSmemMax = 232448 - 1024;
 
@@ -69,15 +68,15 @@ struct Shape {
   // group is 32 bytes off so that the 8 lanes of a store phase, two groups of four, miss each other
   static constexpr int kPGroup = NR * 16 + 32, kPStep = 2 * kPGroup;
   static constexpr int kPBytes = 8 * kPStep;
-  // shared memory: B (two stages, hi + lo), P (two stages), q~ hi + lo, small state, records
+  // shared memory: B (two stages, hi + lo), P (two stages), q~ hi + lo of two segments, small state, records
   static constexpr int kBOff = 0;
   static constexpr int kPOff = 2 * 2 * kBHalf;
   static constexpr int kQOff = kPOff + 2 * kPBytes;
-  static constexpr int kSmallOff = kQOff + 2 * kBHalf;
-  // floats: qz [4][NR], -reference, row maximum, shift, rescale, row limit [NR] each, per warp [4][NR]
-  static constexpr int kSmallFloats = (4 + 5 + 4) * NR;
+  static constexpr int kSmallOff = kQOff + 2 * 2 * kBHalf;
+  // floats: qz [4][NR], -reference, row maximum, shift, rescale [NR] each, row limit [2][NR], per warp [4][NR]
+  static constexpr int kSmallFloats = (4 + 4 + 2 + 4) * NR;
   static constexpr int kBarOff = kSmallOff + kSmallFloats * 4;
-  static constexpr int kNumBars = 2 * kMaxSlots + 2 * 4;
+  static constexpr int kNumBars = 2 * kMaxSlots + 2 * 4 + 4;
   static constexpr int kRecOff = (kBarOff + kNumBars * 8 + 127) & ~127;
   // tensor memory columns
   static constexpr uint32_t kColK = 0, kColV = 2 * (D / 2);
@@ -322,6 +321,8 @@ __global__ void __launch_bounds__(blk::kThreads, 1) block_cache_kernel(BlockPara
   uint64_t* rec_empty = rec_full + kMaxSlots;
   uint64_t* qk_full = rec_empty + kMaxSlots;  // [part][stage]: QK done (K codes and B are free)
   uint64_t* pv_done = qk_full + 4;            // [part][stage]: PV done: V and P are free, O is up to date
+  uint64_t* seg_full = pv_done + 4;           // [segment % 2]: its walk, q~ and row limits written
+  uint64_t* seg_empty = seg_full + 2;         // [segment % 2]: no role needs them any more
   constexpr int kOpsThreads = 256 + 32 * NP;           // kOpsK, kSFree, kOpsV
   constexpr int kPThreads = 256 / NP + 32;             // kPFull
   float* qz_s = reinterpret_cast<float*>(sm + S::kSmallOff);  // [4][NR]: page g's at g % 4
@@ -329,11 +330,10 @@ __global__ void __launch_bounds__(blk::kThreads, 1) block_cache_kernel(BlockPara
   float* max_s = nref_s + NR;      // the row's maximum when the reference was set (-inf: none yet)
   float* shift_s = max_s + NR;     // old reference - new reference
   float* alpha_s = shift_s + NR;   // rescale of l and O
-  int* lim_s = reinterpret_cast<int*>(alpha_s + NR);  // position from which the row's window sees
-  float* warp_s = reinterpret_cast<float*>(lim_s + NR);  // [4][NR]
+  int* lim_all = reinterpret_cast<int*>(alpha_s + NR);  // [2][NR]: position from which a row's window sees
+  float* warp_s = reinterpret_cast<float*>(lim_all + 2 * NR);  // [4][NR]
   uint8_t* recs = sm + S::kRecOff;
-  uint8_t* q_hi = sm + S::kQOff;
-  uint8_t* q_lo = q_hi + S::kBHalf;
+  auto q_of = [&](int k) { return sm + S::kQOff + (k & 1) * 2 * S::kBHalf; };  // hi, then lo
 
   // The kernel before this one (block_raw_kernel) waited for everything ahead of it before it let
   // this grid start, so the inputs are complete; its own partials are read by the merge only.
@@ -353,6 +353,10 @@ __global__ void __launch_bounds__(blk::kThreads, 1) block_cache_kernel(BlockPara
     for (int s = 0; s < 4; ++s) {
       mbar_init(&qk_full[s], 2);
       mbar_init(&pv_done[s], 1);
+    }
+    for (int s = 0; s < 2; ++s) {
+      mbar_init(&seg_full[s], 3);
+      mbar_init(&seg_empty[s], 4 + 2 * NP);  // K, V, two softmax groups, the MMA warps
     }
     abort_flag = 0;
     for (int i = 0; i < 4; ++i) issued_s[i] = 0;
@@ -377,19 +381,31 @@ __global__ void __launch_bounds__(blk::kThreads, 1) block_cache_kernel(BlockPara
   auto wait_pv = [&](int m, int j) {
     if (j >= 0) wait_one(&pv_done[2 * m + (j & 1)], (uint32_t)((j >> 1) & 1), abort_v, issued + 2 + m, j + 1);
   };
-  // Segment k of this CTA's range, or false at its end: the same for all warps but the loader's.
-  auto segment = [&](int k) -> bool {
-    bar_sync(kRoleBar, kRoleThreads);
+  // Segments pass through two buffers: the query warps write segment k + 1 (walk, q~, row limits)
+  // while the others work on segment k.  These waits do not look at the abort flag: the query warps
+  // and the roles keep going after it is set.
+  auto wait_segment = [&](int k) {
+    for (uint32_t n = 0; k > 0 && n < (1u << 26) && !mbar_try_wait(&seg_full[k & 1], (uint32_t)((k - 1) >> 1) & 1u); ++n) {
+    }
+  };
+  // Segment k for a group of warps that meets at barrier `id`; false past the end of the range.
+  auto segment = [&](int k, int id, int threads, bool leader) -> bool {
+    if (leader) wait_segment(k);
+    bar_sync(id, threads);
+    if (leader && lane == 0 && k > 0) mbar_arrive(&seg_empty[(k - 1) & 1]);  // the group is past it
     return seg_s[k & 1].left > 0;
   };
-  // q~ of a segment's rows, hi + lo, in the order and layout of the QK operand, by the 24 warps of
-  // the softmax, K and V roles.
-  auto stage_queries = [&](const TileWalk& w) {
+  // q~ of rows n0, n0 + step, .. of segment k, hi + lo, in the order and layout of the QK operand.
+  auto stage_queries = [&](int k, int n0, int step) {
+    const TileWalk& w = seg_s[k & 1];
+    uint8_t* q_hi = q_of(k);
+    uint8_t* q_lo = q_hi + S::kBHalf;
+    int* lim_s = lim_all + (k & 1) * NR;
     const float sc = p.qscale * inv_sqrt_d<D>();
     const float h0 = lift0(p.kb), h1 = lift1(p.kb);
     const bool q4 = (reinterpret_cast<uintptr_t>(p.q) & 3u) == 0u;
 #pragma unroll 1
-    for (int n = warp; n < NR; n += 24) {
+    for (int n = n0; n < NR; n += step) {
       const int r = w.t * NR + n, c = r / p.group;
       const bool live = c < w.nl;
       float v[D / 32];
@@ -422,6 +438,8 @@ __global__ void __launch_bounds__(blk::kThreads, 1) block_cache_kernel(BlockPara
       if (lane == 0) lim_s[n] = live ? w.len + c + 1 - p.window : INT32_MIN;
     }
   };
+  if (seg_s[0].left > 0) stage_queries(0, warp, kThreads / 32);
+  __syncthreads();
   // the roles' place in the line of pages and in the ring of records
   int g = 0;
   int r = 0;
@@ -447,9 +465,9 @@ __global__ void __launch_bounds__(blk::kThreads, 1) block_cache_kernel(BlockPara
     const int kpos = 4 * ((u >> 1) & 3) + 2 * ((u >> 3) & 1) + (u & 1);
     const int poff = (u >> 4) * S::kPStep + (kpos >> 3) * S::kPGroup + (kpos & 7) * 16 + 16 * c0;
     const float cf = kTwo24 / lift0(p.kb) * (p.kb == 2 && ((u >> 4) & 1) ? 0.0625f : 1.0f);
-    for (int k = 0; segment(k); ++k) {
+    for (int k = 0; segment(k, sbar, 128, wq == 0); ++k) {
       const TileWalk w = seg_s[k & 1];
-      stage_queries(w);
+      const int* lim_s = lim_all + (k & 1) * NR;
       const int cnt = w.count();
       const int64_t row = w.row(p);
       const int c1 = min((w.t * NR + NR - 1) / p.group, w.nl - 1);  // the tile's last new token
@@ -461,7 +479,6 @@ __global__ void __launch_bounds__(blk::kThreads, 1) block_cache_kernel(BlockPara
         nref_s[c0 + u] = 0.0f;
         max_s[c0 + u] = -INFINITY;
       }
-      bar_sync(kRoleBar, kRoleThreads);
       bool unset = true;  // some row has no reference yet
       for (int i = 0; i < cnt; ++i, ++g) {
         const int s = (int)(g & 1);
@@ -631,10 +648,10 @@ __global__ void __launch_bounds__(blk::kThreads, 1) block_cache_kernel(BlockPara
       const int rg = (codes ? 0 : NR / 16) + (D == 64 && NR > 16 ? 2 * e + (grp >> 3) : e);
       return (oc >> 1) * S::kStep + rg * 256 + (oc & 1) * 128 + nl * 16;
     };
-    for (int k = 0; segment(k); ++k) {
-      stage_queries(seg_s[k & 1]);
+    for (int k = 0; segment(k, kKBar, 256, warp == kKWarp); ++k) {
       const int cnt = seg_s[k & 1].count();
-      bar_sync(kRoleBar, kRoleThreads);
+      const uint8_t* q_hi = q_of(k);
+      const uint8_t* q_lo = q_hi + S::kBHalf;
       uint4 qh[kPairs][kRows], ql[kPairs][kRows];
 #pragma unroll
       for (int c2 = 0; c2 < kPairs; ++c2)
@@ -778,10 +795,8 @@ __global__ void __launch_bounds__(blk::kThreads, 1) block_cache_kernel(BlockPara
     // 32 channels of each 128 and half the tokens ----
     const int q = warp & 3, th = (warp - kVWarp) >> 2;
     const int gq = lane >> 2;
-    for (int k = 0; segment(k); ++k) {
-      stage_queries(seg_s[k & 1]);
+    for (int k = 0; segment(k, kVBar, 256, warp == kVWarp); ++k) {
       const int cnt = seg_s[k & 1].count();
-      bar_sync(kRoleBar, kRoleThreads);
       for (int i = 0; i < cnt; ++i, ++g) {
         const int s = (int)(g & 1);
         const int vs = S::kVStages == 2 ? s : 0;
@@ -892,25 +907,32 @@ __global__ void __launch_bounds__(blk::kThreads, 1) block_cache_kernel(BlockPara
           wait(&rec_full[k % slots], (uint32_t)((k / slots) & 1));
       }
       __syncwarp();
-    } else if (warp == kWalkWarp) {
-      // ---- the segments: the next one while the roles work on this one ----
-      for (int k = 0; segment(k); ++k) {
-        bar_sync(kRoleBar, kRoleThreads);
-        if (lane == 0) {
-          TileWalk w = seg_s[k & 1];
-          w.next(p, part_s.fix);
-          seg_s[(k + 1) & 1] = w;
+    } else if (warp >= kQueryWarp) {
+      // ---- the segments' walk and queries, one segment ahead of the roles ----
+      for (int k = 1; seg_s[(k - 1) & 1].left > 0; ++k) {
+        for (uint32_t n = 0; k > 1 && n < (1u << 26) && !mbar_try_wait(&seg_empty[k & 1], (uint32_t)((k - 2) >> 1) & 1u);
+             ++n) {
         }
+        if (warp == kQueryWarp && lane == 0) {
+          TileWalk w = seg_s[(k - 1) & 1];
+          w.next(p, part_s.fix);
+          seg_s[k & 1] = w;
+        }
+        bar_sync(kQueryBar, 96);
+        if (seg_s[k & 1].left > 0) stage_queries(k, warp - kQueryWarp, 3);
         __syncwarp();
+        if (lane == 0) mbar_arrive(&seg_full[k & 1]);
       }
-    } else if (warp < kWalkWarp) {
+    } else if (warp - (warp >= kPvWarp ? kPvWarp : kQkWarp) < NP) {
       // ---- MMA issue: QK and PV, a warp for each row half ----
       const bool is_pv = warp >= kPvWarp;
       const int part = is_pv ? warp - kPvWarp : warp - kQkWarp;
-      for (int k = 0; segment(k); ++k) {
-        const int cnt = seg_s[k & 1].count();
-        bar_sync(kRoleBar, kRoleThreads);
-        if (part >= NP) continue;
+      for (int k = 0;; ++k) {
+        wait_segment(k);
+        const int cnt = seg_s[k & 1].left > 0 ? seg_s[k & 1].count() : 0;
+        __syncwarp();
+        if (lane == 0) mbar_arrive(&seg_empty[k & 1]);
+        if (cnt == 0) break;
         for (int i = 0; i < cnt; ++i, ++g) {
           const int s = g & 1;
           if (is_pv) {
@@ -949,7 +971,7 @@ __global__ void __launch_bounds__(blk::kThreads, 1) block_cache_kernel(BlockPara
           }
         }
       }
-      if (g > 0 && part < NP) {
+      if (g > 0) {
         // the last MMAs have completed; the arrivals for pages that do not follow are taken
         if (is_pv) wait_pv(part, g - 1);
         else wait_qk(part, g - 1);
@@ -957,8 +979,6 @@ __global__ void __launch_bounds__(blk::kThreads, 1) block_cache_kernel(BlockPara
           for (int i = g > 1 ? g - 2 : 0; i < g; ++i) bar_sync(kSFree + (i & 1), kOpsThreads);
       }
       __syncwarp();
-    } else {
-      for (int k = 0; segment(k); ++k) bar_sync(kRoleBar, kRoleThreads);
     }
   }
 
@@ -1343,8 +1363,9 @@ static int launch_block_t(const BlockParams& p, cudaStream_t stream) {
   return cudaLaunchKernelEx(&cfg, block_merge_kernel<D>, p) == cudaSuccess ? KVARN_OK : KVARN_ERR_CUDA;
 }
 
-int block_tile_rows(int d, int64_t rows) {
-  if (rows <= 16) return 16;
+int block_tile_rows(int d, int64_t rows, int kb, int vb) {
+  // head_dim 256 with 12 bits a code pair: two page records fit beside 16 rows only
+  if (rows <= 16 || (d > 128 && kb + vb > 8)) return 16;
   if (rows <= 32 || d > 128) return 32;
   return 64;
 }

@@ -482,7 +482,7 @@ struct BlockLayout {
 static BlockLayout block_layout(const kvarn_desc* desc, int batch, int num_q_heads, int block_len) {
   BlockLayout L;
   const int64_t rows = (int64_t)block_len * (num_q_heads / desc->num_kv_heads);
-  L.tile_rows = block_tile_rows(desc->head_dim_padded, rows);
+  L.tile_rows = block_tile_rows(desc->head_dim_padded, rows, desc->k_bits, desc->v_bits);
   L.tiles = (rows + L.tile_rows - 1) / L.tile_rows;
   L.row_tiles = (int64_t)batch * desc->num_kv_heads * L.tiles;
   L.slot_floats = L.tile_rows * (desc->head_dim_padded + 4);

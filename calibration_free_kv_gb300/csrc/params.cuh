@@ -159,9 +159,9 @@ int launch_window_decode(int d, int nt, int kb, int vb, const DecodeParams& p, c
 constexpr int kDecodeMinRange = 32, kWindowMinRange = 16;
 // Block attention: the CTAs its page line is cut for (a GB300's SMs; the workspace's layout, not a
 // requirement on the device), the query rows of a row tile for `rows` rows of one (sequence, kv
-// head), and the launch of its three kernels.
+// head) and the code bits, and the launch of its three kernels.
 constexpr int kBlockCtas = 152;
-int block_tile_rows(int d, int64_t rows);
+int block_tile_rows(int d, int64_t rows, int kb, int vb);
 int launch_block_attention(int d, const BlockParams& p, cudaStream_t stream);
 int launch_dequant_any(int d, int kb, int vb, const DequantParams& p, int num_pages, cudaStream_t stream);
 
