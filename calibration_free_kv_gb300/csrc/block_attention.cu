@@ -356,7 +356,7 @@ __global__ void __launch_bounds__(blk::kThreads, 1) block_cache_kernel(BlockPara
     }
     for (int s = 0; s < 2; ++s) {
       mbar_init(&seg_full[s], 3);
-      mbar_init(&seg_empty[s], 4 + 2 * NP);  // K, V, two softmax groups, the MMA warps
+      mbar_init(&seg_empty[s], 5 + 2 * NP);  // loader, K, V, two softmax groups, the MMA warps
     }
     abort_flag = 0;
     for (int i = 0; i < 4; ++i) issued_s[i] = 0;
@@ -395,48 +395,88 @@ __global__ void __launch_bounds__(blk::kThreads, 1) block_cache_kernel(BlockPara
     if (leader && lane == 0 && k > 0) mbar_arrive(&seg_empty[(k - 1) & 1]);  // the group is past it
     return seg_s[k & 1].left > 0;
   };
-  // q~ of rows n0, n0 + step, .. of segment k, hi + lo, in the order and layout of the QK operand.
+  // q~ of segment k, hi + lo, in the order and layout of the QK operand: passes n0, n0 + step, .. of
+  // 512 / D rows.  A lane takes one 16-channel block of a row (four butterfly stages within the lane,
+  // the rest across lanes, every shuffle of a stage in flight together), which is one K step's two
+  // 16-byte chunks.
   auto stage_queries = [&](int k, int n0, int step) {
-    const TileWalk& w = seg_s[k & 1];
+    constexpr int kRowsPass = 512 / D;
+    const int row0 = seg_s[k & 1].t * NR, nl = seg_s[k & 1].nl, lim0 = seg_s[k & 1].len + 1 - p.window;
+    const __half* base = p.q + ((int64_t)seg_s[k & 1].b * p.block * p.num_q_heads + seg_s[k & 1].h * p.group) * p.d0;
     uint8_t* q_hi = q_of(k);
-    uint8_t* q_lo = q_hi + S::kBHalf;
     int* lim_s = lim_all + (k & 1) * NR;
     const float sc = p.qscale * inv_sqrt_d<D>();
-    const float h0 = lift0(p.kb), h1 = lift1(p.kb);
-    const bool q4 = (reinterpret_cast<uintptr_t>(p.q) & 3u) == 0u;
+    const bool q16 = (reinterpret_cast<uintptr_t>(p.q) & 15u) == 0u;
+    const int shift = 31 - __clz(p.group);  // the group is a power of two
+    const int blk = lane / kRowsPass;
 #pragma unroll 1
-    for (int n = n0; n < NR; n += step) {
-      const int r = w.t * NR + n, c = r / p.group;
-      const bool live = c < w.nl;
-      float v[D / 32];
-      const __half* src =
-          p.q + (((int64_t)w.b * p.block + (live ? c : 0)) * p.num_q_heads + w.h * p.group + (r - c * p.group)) * p.d0;
+    for (int pass = n0; pass < NR / kRowsPass; pass += step) {
+      const int n = pass * kRowsPass + lane % kRowsPass;
+      const int r = row0 + n, c = r >> shift;
+      const bool live = c < nl;
+      const __half* src = base + ((int64_t)c * p.num_q_heads + (r & (p.group - 1))) * p.d0 + 16 * blk;
+      float v[16];
 #pragma unroll
-      for (int e = 0; e < D / 32; e += 2) {
-        const int j = lane * (D / 32) + e;
-        float2 f = make_float2(0.0f, 0.0f);
-        if (live && j < p.d0)
-          f = q4 ? __half22float2(*reinterpret_cast<const __half2*>(src + j))
-                 : make_float2(__half2float(src[j]), __half2float(src[j + 1]));
-        v[e] = f.x;
-        v[e + 1] = f.y;
+      for (int h = 0; h < 2; ++h) {  // d0 is a multiple of 8
+        uint4 w = make_uint4(0u, 0u, 0u, 0u);
+        if (live && 16 * blk + 8 * h < p.d0) {
+          if (q16) {
+            w = *reinterpret_cast<const uint4*>(src + 8 * h);
+          } else {
+            const uint16_t* x = reinterpret_cast<const uint16_t*>(src + 8 * h);
+            w = make_uint4(x[0] | x[1] << 16, x[2] | x[3] << 16, x[4] | x[5] << 16, x[6] | x[7] << 16);
+          }
+        }
+        const uint32_t ws[4] = {w.x, w.y, w.z, w.w};
+#pragma unroll
+        for (int e = 0; e < 4; ++e) {
+          const float2 f = __half22float2(u2h2(ws[e]));
+          v[8 * h + 2 * e] = f.x;
+          v[8 * h + 2 * e + 1] = f.y;
+        }
       }
-      warp_fwht<D>(v, lane);
 #pragma unroll
-      for (int e = 0; e < D / 32; e += 2) {
-        const int j = lane * (D / 32) + e, c16 = j & 15;
-        const float f = sc * (c16 < 8 ? h0 : h1);
-        const float x = v[e] * f, y = v[e + 1] * f;
-        const __half2 hi = __floats2half2_rn(x, y);
-        const float2 hf = __half22float2(hi);
-        const int kpos = 4 * ((c16 & 7) >> 1) + 2 * (c16 >> 3);
-        const int at = (j >> 4) * S::kStep + (n >> 3) * 256 + (kpos >> 3) * 128 + (n & 7) * 16 + (kpos & 7) * 2;
-        *reinterpret_cast<__half2*>(q_hi + at) = hi;
-        *reinterpret_cast<__half2*>(q_lo + at) = __floats2half2_rn(x - hf.x, y - hf.y);
+      for (int st = 1; st < 16; st <<= 1)
+#pragma unroll
+        for (int i = 0; i < 16; ++i)
+          if ((i & st) == 0) {
+            const float x = v[i], y = v[i + st];
+            v[i] = x + y;
+            v[i + st] = x - y;
+          }
+#pragma unroll
+      for (int m = kRowsPass; m < 32; m <<= 1) {
+        const float sign = (lane & m) != 0 ? -1.0f : 1.0f;
+#pragma unroll
+        for (int i = 0; i < 16; ++i) v[i] = fmaf(sign, v[i], __shfl_xor_sync(0xffffffffu, v[i], m));
+      }
+      uint8_t* dst = q_hi + blk * S::kStep + (n >> 3) * 256 + (n & 7) * 16;
+#pragma unroll
+      for (int kb = 0; kb < 2; ++kb) {
+        uint32_t hi[4], lo[4];
+#pragma unroll
+        for (int e = 0; e < 4; ++e) {  // channels 4kb + {0, 1}, {8, 9}, {2, 3}, {10, 11}
+          const int ch = 4 * kb + 8 * (e & 1) + 2 * (e >> 1);
+          const float f = sc * ((e & 1) ? lift1(p.kb) : lift0(p.kb));
+          const float x = v[ch] * f, y = v[ch + 1] * f;
+          const __half2 h2 = __floats2half2_rn(x, y);
+          const float2 hf = __half22float2(h2);
+          hi[e] = h2u(h2);
+          lo[e] = h2u(__floats2half2_rn(x - hf.x, y - hf.y));
+        }
+        *reinterpret_cast<uint4*>(dst + 128 * kb) = make_uint4(hi[0], hi[1], hi[2], hi[3]);
+        *reinterpret_cast<uint4*>(dst + S::kBHalf + 128 * kb) = make_uint4(lo[0], lo[1], lo[2], lo[3]);
       }
       // padding rows see everything: they get a reference on the first page
-      if (lane == 0) lim_s[n] = live ? w.len + c + 1 - p.window : INT32_MIN;
+      if (blk == 0) lim_s[n] = live ? lim0 + c : INT32_MIN;
     }
+  };
+  // where the merge finds the partials of the row tile that segment w begins, if it begins one
+  auto note_slots = [&](const TileWalk& w) {
+    if (w.left <= 0 || w.j != 0) return;
+    const int64_t row = w.row(p);
+    const int64_t last = owner_cta(part_s, w.row0 + part_s.fix + w.span.count - 1);
+    p.row_info[row] = make_int2((int)((int64_t)blockIdx.x + row), (int)(last - blockIdx.x + 1));
   };
   if (seg_s[0].left > 0) stage_queries(0, warp, kThreads / 32);
   __syncthreads();
@@ -452,7 +492,7 @@ __global__ void __launch_bounds__(blk::kThreads, 1) block_cache_kernel(BlockPara
   };
 
   // Registers of the 65,536 the CTA is launched with: 104 a thread for the softmax, which holds a
-  // token's NR / 2 logits and as many sums, 72 for K, which holds its share of q~, 48 for V, 32 for the rest.
+  // token's NR / 2 logits and as many sums, 72 for K, which holds its share of q~, 40 for the rest.
   if (warp < kKWarp) {
     asm volatile("setmaxnreg.inc.sync.aligned.u32 104;");
     // ---- softmax (thread = token, rows c0 ..), rescale and the segment's partial (thread = channel) ----
@@ -466,12 +506,8 @@ __global__ void __launch_bounds__(blk::kThreads, 1) block_cache_kernel(BlockPara
     const int poff = (u >> 4) * S::kPStep + (kpos >> 3) * S::kPGroup + (kpos & 7) * 16 + 16 * c0;
     const float cf = kTwo24 / lift0(p.kb) * (p.kb == 2 && ((u >> 4) & 1) ? 0.0625f : 1.0f);
     for (int k = 0; segment(k, sbar, 128, wq == 0); ++k) {
-      const TileWalk w = seg_s[k & 1];
-      const int* lim_s = lim_all + (k & 1) * NR;
+      const TileWalk& w = seg_s[k & 1];  // read where it is needed: registers are short here
       const int cnt = w.count();
-      const int64_t row = w.row(p);
-      const int c1 = min((w.t * NR + NR - 1) / p.group, w.nl - 1);  // the tile's last new token
-      const int sure = w.len + c1 + 1 - p.window;  // from here on every row's window sees
       float2 l[NC / 2];
 #pragma unroll
       for (int i = 0; i < NC / 2; ++i) l[i] = make_float2(0.0f, 0.0f);
@@ -513,7 +549,11 @@ __global__ void __launch_bounds__(blk::kThreads, 1) block_cache_kernel(BlockPara
           bar_arrive(kSFree + s, kOpsThreads);
           if (p.window > 0) {
             const int at0 = w.span.page(w.j + i) * kTile;
-            if (at0 + kTile > p.sink && at0 < sure) {  // an edge page of the window or of the first tokens
+            const int* lim_s = lim_all + (k & 1) * NR;
+            // an edge page of the window or of the first tokens: the tile's last row does not see all of
+            // it (from `sure` on its window sees)
+            const int sure = w.len + min((w.t * NR + NR - 1) / p.group, w.nl - 1) + 1 - p.window;
+            if (at0 + kTile > p.sink && at0 < sure) {
               const int pos = at0 + u;
 #pragma unroll
               for (int n = 0; n < NC; ++n)
@@ -590,25 +630,36 @@ __global__ void __launch_bounds__(blk::kThreads, 1) block_cache_kernel(BlockPara
         bar_arrive(kPFull + 2 * part + s, kPThreads);
       }
       // the segment's partial: l over the tokens, O once its last PV is done
+      // (a butterfly that halves the rows a lane holds: row lane % NC ends in lane's first value)
+      float v[NC];
 #pragma unroll
-      for (int n = 0; n < NC; ++n) {
-        float v = (n & 1) ? l[n / 2].y : l[n / 2].x;
-#pragma unroll
-        for (int m = 16; m > 0; m >>= 1) v += __shfl_xor_sync(0xffffffffu, v, m);
-        if (lane == n) warp_s[wq * NR + c0 + n] = v;
+      for (int n = 0; n < NC; n += 2) {
+        v[n] = l[n / 2].x;
+        v[n + 1] = l[n / 2].y;
       }
+#pragma unroll
+      for (int m = 16; m >= NC; m >>= 1)
+#pragma unroll
+        for (int n = 0; n < NC; ++n) v[n] += __shfl_xor_sync(0xffffffffu, v[n], m);
+#pragma unroll
+      for (int m = NC / 2; m > 0; m >>= 1) {
+        const bool up = (lane & m) != 0;
+#pragma unroll
+        for (int n = 0; n < m; ++n) {
+          const float send = up ? v[n] : v[n + m];
+          const float keep = up ? v[n + m] : v[n];
+          v[n] = keep + __shfl_xor_sync(0xffffffffu, send, m);
+        }
+      }
+      if (lane < NC) warp_s[wq * NR + c0 + lane] = v[0];
       bar_sync(sbar, 128);
       const int live = min(NR, w.nl * p.group - w.t * NR) - c0;  // rows of this half that exist
-      float* dst = p.part + (((int64_t)blockIdx.x + row) * NR + c0) * (D + 4);
+      float* dst = p.part + (((int64_t)blockIdx.x + w.row(p)) * NR + c0) * (D + 4);
       if (u < min(live, NC)) {
         const int n = c0 + u;
         float* d = dst + (int64_t)u * (D + 4);
         d[0] = max_s[n];
         d[1] = (warp_s[n] + warp_s[NR + n]) + (warp_s[2 * NR + n] + warp_s[3 * NR + n]);
-      }
-      if (w.j == 0 && threadIdx.x == 0) {
-        const int64_t last = owner_cta(part_s, w.row0 + part_s.fix + w.span.count - 1);
-        p.row_info[row] = make_int2((int)((int64_t)blockIdx.x + row), (int)(last - blockIdx.x + 1));
       }
       wait_pv(part, g - 1);
       __syncwarp();
@@ -790,7 +841,7 @@ __global__ void __launch_bounds__(blk::kThreads, 1) block_cache_kernel(BlockPara
       }
     }
   } else if (warp < kMiscWarp) {
-    asm volatile("setmaxnreg.dec.sync.aligned.u32 48;");
+    asm volatile("setmaxnreg.dec.sync.aligned.u32 40;");
     // ---- V~ -> tensor memory: channels on the lanes, tokens along K; a warp takes its quarter's
     // 32 channels of each 128 and half the tokens ----
     const int q = warp & 3, th = (warp - kVWarp) >> 2;
@@ -880,15 +931,21 @@ __global__ void __launch_bounds__(blk::kThreads, 1) block_cache_kernel(BlockPara
       }
     }
   } else {
-    asm volatile("setmaxnreg.dec.sync.aligned.u32 32;");
+    asm volatile("setmaxnreg.dec.sync.aligned.u32 40;");
     if (warp == kLoadWarp) {
       // ---- page records -> the ring ----
       if (lane == 0) {
-        for (TileWalk w = seg_s[0]; w.left > 0; w.next(p, part_s.fix)) {
-          const int cnt = w.count();
+        for (int k = 0;; ++k) {
+          wait_segment(k);
+          const TileWalk& w = seg_s[k & 1];
+          const int cnt = w.left > 0 ? w.count() : 0;
+          const int j = w.j, sinks = w.span.sinks, skip = w.span.first - w.span.sinks;
           const int32_t* bt = p.block_table + (int64_t)w.b * p.max_pages;
-          for (int i = 0; i < cnt; ++i, ++g) {
-            int64_t id = bt[w.span.page(w.j + i)];
+          const uint8_t* src = p.pool + (int64_t)w.h * rec;
+          mbar_arrive(&seg_empty[k & 1]);
+          if (cnt == 0) break;
+          for (int i = j; i < j + cnt; ++i, ++g) {
+            int64_t id = bt[i < sinks ? i : i + skip];
             if (id < 0 || id >= p.num_pool_pages) {
               flag_error(p.status, KVARN_DEV_BAD_PAGE_ID);
               id = 0;
@@ -897,8 +954,7 @@ __global__ void __launch_bounds__(blk::kThreads, 1) block_cache_kernel(BlockPara
             if (*abort_v != 0) continue;  // nobody waits for the copies any more
             fence_proxy_async_smem();
             mbar_expect_tx(&rec_full[r], (uint32_t)rec);
-            bulk_copy_g2s(recs + r * rec, p.pool + (id * p.num_kv_heads + w.h) * (int64_t)rec, (uint32_t)rec,
-                          &rec_full[r]);
+            bulk_copy_g2s(recs + r * rec, src + id * p.num_kv_heads * (int64_t)rec, (uint32_t)rec, &rec_full[r]);
             next_record();
           }
         }
@@ -909,6 +965,7 @@ __global__ void __launch_bounds__(blk::kThreads, 1) block_cache_kernel(BlockPara
       __syncwarp();
     } else if (warp >= kQueryWarp) {
       // ---- the segments' walk and queries, one segment ahead of the roles ----
+      if (warp == kQueryWarp && lane == 0) note_slots(seg_s[0]);
       for (int k = 1; seg_s[(k - 1) & 1].left > 0; ++k) {
         for (uint32_t n = 0; k > 1 && n < (1u << 26) && !mbar_try_wait(&seg_empty[k & 1], (uint32_t)((k - 2) >> 1) & 1u);
              ++n) {
@@ -917,6 +974,7 @@ __global__ void __launch_bounds__(blk::kThreads, 1) block_cache_kernel(BlockPara
           TileWalk w = seg_s[(k - 1) & 1];
           w.next(p, part_s.fix);
           seg_s[k & 1] = w;
+          note_slots(w);
         }
         bar_sync(kQueryBar, 96);
         if (seg_s[k & 1].left > 0) stage_queries(k, warp - kQueryWarp, 3);
