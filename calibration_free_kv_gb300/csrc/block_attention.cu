@@ -43,6 +43,9 @@ constexpr int kThreads = 1024;
 constexpr int kKWarp = 8, kVWarp = 16, kMiscWarp = 24;
 constexpr int kLoadWarp = 24, kQkWarp = 25, kPvWarp = 27, kQueryWarp = 29;
 constexpr int kMaxSlots = 8;
+// Segments in flight, a power of two: the query warps are at most two ahead of the K warps, and the
+// roles that trail (V by up to six pages, each a segment of its own at worst) are within 8 of those.
+constexpr int kSegs = 16;
 // Named barriers.  Warps hand work to each other through them: a warp waiting at one issues nothing,
 // while polls of mbarriers by 13 warps (one every ~23 cycles each) kept the arrivals of the others
 // waiting and cost more than the work itself.  mbarriers remain where the hardware signals (bulk
@@ -54,7 +57,7 @@ constexpr int kQueryBar = 1, kSmBar = 2, kKBar = 4, kVBar = 5, kOpsK = 6, kSFree
 // Units of the line ahead of a row tile's pages for a segment's fixed work, and the smallest range.
 constexpr int kFixUnits = 3, kMinUnits = 3;
 constexpr float kSlack = 8.0f;  // log2 units a logit may pass its row's reference by
-constexpr int kSmemMax = 232448 - 1024;
+constexpr int kSmemMax = 232448 - 2048;  // the rest is for the static part
 
 template <int D, int NR>
 struct Shape {
@@ -73,10 +76,10 @@ struct Shape {
   static constexpr int kPOff = 2 * 2 * kBHalf;
   static constexpr int kQOff = kPOff + 2 * kPBytes;
   static constexpr int kSmallOff = kQOff + 2 * 2 * kBHalf;
-  // floats: qz [4][NR], -reference, row maximum, shift, rescale [NR] each, row limit [2][NR], per warp [4][NR]
-  static constexpr int kSmallFloats = (4 + 4 + 2 + 4) * NR;
+  // floats: qz [4][NR], -reference, row maximum, shift, rescale [NR] each, row limit [kSegs][NR], per warp [4][NR]
+  static constexpr int kSmallFloats = (4 + 4 + kSegs + 4) * NR;
   static constexpr int kBarOff = kSmallOff + kSmallFloats * 4;
-  static constexpr int kNumBars = 2 * kMaxSlots + 2 * 4 + 4;
+  static constexpr int kNumBars = 2 * kMaxSlots + 2 * 4 + kSegs + 2;
   static constexpr int kRecOff = (kBarOff + kNumBars * 8 + 127) & ~127;
   // tensor memory columns
   static constexpr uint32_t kColK = 0, kColV = 2 * (D / 2);
@@ -309,7 +312,7 @@ __global__ void __launch_bounds__(blk::kThreads, 1) block_cache_kernel(BlockPara
   constexpr int NP = S::kParts;    // MMA column parts
   constexpr int NM = NR / NP;      // columns of one MMA
   extern __shared__ __align__(1024) uint8_t sm[];
-  __shared__ TileWalk seg_s[2];
+  __shared__ TileWalk seg_s[kSegs];
   __shared__ Partition part_s;
   __shared__ uint32_t tslot;
   __shared__ int abort_flag;
@@ -321,8 +324,8 @@ __global__ void __launch_bounds__(blk::kThreads, 1) block_cache_kernel(BlockPara
   uint64_t* rec_empty = rec_full + kMaxSlots;
   uint64_t* qk_full = rec_empty + kMaxSlots;  // [part][stage]: QK done (K codes and B are free)
   uint64_t* pv_done = qk_full + 4;            // [part][stage]: PV done: V and P are free, O is up to date
-  uint64_t* seg_full = pv_done + 4;           // [segment % 2]: its walk, q~ and row limits written
-  uint64_t* seg_empty = seg_full + 2;         // [segment % 2]: no role needs them any more
+  uint64_t* seg_full = pv_done + 4;           // [segment % kSegs]: its walk, q~ and row limits written
+  uint64_t* q_empty = seg_full + kSegs;       // [segment % 2]: the K warps are done with its q~
   constexpr int kOpsThreads = 256 + 32 * NP;           // kOpsK, kSFree, kOpsV
   constexpr int kPThreads = 256 / NP + 32;             // kPFull
   float* qz_s = reinterpret_cast<float*>(sm + S::kSmallOff);  // [4][NR]: page g's at g % 4
@@ -330,8 +333,8 @@ __global__ void __launch_bounds__(blk::kThreads, 1) block_cache_kernel(BlockPara
   float* max_s = nref_s + NR;      // the row's maximum when the reference was set (-inf: none yet)
   float* shift_s = max_s + NR;     // old reference - new reference
   float* alpha_s = shift_s + NR;   // rescale of l and O
-  int* lim_all = reinterpret_cast<int*>(alpha_s + NR);  // [2][NR]: position from which a row's window sees
-  float* warp_s = reinterpret_cast<float*>(lim_all + 2 * NR);  // [4][NR]
+  int* lim_all = reinterpret_cast<int*>(alpha_s + NR);  // [kSegs][NR]: position from which a row's window sees
+  float* warp_s = reinterpret_cast<float*>(lim_all + kSegs * NR);  // [4][NR]
   uint8_t* recs = sm + S::kRecOff;
   auto q_of = [&](int k) { return sm + S::kQOff + (k & 1) * 2 * S::kBHalf; };  // hi, then lo
 
@@ -354,10 +357,8 @@ __global__ void __launch_bounds__(blk::kThreads, 1) block_cache_kernel(BlockPara
       mbar_init(&qk_full[s], 2);
       mbar_init(&pv_done[s], 1);
     }
-    for (int s = 0; s < 2; ++s) {
-      mbar_init(&seg_full[s], 3);
-      mbar_init(&seg_empty[s], 5 + 2 * NP);  // loader, K, V, two softmax groups, the MMA warps
-    }
+    for (int s = 0; s < kSegs; ++s) mbar_init(&seg_full[s], 3);
+    for (int s = 0; s < 2; ++s) mbar_init(&q_empty[s], 1);
     abort_flag = 0;
     for (int i = 0; i < 4; ++i) issued_s[i] = 0;
     fence_mbar_init();
@@ -381,19 +382,20 @@ __global__ void __launch_bounds__(blk::kThreads, 1) block_cache_kernel(BlockPara
   auto wait_pv = [&](int m, int j) {
     if (j >= 0) wait_one(&pv_done[2 * m + (j & 1)], (uint32_t)((j >> 1) & 1), abort_v, issued + 2 + m, j + 1);
   };
-  // Segments pass through two buffers: the query warps write segment k + 1 (walk, q~, row limits)
+  // Segments pass through a ring (their q~ through two buffers): the query warps write segment k + 1
   // while the others work on segment k.  These waits do not look at the abort flag: the query warps
   // and the roles keep going after it is set.
+  auto seg = [&](int k) -> const TileWalk& { return seg_s[k & (kSegs - 1)]; };
   auto wait_segment = [&](int k) {
-    for (uint32_t n = 0; k > 0 && n < (1u << 26) && !mbar_try_wait(&seg_full[k & 1], (uint32_t)((k - 1) >> 1) & 1u); ++n) {
+    uint64_t* bar = &seg_full[k & (kSegs - 1)];
+    for (uint32_t n = 0; n < (1u << 26) && !mbar_try_wait(bar, (uint32_t)(k / kSegs) & 1u); ++n) {
     }
   };
   // Segment k for a group of warps that meets at barrier `id`; false past the end of the range.
   auto segment = [&](int k, int id, int threads, bool leader) -> bool {
     if (leader) wait_segment(k);
     bar_sync(id, threads);
-    if (leader && lane == 0 && k > 0) mbar_arrive(&seg_empty[(k - 1) & 1]);  // the group is past it
-    return seg_s[k & 1].left > 0;
+    return seg(k).left > 0;
   };
   // q~ of segment k, hi + lo, in the order and layout of the QK operand: passes n0, n0 + step, .. of
   // 512 / D rows.  A lane takes one 16-channel block of a row (four butterfly stages within the lane,
@@ -401,10 +403,10 @@ __global__ void __launch_bounds__(blk::kThreads, 1) block_cache_kernel(BlockPara
   // 16-byte chunks.
   auto stage_queries = [&](int k, int n0, int step) {
     constexpr int kRowsPass = 512 / D;
-    const int row0 = seg_s[k & 1].t * NR, nl = seg_s[k & 1].nl, lim0 = seg_s[k & 1].len + 1 - p.window;
-    const __half* base = p.q + ((int64_t)seg_s[k & 1].b * p.block * p.num_q_heads + seg_s[k & 1].h * p.group) * p.d0;
+    const int row0 = seg(k).t * NR, nl = seg(k).nl, lim0 = seg(k).len + 1 - p.window;
+    const __half* base = p.q + ((int64_t)seg(k).b * p.block * p.num_q_heads + seg(k).h * p.group) * p.d0;
     uint8_t* q_hi = q_of(k);
-    int* lim_s = lim_all + (k & 1) * NR;
+    int* lim_s = lim_all + (k & (kSegs - 1)) * NR;
     const float sc = p.qscale * inv_sqrt_d<D>();
     const bool q16 = (reinterpret_cast<uintptr_t>(p.q) & 15u) == 0u;
     const int shift = 31 - __clz(p.group);  // the group is a power of two
@@ -506,7 +508,7 @@ __global__ void __launch_bounds__(blk::kThreads, 1) block_cache_kernel(BlockPara
     const int poff = (u >> 4) * S::kPStep + (kpos >> 3) * S::kPGroup + (kpos & 7) * 16 + 16 * c0;
     const float cf = kTwo24 / lift0(p.kb) * (p.kb == 2 && ((u >> 4) & 1) ? 0.0625f : 1.0f);
     for (int k = 0; segment(k, sbar, 128, wq == 0); ++k) {
-      const TileWalk& w = seg_s[k & 1];  // read where it is needed: registers are short here
+      const TileWalk& w = seg(k);  // read where it is needed: registers are short here
       const int cnt = w.count();
       float2 l[NC / 2];
 #pragma unroll
@@ -549,7 +551,7 @@ __global__ void __launch_bounds__(blk::kThreads, 1) block_cache_kernel(BlockPara
           bar_arrive(kSFree + s, kOpsThreads);
           if (p.window > 0) {
             const int at0 = w.span.page(w.j + i) * kTile;
-            const int* lim_s = lim_all + (k & 1) * NR;
+            const int* lim_s = lim_all + (k & (kSegs - 1)) * NR;
             // an edge page of the window or of the first tokens: the tile's last row does not see all of
             // it (from `sure` on its window sees)
             const int sure = w.len + min((w.t * NR + NR - 1) / p.group, w.nl - 1) + 1 - p.window;
@@ -700,9 +702,10 @@ __global__ void __launch_bounds__(blk::kThreads, 1) block_cache_kernel(BlockPara
       return (oc >> 1) * S::kStep + rg * 256 + (oc & 1) * 128 + nl * 16;
     };
     for (int k = 0; segment(k, kKBar, 256, warp == kKWarp); ++k) {
-      const int cnt = seg_s[k & 1].count();
+      const int cnt = seg(k).count();
       const uint8_t* q_hi = q_of(k);
       const uint8_t* q_lo = q_hi + S::kBHalf;
+      if (k > 0 && t == 0 && codes) mbar_arrive(&q_empty[(k - 1) & 1]);  // every K warp is past it
       uint4 qh[kPairs][kRows], ql[kPairs][kRows];
 #pragma unroll
       for (int c2 = 0; c2 < kPairs; ++c2)
@@ -847,7 +850,7 @@ __global__ void __launch_bounds__(blk::kThreads, 1) block_cache_kernel(BlockPara
     const int q = warp & 3, th = (warp - kVWarp) >> 2;
     const int gq = lane >> 2;
     for (int k = 0; segment(k, kVBar, 256, warp == kVWarp); ++k) {
-      const int cnt = seg_s[k & 1].count();
+      const int cnt = seg(k).count();
       for (int i = 0; i < cnt; ++i, ++g) {
         const int s = (int)(g & 1);
         const int vs = S::kVStages == 2 ? s : 0;
@@ -937,12 +940,11 @@ __global__ void __launch_bounds__(blk::kThreads, 1) block_cache_kernel(BlockPara
       if (lane == 0) {
         for (int k = 0;; ++k) {
           wait_segment(k);
-          const TileWalk& w = seg_s[k & 1];
+          const TileWalk& w = seg(k);
           const int cnt = w.left > 0 ? w.count() : 0;
           const int j = w.j, sinks = w.span.sinks, skip = w.span.first - w.span.sinks;
           const int32_t* bt = p.block_table + (int64_t)w.b * p.max_pages;
           const uint8_t* src = p.pool + (int64_t)w.h * rec;
-          mbar_arrive(&seg_empty[k & 1]);
           if (cnt == 0) break;
           for (int i = j; i < j + cnt; ++i, ++g) {
             int64_t id = bt[i < sinks ? i : i + skip];
@@ -965,21 +967,22 @@ __global__ void __launch_bounds__(blk::kThreads, 1) block_cache_kernel(BlockPara
       __syncwarp();
     } else if (warp >= kQueryWarp) {
       // ---- the segments' walk and queries, one segment ahead of the roles ----
-      if (warp == kQueryWarp && lane == 0) note_slots(seg_s[0]);
-      for (int k = 1; seg_s[(k - 1) & 1].left > 0; ++k) {
-        for (uint32_t n = 0; k > 1 && n < (1u << 26) && !mbar_try_wait(&seg_empty[k & 1], (uint32_t)((k - 2) >> 1) & 1u);
-             ++n) {
-        }
+      if (lane == 0) mbar_arrive(&seg_full[0]);  // staged above
+      if (warp == kQueryWarp && lane == 0) note_slots(seg(0));
+      for (int k = 1; seg(k - 1).left > 0; ++k) {
         if (warp == kQueryWarp && lane == 0) {
-          TileWalk w = seg_s[(k - 1) & 1];
+          TileWalk w = seg(k - 1);
           w.next(p, part_s.fix);
-          seg_s[k & 1] = w;
+          seg_s[k & (kSegs - 1)] = w;
           note_slots(w);
         }
+        for (uint32_t n = 0; k > 1 && n < (1u << 26) && !mbar_try_wait(&q_empty[k & 1], (uint32_t)((k - 2) >> 1) & 1u);
+             ++n) {
+        }
         bar_sync(kQueryBar, 96);
-        if (seg_s[k & 1].left > 0) stage_queries(k, warp - kQueryWarp, 3);
+        if (seg(k).left > 0) stage_queries(k, warp - kQueryWarp, 3);
         __syncwarp();
-        if (lane == 0) mbar_arrive(&seg_full[k & 1]);
+        if (lane == 0) mbar_arrive(&seg_full[k & (kSegs - 1)]);
       }
     } else if (warp - (warp >= kPvWarp ? kPvWarp : kQkWarp) < NP) {
       // ---- MMA issue: QK and PV, a warp for each row half ----
@@ -987,9 +990,7 @@ __global__ void __launch_bounds__(blk::kThreads, 1) block_cache_kernel(BlockPara
       const int part = is_pv ? warp - kPvWarp : warp - kQkWarp;
       for (int k = 0;; ++k) {
         wait_segment(k);
-        const int cnt = seg_s[k & 1].left > 0 ? seg_s[k & 1].count() : 0;
-        __syncwarp();
-        if (lane == 0) mbar_arrive(&seg_empty[k & 1]);
+        const int cnt = seg(k).left > 0 ? seg(k).count() : 0;
         if (cnt == 0) break;
         for (int i = 0; i < cnt; ++i, ++g) {
           const int s = g & 1;
