@@ -57,7 +57,7 @@ constexpr int kQueryBar = 1, kSmBar = 2, kKBar = 4, kVBar = 5, kOpsK = 6, kSFree
 // Units of the line ahead of a row tile's pages for a segment's fixed work, and the smallest range.
 constexpr int kFixUnits = 3, kMinUnits = 3;
 constexpr float kSlack = 8.0f;  // log2 units a logit may pass its row's reference by
-constexpr int kSmemMax = 232448 - 2048;  // the rest is for the static part
+constexpr int kSmemMax = 232448 - 1536;  // the rest is for the static part
 
 template <int D, int NR>
 struct Shape {
@@ -76,8 +76,9 @@ struct Shape {
   static constexpr int kPOff = 2 * 2 * kBHalf;
   static constexpr int kQOff = kPOff + 2 * kPBytes;
   static constexpr int kSmallOff = kQOff + 2 * 2 * kBHalf;
-  // floats: qz [4][NR], -reference, row maximum, shift, rescale [NR] each, row limit [kSegs][NR], per warp [4][NR]
-  static constexpr int kSmallFloats = (4 + 4 + kSegs + 4) * NR;
+  // floats: qz [4][NR], -reference, row maximum, shift, rescale [NR] each, row limit [kSegs][NR], per
+  // warp [4][NR], token factors [4][128]
+  static constexpr int kSmallFloats = (4 + 4 + kSegs + 4) * NR + 4 * kTile;
   static constexpr int kBarOff = kSmallOff + kSmallFloats * 4;
   static constexpr int kNumBars = 2 * kMaxSlots + 2 * 4 + kSegs + 2;
   static constexpr int kRecOff = (kBarOff + kNumBars * 8 + 127) & ~127;
@@ -335,6 +336,7 @@ __global__ void __launch_bounds__(blk::kThreads, 1) block_cache_kernel(BlockPara
   float* alpha_s = shift_s + NR;   // rescale of l and O
   int* lim_all = reinterpret_cast<int*>(alpha_s + NR);  // [kSegs][NR]: position from which a row's window sees
   float* warp_s = reinterpret_cast<float*>(lim_all + kSegs * NR);  // [4][NR]
+  float* rt_s = warp_s + 4 * NR;  // [4][128]: the token factors of page g at g % 4
   uint8_t* recs = sm + S::kRecOff;
   auto q_of = [&](int k) { return sm + S::kQOff + (k & 1) * 2 * S::kBHalf; };  // hi, then lo
 
@@ -351,7 +353,7 @@ __global__ void __launch_bounds__(blk::kThreads, 1) block_cache_kernel(BlockPara
   if (threadIdx.x == 0) {
     for (int i = 0; i < kMaxSlots; ++i) {
       mbar_init(&rec_full[i], 1);
-      mbar_init(&rec_empty[i], 4);  // the K and V roles and the two row halves of the softmax
+      mbar_init(&rec_empty[i], 16);  // the K and V warps
     }
     for (int s = 0; s < 4; ++s) {
       mbar_init(&qk_full[s], 2);
@@ -527,11 +529,10 @@ __global__ void __launch_bounds__(blk::kThreads, 1) block_cache_kernel(BlockPara
           wait_pv(part, g - 2);
         }
         bar_sync(sbar, 128);
-        if (g > 0 && u == 0) mbar_arrive(&rec_empty[r == 0 ? slots - 1 : r - 1]);  // all warps are past the last page
         {
           fence_after();
           ld_cols<NC>(tmem + S::kColS + (uint32_t)(s * NR + c0) + lanes, x);
-          const float rt = __half2float(reinterpret_cast<const __half*>(recs + r * rec + RL.kfactor)[u]);
+          const float rt = rt_s[(g & 3) * kTile + u];
           const float at = rt * cf;
           const float* qz = qz_s + (g & 3) * NR + c0;
 #pragma unroll
@@ -563,7 +564,6 @@ __global__ void __launch_bounds__(blk::kThreads, 1) block_cache_kernel(BlockPara
             }
           }
         }
-        next_record();
         float mx = -INFINITY;
 #pragma unroll
         for (int n = 0; n < NC; n += 2) mx = fmax3(mx, x[n], x[n + 1]);
@@ -723,7 +723,6 @@ __global__ void __launch_bounds__(blk::kThreads, 1) block_cache_kernel(BlockPara
           for (int m = 0; m < NP; ++m) wait_qk(m, g - 2);
         }
         bar_sync(kKBar, 256);
-        if (g > 0 && t == 0 && codes) mbar_arrive(&rec_empty[r == 0 ? slots - 1 : r - 1]);
         fence_after();
         const uint8_t* R = recs + r * rec;
         if (codes) {
@@ -812,6 +811,7 @@ __global__ void __launch_bounds__(blk::kThreads, 1) block_cache_kernel(BlockPara
             qz[8] = (acc[0][2] + acc[1][2]) * i0 + (acc[0][3] + acc[1][3]) * i1;
           }
         }
+        if (!codes) rt_s[(g & 3) * kTile + t] = __half2float(reinterpret_cast<const __half*>(R + RL.kfactor)[t]);
         uint8_t* bs = sm + S::kBOff + s * 2 * S::kBHalf;
         if (builds) {
 #pragma unroll
@@ -836,6 +836,8 @@ __global__ void __launch_bounds__(blk::kThreads, 1) block_cache_kernel(BlockPara
             }
           }
         }
+        __syncwarp();
+        if (lane == 0) mbar_arrive(&rec_empty[r]);
         if (codes) wait_st();
         fence_proxy_async_smem();
         fence_before();
@@ -861,7 +863,6 @@ __global__ void __launch_bounds__(blk::kThreads, 1) block_cache_kernel(BlockPara
           for (int m = 0; m < NP; ++m) wait_pv(m, g - S::kVStages);
         }
         bar_sync(kVBar, 256);
-        if (g > 0 && warp == kVWarp && lane == 0) mbar_arrive(&rec_empty[r == 0 ? slots - 1 : r - 1]);
         fence_after();
         const uint8_t* R = recs + r * rec;
         const uint32_t sz = smem_u32(R + RL.vscale) + 16 * (lane >> 3);  // group lane / 8 of a pair's four
@@ -927,6 +928,8 @@ __global__ void __launch_bounds__(blk::kThreads, 1) block_cache_kernel(BlockPara
             else tile(IntC<4>{});
           }
         }
+        __syncwarp();
+        if (lane == 0) mbar_arrive(&rec_empty[r]);
         wait_st();
         fence_before();
         bar_arrive(kOpsV + s, kOpsThreads);
