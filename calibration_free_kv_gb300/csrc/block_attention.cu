@@ -1059,11 +1059,13 @@ __global__ void __launch_bounds__(blk::kThreads, 1) block_cache_kernel(BlockPara
 // One CTA of 8 warps per (128 query rows, kv head, sequence), warp w taking rows 16w..16w+15; K and
 // V rows stream through shared memory 64 tokens at a time (cp.async into swizzled fp16 rows, two
 // stages), the open tile's first, then the new tokens'.  mma.sync m16n8k16: A = the fp16 queries
-// (exact products; the scale applied to the fp32 sums), B = K rows by ldmatrix; online softmax in
-// the log2 domain; PV with the probabilities as fp16 hi + lo.  A row that sees nothing leaves
-// m = -inf, l = 0, o = 0.
+// (exact products; the scale applied to the fp32 sums) by ldmatrix, B = K rows by ldmatrix; online
+// softmax in the log2 domain; PV with the probabilities rounded once to fp16 (they move the output
+// like its own rounding).  A row that sees nothing leaves m = -inf, l = 0, o = 0.  The queries stay in
+// shared memory so that two CTAs (16 warps) fit an SM at head_dim 64 and 128: with them in registers,
+// one CTA an SM and fp16 hi + lo probabilities a 2 x 2048-token chunk took 482 us.
 template <int D>
-__global__ void __launch_bounds__(256, 1) block_raw_kernel(BlockParams p) {
+__global__ void __launch_bounds__(256, D <= 128 ? 2 : 1) block_raw_kernel(BlockParams p) {
   constexpr int NB = 64;      // tokens per stage
   constexpr int NN = D / 8;   // channel n-tiles
   constexpr int KK = D / 16;  // channel k-steps
@@ -1084,7 +1086,7 @@ __global__ void __launch_bounds__(256, 1) block_raw_kernel(BlockParams p) {
   if (p.partial_k == nullptr) n_part = 0;
   const int part0 = len - len % kTile;  // position of the open tile's first token
   const int rows = nl * G;
-  const int rbase = blockIdx.x * 128;
+  const int rbase = ((int)gridDim.x - 1 - (int)blockIdx.x) * 128;  // the longest causal rows first
   if (rbase >= rows) return;
   const int r0 = rbase + 16 * wi;  // this warp's first query row
   const bool warp_live = r0 < rows;
@@ -1092,6 +1094,7 @@ __global__ void __launch_bounds__(256, 1) block_raw_kernel(BlockParams p) {
   const int ra = r0 + g, rb = r0 + g + 8;
   const int ca = ra < rows ? ra / G : -1, cb = rb < rows ? rb / G : -1;  // -1: padding row
   const uint32_t sbase = smem_u32(cs);
+  const uint32_t qbase = sbase + 2 * kStage;  // [128][D] fp16 query rows, swizzled
   const int64_t rstride = (int64_t)p.num_kv_heads * p.d0;
   const int64_t nbase = ((int64_t)b * p.block * p.num_kv_heads + h) * p.d0;
   const int64_t pbase = ((int64_t)b * p.num_kv_heads + h) * kTile * p.d0;
@@ -1130,30 +1133,24 @@ __global__ void __launch_bounds__(256, 1) block_raw_kernel(BlockParams p) {
   };
   int blk = next_blk(-1);
   if (blk < nblk) stage(blk, 0);
-  auto qrow = [&](int r) {
-    const int c = r / G, j = r - c * G;
-    return p.q + (((int64_t)b * p.block + c) * p.num_q_heads + h * G + j) * p.d0;
-  };
-  const __half* qa = qrow(ca >= 0 ? ra : 0);
-  const __half* qb = qrow(cb >= 0 ? rb : 0);
-  const bool q4 = (reinterpret_cast<uintptr_t>(p.q) & 3u) == 0u;
-  auto pair = [&](const __half* row, bool ok, int ch) -> uint32_t {
-    if (!(ok && ch < p.d0)) return 0u;
-    return q4 ? *reinterpret_cast<const uint32_t*>(row + ch) : h2u(__halves2half2(row[ch], row[ch + 1]));
-  };
-  // A fragment of channels 16kk..: rows g (ra) and g + 8 (rb)
-  auto afrag = [&](int kk, uint32_t (&a)[4]) {
-    const int ch = 16 * kk + 2 * tq;
-    a[0] = pair(qa, ca >= 0, ch);
-    a[1] = pair(qb, cb >= 0, ch);
-    a[2] = pair(qa, ca >= 0, ch + 8);
-    a[3] = pair(qb, cb >= 0, ch + 8);
-  };
-  constexpr bool kKeepQ = D <= 128;  // head_dim 256 reads the fragments again for every stage
-  uint32_t aq[kKeepQ ? KK : 1][4];
-  if constexpr (kKeepQ) {
-#pragma unroll
-    for (int kk = 0; kk < KK; ++kk) afrag(kk, aq[kk]);
+  {
+    // the CTA's queries (zero past the rows and past d0); rows start at multiples of 8 elements
+    const bool q16 = (reinterpret_cast<uintptr_t>(p.q) & 15u) == 0u;
+    for (int qi = threadIdx.x; qi < 128 * (D / 8); qi += blockDim.x) {
+      const int n = qi / (D / 8), ch = qi - n * (D / 8);
+      const int r = rbase + n, c = r / G;
+      uint4 w = make_uint4(0u, 0u, 0u, 0u);
+      if (r < rows && ch < dch) {
+        const __half* src = p.q + (((int64_t)b * p.block + c) * p.num_q_heads + h * G + (r - c * G)) * p.d0 + 8 * ch;
+        if (q16) {
+          w = *reinterpret_cast<const uint4*>(src);
+        } else {
+          const uint16_t* x = reinterpret_cast<const uint16_t*>(src);
+          w = make_uint4(x[0] | x[1] << 16, x[2] | x[3] << 16, x[4] | x[5] << 16, x[6] | x[7] << 16);
+        }
+      }
+      *reinterpret_cast<uint4*>(cs + 2 * kStage + swz_row<D>(n, ch)) = w;
+    }
   }
   float ma = -INFINITY, mb = -INFINITY, la = 0.0f, lb = 0.0f;  // l: this lane's share
   float o[NN][4];
@@ -1211,13 +1208,8 @@ __global__ void __launch_bounds__(256, 1) block_raw_kernel(BlockParams p) {
       for (int nt = 0; nt < NB / 8; ++nt) s[nt][0] = s[nt][1] = s[nt][2] = s[nt][3] = 0.0f;
 #pragma unroll
       for (int kk = 0; kk < KK; ++kk) {
-        uint32_t a[4];
-        if constexpr (kKeepQ) {
-#pragma unroll
-          for (int e = 0; e < 4; ++e) a[e] = aq[kk][e];
-        } else {
-          afrag(kk, a);
-        }
+        uint32_t a[4];  // rows 16wi + .., channels 16kk + ..
+        ldsm_x4(qbase + swz_row<D>(16 * wi + (lane & 15), 2 * kk + (lane >> 4)), a);
 #pragma unroll
         for (int np = 0; np < NB / 16; ++np) {  // token n-tiles 2np, 2np + 1
           uint32_t bk[4];
@@ -1251,43 +1243,38 @@ __global__ void __launch_bounds__(256, 1) block_raw_kernel(BlockParams p) {
       float pa = 0.0f, pb = 0.0f;
 #pragma unroll
       for (int nt = 0; nt < NB / 8; ++nt) {
-        s[nt][0] = exp2f(s[nt][0] - sa);
-        s[nt][1] = exp2f(s[nt][1] - sa);
-        s[nt][2] = exp2f(s[nt][2] - sb);
-        s[nt][3] = exp2f(s[nt][3] - sb);
+        s[nt][0] = ex2_approx(s[nt][0] - sa);
+        s[nt][1] = ex2_approx(s[nt][1] - sa);
+        s[nt][2] = ex2_approx(s[nt][2] - sb);
+        s[nt][3] = ex2_approx(s[nt][3] - sb);
         pa += s[nt][0] + s[nt][1];
         pb += s[nt][2] + s[nt][3];
       }
       la = fmaf(la, aa, pa);
       lb = fmaf(lb, ab, pb);
+      if (__any_sync(0xffffffffu, aa != 1.0f || ab != 1.0f)) {  // some row's maximum moved
 #pragma unroll
-      for (int n2 = 0; n2 < NN; ++n2) {
-        o[n2][0] *= aa;
-        o[n2][1] *= aa;
-        o[n2][2] *= ab;
-        o[n2][3] *= ab;
+        for (int n2 = 0; n2 < NN; ++n2) {
+          o[n2][0] *= aa;
+          o[n2][1] *= aa;
+          o[n2][2] *= ab;
+          o[n2][3] *= ab;
+        }
       }
 #pragma unroll
       for (int ks = 0; ks < NB / 16; ++ks) {
         if (t0 + 16 * ks >= n) break;  // past the tokens (warp-uniform)
-        // A = p of tokens t0 + 16ks..: n-tiles 2ks (k 0..7) and 2ks + 1 (k 8..15), hi + lo
-        uint32_t ah[4], al[4];
+        // A = p of tokens t0 + 16ks..: n-tiles 2ks (k 0..7) and 2ks + 1 (k 8..15)
+        uint32_t ah[4];
 #pragma unroll
-        for (int i = 0; i < 4; ++i) {
-          const float x = s[2 * ks + (i >> 1)][2 * (i & 1)], y = s[2 * ks + (i >> 1)][2 * (i & 1) + 1];
-          const __half2 hi = __floats2half2_rn(x, y);
-          const float2 hf = __half22float2(hi);
-          ah[i] = h2u(hi);
-          al[i] = h2u(__floats2half2_rn(x - hf.x, y - hf.y));
-        }
+        for (int i = 0; i < 4; ++i)
+          ah[i] = h2u(__floats2half2_rn(s[2 * ks + (i >> 1)][2 * (i & 1)], s[2 * ks + (i >> 1)][2 * (i & 1) + 1]));
 #pragma unroll
         for (int np = 0; np < NN / 2; ++np) {  // channel n-tiles 2np, 2np + 1
           uint32_t bv[4];
           ldsm_x4_trans(base + swz_row<D>(NB + 16 * ks + (lane & 7) + 8 * ((lane >> 3) & 1), 2 * np + (lane >> 4)), bv);
           mma16816(o[2 * np], ah, bv[0], bv[1]);
-          mma16816(o[2 * np], al, bv[0], bv[1]);
           mma16816(o[2 * np + 1], ah, bv[2], bv[3]);
-          mma16816(o[2 * np + 1], al, bv[2], bv[3]);
         }
       }
     }
@@ -1312,75 +1299,104 @@ __global__ void __launch_bounds__(256, 1) block_raw_kernel(BlockParams p) {
 }
 
 // ---- the merge -------------------------------------------------------------------------------
-// One warp per (sequence, new token, query head): the cache partials of the row's tile are summed
-// with their weights and rotated back [R is orthonormal and symmetric], the raw partial joins in the
-// original basis.  Rows past a sequence's new tokens are not written.
+// A warp takes two neighbouring (sequence, new token, query head) rows, so that the loads of one
+// cover the latency of the other's: the cache partials of the row's tile are summed with their
+// weights and rotated back [R is orthonormal and symmetric], the raw partial joins in the original
+// basis.  Rows past a sequence's new tokens are not written.
 template <int D>
 __global__ void __launch_bounds__(128) block_merge_kernel(BlockParams p) {
   constexpr int E = D / 32;
+  constexpr int kRows = 2;
   const int lane = threadIdx.x & 31;
-  const int64_t gw = (int64_t)blockIdx.x * 4 + (threadIdx.x >> 5);
+  const int64_t gw0 = ((int64_t)blockIdx.x * 4 + (threadIdx.x >> 5)) * kRows;
   grid_dependency_wait();
   grid_launch_dependents();
-  if (gw >= (int64_t)p.batch * p.block * p.num_q_heads) return;
-  const int hq = (int)(gw % p.num_q_heads);
-  const int64_t bc = gw / p.num_q_heads;
-  const int b = (int)(bc / p.block), c = (int)(bc - (int64_t)b * p.block);
-  const int len = blk::cached_len(p, b), nl = blk::new_len(p, b);
-  if (c >= nl) return;
-  const int h = hq / p.group;
-  const int r = c * p.group + (hq - h * p.group);
-  const int t = r / p.tile_rows;
-  const int64_t row = ((int64_t)b * p.num_kv_heads + h) * p.tiles + t;
-  const int in_tile = r - t * p.tile_rows;
-  const float* raw = p.raw_part + (row * p.tile_rows + in_tile) * (D + 4);
-  const float2 rml = *reinterpret_cast<const float2*>(raw);
-  float ro[E];
-  load_f32<E>(raw + 4 + lane * E, ro);
-  float M = rml.x, lsum = 0.0f;
-  float v[E];
-#pragma unroll
-  for (int e = 0; e < E; ++e) v[e] = 0.0f;
-  // the row tile's slots; a CTA of the cache kernel whose waits ran out leaves its entries unwritten
-  int2 info = make_int2(0, 0);
-  if (blk::tile_span(p, len, nl, t).count > 0) info = p.row_info[row];
+  const int64_t step = (int64_t)p.tile_rows * (D + 4);
   const int64_t all_slots = kBlockCtas + (int64_t)p.batch * p.num_kv_heads * p.tiles;
-  if (info.y > 0 && info.x >= 0 && (int64_t)info.x + info.y <= all_slots) {
-    const int64_t step = (int64_t)p.tile_rows * (D + 4);
-    const float* base = p.part + (int64_t)info.x * step + (int64_t)in_tile * (D + 4);
-    for (int s = lane; s < info.y; s += 32) M = fmaxf(M, base[s * step]);
+  bool live[kRows];
+  const float* raw[kRows];   // the row's raw partial
+  const float* base[kRows];  // its first cache partial
+  int slots[kRows];
 #pragma unroll
-    for (int m = 16; m > 0; m >>= 1) M = fmaxf(M, __shfl_xor_sync(0xffffffffu, M, m));
-    const float ref = M == -INFINITY ? 0.0f : M;
-    for (int s0 = 0; s0 < info.y; s0 += 32) {
-      const int s = s0 + lane;
-      float2 ml = make_float2(-INFINITY, 0.0f);
-      if (s < info.y) ml = *reinterpret_cast<const float2*>(base + s * step);
-      const float wt = exp2f(ml.x - ref);
-      float lw = wt * ml.y;
-#pragma unroll
-      for (int m = 16; m > 0; m >>= 1) lw += __shfl_xor_sync(0xffffffffu, lw, m);
-      lsum += lw;
-      const int cnt = min(32, info.y - s0);
-#pragma unroll 4
-      for (int i = 0; i < cnt; ++i) {
-        const float wi = __shfl_sync(0xffffffffu, wt, i);
-        float o[E];
-        load_f32<E>(base + (s0 + i) * step + 4 + lane * E, o);
-#pragma unroll
-        for (int e = 0; e < E; ++e) v[e] = fmaf(wi, o[e], v[e]);
+  for (int i = 0; i < kRows; ++i) {
+    const int64_t gw = gw0 + i;
+    live[i] = gw < (int64_t)p.batch * p.block * p.num_q_heads;
+    slots[i] = 0;
+    base[i] = p.part;
+    raw[i] = p.raw_part;
+    if (!live[i]) continue;
+    const int hq = (int)(gw % p.num_q_heads);
+    const int64_t bc = gw / p.num_q_heads;
+    const int b = (int)(bc / p.block), c = (int)(bc - (int64_t)b * p.block);
+    const int len = blk::cached_len(p, b), nl = blk::new_len(p, b);
+    live[i] = c < nl;
+    if (!live[i]) continue;
+    const int h = hq / p.group;
+    const int r = c * p.group + (hq - h * p.group);
+    const int t = r / p.tile_rows;
+    const int64_t row = ((int64_t)b * p.num_kv_heads + h) * p.tiles + t;
+    const int64_t in_tile = (int64_t)(r - t * p.tile_rows) * (D + 4);
+    raw[i] += row * step + in_tile;
+    // the row tile's slots; a CTA of the cache kernel whose waits ran out may leave its entries unwritten
+    if (blk::tile_span(p, len, nl, t).count > 0) {
+      const int2 info = p.row_info[row];
+      if (info.y > 0 && info.x >= 0 && (int64_t)info.x + info.y <= all_slots) {
+        slots[i] = info.y;
+        base[i] += (int64_t)info.x * step + in_tile;
       }
     }
-    warp_fwht<D>(v, lane);
   }
-  const float wr = rml.x == -INFINITY ? 0.0f : exp2f(rml.x - M);
-  lsum = fmaf(wr, rml.y, lsum);
-  const float inv = lsum > 0.0f ? 1.0f / lsum : 0.0f;
-  __half* dst = p.out + gw * p.d0;
+  float2 rml[kRows];
+  float ro[kRows][E], v[kRows][E], M[kRows], l[kRows];
 #pragma unroll
-  for (int e = 0; e < E; ++e) {
-    const int j = lane * E + e;
-    if (j < p.d0) dst[j] = __float2half_rn(fmaf(v[e], inv_sqrt_d<D>(), wr * ro[e]) * inv);
+  for (int i = 0; i < kRows; ++i) {
+    rml[i] = make_float2(-INFINITY, 0.0f);
+    if (live[i]) rml[i] = *reinterpret_cast<const float2*>(raw[i]);
+#pragma unroll
+    for (int e = 0; e < E; ++e) ro[i][e] = v[i][e] = 0.0f;
+    if (live[i]) load_f32<E>(raw[i] + 4 + lane * E, ro[i]);
+    M[i] = rml[i].x;
+    l[i] = 0.0f;
+  }
+  const int most = max(slots[0], slots[1]);
+#pragma unroll 2
+  for (int s = 0; s < most; ++s) {
+    float2 ml[kRows];
+    float o[kRows][E];
+#pragma unroll
+    for (int i = 0; i < kRows; ++i) {
+      ml[i] = make_float2(-INFINITY, 0.0f);
+#pragma unroll
+      for (int e = 0; e < E; ++e) o[i][e] = 0.0f;
+      if (s < slots[i]) {
+        ml[i] = *reinterpret_cast<const float2*>(base[i] + s * step);
+        load_f32<E>(base[i] + s * step + 4 + lane * E, o[i]);
+      }
+    }
+#pragma unroll
+    for (int i = 0; i < kRows; ++i) {
+      if (ml[i].x == -INFINITY) continue;  // a partial that saw no token
+      const float mn = fmaxf(M[i], ml[i].x);
+      const float keep = M[i] == -INFINITY ? 0.0f : exp2f(M[i] - mn), w = exp2f(ml[i].x - mn);
+      M[i] = mn;
+      l[i] = fmaf(l[i], keep, w * ml[i].y);
+#pragma unroll
+      for (int e = 0; e < E; ++e) v[i][e] = fmaf(v[i][e], keep, w * o[i][e]);
+    }
+  }
+#pragma unroll
+  for (int i = 0; i < kRows; ++i) {
+    if (slots[i] > 0) warp_fwht<D>(v[i], lane);
+    const float wr = rml[i].x == -INFINITY ? 0.0f : exp2f(rml[i].x - M[i]);
+    const float sum = fmaf(wr, rml[i].y, l[i]);
+    const float inv = sum > 0.0f ? 1.0f / sum : 0.0f;
+    if (!live[i]) continue;
+    __half* dst = p.out + (gw0 + i) * p.d0;
+#pragma unroll
+    for (int e = 0; e < E; ++e) {
+      const int j = lane * E + e;
+      if (j < p.d0) dst[j] = __float2half_rn(fmaf(v[i][e], inv_sqrt_d<D>(), wr * ro[i][e]) * inv);
+    }
   }
 }
 
@@ -1396,7 +1412,7 @@ static int launch_block_t(const BlockParams& p, cudaStream_t stream) {
   cfg.attrs = attr;
   cfg.numAttrs = 1;
   {
-    constexpr int kSmem = 2 * 2 * 64 * 2 * D;
+    constexpr int kSmem = 2 * 2 * 64 * 2 * D + 128 * 2 * D;  // two stages of K and V rows, the queries
     static PerDeviceOnce once;
     const void* fn = reinterpret_cast<const void*>(block_raw_kernel<D>);
     if (const int st = set_smem_limit(once, fn, kSmem); st != KVARN_OK) return st;
@@ -1418,8 +1434,8 @@ static int launch_block_t(const BlockParams& p, cudaStream_t stream) {
     cfg.dynamicSmemBytes = S::kRecOff + slots * rec;
     if (cudaLaunchKernelEx(&cfg, block_cache_kernel<D, NR>, p, slots) != cudaSuccess) return KVARN_ERR_CUDA;
   }
-  const int64_t warps = (int64_t)p.batch * p.block * p.num_q_heads;
-  cfg.gridDim = dim3((unsigned)((warps + 3) / 4));
+  const int64_t rows = (int64_t)p.batch * p.block * p.num_q_heads;
+  cfg.gridDim = dim3((unsigned)((rows + 7) / 8));
   cfg.blockDim = dim3(128);
   cfg.dynamicSmemBytes = 0;
   return cudaLaunchKernelEx(&cfg, block_merge_kernel<D>, p) == cudaSuccess ? KVARN_OK : KVARN_ERR_CUDA;

@@ -292,14 +292,15 @@ def prefill_attention(desc: KvarnDesc, q, chunk_k, chunk_v, pool, block_table, c
 
 
 def _arg(name, t, device, dtype, shape):
-    """Device pointer of a contiguous tensor argument on `device` of the given dtype and shape."""
-    if t.dtype is not dtype or t.shape != shape or t.device != device or not t.is_contiguous():
-        _ptr(t)
-        if t.device != device:
-            raise ValueError("%s is on %s, q on %s" % (name, t.device, device))
-        raise ValueError("%s must be a contiguous %s tensor of shape %s, got %s of shape %s (strides %s)" %
-                         (name, dtype, list(shape), t.dtype, list(t.shape), list(t.stride())))
-    return t.data_ptr()
+    """Device pointer of a contiguous tensor argument on CUDA device `device` (its index) of the
+    given dtype and shape."""
+    if t.dtype is dtype and t.shape == shape and t.get_device() == device and t.is_contiguous():
+        return t.data_ptr()
+    _ptr(t)
+    if t.get_device() != device:
+        raise ValueError("%s is on %s, q on cuda:%d" % (name, t.device, device))
+    raise ValueError("%s must be a contiguous %s tensor of shape %s, got %s of shape %s (strides %s)" %
+                     (name, dtype, list(shape), t.dtype, list(t.shape), list(t.stride())))
 
 
 def _opt(name, t, device, dtype, shape):
@@ -307,24 +308,33 @@ def _opt(name, t, device, dtype, shape):
 
 
 def _status_arg(status, device):
-    return None if status is None else _arg("status", status, device, torch.int32, status.shape)
+    if status is None:
+        return None
+    if status.numel() < 1:
+        raise ValueError("status must hold one int32")
+    return _arg("status", status, device, torch.int32, status.shape)
 
 
 def _workspace_arg(workspace, device):
-    return (_arg("workspace", workspace, device, workspace.dtype, workspace.shape),
-            workspace.numel() * workspace.element_size())
+    return _arg("workspace", workspace, device, workspace.dtype, workspace.shape), workspace.nbytes
 
 
-def _launch(fn, where, device, stream, *args):
-    """Call fn(*args, stream) with `device` current, on `stream` or the device's current stream."""
-    if stream is None:
-        stream = torch.cuda.current_stream(device)
-    if torch.cuda.current_device() == device.index:
-        status = fn(*args, stream.cuda_stream)
+def _tokens(n) -> int:
+    """A token count that may exceed any sequence, as the C int it is passed as."""
+    return min(max(int(n), -1), 0x7FFFFFFF)
+
+
+def _launch(fn, device, stream, *args):
+    """Call fn(*args, stream) with CUDA device `device` current, on `stream` or the device's current
+    stream."""
+    raw = torch._C._cuda_getCurrentRawStream(device) if stream is None else stream.cuda_stream
+    if torch.cuda.current_device() == device:
+        status = fn(*args, raw)
     else:
         with torch.cuda.device(device):
-            status = fn(*args, stream.cuda_stream)
-    _check(status, where)
+            status = fn(*args, raw)
+    if status != KVARN_OK:
+        raise KvarnError(status, fn.__name__)
 
 
 def _alloc_bytes(n: int, what: str, device):
@@ -336,7 +346,7 @@ def _alloc_bytes(n: int, what: str, device):
 def window_decode_workspace_bytes(desc: KvarnDesc, batch: int, num_q_heads: int, max_pages: int,
                                   sink_tokens: int, window: int) -> int:
     return int(_lib.kvarn_window_decode_workspace_bytes(ctypes.byref(desc), batch, num_q_heads, max_pages,
-                                                        sink_tokens, window))
+                                                        _tokens(sink_tokens), _tokens(window)))
 
 
 def alloc_window_decode_workspace(desc: KvarnDesc, batch: int, num_q_heads: int, max_pages: int,
@@ -352,25 +362,24 @@ def window_decode_attention(desc: KvarnDesc, q, pool, block_table, seq_lens, out
     ones (their own, token seq_lens[b] - 1, included).  q, out: fp16 [batch, Hq, d0].  Block-table
     entries of pages between the two are not read."""
     batch, hq, d0 = q.shape
-    dev, hkv, half, i32 = q.device, desc.num_kv_heads, torch.float16, torch.int32
+    dev, hkv, half, i32 = q.get_device(), desc.num_kv_heads, torch.float16, torch.int32
     rows, tile = (batch, hq, desc.head_dim), (batch, hkv, 128, desc.head_dim)
     pages, width = pool.shape[0], block_table.shape[-1]
-    ws, ws_bytes = _workspace_arg(workspace, dev)
     _ptr(q)
-    _launch(_lib.kvarn_window_decode_attention, "kvarn_window_decode_attention", dev, stream,
+    _launch(_lib.kvarn_window_decode_attention, dev, stream,
             ctypes.byref(desc), batch, hq, _arg("q", q, dev, half, rows),
             _arg("pool", pool, dev, torch.uint8, (pages, hkv, desc.page_record_bytes)), pages,
             _arg("block_table", block_table, dev, i32, (batch, width)), width,
             _arg("seq_lens", seq_lens, dev, i32, (batch,)), _opt("partial_k", partial_k, dev, half, tile),
-            _opt("partial_v", partial_v, dev, half, tile), sink_tokens, window,
+            _opt("partial_v", partial_v, dev, half, tile), _tokens(sink_tokens), _tokens(window),
             1.0 / math.sqrt(d0) if softmax_scale is None else softmax_scale, _arg("out", out, dev, half, rows),
-            ws, ws_bytes, _status_arg(status, dev))
+            *_workspace_arg(workspace, dev), _status_arg(status, dev))
 
 
 def window_prefill_workspace_bytes(desc: KvarnDesc, batch: int, num_q_heads: int, chunk_len: int, max_pages: int,
                                    sink_tokens: int, window: int) -> int:
     return int(_lib.kvarn_window_prefill_workspace_bytes(ctypes.byref(desc), batch, num_q_heads, chunk_len,
-                                                         max_pages, sink_tokens, window))
+                                                         max_pages, _tokens(sink_tokens), _tokens(window)))
 
 
 def alloc_window_prefill_workspace(desc: KvarnDesc, batch: int, num_q_heads: int, chunk_len: int, max_pages: int,
@@ -384,7 +393,7 @@ def _block_args(desc, what, q, new_k, new_v, new_lens, pool, block_table, cache_
     parameters (the mask, which only one has, apart)."""
     batch, block, hq, _ = q.shape
     _ptr(q)
-    dev, hkv, d0, half, i32 = q.device, desc.num_kv_heads, desc.head_dim, torch.float16, torch.int32
+    dev, hkv, d0, half, i32 = q.get_device(), desc.num_kv_heads, desc.head_dim, torch.float16, torch.int32
     kv, tile = (batch, block, hkv, d0), (batch, hkv, 128, d0)
     pages, width = pool.shape[0], block_table.shape[-1]
     return ((_arg("q", q, dev, half, (batch, block, hq, d0)), _arg(what + "_k", new_k, dev, half, kv),
@@ -405,13 +414,12 @@ def window_prefill_attention(desc: KvarnDesc, q, chunk_k, chunk_v, pool, block_t
     batch, chunk, hq, d0 = q.shape
     new, lens, cache = _block_args(desc, "chunk", q, chunk_k, chunk_v, chunk_lens, pool, block_table, cache_lens,
                                    partial_k, partial_v)
-    dev = q.device
-    ws, ws_bytes = _workspace_arg(workspace, dev)
-    _launch(_lib.kvarn_window_prefill_attention, "kvarn_window_prefill_attention", dev, stream,
-            ctypes.byref(desc), batch, hq, chunk, *new, lens, *cache, sink_tokens, window,
+    dev = q.get_device()
+    _launch(_lib.kvarn_window_prefill_attention, dev, stream,
+            ctypes.byref(desc), batch, hq, chunk, *new, lens, *cache, _tokens(sink_tokens), _tokens(window),
             1.0 / math.sqrt(d0) if softmax_scale is None else softmax_scale,
-            _arg("out", out, dev, torch.float16, (batch, chunk, hq, desc.head_dim)), ws, ws_bytes,
-            _status_arg(status, dev))
+            _arg("out", out, dev, torch.float16, (batch, chunk, hq, desc.head_dim)),
+            *_workspace_arg(workspace, dev), _status_arg(status, dev))
 
 
 def tree_workspace_bytes(desc: KvarnDesc, batch: int, num_q_heads: int, tree_len: int, max_pages: int) -> int:
@@ -433,16 +441,15 @@ def tree_attention(desc: KvarnDesc, q, tree_k, tree_v, tree_mask, pool, block_ta
     batch, nodes, hq, d0 = q.shape
     new, lens, cache = _block_args(desc, "tree", q, tree_k, tree_v, tree_lens, pool, block_table, cache_lens,
                                    partial_k, partial_v)
-    dev = q.device
-    ws, ws_bytes = _workspace_arg(workspace, dev)
+    dev = q.get_device()
     if tree_mask is not None and tree_mask.dtype is torch.uint32:
         tree_mask = tree_mask.view(torch.int32)
-    _launch(_lib.kvarn_tree_attention, "kvarn_tree_attention", dev, stream,
+    _launch(_lib.kvarn_tree_attention, dev, stream,
             ctypes.byref(desc), batch, hq, nodes, *new,
             _opt("tree_mask", tree_mask, dev, torch.int32, (batch, nodes, (nodes + 31) // 32)), lens, *cache,
             1.0 / math.sqrt(d0) if softmax_scale is None else softmax_scale,
-            _arg("out", out, dev, torch.float16, (batch, nodes, hq, desc.head_dim)), ws, ws_bytes,
-            _status_arg(status, dev))
+            _arg("out", out, dev, torch.float16, (batch, nodes, hq, desc.head_dim)),
+            *_workspace_arg(workspace, dev), _status_arg(status, dev))
 
 
 def decode_attention_noalloc(desc: KvarnDesc, q, pool, block_table, seq_lens, out, partial_k=None,
