@@ -522,19 +522,29 @@ __global__ void __launch_bounds__(blk::kThreads, 1) block_cache_kernel(BlockPara
       bool unset = true;  // some row has no reference yet
       for (int i = 0; i < cnt; ++i, ++g) {
         const int s = (int)(g & 1);
-        float x[NC];
         // S of the page, and PV of the page before the last, which has read this stage's P
         if (wq == 0) {
           wait_qk(part, g);
           wait_pv(part, g - 2);
         }
         bar_sync(sbar, 128);
-        {
-          fence_after();
-          ld_cols<NC>(tmem + S::kColS + (uint32_t)(s * NR + c0) + lanes, x);
-          const float rt = rt_s[(g & 3) * kTile + u];
-          const float at = rt * cf;
-          const float* qz = qz_s + (g & 3) * NR + c0;
+        fence_after();
+        const uint32_t ts = tmem + S::kColS + (uint32_t)(s * NR + c0) + lanes;
+        const float rt = rt_s[(g & 3) * kTile + u], at = rt * cf;
+        const float* qz = qz_s + (g & 3) * NR + c0;
+        const int* lim_s = nullptr;  // the rows' limits on an edge page of the window or the first tokens
+        int pos = 0;
+        if (p.window > 0) {
+          pos = w.span.page(w.j + i) * kTile;
+          // from `sure` on the window of the tile's last row sees
+          const int sure = w.len + min((w.t * NR + NR - 1) / p.group, w.nl - 1) + 1 - p.window;
+          if (pos + kTile > p.sink && pos < sure) lim_s = lim_all + (k & (kSegs - 1)) * NR + c0;
+          pos += u;
+          if (pos < p.sink) lim_s = nullptr;  // this token is one of the first
+        }
+        float x[NC];  // logits less their rows' references
+        for (bool moved = false;; moved = true) {
+          ld_cols<NC>(ts, x);
 #pragma unroll
           for (int n = 0; n < NC; n += 4) {
             const float4 z = *reinterpret_cast<const float4*>(qz + n);
@@ -548,55 +558,51 @@ __global__ void __launch_bounds__(blk::kThreads, 1) block_cache_kernel(BlockPara
             x[n + 2] = c.x;
             x[n + 3] = c.y;
           }
-          fence_before();
-          bar_arrive(kSFree + s, kOpsThreads);
-          if (p.window > 0) {
-            const int at0 = w.span.page(w.j + i) * kTile;
-            const int* lim_s = lim_all + (k & (kSegs - 1)) * NR;
-            // an edge page of the window or of the first tokens: the tile's last row does not see all of
-            // it (from `sure` on its window sees)
-            const int sure = w.len + min((w.t * NR + NR - 1) / p.group, w.nl - 1) + 1 - p.window;
-            if (at0 + kTile > p.sink && at0 < sure) {
-              const int pos = at0 + u;
+          if (lim_s != nullptr) {
 #pragma unroll
-              for (int n = 0; n < NC; ++n)
-                if (pos >= p.sink && pos < lim_s[c0 + n]) x[n] = -INFINITY;
-            }
+            for (int n = 0; n < NC; ++n)
+              if (pos < lim_s[n]) x[n] = -INFINITY;
           }
-        }
-        float mx = -INFINITY;
+          float mx = -INFINITY;
 #pragma unroll
-        for (int n = 0; n < NC; n += 2) mx = fmax3(mx, x[n], x[n + 1]);
-        if (bar_any(sbar, 128, unset || mx > kSlack)) {
-          // move the references to the rows' maxima
+          for (int n = 0; n < NC; n += 2) mx = fmax3(mx, x[n], x[n + 1]);
+          if (!bar_any(sbar, 128, !moved && (unset || mx > kSlack))) break;
+          // Move the references to the rows' maxima, then take the logits again.  This runs once or
+          // twice a segment, from a cold instruction cache that costs ~200 cycles for eight
+          // instructions: short loops over eight rows here, and the code above for the rest.
+#pragma unroll 1
+          for (int n0 = 0; n0 < NC; n0 += 8) {
+            float y[8];
+            ld_cols<8>(ts + n0, y);
+            float mine = 0.0f;
 #pragma unroll
-          for (int n = 0; n < NC; ++n) {
-            const float v = warp_max(x[n]);
-            if (lane == n) warp_s[wq * NR + c0 + n] = v;
+            for (int n = 0; n < 8; ++n) {
+              y[n] = fmaf(at, y[n], rt * qz[n0 + n]);
+              if (lim_s != nullptr && pos < lim_s[n0 + n]) y[n] = -INFINITY;
+              const float v = warp_max(y[n]);
+              if (lane == n) mine = v;
+            }
+            if (lane < 8) warp_s[wq * NR + c0 + n0 + lane] = mine;
           }
           bar_sync(sbar, 128);
           bool none = false;
           if (u < NC) {
             const int n = c0 + u;
-            const float old = max_s[n], ref = -nref_s[n];
-            const float pm =
-                fmaxf(fmaxf(warp_s[n], warp_s[NR + n]), fmaxf(warp_s[2 * NR + n], warp_s[3 * NR + n])) + ref;
+            const float old = max_s[n];
+            const float pm = fmaxf(fmaxf(warp_s[n], warp_s[NR + n]), fmaxf(warp_s[2 * NR + n], warp_s[3 * NR + n]));
             const float mn = fmaxf(old, pm);
             none = mn == -INFINITY;
-            const float to = none ? 0.0f : mn;
             max_s[n] = mn;
-            nref_s[n] = -to;
-            shift_s[n] = ref - to;
+            nref_s[n] = none ? 0.0f : -mn;
             alpha_s[n] = old == -INFINITY ? 0.0f : ex2_approx(old - mn);
           }
           unset = bar_any(sbar, 128, none);
+          if (i > 0) {  // l and O of the pages before this one
 #pragma unroll
-          for (int n = 0; n < NC; n += 2) {
-            x[n] += shift_s[c0 + n];
-            x[n + 1] += shift_s[c0 + n + 1];
-            l[n / 2] = mul2(l[n / 2], make_float2(alpha_s[c0 + n], alpha_s[c0 + n + 1]));
-          }
-          if (i > 0) {  // O of the pages before this one
+            for (int n = 0; n < NC; n += 2) {
+              const float2 al = *reinterpret_cast<const float2*>(alpha_s + c0 + n);
+              l[n / 2] = mul2(l[n / 2], al);
+            }
             wait_pv(part, g - 1);
             __syncwarp();
             fence_after();
@@ -615,6 +621,8 @@ __global__ void __launch_bounds__(blk::kThreads, 1) block_cache_kernel(BlockPara
             wait_st();
           }
         }
+        fence_before();
+        bar_arrive(kSFree + s, kOpsThreads);
         uint8_t* pb = sm + S::kPOff + s * S::kPBytes + poff;
 #pragma unroll
         for (int n = 0; n < NC; n += 8) {
