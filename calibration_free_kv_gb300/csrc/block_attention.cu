@@ -1307,27 +1307,29 @@ __global__ void __launch_bounds__(256, D <= 128 ? 2 : 1) block_raw_kernel(BlockP
 }
 
 // ---- the merge -------------------------------------------------------------------------------
-// A warp takes two neighbouring (sequence, new token, query head) rows, so that the loads of one
-// cover the latency of the other's: the cache partials of the row's tile are summed with their
-// weights and rotated back [R is orthonormal and symmetric], the raw partial joins in the original
-// basis.  Rows past a sequence's new tokens are not written.
-template <int D>
+// A warp takes one, or in large calls two neighbouring, (sequence, new token, query head) rows: the
+// cache partials of the row's tile are summed with their weights and rotated back [R is orthonormal
+// and symmetric], the raw partial joins in the original basis.  Rows past a sequence's new tokens are
+// not written.  Two rows a warp cover each other's load latency (a 2 x 2048-token chunk 81 -> 64 us);
+// where all warps fit the SMs at once one row a warp is quicker (8 nodes 7 -> 6 us).
+template <int D, int kRows>
 __global__ void __launch_bounds__(128) block_merge_kernel(BlockParams p) {
   constexpr int E = D / 32;
-  constexpr int kRows = 2;
   const int lane = threadIdx.x & 31;
   const int64_t gw0 = ((int64_t)blockIdx.x * 4 + (threadIdx.x >> 5)) * kRows;
-  grid_dependency_wait();
-  grid_launch_dependents();
   const int64_t step = (int64_t)p.tile_rows * (D + 4);
   const int64_t all_slots = kBlockCtas + (int64_t)p.batch * p.num_kv_heads * p.tiles;
   bool live[kRows];
   const float* raw[kRows];   // the row's raw partial
   const float* base[kRows];  // its first cache partial
   int slots[kRows];
+  const int2* info_at[kRows];  // its row tile's slots, null where no sealed page is seen
+  // The lengths come from before block_raw_kernel, which waited for their writer: they are read ahead
+  // of the wait for the partials.
 #pragma unroll
   for (int i = 0; i < kRows; ++i) {
     const int64_t gw = gw0 + i;
+    info_at[i] = nullptr;
     live[i] = gw < (int64_t)p.batch * p.block * p.num_q_heads;
     slots[i] = 0;
     base[i] = p.part;
@@ -1345,15 +1347,14 @@ __global__ void __launch_bounds__(128) block_merge_kernel(BlockParams p) {
     const int64_t row = ((int64_t)b * p.num_kv_heads + h) * p.tiles + t;
     const int64_t in_tile = (int64_t)(r - t * p.tile_rows) * (D + 4);
     raw[i] += row * step + in_tile;
-    // the row tile's slots; a CTA of the cache kernel whose waits ran out may leave its entries unwritten
-    if (blk::tile_span(p, len, nl, t).count > 0) {
-      const int2 info = p.row_info[row];
-      if (info.y > 0 && info.x >= 0 && (int64_t)info.x + info.y <= all_slots) {
-        slots[i] = info.y;
-        base[i] += (int64_t)info.x * step + in_tile;
-      }
-    }
+    base[i] += in_tile;
+    if (blk::tile_span(p, len, nl, t).count > 0) info_at[i] = p.row_info + row;
   }
+  grid_dependency_wait();
+  grid_launch_dependents();
+  int2 info[kRows];
+#pragma unroll
+  for (int i = 0; i < kRows; ++i) info[i] = info_at[i] != nullptr ? *info_at[i] : make_int2(0, 0);
   float2 rml[kRows];
   float ro[kRows][E], v[kRows][E], M[kRows], l[kRows];
 #pragma unroll
@@ -1366,7 +1367,16 @@ __global__ void __launch_bounds__(128) block_merge_kernel(BlockParams p) {
     M[i] = rml[i].x;
     l[i] = 0.0f;
   }
-  const int most = max(slots[0], slots[1]);
+  int most = 0;
+#pragma unroll
+  for (int i = 0; i < kRows; ++i) {
+    // checked: a CTA of the cache kernel whose waits ran out may leave its entries unwritten
+    if (info[i].y > 0 && info[i].x >= 0 && (int64_t)info[i].x + info[i].y <= all_slots) {
+      slots[i] = info[i].y;
+      base[i] += (int64_t)info[i].x * step;
+      most = max(most, slots[i]);
+    }
+  }
 #pragma unroll 2
   for (int s = 0; s < most; ++s) {
     float2 ml[kRows];
@@ -1443,10 +1453,14 @@ static int launch_block_t(const BlockParams& p, cudaStream_t stream) {
     if (cudaLaunchKernelEx(&cfg, block_cache_kernel<D, NR>, p, slots) != cudaSuccess) return KVARN_ERR_CUDA;
   }
   const int64_t rows = (int64_t)p.batch * p.block * p.num_q_heads;
-  cfg.gridDim = dim3((unsigned)((rows + 7) / 8));
   cfg.blockDim = dim3(128);
   cfg.dynamicSmemBytes = 0;
-  return cudaLaunchKernelEx(&cfg, block_merge_kernel<D>, p) == cudaSuccess ? KVARN_OK : KVARN_ERR_CUDA;
+  if (rows <= 4096) {  // 27 warps an SM
+    cfg.gridDim = dim3((unsigned)((rows + 3) / 4));
+    return cudaLaunchKernelEx(&cfg, block_merge_kernel<D, 1>, p) == cudaSuccess ? KVARN_OK : KVARN_ERR_CUDA;
+  }
+  cfg.gridDim = dim3((unsigned)((rows + 7) / 8));
+  return cudaLaunchKernelEx(&cfg, block_merge_kernel<D, 2>, p) == cudaSuccess ? KVARN_OK : KVARN_ERR_CUDA;
 }
 
 int block_tile_rows(int d, int64_t rows, int kb, int vb) {
