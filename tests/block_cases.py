@@ -39,6 +39,7 @@ class Cache:
         self.pk = torch.zeros((len(lens), hkv, 128, d0), dtype=torch.float16)
         self.pv = torch.zeros_like(self.pk)
         self.k, self.v = [], []
+        self.free_page = int(perm[sum(pages)])  # a page that no sequence uses
         at = 0
         for b, n in enumerate(lens):
             if plain:

@@ -138,8 +138,8 @@ def test_window_prefill_then_append_then_decode(kv):
     g = torch.Generator().manual_seed(32)
     q = torch.randn((3, 1, 8, 128), generator=g).half().cuda()
     k, v = (torch.randn((3, 1, 2, 128), generator=g).half().cuda() for _ in range(2))
-    table = torch.cat([cache.table, torch.full((3, 1), cache.n_pool - 1, dtype=torch.int32)], 1).cuda()
-    table[1, 0] = cache.n_pool - 1
+    table = torch.cat([cache.table, torch.full((3, 1), cache.free_page, dtype=torch.int32)], 1).cuda()
+    table[1, 0] = cache.free_page
     a = torch.empty_like(q)
     kv.window_prefill_attention(cache.desc, q, k, v, cache.pool, table, cache.lens_t, a,
                                 kv.alloc_window_prefill_workspace(cache.desc, 3, 8, 1, table.shape[1], 4, 300), 4, 300,
