@@ -523,10 +523,9 @@ __global__ void __launch_bounds__(blk::kThreads, 1) block_cache_kernel(BlockPara
       for (int i = 0; i < cnt; ++i, ++g) {
         const int s = (int)(g & 1);
         // S of the page, and PV of the page before the last, which has read this stage's P
-        if (wq == 0) {
-          wait_qk(part, g);
-          wait_pv(part, g - 2);
-        }
+        // (a poll takes ~150 cycles even when it succeeds, so each is another warp's)
+        if (wq == 0) wait_qk(part, g);
+        if (wq == 1) wait_pv(part, g - 2);
         bar_sync(sbar, 128);
         fence_after();
         const uint32_t ts = tmem + S::kColS + (uint32_t)(s * NR + c0) + lanes;
@@ -725,11 +724,8 @@ __global__ void __launch_bounds__(blk::kThreads, 1) block_cache_kernel(BlockPara
       for (int i = 0; i < cnt; ++i, ++g) {
         const int s = (int)(g & 1);
         // QK of the page before the last has read the codes and B
-        if (warp == kKWarp) {
-          wait(&rec_full[r], rph);
-#pragma unroll
-          for (int m = 0; m < NP; ++m) wait_qk(m, g - 2);
-        }
+        if (warp == kKWarp) wait(&rec_full[r], rph);
+        if (warp > kKWarp && warp <= kKWarp + NP) wait_qk(warp - kKWarp - 1, g - 2);
         bar_sync(kKBar, 256);
         fence_after();
         const uint8_t* R = recs + r * rec;
@@ -865,11 +861,8 @@ __global__ void __launch_bounds__(blk::kThreads, 1) block_cache_kernel(BlockPara
         const int s = (int)(g & 1);
         const int vs = S::kVStages == 2 ? s : 0;
         // PV of the page that last used this buffer
-        if (warp == kVWarp) {
-          wait(&rec_full[r], rph);
-#pragma unroll
-          for (int m = 0; m < NP; ++m) wait_pv(m, g - S::kVStages);
-        }
+        if (warp == kVWarp) wait(&rec_full[r], rph);
+        if (warp > kVWarp && warp <= kVWarp + NP) wait_pv(warp - kVWarp - 1, g - S::kVStages);
         bar_sync(kVBar, 256);
         fence_after();
         const uint8_t* R = recs + r * rec;
