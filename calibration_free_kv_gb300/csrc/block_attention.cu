@@ -1219,40 +1219,51 @@ __global__ void __launch_bounds__(256, D <= 128 ? 2 : 1) block_raw_kernel(BlockP
           mma16816(s[2 * np + 1], a, bk[2], bk[3]);
         }
       }
+      // masks, where some row does not see the whole stage (the bit tests are a third of the
+      // instructions of a stage that needs them)
+      if (!__all_sync(0xffffffffu, (va & vb) == ~0ull)) {
+#pragma unroll
+        for (int nt = 0; nt < NB / 8; ++nt) {
+          const uint32_t ba = (uint32_t)(va >> (8 * nt)) >> (2 * tq), bb = (uint32_t)(vb >> (8 * nt)) >> (2 * tq);
+#pragma unroll
+          for (int e = 0; e < 2; ++e) {
+            if (((ba >> e) & 1u) == 0u) s[nt][e] = -INFINITY;
+            if (((bb >> e) & 1u) == 0u) s[nt][2 + e] = -INFINITY;
+          }
+        }
+      }
       float mxa = -INFINITY, mxb = -INFINITY;
 #pragma unroll
       for (int nt = 0; nt < NB / 8; ++nt) {
-#pragma unroll
-        for (int e = 0; e < 2; ++e) {
-          const int t = 8 * nt + 2 * tq + e;
-          s[nt][e] = ((va >> t) & 1u) ? s[nt][e] * p.qscale : -INFINITY;
-          s[nt][2 + e] = ((vb >> t) & 1u) ? s[nt][2 + e] * p.qscale : -INFINITY;
-          mxa = fmaxf(mxa, s[nt][e]);
-          mxb = fmaxf(mxb, s[nt][2 + e]);
-        }
+        mxa = fmax3(mxa, s[nt][0], s[nt][1]);
+        mxb = fmax3(mxb, s[nt][2], s[nt][3]);
       }
       mxa = fmaxf(mxa, __shfl_xor_sync(0xffffffffu, mxa, 1));
       mxa = fmaxf(mxa, __shfl_xor_sync(0xffffffffu, mxa, 2));
       mxb = fmaxf(mxb, __shfl_xor_sync(0xffffffffu, mxb, 1));
       mxb = fmaxf(mxb, __shfl_xor_sync(0xffffffffu, mxb, 2));
-      const float na = fmaxf(ma, mxa), nb = fmaxf(mb, mxb);
-      const float sa = na == -INFINITY ? 0.0f : na, sb = nb == -INFINITY ? 0.0f : nb;
+      // maxima in the log2 domain; qscale > 0
+      const float na = fmaxf(ma, mxa * p.qscale), nb = fmaxf(mb, mxb * p.qscale);
+      const float sa = na == -INFINITY ? 0.0f : -na, sb = nb == -INFINITY ? 0.0f : -nb;
       const float aa = ma == -INFINITY ? 0.0f : exp2f(ma - na);
       const float ab = mb == -INFINITY ? 0.0f : exp2f(mb - nb);
       ma = na;
       mb = nb;
-      float pa = 0.0f, pb = 0.0f;
+      float2 pa = make_float2(0.0f, 0.0f), pb = pa;
+      const float2 q2 = make_float2(p.qscale, p.qscale), sa2 = make_float2(sa, sa), sb2 = make_float2(sb, sb);
 #pragma unroll
       for (int nt = 0; nt < NB / 8; ++nt) {
-        s[nt][0] = ex2_approx(s[nt][0] - sa);
-        s[nt][1] = ex2_approx(s[nt][1] - sa);
-        s[nt][2] = ex2_approx(s[nt][2] - sb);
-        s[nt][3] = ex2_approx(s[nt][3] - sb);
-        pa += s[nt][0] + s[nt][1];
-        pb += s[nt][2] + s[nt][3];
+        const float2 x = fma2(make_float2(s[nt][0], s[nt][1]), q2, sa2);
+        const float2 y = fma2(make_float2(s[nt][2], s[nt][3]), q2, sb2);
+        s[nt][0] = ex2_approx(x.x);
+        s[nt][1] = ex2_approx(x.y);
+        s[nt][2] = ex2_approx(y.x);
+        s[nt][3] = ex2_approx(y.y);
+        pa = add2(pa, make_float2(s[nt][0], s[nt][1]));
+        pb = add2(pb, make_float2(s[nt][2], s[nt][3]));
       }
-      la = fmaf(la, aa, pa);
-      lb = fmaf(lb, ab, pb);
+      la = fmaf(la, aa, pa.x + pa.y);
+      lb = fmaf(lb, ab, pb.x + pb.y);
       if (__any_sync(0xffffffffu, aa != 1.0f || ab != 1.0f)) {  // some row's maximum moved
 #pragma unroll
         for (int n2 = 0; n2 < NN; ++n2) {
