@@ -13,7 +13,7 @@
 //  block_merge_kernel  joins the partials, undoes the rotation, rounds once to fp16.
 //
 // block_cache_kernel.  The G * block query rows of one (sequence, kv head) are cut into row tiles of
-// NR = 16, 32 or 64 rows.  The (row tile, visible page) pairs lie on a line that is cut into equal
+// NR = 16, 32, 48 or 64 rows.  The (row tile, visible page) pairs lie on a line that is cut into equal
 // ranges, one per CTA and one CTA per SM.  Tokens sit on the MMA's M axis (a page is exactly its
 // 128 rows) and query rows on N, so that the MMA time follows the rows a tile has.  Per page:
 //  QK  S[t][r] = sum_j A_K[t][j] B[j][r]; A_K = the codes in tensor memory as exact fp16 subnormals
@@ -63,7 +63,7 @@ template <int D, int NR>
 struct Shape {
   static constexpr int kSteps = D / 16;           // K steps of QK
   static constexpr int kHalves = D > 128 ? 2 : 1; // 128-channel blocks of PV
-  static constexpr int kParts = NR >= 32 ? 2 : 1; // column parts of the MMAs (N at least 16)
+  static constexpr int kParts = NR % 32 == 0 ? 2 : 1; // column parts of the MMAs (N a multiple of 16)
   static constexpr int kVStages = D > 128 ? 1 : 2;
   static constexpr int kStep = NR * 32;           // bytes of one K step of a B operand
   static constexpr int kBHalf = NR * D * 2;       // q~ s' hi (or lo) of one page
@@ -639,19 +639,20 @@ __global__ void __launch_bounds__(blk::kThreads, 1) block_cache_kernel(BlockPara
         bar_arrive(kPFull + 2 * part + s, kPThreads);
       }
       // the segment's partial: l over the tokens, O once its last PV is done
-      // (a butterfly that halves the rows a lane holds: row lane % NC ends in lane's first value)
-      float v[NC];
+      // (a butterfly that halves the rows a lane holds: row lane ends in lane's first value)
+      constexpr int kPow = NC == 24 ? 32 : NC;
+      float v[kPow];
 #pragma unroll
-      for (int n = 0; n < NC; n += 2) {
-        v[n] = l[n / 2].x;
-        v[n + 1] = l[n / 2].y;
+      for (int n = 0; n < kPow; n += 2) {
+        v[n] = n < NC ? l[n / 2 < NC / 2 ? n / 2 : 0].x : 0.0f;
+        v[n + 1] = n < NC ? l[n / 2 < NC / 2 ? n / 2 : 0].y : 0.0f;
       }
 #pragma unroll
-      for (int m = 16; m >= NC; m >>= 1)
+      for (int m = 16; m >= kPow; m >>= 1)
 #pragma unroll
-        for (int n = 0; n < NC; ++n) v[n] += __shfl_xor_sync(0xffffffffu, v[n], m);
+        for (int n = 0; n < kPow; ++n) v[n] += __shfl_xor_sync(0xffffffffu, v[n], m);
 #pragma unroll
-      for (int m = NC / 2; m > 0; m >>= 1) {
+      for (int m = kPow / 2; m > 0; m >>= 1) {
         const bool up = (lane & m) != 0;
 #pragma unroll
         for (int n = 0; n < m; ++n) {
@@ -700,12 +701,12 @@ __global__ void __launch_bounds__(blk::kThreads, 1) block_cache_kernel(BlockPara
     // 11}): the 16 thread groups of 8 take the D / 8 (kk, kb) pairs and, each warpgroup, half the rows.
     // A thread's q~ stay in registers for the segment.
     constexpr int kPairs = D > 128 ? 2 : 1;
-    constexpr int kRows = D == 64 ? (NR > 16 ? NR / 32 : 1) : NR / 16;
-    const bool builds = !(D == 64 && NR == 16 && grp >= 8);
+    constexpr int kRows = D == 64 ? (NR / 16 + 1) / 2 : NR / 16;
+    auto builds = [&](int e) { return D > 64 || 2 * e + (grp >> 3) < NR / 16; };  // whether row group e is there
     auto pair_of = [&](int c2) { return D == 64 ? (grp & 7) : grp + 16 * c2; };
     auto b_at = [&](int c2, int e) {
       const int oc = pair_of(c2);
-      const int rg = (codes ? 0 : NR / 16) + (D == 64 && NR > 16 ? 2 * e + (grp >> 3) : e);
+      const int rg = (codes ? 0 : NR / 16) + (D == 64 ? 2 * e + (grp >> 3) : e);
       return (oc >> 1) * S::kStep + rg * 256 + (oc & 1) * 128 + nl * 16;
     };
     for (int k = 0; segment(k, kKBar, 256, warp == kKWarp); ++k) {
@@ -718,8 +719,11 @@ __global__ void __launch_bounds__(blk::kThreads, 1) block_cache_kernel(BlockPara
       for (int c2 = 0; c2 < kPairs; ++c2)
 #pragma unroll
         for (int e = 0; e < kRows; ++e) {
-          qh[c2][e] = *reinterpret_cast<const uint4*>(q_hi + b_at(c2, e));
-          ql[c2][e] = *reinterpret_cast<const uint4*>(q_lo + b_at(c2, e));
+          qh[c2][e] = ql[c2][e] = make_uint4(0u, 0u, 0u, 0u);
+          if (builds(e)) {
+            qh[c2][e] = *reinterpret_cast<const uint4*>(q_hi + b_at(c2, e));
+            ql[c2][e] = *reinterpret_cast<const uint4*>(q_lo + b_at(c2, e));
+          }
         }
       for (int i = 0; i < cnt; ++i, ++g) {
         const int s = (int)(g & 1);
@@ -817,27 +821,26 @@ __global__ void __launch_bounds__(blk::kThreads, 1) block_cache_kernel(BlockPara
         }
         if (!codes) rt_s[(g & 3) * kTile + t] = __half2float(reinterpret_cast<const __half*>(R + RL.kfactor)[t]);
         uint8_t* bs = sm + S::kBOff + s * 2 * S::kBHalf;
-        if (builds) {
 #pragma unroll
-          for (int c2 = 0; c2 < kPairs; ++c2) {
-            const int oc = pair_of(c2), cb = 16 * (oc >> 1) + 4 * (oc & 1);
-            const uint2 sa = *reinterpret_cast<const uint2*>(R + RL.kscale + 2 * cb);
-            const uint2 sb = *reinterpret_cast<const uint2*>(R + RL.kscale + 2 * (cb + 8));
-            const __half2 sv[4] = {u2h2(sa.x), u2h2(sb.x), u2h2(sa.y), u2h2(sb.y)};
+        for (int c2 = 0; c2 < kPairs; ++c2) {
+          const int oc = pair_of(c2), cb = 16 * (oc >> 1) + 4 * (oc & 1);
+          const uint2 sa = *reinterpret_cast<const uint2*>(R + RL.kscale + 2 * cb);
+          const uint2 sb = *reinterpret_cast<const uint2*>(R + RL.kscale + 2 * (cb + 8));
+          const __half2 sv[4] = {u2h2(sa.x), u2h2(sb.x), u2h2(sa.y), u2h2(sb.y)};
 #pragma unroll
-            for (int e = 0; e < kRows; ++e) {
-              const __half2 h4[4] = {u2h2(qh[c2][e].x), u2h2(qh[c2][e].y), u2h2(qh[c2][e].z), u2h2(qh[c2][e].w)};
-              const __half2 l4[4] = {u2h2(ql[c2][e].x), u2h2(ql[c2][e].y), u2h2(ql[c2][e].z), u2h2(ql[c2][e].w)};
-              uint32_t hi[4], lo[4];
+          for (int e = 0; e < kRows; ++e) {
+            if (!builds(e)) continue;
+            const __half2 h4[4] = {u2h2(qh[c2][e].x), u2h2(qh[c2][e].y), u2h2(qh[c2][e].z), u2h2(qh[c2][e].w)};
+            const __half2 l4[4] = {u2h2(ql[c2][e].x), u2h2(ql[c2][e].y), u2h2(ql[c2][e].z), u2h2(ql[c2][e].w)};
+            uint32_t hi[4], lo[4];
 #pragma unroll
-              for (int j = 0; j < 4; ++j) {
-                const __half2 hv = __hmul2(h4[j], sv[j]);
-                hi[j] = h2u(hv);
-                lo[j] = h2u(__hfma2(l4[j], sv[j], __hfma2(h4[j], sv[j], __hneg2(hv))));
-              }
-              *reinterpret_cast<uint4*>(bs + b_at(c2, e)) = make_uint4(hi[0], hi[1], hi[2], hi[3]);
-              *reinterpret_cast<uint4*>(bs + S::kBHalf + b_at(c2, e)) = make_uint4(lo[0], lo[1], lo[2], lo[3]);
+            for (int j = 0; j < 4; ++j) {
+              const __half2 hv = __hmul2(h4[j], sv[j]);
+              hi[j] = h2u(hv);
+              lo[j] = h2u(__hfma2(l4[j], sv[j], __hfma2(h4[j], sv[j], __hneg2(hv))));
             }
+            *reinterpret_cast<uint4*>(bs + b_at(c2, e)) = make_uint4(hi[0], hi[1], hi[2], hi[3]);
+            *reinterpret_cast<uint4*>(bs + S::kBHalf + b_at(c2, e)) = make_uint4(lo[0], lo[1], lo[2], lo[3]);
           }
         }
         __syncwarp();
@@ -1467,21 +1470,25 @@ static int launch_block_t(const BlockParams& p, cudaStream_t stream) {
   return cudaLaunchKernelEx(&cfg, block_merge_kernel<D, 2>, p) == cudaSuccess ? KVARN_OK : KVARN_ERR_CUDA;
 }
 
+// The least tile that holds the rows, or 64 rows a tile: QK, PV, the softmax and B follow the rows of
+// a tile, the K and V conversion does not.  Tiles of 48 rows against tiles of 64: 40 rows of 32
+// sequences over 8k, head_dim 128, 186 -> 168 us; 33 rows of 8 sequences, head_dim 64, 42.5 -> 37.7 us.
+// head_dim 256 has tensor memory for 32 rows, and with 12 bits a code pair shared memory for 16.
 int block_tile_rows(int d, int64_t rows, int kb, int vb) {
-  // head_dim 256 with 12 bits a code pair: two page records fit beside 16 rows only
-  if (rows <= 16 || (d > 128 && kb + vb > 8)) return 16;
-  if (rows <= 32 || d > 128) return 32;
-  return 64;
+  const int most = d <= 128 ? 64 : (kb + vb > 8 ? 16 : 32);
+  return rows < most ? (int)((rows + 15) / 16 * 16) : most;
 }
 
 int launch_block_attention(int d, const BlockParams& p, cudaStream_t stream) {
   if (d == 64) {
     if (p.tile_rows == 16) return launch_block_t<64, 16>(p, stream);
     if (p.tile_rows == 32) return launch_block_t<64, 32>(p, stream);
+    if (p.tile_rows == 48) return launch_block_t<64, 48>(p, stream);
     if (p.tile_rows == 64) return launch_block_t<64, 64>(p, stream);
   } else if (d == 128) {
     if (p.tile_rows == 16) return launch_block_t<128, 16>(p, stream);
     if (p.tile_rows == 32) return launch_block_t<128, 32>(p, stream);
+    if (p.tile_rows == 48) return launch_block_t<128, 48>(p, stream);
     if (p.tile_rows == 64) return launch_block_t<128, 64>(p, stream);
   } else if (d == 256) {
     if (p.tile_rows == 16) return launch_block_t<256, 16>(p, stream);

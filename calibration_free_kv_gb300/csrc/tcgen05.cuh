@@ -101,10 +101,15 @@ __device__ __forceinline__ void wait_ld_x32(float* f) {
 }
 template <int N>
 __device__ __forceinline__ void ld_cols(uint32_t taddr, float (&f)[N]) {
-  static_assert(N == 8 || N == 16 || N == 32, "8, 16 or 32 columns");
+  static_assert(N == 8 || N == 16 || N == 24 || N == 32, "8, 16, 24 or 32 columns");
   if constexpr (N == 8) {
     ld_32x32b_x8_async(taddr, f);
     wait_ld_x8(f);
+  } else if constexpr (N == 24) {
+    ld_32x32b_x16_async(taddr, f);
+    ld_32x32b_x8_async(taddr + 16, f + 16);
+    wait_ld_x16(f);
+    wait_ld_x8(f + 16);
   } else if constexpr (N == 16) {
     ld_32x32b_x16_async(taddr, f);
     wait_ld_x16(f);

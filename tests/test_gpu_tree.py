@@ -67,6 +67,13 @@ def test_tree_parity(kv, nodes, group, d0):
     print("tree nodes=%d G=%d d0=%d: max scaled error %.2e" % (nodes, group, d0, err))
 
 
+@pytest.mark.parametrize("nodes,group,d0", [(33, 1, 128), (10, 4, 128), (12, 4, 80), (17, 2, 64), (11, 4, 64), (47, 1, 64)])
+def test_tree_tiles_of_48_rows(kv, nodes, group, d0):
+    # 33 to 48 rows: their last row group full, ragged and a single row
+    err = _check(kv, [0, 77, 128, 1000, 4096 + 5], nodes, 2, group, d0, seed=nodes + group + d0)
+    print("tree nodes=%d G=%d d0=%d: max scaled error %.2e" % (nodes, group, d0, err))
+
+
 @pytest.mark.parametrize("preset", ["kvarn_k4v4_g128", "kvarn_k2v2_g128", "kvarn_k8v4_g128"])
 @pytest.mark.parametrize("d0", [64, 128, 256])
 def test_tree_presets(kv, preset, d0):
