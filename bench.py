@@ -56,11 +56,11 @@ def _peaks():
 
 # DRAM traffic / algorithmic bytes of one decode_kernel launch, from an ncu capture
 # (dram__bytes_read.sum + dram__bytes_write.sum at batch 24), valid only for the sources it was
-# taken on (decode.cu and decode_util.cuh, which holds the page partition): the traffic is
-# reported as null once either changes.
-DECODE_TRAFFIC = {"sources_sha256": "254ea2120da7c12ce795533a3645deee08d4b37d5c670276bcc800834b4d1815",
-                  "dram_over_algorithmic": 1.0235}
-DECODE_SOURCES = ("decode.cu", "decode_util.cuh")
+# taken on (decode_kernel.cuh, decode.cu and decode_util.cuh, which holds the page partition): the
+# traffic is reported as null once one of them changes.
+DECODE_TRAFFIC = {"sources_sha256": "594813e49d33e543ba2e867955d85ed2eac5f1f3e36af7bf9922c2cecc55972d",
+                  "dram_over_algorithmic": 1.0251}
+DECODE_SOURCES = ("decode_kernel.cuh", "decode.cu", "decode_util.cuh")
 
 
 def _decode_sources_digest():
@@ -941,8 +941,9 @@ def _run_kvarn(args, torch, world, rank):
             "traffic": (None if _decode_traffic_ratio() is None
                         else _decode_traffic_ratio() * statistics.mean(dec_bytes)),
             "traffic_source": "ncu dram__bytes_read+write of one decode_kernel launch at batch 24 "
-                              "(DECODE_TRAFFIC), scaled by algorithmic bytes; null when decode.cu "
-                              "or decode_util.cuh changed since that capture",
+                              "(DECODE_TRAFFIC), scaled by algorithmic bytes; null when "
+                              "decode_kernel.cuh, decode.cu or decode_util.cuh changed since that "
+                              "capture",
             "algorithmic_bytes_per_launch": statistics.mean(dec_bytes),
             "duration_source": "CUDA events on the launching stream around decode_kernel (the "
                                "decode call as kvarn_decode_partials + kvarn_decode_combine, an "

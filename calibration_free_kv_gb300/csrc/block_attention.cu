@@ -22,12 +22,17 @@
 //      one fp16 rounding of q~ s' (2^-11 relative) would move them by 0.1;
 //  PV  O[c][r] += sum_t A_V[c][t] P[t][r]; A_V = V~ rounded twice to fp16 (once per product),
 //      P = exp2 rounded once to fp16.  Both roundings move the output like its own fp16 rounding.
-// Softmax: a thread owns a token and all NR rows; each row's reference maximum is kept from page to
-// page and moved only when a logit passes it by 2^8 (then O and l are rescaled), so no maximum is
-// exchanged on the usual page; P stays below 2^8 and l is fp32.
-// Warps: 0-3 softmax (and the rescale and the row tile's partial at its end), 4-7 K codes and B and
-// q~ . z', 8-11 V, 12 page records (1-D bulk copies into a ring), 13 / 14 QK of even / odd pages,
-// 15 PV.  Operand and score buffers are double; every hand-off is an mbarrier, every wait bounded.
+// Softmax: a thread owns a token and half the rows of the tile; each row's reference maximum is kept
+// from page to page and moved only when a logit passes it by 2^8 (then O and l are rescaled), so no
+// maximum is exchanged on the usual page; P stays below 2^8 and l is fp32.
+// Warps: 0-7 softmax (two warpgroups, one per row half: also the rescale and the row tile's partial at
+// its end), 8-11 K codes, 12-15 q~ . z' (both groups: half of B each), 16-23 V, 24 page records (1-D
+// bulk copies into a ring), 25-26 QK and 27-28 PV (one warp per column part), 29-31 the walk and q~ of
+// the next segment.  Operand and score buffers are double; every wait on an mbarrier is bounded.
+// What bounds it: the conversion of codes and the softmax on the ordinary pipes, not memory and not the
+// tensor cores.  With 64 rows, head_dim 128 and K4V2 a page takes about 1.27 us a SM (2500 cycles, 6650
+// instructions; on 16 trees of 26 nodes issue slots 62 % used, shared memory's data pipe 52 %, tensor
+// pipe 31 %, DRAM 14 %), a segment about 10 us on top: 16 trees of 64 rows over 16k 622 us, a 2 x 2048-token windowed chunk 693 us of this kernel.
 #include "common.cuh"
 #include "decode_util.cuh"
 #include "params.cuh"
@@ -54,7 +59,8 @@ constexpr int kSegs = 16;
 //   kKBar, kVBar the K and V warps; per stage kOpsK (K warps -> QK), kSFree (softmax -> QK),
 //   kOpsV (V warps -> PV); kPFull + 2 part + stage (softmax -> PV).
 constexpr int kQueryBar = 1, kSmBar = 2, kKBar = 4, kVBar = 5, kOpsK = 6, kSFree = 8, kOpsV = 10, kPFull = 12;
-// Units of the line ahead of a row tile's pages for a segment's fixed work, and the smallest range.
+// Units of the line ahead of a row tile's pages for a segment's fixed work, and the smallest range
+// (5, 8 and 14 units took no less time than 3).
 constexpr int kFixUnits = 3, kMinUnits = 3;
 constexpr float kSlack = 8.0f;  // log2 units a logit may pass its row's reference by
 constexpr int kSmemMax = 232448 - 1536;  // the rest is for the static part
@@ -1067,7 +1073,10 @@ __global__ void __launch_bounds__(blk::kThreads, 1) block_cache_kernel(BlockPara
 // softmax in the log2 domain; PV with the probabilities rounded once to fp16 (they move the output
 // like its own rounding).  A row that sees nothing leaves m = -inf, l = 0, o = 0.  The queries stay in
 // shared memory so that two CTAs (16 warps) fit an SM at head_dim 64 and 128: with them in registers,
-// one CTA an SM and fp16 hi + lo probabilities a 2 x 2048-token chunk took 482 us.
+// one CTA an SM and fp16 hi + lo probabilities a 2 x 2048-token chunk took 482 us.  Masks are looked at
+// only in stages that some row of the warp does not see whole: that chunk 386 -> 332 us; latency
+// bounds it (8 x 256 tokens: issue slots 38 % used, tensor pipe 28 %, 16 warps an SM).  32 rows a
+// warp took longer (395 against 386 us, before that step).
 template <int D>
 __global__ void __launch_bounds__(256, D <= 128 ? 2 : 1) block_raw_kernel(BlockParams p) {
   constexpr int NB = 64;      // tokens per stage

@@ -241,6 +241,8 @@ int kvarn_prefill_attention(const kvarn_desc* desc, int batch, int num_q_heads, 
  * of the call sees are never looked up: their block-table entries may hold anything (the pages
  * may have been given to another sequence), as long as the entries of visible pages hold.
  * sink_tokens >= 0 and window >= 1 (else INVALID_ARG); either may exceed the sequence.
+ * A page or a block of raw tokens that some query sees in part is read whole: the values in it have
+ * to be finite, also those of tokens a query does not see (a weight of 0 times infinity is NaN).
  * max_pages up to 2^23 (else UNSUPPORTED). */
 
 /* Workspace bytes of kvarn_window_decode_attention (host only; 0 if invalid).  It does not grow
@@ -292,7 +294,8 @@ size_t kvarn_tree_workspace_bytes(const kvarn_desc* desc, int batch, int num_q_h
  *  tree_lens    device int32 [batch] or NULL (all tree_len): nodes of each sequence, 0..tree_len
  *               (else clamped, KVARN_DEV_SEQ_TOO_LONG).  Rows of absent nodes are not used, and
  *               those of out stay as they were.
- *  A node that sees nothing (no cached token, an empty mask row) gives zeros.
+ *  A node that sees nothing (no cached token, an empty mask row) gives zeros.  The values of present
+ *  nodes have to be finite, also for the rows that do not see them (0 times infinity is NaN).
  *  Other arguments as kvarn_prefill_attention; limits as kvarn_window_prefill_attention. */
 int kvarn_tree_attention(const kvarn_desc* desc, int batch, int num_q_heads, int tree_len,
                          const void* q, const void* tree_k, const void* tree_v,
