@@ -21,7 +21,10 @@
 //      accumulator).  hi + lo because keys with outlier channels give logits in the hundreds, and
 //      one fp16 rounding of q~ s' (2^-11 relative) would move them by 0.1;
 //  PV  O[c][r] += sum_t A_V[c][t] P[t][r]; A_V = V~ rounded twice to fp16 (once per product),
-//      P = exp2 rounded once to fp16.  Both roundings move the output like its own fp16 rounding.
+//      P = exp2 rounded once to fp16.  These roundings cost precision: against 64 bits the output is
+//      off by 3.3e-4 to 3.8e-4 (relative 2-norm), by 2.1e-4 where only it is rounded.  Without either
+//      V~'s second rounding or P's it would still be near 3e-4, and going without both takes fp32
+//      conversions and a second PV pass on the pipes that bound this kernel.
 // Softmax: a thread owns a token and half the rows of the tile; each row's reference maximum is kept
 // from page to page and moved only when a logit passes it by 2^8 (then O and l are rescaled), so no
 // maximum is exchanged on the usual page; P stays below 2^8 and l is fp32.
@@ -32,7 +35,7 @@
 // What bounds it: the conversion of codes and the softmax on the ordinary pipes, not memory and not the
 // tensor cores.  With 64 rows, head_dim 128 and K4V2 a page takes about 1.27 us a SM (2500 cycles, 6650
 // instructions; on 16 trees of 26 nodes issue slots 62 % used, shared memory's data pipe 52 %, tensor
-// pipe 31 %, DRAM 14 %), a segment about 10 us on top: 16 trees of 64 rows over 16k 622 us, a 2 x 2048-token windowed chunk 693 us of this kernel.
+// pipe 31 %, DRAM 14 %), a segment about 10 us on top: 16 trees of 64 nodes over 16k 622 us, a 2 x 2048-token windowed chunk 693 us of this kernel.
 #include "common.cuh"
 #include "decode_util.cuh"
 #include "params.cuh"
