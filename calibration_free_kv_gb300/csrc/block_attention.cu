@@ -39,6 +39,7 @@
 #include "common.cuh"
 #include "decode_util.cuh"
 #include "params.cuh"
+#include "role_waits.h"
 #include "tcgen05.cuh"
 
 namespace kvarn {
@@ -327,6 +328,7 @@ __global__ void __launch_bounds__(blk::kThreads, 1) block_cache_kernel(BlockPara
   __shared__ uint32_t tslot;
   __shared__ int abort_flag;
   __shared__ int issued_s[4];  // pages whose QK (parts 0, 1) and PV (parts 0, 1) are issued
+  __shared__ __align__(8) uint64_t drained_s[4];  // every MMA of an issuing warp has completed
   const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
   const RecordLayout RL = record_layout(D, p.kb, p.vb);
   const int rec = RL.bytes;
@@ -370,6 +372,7 @@ __global__ void __launch_bounds__(blk::kThreads, 1) block_cache_kernel(BlockPara
     }
     for (int s = 0; s < kSegs; ++s) mbar_init(&seg_full[s], 3);
     for (int s = 0; s < 2; ++s) mbar_init(&q_empty[s], 1);
+    for (int i = 0; i < 4; ++i) mbar_init(&drained_s[i], 1);
     abort_flag = 0;
     for (int i = 0; i < 4; ++i) issued_s[i] = 0;
     fence_mbar_init();
@@ -954,6 +957,7 @@ __global__ void __launch_bounds__(blk::kThreads, 1) block_cache_kernel(BlockPara
     if (warp == kLoadWarp) {
       // ---- page records -> the ring ----
       if (lane == 0) {
+        CopyRing ring(slots);
         for (int k = 0;; ++k) {
           wait_segment(k);
           const TileWalk& w = seg(k);
@@ -962,23 +966,24 @@ __global__ void __launch_bounds__(blk::kThreads, 1) block_cache_kernel(BlockPara
           const int32_t* bt = p.block_table + (int64_t)w.b * p.max_pages;
           const uint8_t* src = p.pool + (int64_t)w.h * rec;
           if (cnt == 0) break;
-          for (int i = j; i < j + cnt; ++i, ++g) {
+          for (int i = j; i < j + cnt; ++i) {
             int64_t id = bt[i < sinks ? i : i + skip];
             if (id < 0 || id >= p.num_pool_pages) {
               flag_error(p.status, KVARN_DEV_BAD_PAGE_ID);
               id = 0;
             }
-            wait(&rec_empty[r], rph ^ 1u);
+            uint64_t* full = &rec_full[ring.slot];
+            wait(&rec_empty[ring.slot], ring.phase ^ 1u);
             if (*abort_v != 0) continue;  // nobody waits for the copies any more
             fence_proxy_async_smem();
-            mbar_expect_tx(&rec_full[r], (uint32_t)rec);
-            bulk_copy_g2s(recs + r * rec, src + id * p.num_kv_heads * (int64_t)rec, (uint32_t)rec, &rec_full[r]);
-            next_record();
+            mbar_expect_tx(full, (uint32_t)rec);
+            bulk_copy_g2s(recs + ring.slot * rec, src + id * p.num_kv_heads * (int64_t)rec, (uint32_t)rec, full);
+            ring.next();
           }
         }
-        // copies still in flight land before the CTA may leave
-        for (int k = g > slots ? g - slots : 0; k < g; ++k)
-          wait(&rec_full[k % slots], (uint32_t)((k / slots) & 1));
+        // The copies still in flight land before the CTA may leave, whatever has run out elsewhere:
+        // these waits do not look at the abort flag.
+        if (!ring.drain([&](int slot, uint32_t parity) { return mbar_wait(&rec_full[slot], parity); })) *abort_v = 1;
       }
       __syncwarp();
     } else if (warp >= kQueryWarp) {
@@ -1047,9 +1052,15 @@ __global__ void __launch_bounds__(blk::kThreads, 1) block_cache_kernel(BlockPara
         }
       }
       if (g > 0) {
-        // the last MMAs have completed; the arrivals for pages that do not follow are taken
-        if (is_pv) wait_pv(part, g - 1);
-        else wait_qk(part, g - 1);
+        // The MMAs have completed before tensor memory is given back: one more commit arrives once
+        // all of this thread's have, and the wait does not look at the abort flag (after an abort
+        // the pages' own barriers say only what was issued).  The arrivals for pages that do not
+        // follow are taken.
+        uint64_t* drained = &drained_s[(is_pv ? 2 : 0) + part];
+        if (elect_one()) mma_commit(drained);
+        __syncwarp();
+        if (!mbar_wait(drained, 0)) *abort_v = 1;
+        __syncwarp();
         if (!is_pv)
           for (int i = g > 1 ? g - 2 : 0; i < g; ++i) bar_sync(kSFree + (i & 1), kOpsThreads);
       }
