@@ -327,6 +327,7 @@ __global__ void __launch_bounds__(blk::kThreads, 1) block_cache_kernel(BlockPara
   __shared__ Partition part_s;
   __shared__ uint32_t tslot;
   __shared__ int abort_flag;
+  __shared__ uint32_t gate_s;  // segments published, and kGateClosed (role_waits.h)
   __shared__ int issued_s[4];  // pages whose QK (parts 0, 1) and PV (parts 0, 1) are issued
   __shared__ __align__(8) uint64_t drained_s[4];  // every MMA of an issuing warp has completed
   const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
@@ -370,10 +371,11 @@ __global__ void __launch_bounds__(blk::kThreads, 1) block_cache_kernel(BlockPara
       mbar_init(&qk_full[s], 2);
       mbar_init(&pv_done[s], 1);
     }
-    for (int s = 0; s < kSegs; ++s) mbar_init(&seg_full[s], 3);
+    for (int s = 0; s < kSegs; ++s) mbar_init(&seg_full[s], 1);
     for (int s = 0; s < 2; ++s) mbar_init(&q_empty[s], 1);
     for (int i = 0; i < 4; ++i) mbar_init(&drained_s[i], 1);
     abort_flag = 0;
+    gate_s = 1;  // segment 0 is staged below, by all warps
     for (int i = 0; i < 4; ++i) issued_s[i] = 0;
     fence_mbar_init();
   }
@@ -398,18 +400,27 @@ __global__ void __launch_bounds__(blk::kThreads, 1) block_cache_kernel(BlockPara
   };
   // Segments pass through a ring (their q~ through two buffers): the query warps write segment k + 1
   // while the others work on segment k.  These waits do not look at the abort flag: the query warps
-  // and the roles keep going after it is set.
+  // and the roles keep going after it is set, for as long as pages are issued.
   auto seg = [&](int k) -> const TileWalk& { return seg_s[k & (kSegs - 1)]; };
-  auto wait_segment = [&](int k) {
-    uint64_t* bar = &seg_full[k & (kSegs - 1)];
-    for (uint32_t n = 0; n < (1u << 26) && !mbar_try_wait(bar, (uint32_t)(k / kSegs) & 1u); ++n) {
-    }
+  auto wait_handoff = [&](uint64_t* bar, uint32_t parity) -> bool {
+    return wait_progress([&] { return mbar_try_wait(bar, parity); }, [&] { return issued[0]; }, global_timer_ns);
   };
-  // Segment k for a group of warps that meets at barrier `id`; false past the end of the range.
+  auto wait_segment = [&](int k) {
+    if (wait_handoff(&seg_full[k & (kSegs - 1)], (uint32_t)(k / kSegs) & 1u)) return;
+    *abort_v = 1;
+    atomicOr(&gate_s, kGateClosed);
+    __threadfence_block();
+  };
+  // Segment k, once waited for, is there: false past the end of the range, and for every role alike
+  // past the segments published when some role gave up waiting.
+  auto there = [&](int k) -> bool {
+    return gate_open(*const_cast<volatile uint32_t*>(&gate_s), k) && seg(k).left > 0;
+  };
+  // Segment k for a group of warps that meets at barrier `id`.
   auto segment = [&](int k, int id, int threads, bool leader) -> bool {
     if (leader) wait_segment(k);
     bar_sync(id, threads);
-    return seg(k).left > 0;
+    return there(k);
   };
   // q~ of segment k, hi + lo, in the order and layout of the QK operand: passes n0, n0 + step, .. of
   // 512 / D rows.  A lane takes one 16-channel block of a row (four butterfly stages within the lane,
@@ -961,7 +972,7 @@ __global__ void __launch_bounds__(blk::kThreads, 1) block_cache_kernel(BlockPara
         for (int k = 0;; ++k) {
           wait_segment(k);
           const TileWalk& w = seg(k);
-          const int cnt = w.left > 0 ? w.count() : 0;
+          const int cnt = there(k) ? w.count() : 0;
           const int j = w.j, sinks = w.span.sinks, skip = w.span.first - w.span.sinks;
           const int32_t* bt = p.block_table + (int64_t)w.b * p.max_pages;
           const uint8_t* src = p.pool + (int64_t)w.h * rec;
@@ -988,22 +999,41 @@ __global__ void __launch_bounds__(blk::kThreads, 1) block_cache_kernel(BlockPara
       __syncwarp();
     } else if (warp >= kQueryWarp) {
       // ---- the segments' walk and queries, one segment ahead of the roles ----
-      if (lane == 0) mbar_arrive(&seg_full[0]);  // staged above
-      if (warp == kQueryWarp && lane == 0) note_slots(seg(0));
+      const bool lead = warp == kQueryWarp;
+      if (lead && lane == 0) {
+        mbar_arrive(&seg_full[0]);  // staged above
+        note_slots(seg(0));
+      }
+      bool open = true;  // the segments so far were published before any role gave up
       for (int k = 1; seg(k - 1).left > 0; ++k) {
-        if (warp == kQueryWarp && lane == 0) {
-          TileWalk w = seg(k - 1);
-          w.next(p, part_s.fix);
-          seg_s[k & (kSegs - 1)] = w;
-          note_slots(w);
-        }
-        for (uint32_t n = 0; k > 1 && n < (1u << 26) && !mbar_try_wait(&q_empty[k & 1], (uint32_t)((k - 2) >> 1) & 1u);
-             ++n) {
+        if (lead) {
+          TileWalk& w = seg_s[k & (kSegs - 1)];
+          if (lane == 0) {
+            w = seg(k - 1);
+            w.next(p, part_s.fix);
+          }
+          // the K warps are done with the queries of the segment before the last
+          const bool free_q = k < 2 || wait_handoff(&q_empty[k & 1], (uint32_t)((k - 2) >> 1) & 1u);
+          open = __all_sync(0xffffffffu, free_q) && open;
+          if (!open) *abort_v = 1;
+          if (lane == 0) {
+            if (!open) w.left = 0;  // the last segment
+            note_slots(w);
+          }
+          __syncwarp();
         }
         bar_sync(kQueryBar, 96);
         if (seg(k).left > 0) stage_queries(k, warp - kQueryWarp, 3);
-        __syncwarp();
-        if (lane == 0) mbar_arrive(&seg_full[k & (kSegs - 1)]);
+        bar_sync(kQueryBar, 96);
+        if (lead) {
+          int published = 1;
+          if (lane == 0) {
+            __threadfence_block();
+            published = gate_publish([&](uint32_t was, uint32_t is) { return atomicCAS(&gate_s, was, is); }, k);
+            mbar_arrive(&seg_full[k & (kSegs - 1)]);
+          }
+          open = __shfl_sync(0xffffffffu, published, 0) != 0 && open;
+        }
       }
     } else if (warp - (warp >= kPvWarp ? kPvWarp : kQkWarp) < NP) {
       // ---- MMA issue: QK and PV, a warp for each row half ----
@@ -1011,7 +1041,7 @@ __global__ void __launch_bounds__(blk::kThreads, 1) block_cache_kernel(BlockPara
       const int part = is_pv ? warp - kPvWarp : warp - kQkWarp;
       for (int k = 0;; ++k) {
         wait_segment(k);
-        const int cnt = seg(k).left > 0 ? seg(k).count() : 0;
+        const int cnt = there(k) ? seg(k).count() : 0;
         if (cnt == 0) break;
         for (int i = 0; i < cnt; ++i, ++g) {
           const int s = g & 1;

@@ -37,5 +37,43 @@ struct CopyRing {
   }
 };
 
+// A wait for work that may rightly last as long as a segment: it gives up, and returns false, once
+// progress() (pages issued) has not moved for kNoProgressNs.
+constexpr uint64_t kNoProgressNs = 4000000000ull;
+template <class Poll, class Progress, class Now>
+KVARN_ROLE bool wait_progress(Poll poll, Progress progress, Now now) {
+  if (poll()) return true;
+  int seen = progress();
+  uint64_t t0 = now();
+  for (uint32_t n = 1; n != 0; ++n) {
+    if (poll()) return true;
+    if ((n & 255u) != 0) continue;
+    const int at = progress();
+    const uint64_t t = now();
+    if (at != seen) {
+      seen = at;
+      t0 = t;
+    } else if (t - t0 >= kNoProgressNs) {
+      return false;
+    }
+  }
+  return false;
+}
+
+// The query warps publish segments 0, 1, .. and every role takes them in order.  A role that gave up
+// waiting must not end alone: the others meet it at named barriers, which nothing bounds.  So the
+// number of published segments and the end are one word: publishing takes it from k to k + 1 in one
+// step, a role that gives up sets kGateClosed, which freezes the number, and every role ends after
+// the same segments, whichever of the two came first.
+constexpr uint32_t kGateClosed = 1u << 31;
+template <class Cas>
+KVARN_ROLE bool gate_publish(Cas cas, int k) {  // cas(expected, desired) returns the value before
+  return cas((uint32_t)k, (uint32_t)k + 1u) == (uint32_t)k;
+}
+// Whether segment k is there for a role that has waited for it (or given up and closed the gate).
+KVARN_ROLE bool gate_open(uint32_t gate, int k) {
+  return (gate & kGateClosed) == 0u || (gate & ~kGateClosed) > (uint32_t)k;
+}
+
 }  // namespace blk
 }  // namespace kvarn

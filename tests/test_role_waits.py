@@ -80,3 +80,76 @@ int main() {
 }
 """)
     assert lines == ["1 4"] + ["0 4"] * 4
+
+
+def test_roles_end_after_the_same_segments(tmp_path):
+    # a publisher and four roles in any order of steps; at each step a role whose segment is not there
+    # may give up.  No role takes a segment that was not published, and all end at the same one.
+    lines = _run(tmp_path, r"""
+#include <random>
+int main() {
+  std::mt19937 rng(1);
+  int early = 0, whole = 0;
+  for (int trial = 0; trial < 20000; ++trial) {
+    uint32_t gate = 1;              // segment 0 is published from the start
+    const int segments = 1 + rng() % 6;
+    const int impatience = 2 + rng() % 60;
+    int next = 1, at[4] = {}, ended[4] = {};
+    bool closed_seen = false;
+    auto cas = [&](uint32_t was, uint32_t is) {
+      const uint32_t old = gate;
+      if (old == was) gate = is;
+      return old;
+    };
+    std::vector<char> left(64, 0);  // whether the segment has pages: what a publisher writes first
+    left[0] = 1;
+    int published = 1;
+    for (int step = 0; step < 4000; ++step) {
+      const int who = rng() % 5;
+      if (who == 4) {  // publishes the segments, then the end; a closed gate ends it too
+        if (next <= segments && !closed_seen) {
+          left[next] = next < segments;
+          if (gate_publish(cas, next)) published = next + 1;
+          else closed_seen = true;
+          ++next;
+        }
+        continue;
+      }
+      if (ended[who]) continue;
+      const int k = at[who];
+      const bool complete = published > k;
+      if (!complete && rng() % impatience != 0) continue;
+      if (!complete) gate |= kGateClosed;
+      if (gate_open(gate, k) && !complete) return 1;  // would take what is not there
+      if (gate_open(gate, k) && left[k]) at[who] = k + 1;
+      else ended[who] = 1;
+    }
+    for (int r = 0; r < 4; ++r)
+      if (!ended[r] || at[r] != at[0]) return 2;
+    at[0] < segments ? ++early : ++whole;
+  }
+  printf("%d %d\n", early > 1000, whole > 1000);
+}
+""")
+    assert lines == ["1 1"]
+
+
+def test_a_wait_for_a_long_segment_lasts_while_pages_are_issued(tmp_path):
+    # made-up time, 1 ms a look at the clock: pages issued every 3 s keep a wait of 60 s alive, none
+    # for 4 s ends it
+    lines = _run(tmp_path, r"""
+int main() {
+  for (int every : {3, 5}) {
+    uint64_t t = 0;
+    long polls = 0;
+    const bool done = wait_progress([&] { ++polls; return t >= 60000000000ull; },
+                                    [&] { return (int)(t / (every * 1000000000ull)); },
+                                    [&] { return t += 1000000; });
+    printf("%d %llu\n", (int)done, (unsigned long long)(t / 1000000000ull));
+  }
+  int looks = 0;
+  printf("%d\n", (int)wait_progress([] { return true; }, [&] { return ++looks; }, [&] { return (uint64_t)++looks; }));
+  printf("%d\n", looks);
+}
+""")
+    assert lines == ["1 60", "0 4", "1", "0"]
