@@ -128,21 +128,12 @@ __device__ __forceinline__ bool bar_any(int id, int threads, bool flag) {
   return out != 0;
 }
 
-// Bounded wait (2^25 polls, about a second) on an mbarrier.  When one runs out, *abort_flag is set and the
-// role goes on all the same: every role runs through all its pages, so that no named barrier is left
-// waiting, and the call's results are flagged.  From then on a wait ends once the MMA warp it waits
-// for has issued page `need` - 1 (*issued >= need; null: at once), which keeps the roles within two
-// pages of each other as the completed MMAs would.
+// Bounded wait (2^25 polls, about a second) on an mbarrier, for page `need` - 1 of the MMA warp whose
+// count of issued pages is *issued (null: none, as for copies); see wait_page.
 __device__ __forceinline__ void wait_one(uint64_t* bar, uint32_t parity, volatile int* abort_flag,
                                          const volatile int* issued, int need) {
-  for (uint32_t n = 0; n < (1u << 26); ++n) {
-    if (mbar_try_wait(bar, parity)) return;
-    if ((n & 255u) == 255u) {
-      if (n >= (1u << 25)) *abort_flag = 1;
-      if (*abort_flag != 0 && (issued == nullptr || *issued >= need)) return;
-    }
-  }
-  *abort_flag = 1;
+  wait_page([&] { return mbar_try_wait(bar, parity); }, [&] { return issued == nullptr || *issued >= need; },
+            [&] { return *abort_flag != 0; }, [&] { *abort_flag = 1; });
 }
 // One lane of a converged warp.  MMAs are issued under it: the compiler then knows that a single
 // thread runs them and keeps their operands in uniform registers.

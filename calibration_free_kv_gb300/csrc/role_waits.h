@@ -37,6 +37,27 @@ struct CopyRing {
   }
 };
 
+// A wait for a page's copy or MMAs.  poll() asks the barrier; issued() says whether the MMA warp it
+// waits for has issued the page (true where no MMA is waited for).  The barrier alone is not enough:
+// a completion that never came leaves its phase behind, and a phase one behind reads as complete for
+// a page that is not issued yet.  The role would run ahead and arrive twice at a named barrier that
+// its partner has not passed.  When the wait runs out, abort() is called and the role goes on all the
+// same: every role runs through all its pages, so that no named barrier is left waiting, and the
+// call's results are flagged.  From then on a wait ends once the page is issued, which keeps the
+// roles within two pages of each other as the completed MMAs would.
+template <class Poll, class Issued, class Aborted, class Abort>
+KVARN_ROLE void wait_page(Poll poll, Issued issued, Aborted aborted, Abort abort) {
+  for (uint32_t n = 0; n < (1u << 26); ++n) {
+    const bool go = issued();  // read ahead of the poll, whose latency covers it
+    if (poll() && go) return;
+    if ((n & 255u) == 255u) {
+      if (n >= (1u << 25)) abort();
+      if (aborted() && go) return;
+    }
+  }
+  abort();
+}
+
 // A wait for work that may rightly last as long as a segment: it gives up, and returns false, once
 // progress() (pages issued) has not moved for kNoProgressNs.
 constexpr uint64_t kNoProgressNs = 4000000000ull;

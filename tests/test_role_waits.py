@@ -153,3 +153,37 @@ int main() {
 }
 """)
     assert lines == ["1 60", "0 4", "1", "0"]
+
+
+def test_a_phase_left_behind_does_not_pass_for_a_page(tmp_path):
+    # one stage's barrier of two arrivals a page (the MMAs' completion and the issuing thread's).  The
+    # completion of the stage's first page never comes; the pages are then issued one by one after the
+    # abort, and a wait for a page may not end before that page is issued, though the barrier's parity
+    # reads as complete a page early.
+    lines = _run(tmp_path, r"""
+int main() {
+  int arrivals = 0, issued = 0, misread = 0;
+  auto phase = [&] { return arrivals / 2; };
+  for (int page = 0; page < 6; ++page) {
+    // the wait of a role that is a page ahead of the MMA warp: the page is issued after 1000 looks
+    int looks = 0, ended_at = -1;
+    auto issue = [&] {
+      arrivals += page == 0 ? 1 : 2;  // the first completion is lost
+      ++issued;
+    };
+    wait_page(
+        [&] {
+          if (++looks == 1000) issue();
+          const bool complete = (phase() & 1) != (page & 1);
+          if (complete && issued <= page) ++misread;
+          return complete;
+        },
+        [&] { return issued > page; }, [] { return true; }, [] {});
+    ended_at = looks;
+    printf("%d %d\n", issued, (int)(ended_at >= 1000));
+  }
+  printf("%d\n", (int)(misread > 0));
+}
+""")
+    # the model does meet a barrier that reads as complete too early
+    assert lines == ["%d 1" % (i + 1) for i in range(6)] + ["1"]
