@@ -128,12 +128,12 @@ __device__ __forceinline__ bool bar_any(int id, int threads, bool flag) {
   return out != 0;
 }
 
-// Bounded wait (2^25 polls, about a second) on an mbarrier, for page `need` - 1 of the MMA warp whose
+// Bounded wait (2 s, as the other kernels') on an mbarrier, for page `need` - 1 of the MMA warp whose
 // count of issued pages is *issued (null: none, as for copies); see wait_page.
 __device__ __forceinline__ void wait_one(uint64_t* bar, uint32_t parity, volatile int* abort_flag,
                                          const volatile int* issued, int need) {
   wait_page([&] { return mbar_try_wait(bar, parity); }, [&] { return issued == nullptr || *issued >= need; },
-            [&] { return *abort_flag != 0; }, [&] { *abort_flag = 1; });
+            [&] { return *abort_flag != 0; }, [&] { *abort_flag = 1; }, global_timer_ns);
 }
 // One lane of a converged warp.  MMAs are issued under it: the compiler then knows that a single
 // thread runs them and keeps their operands in uniform registers.

@@ -45,17 +45,22 @@ struct CopyRing {
 // same: every role runs through all its pages, so that no named barrier is left waiting, and the
 // call's results are flagged.  From then on a wait ends once the page is issued, which keeps the
 // roles within two pages of each other as the completed MMAs would.
-template <class Poll, class Issued, class Aborted, class Abort>
-KVARN_ROLE void wait_page(Poll poll, Issued issued, Aborted aborted, Abort abort) {
-  for (uint32_t n = 0; n < (1u << 26); ++n) {
+// A wait runs out after kWaitNs of wall time; kEndNs ends it even if the page is still not issued
+// (the roles that issue it give up their own waits in between, so this is not reached).
+constexpr uint64_t kWaitNs = 2000000000ull, kEndNs = 10000000000ull;
+template <class Poll, class Issued, class Aborted, class Abort, class Now>
+KVARN_ROLE void wait_page(Poll poll, Issued issued, Aborted aborted, Abort abort, Now now) {
+  uint64_t t0 = 0;
+  for (uint32_t n = 1; n != 0; ++n) {
     const bool go = issued();  // read ahead of the poll, whose latency covers it
     if (poll() && go) return;
-    if ((n & 255u) == 255u) {
-      if (n >= (1u << 25)) abort();
-      if (aborted() && go) return;
-    }
+    if ((n & 255u) != 0) continue;
+    const uint64_t t = now();
+    if (t0 == 0) t0 = t;
+    if (t - t0 >= kWaitNs) abort();
+    if (aborted() && go) return;
+    if (t - t0 >= kEndNs) return;
   }
-  abort();
 }
 
 // A wait for work that may rightly last as long as a segment: it gives up, and returns false, once

@@ -80,7 +80,7 @@ extern "C" {
 
 #define KVARN_DEV_BAD_PAGE_ID 1      /* a page id outside [0, num_pool_pages): page 0 used   */
 #define KVARN_DEV_SEQ_TOO_LONG 2     /* seq_len < 0, or its pages exceed the block table row  */
-#define KVARN_DEV_WAIT_TIMEOUT 4     /* an asynchronous page copy did not arrive in ~2 s     */
+#define KVARN_DEV_WAIT_TIMEOUT 4     /* a copy or matrix step was not done in ~2 s: wrong output */
 #define KVARN_DEV_NO_PARTIAL 8       /* a length has a remainder but partial_k/v were NULL   */
 
 /* Method constants of one cache.  Fill it with kvarn_desc_from_preset. */

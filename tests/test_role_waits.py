@@ -178,7 +178,7 @@ int main() {
           if (complete && issued <= page) ++misread;
           return complete;
         },
-        [&] { return issued > page; }, [] { return true; }, [] {});
+        [&] { return issued > page; }, [] { return true; }, [] {}, [] { return (uint64_t)1; });
     ended_at = looks;
     printf("%d %d\n", issued, (int)(ended_at >= 1000));
   }
@@ -187,3 +187,30 @@ int main() {
 """)
     # the model does meet a barrier that reads as complete too early
     assert lines == ["%d 1" % (i + 1) for i in range(6)] + ["1"]
+
+
+def test_a_wait_for_a_page_runs_out_after_two_seconds(tmp_path):
+    # by the clock, however quick or slow a poll is: made-up time that a poll moves by 1 ns or 1 ms
+    lines = _run(tmp_path, r"""
+int main() {
+  for (uint64_t step : {40ull, 1000000ull}) {
+    for (int mode = 0; mode < 4; ++mode) {  // MMAs not issued; issued; a copy; issued by another's abort
+      uint64_t t = 1, aborted_at = 0;
+      bool aborted = mode == 3;
+      wait_page([&] { t += step; return false; }, [&] { return mode != 0; }, [&] { return aborted; },
+                [&] { if (!aborted) aborted_at = t; aborted = true; }, [&] { return t; });
+      printf("%.1f %.1f\n", aborted_at / 1e9, t / 1e9);
+    }
+  }
+  // a page that completes is not reported, and the clock is not read for a quick one
+  int looks = 0, clocks = 0;
+  bool aborted = false;
+  wait_page([&] { return ++looks == 200; }, [] { return true; }, [&] { return aborted; }, [&] { aborted = true; },
+            [&] { return (uint64_t)++clocks; });
+  printf("%d %d %d\n", looks, clocks, (int)aborted);
+}
+""")
+    # the first look at the clock is after 256 polls (0.26 s of the slow ones)
+    assert lines[:4] == ["2.0 10.0", "2.0 2.0", "2.0 2.0", "0.0 0.0"]
+    assert lines[4:8] == ["2.3 10.5", "2.3 2.3", "2.3 2.3", "0.0 0.3"]
+    assert lines[8] == "200 0 0"
