@@ -110,14 +110,19 @@ constexpr uint32_t kIdescPV = kIdescQK<NR> | (1u << 16);
 __device__ __forceinline__ float lift0(int kb) { return kb == 8 ? 256.0f : (kb == 4 ? 16.0f : 4.0f); }
 __device__ __forceinline__ float lift1(int kb) { return kb == 8 ? 256.0f : 1.0f; }
 
+// These barriers want a warp's threads together (the aligned forms), and warps come to them from polls
+// and elected sections that the threads may leave one by one: they meet first.
 __device__ __forceinline__ void bar_sync(int id, int threads) {
+  __syncwarp();
   asm volatile("bar.sync %0, %1;" ::"r"(id), "r"(threads) : "memory");
 }
 __device__ __forceinline__ void bar_arrive(int id, int threads) {
+  __syncwarp();
   asm volatile("bar.arrive %0, %1;" ::"r"(id), "r"(threads) : "memory");
 }
 // Barrier of `threads` threads; returns whether any of them passed `flag`.
 __device__ __forceinline__ bool bar_any(int id, int threads, bool flag) {
+  __syncwarp();
   uint32_t out;
   asm volatile(
       "{\n\t.reg .pred pi, po;\n\tsetp.ne.u32 pi, %1, 0;\n\t"
@@ -1003,8 +1008,9 @@ __global__ void __launch_bounds__(blk::kThreads, 1) block_cache_kernel(BlockPara
             w = seg(k - 1);
             w.next(p, part_s.fix);
           }
-          // the K warps are done with the queries of the segment before the last
-          const bool free_q = k < 2 || wait_handoff(&q_empty[k & 1], (uint32_t)((k - 2) >> 1) & 1u);
+          // the K warps are done with the queries of the segment before the last (after a closed
+          // gate they may have ended)
+          const bool free_q = k < 2 || !open || wait_handoff(&q_empty[k & 1], (uint32_t)((k - 2) >> 1) & 1u);
           open = __all_sync(0xffffffffu, free_q) && open;
           if (!open) *abort_v = 1;
           if (lane == 0) {
@@ -1044,32 +1050,34 @@ __global__ void __launch_bounds__(blk::kThreads, 1) block_cache_kernel(BlockPara
             if (g >= 2) bar_sync(kSFree + s, kOpsThreads);  // S of the page before the last is read
           }
           fence_after();
-          if (!elect_one()) continue;
-          if (is_pv) {
-            const uint64_t pd = smem_desc(smem_u32(sm + S::kPOff + s * S::kPBytes) + part * NR * 8, S::kPGroup, 128);
-            const uint32_t av = tmem + S::kColV + (S::kVStages == 2 ? (uint32_t)(s * 64 * S::kHalves) : 0u);
+          if (elect_one()) {
+            if (is_pv) {
+              const uint64_t pd = smem_desc(smem_u32(sm + S::kPOff + s * S::kPBytes) + part * NR * 8, S::kPGroup, 128);
+              const uint32_t av = tmem + S::kColV + (S::kVStages == 2 ? (uint32_t)(s * 64 * S::kHalves) : 0u);
 #pragma unroll 1
-            for (int hf = 0; hf < S::kHalves; ++hf)
+              for (int hf = 0; hf < S::kHalves; ++hf)
 #pragma unroll
-              for (int o = 0; o < 8; ++o)
-                mma_ts(tmem + S::kColO + hf * NR + part * NM, av + 64 * hf + 8 * o, pd + o * (S::kPStep >> 4),
-                       kIdescPV<NM>, (uint32_t)(i > 0 || o > 0));
-            mma_commit(&pv_done[2 * part + s]);
-            issued[2 + part] = g + 1;
-          } else {
-            const uint64_t bd = smem_desc(smem_u32(sm + S::kBOff + s * 2 * S::kBHalf) + part * NR * 16, 128, 256);
-            const uint32_t ak = tmem + S::kColK + (uint32_t)(s * (D / 2));
+                for (int o = 0; o < 8; ++o)
+                  mma_ts(tmem + S::kColO + hf * NR + part * NM, av + 64 * hf + 8 * o, pd + o * (S::kPStep >> 4),
+                         kIdescPV<NM>, (uint32_t)(i > 0 || o > 0));
+              mma_commit(&pv_done[2 * part + s]);
+              issued[2 + part] = g + 1;
+            } else {
+              const uint64_t bd = smem_desc(smem_u32(sm + S::kBOff + s * 2 * S::kBHalf) + part * NR * 16, 128, 256);
+              const uint32_t ak = tmem + S::kColK + (uint32_t)(s * (D / 2));
 #pragma unroll 1
-            for (int lo = 0; lo < 2; ++lo)
+              for (int lo = 0; lo < 2; ++lo)
 #pragma unroll 8
-              for (int kk = 0; kk < S::kSteps; ++kk)
-                mma_ts(tmem + S::kColS + (uint32_t)(s * NR + part * NM), ak + 8 * kk,
-                       bd + (lo * S::kSteps + kk) * (S::kStep >> 4), kIdescQK<NM>, (uint32_t)(lo + kk > 0));
-            mma_commit(&qk_full[2 * part + s]);
-            // this thread has seen the K warps' writes (q~ . z') and passes them on to the softmax
-            mbar_arrive(&qk_full[2 * part + s]);
-            issued[part] = g + 1;
+                for (int kk = 0; kk < S::kSteps; ++kk)
+                  mma_ts(tmem + S::kColS + (uint32_t)(s * NR + part * NM), ak + 8 * kk,
+                         bd + (lo * S::kSteps + kk) * (S::kStep >> 4), kIdescQK<NM>, (uint32_t)(lo + kk > 0));
+              mma_commit(&qk_full[2 * part + s]);
+              // this thread has seen the K warps' writes (q~ . z') and passes them on to the softmax
+              mbar_arrive(&qk_full[2 * part + s]);
+              issued[part] = g + 1;
+            }
           }
+          __syncwarp();  // the next page's barriers want the whole warp
         }
       }
       if (g > 0) {

@@ -5,6 +5,7 @@ of which never complete, and the tests read what it did.
 """
 
 import os
+import re
 import shutil
 import subprocess
 
@@ -214,3 +215,16 @@ int main() {
     assert lines[:4] == ["2.0 10.0", "2.0 2.0", "2.0 2.0", "0.0 0.0"]
     assert lines[4:8] == ["2.3 10.5", "2.3 2.3", "2.3 2.3", "0.0 0.3"]
     assert lines[8] == "200 0 0"
+
+
+def test_named_barriers_take_converged_warps():
+    # the aligned barriers are reached through three wrappers only, each of which brings the warp's
+    # threads together first, and no thread leaves an elected section for a barrier of its own
+    with open(os.path.join(CSRC, "block_attention.cu")) as fh:
+        text = re.sub(r"//.*", "", fh.read())
+    asm = re.findall(r'"[^"]*\bbar(?:rier)?\.[^"]*"', text)
+    assert len(asm) == 3
+    for name in ("bar_sync", "bar_arrive", "bar_any"):
+        body = re.search(r"%s\(int id[^{]*\{\s*(.*?)\n\}" % name, text, flags=re.S).group(1)
+        assert body.startswith("__syncwarp();") and '"bar.' in body.replace('"{\\n\\t.reg .pred pi, po;', "")
+    assert not re.search(r"elect_one\(\)\s*\)\s*(continue|return|break)", text)
