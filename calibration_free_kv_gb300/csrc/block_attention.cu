@@ -110,19 +110,17 @@ constexpr uint32_t kIdescPV = kIdescQK<NR> | (1u << 16);
 __device__ __forceinline__ float lift0(int kb) { return kb == 8 ? 256.0f : (kb == 4 ? 16.0f : 4.0f); }
 __device__ __forceinline__ float lift1(int kb) { return kb == 8 ? 256.0f : 1.0f; }
 
-// These barriers want a warp's threads together (the aligned forms), and warps come to them from polls
-// and elected sections that the threads may leave one by one: they meet first.
+// These barriers are the aligned forms: a warp's threads come to them together.  Threads may leave a
+// poll or an elected section one by one, so that __syncwarp() follows each (inside the three wrappers,
+// ahead of every barrier, it cost 5 % on 16 trees of 64 nodes: 659 against 624 us).
 __device__ __forceinline__ void bar_sync(int id, int threads) {
-  __syncwarp();
   asm volatile("bar.sync %0, %1;" ::"r"(id), "r"(threads) : "memory");
 }
 __device__ __forceinline__ void bar_arrive(int id, int threads) {
-  __syncwarp();
   asm volatile("bar.arrive %0, %1;" ::"r"(id), "r"(threads) : "memory");
 }
 // Barrier of `threads` threads; returns whether any of them passed `flag`.
 __device__ __forceinline__ bool bar_any(int id, int threads, bool flag) {
-  __syncwarp();
   uint32_t out;
   asm volatile(
       "{\n\t.reg .pred pi, po;\n\tsetp.ne.u32 pi, %1, 0;\n\t"
@@ -415,6 +413,7 @@ __global__ void __launch_bounds__(blk::kThreads, 1) block_cache_kernel(BlockPara
   // Segment k for a group of warps that meets at barrier `id`.
   auto segment = [&](int k, int id, int threads, bool leader) -> bool {
     if (leader) wait_segment(k);
+    __syncwarp();
     bar_sync(id, threads);
     return there(k);
   };
@@ -545,6 +544,7 @@ __global__ void __launch_bounds__(blk::kThreads, 1) block_cache_kernel(BlockPara
         // (a poll takes ~150 cycles even when it succeeds, so each is another warp's)
         if (wq == 0) wait_qk(part, g);
         if (wq == 1) wait_pv(part, g - 2);
+        __syncwarp();
         bar_sync(sbar, 128);
         fence_after();
         const uint32_t ts = tmem + S::kColS + (uint32_t)(s * NR + c0) + lanes;
@@ -749,6 +749,7 @@ __global__ void __launch_bounds__(blk::kThreads, 1) block_cache_kernel(BlockPara
         // QK of the page before the last has read the codes and B
         if (warp == kKWarp) wait(&rec_full[r], rph);
         if (warp > kKWarp && warp <= kKWarp + NP) wait_qk(warp - kKWarp - 1, g - 2);
+        __syncwarp();
         bar_sync(kKBar, 256);
         fence_after();
         const uint8_t* R = recs + r * rec;
@@ -885,6 +886,7 @@ __global__ void __launch_bounds__(blk::kThreads, 1) block_cache_kernel(BlockPara
         // PV of the page that last used this buffer
         if (warp == kVWarp) wait(&rec_full[r], rph);
         if (warp > kVWarp && warp <= kVWarp + NP) wait_pv(warp - kVWarp - 1, g - S::kVStages);
+        __syncwarp();
         bar_sync(kVBar, 256);
         fence_after();
         const uint8_t* R = recs + r * rec;
@@ -1038,6 +1040,7 @@ __global__ void __launch_bounds__(blk::kThreads, 1) block_cache_kernel(BlockPara
       const int part = is_pv ? warp - kPvWarp : warp - kQkWarp;
       for (int k = 0;; ++k) {
         wait_segment(k);
+        __syncwarp();
         const int cnt = there(k) ? seg(k).count() : 0;
         if (cnt == 0) break;
         for (int i = 0; i < cnt; ++i, ++g) {

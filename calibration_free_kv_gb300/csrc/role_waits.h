@@ -6,8 +6,10 @@
 
 #ifdef __CUDACC__
 #define KVARN_ROLE __device__ __forceinline__
+#define KVARN_ROLLED _Pragma("unroll 1")  // a wait is in every role: its code is kept short
 #else
 #define KVARN_ROLE inline
+#define KVARN_ROLLED
 #endif
 
 namespace kvarn {
@@ -31,7 +33,7 @@ struct CopyRing {
   template <class Wait>
   KVARN_ROLE bool drain(Wait wait) const {
     bool all = true;
-    for (int i = issued > slots ? issued - slots : 0; i < issued; ++i)
+    KVARN_ROLLED for (int i = issued > slots ? issued - slots : 0; i < issued; ++i)
       if (!wait(i % slots, (uint32_t)(i / slots) & 1u)) all = false;
     return all;
   }
@@ -51,7 +53,7 @@ constexpr uint64_t kWaitNs = 2000000000ull, kEndNs = 10000000000ull;
 template <class Poll, class Issued, class Aborted, class Abort, class Now>
 KVARN_ROLE void wait_page(Poll poll, Issued issued, Aborted aborted, Abort abort, Now now) {
   uint64_t t0 = 0;
-  for (uint32_t n = 1; n != 0; ++n) {
+  KVARN_ROLLED for (uint32_t n = 1; n != 0; ++n) {
     const bool go = issued();  // read ahead of the poll, whose latency covers it
     if (poll() && go) return;
     if ((n & 255u) != 0) continue;
@@ -71,7 +73,7 @@ KVARN_ROLE bool wait_progress(Poll poll, Progress progress, Now now) {
   if (poll()) return true;
   int seen = progress();
   uint64_t t0 = now();
-  for (uint32_t n = 1; n != 0; ++n) {
+  KVARN_ROLLED for (uint32_t n = 1; n != 0; ++n) {
     if (poll()) return true;
     if ((n & 255u) != 0) continue;
     const int at = progress();

@@ -218,13 +218,30 @@ int main() {
 
 
 def test_named_barriers_take_converged_warps():
-    # the aligned barriers are reached through three wrappers only, each of which brings the warp's
-    # threads together first, and no thread leaves an elected section for a barrier of its own
+    # the aligned barriers are reached through three wrappers only; a warp's threads meet after every
+    # poll and every elected section, and none leaves an elected section for a barrier of its own
     with open(os.path.join(CSRC, "block_attention.cu")) as fh:
         text = re.sub(r"//.*", "", fh.read())
-    asm = re.findall(r'"[^"]*\bbar(?:rier)?\.[^"]*"', text)
-    assert len(asm) == 3
-    for name in ("bar_sync", "bar_arrive", "bar_any"):
-        body = re.search(r"%s\(int id[^{]*\{\s*(.*?)\n\}" % name, text, flags=re.S).group(1)
-        assert body.startswith("__syncwarp();") and '"bar.' in body.replace('"{\\n\\t.reg .pred pi, po;', "")
+    assert len(re.findall(r'"[^"]*\bbar(?:rier)?\.[^"]*"', text)) == 3
     assert not re.search(r"elect_one\(\)\s*\)\s*(continue|return|break)", text)
+    kernel = text[text.index("block_cache_kernel(BlockParams"):text.index("block_raw_kernel(BlockParams")]
+    loader = kernel[kernel.index("if (warp == kLoadWarp)"):kernel.index("} else if (warp >= kQueryWarp)")]
+    roles = kernel[kernel.index("auto segment ="):].replace(loader, "")  # the loader is one thread
+    lines = [line.strip() for line in roles.split("\n") if line.strip()]
+    polls = [i for i, line in enumerate(lines) if re.search(r"\b(wait|wait_qk|wait_pv|wait_segment|mbar_wait)\(", line)]
+    assert len(polls) >= 8
+    for i in polls:
+        rest = lines[i + 1:]
+        while re.search(r"\b(wait|wait_qk|wait_pv)\(", rest[0]):  # polls of other warps of the role
+            rest = rest[1:]
+        assert rest[0] == "__syncwarp();", (lines[i], rest[0])
+    assert loader.rstrip().endswith("__syncwarp();")
+    for m in re.finditer(r"if \(elect_one\(\)\)", roles):
+        after = roles[m.start():]
+        depth, at = 0, after.index(")") + 2
+        while True:  # the end of the elected statement
+            depth += {"{": 1, "}": -1}.get(after[at], 0)
+            if (after[at] == "}" or after[at] == ";") and depth == 0:
+                break
+            at += 1
+        assert after[at + 1:].strip().startswith("__syncwarp();")
