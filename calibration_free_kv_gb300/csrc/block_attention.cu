@@ -25,9 +25,9 @@
 //      off by 3.3e-4 to 3.8e-4 (relative 2-norm), by 2.1e-4 where only it is rounded.  Without either
 //      V~'s second rounding or P's it would still be near 3e-4, and going without both takes fp32
 //      conversions and a second PV pass on the pipes that bound this kernel.
-// Softmax: a thread owns a token and half the rows of the tile; each row's reference maximum is kept
-// from page to page and moved only when a logit passes it by 2^8 (then O and l are rescaled), so no
-// maximum is exchanged on the usual page; P stays below 2^8 and l is fp32.
+// Softmax: a thread owns a token and half the rows of the tile; each row's reference, 2^7 below a maximum
+// of the row, is kept from page to page and moved only when a logit passes that maximum by 2^8 (then O
+// and l are rescaled), so no maximum is exchanged on the usual page; P stays below 2^15 and l is fp32.
 // Warps: 0-7 softmax (two warpgroups, one per row half: also the rescale and the row tile's partial at
 // its end), 8-11 K codes, 12-15 q~ . z' (both groups: half of B each), 16-23 V, 24 page records (1-D
 // bulk copies into a ring), 25-26 QK and 27-28 PV (one warp per column part), 29-31 the walk and q~ of
@@ -66,7 +66,10 @@ constexpr int kQueryBar = 1, kSmBar = 2, kKBar = 4, kVBar = 5, kOpsK = 6, kSFree
 // Units of the line ahead of a row tile's pages for a segment's fixed work, and the smallest range
 // (5, 8 and 14 units took no less time than 3).
 constexpr int kFixUnits = 3, kMinUnits = 3;
-constexpr float kSlack = 8.0f;  // log2 units a logit may pass its row's reference by
+// A row's reference lies kHead (log2 units) below the maximum it was set at, and a logit may pass that
+// maximum by kSlack: P is at most 2^15.  fp16 ends at 2^-24, so that what is lost of a weight lies
+// below 2^-32 of the row's largest (without the head 2^-25, which many tokens can add up to).
+constexpr float kHead = 7.0f, kSlack = 8.0f;
 constexpr int kSmemMax = 232448 - 1536;  // the rest is for the static part
 
 template <int D, int NR>
@@ -86,9 +89,9 @@ struct Shape {
   static constexpr int kPOff = 2 * 2 * kBHalf;
   static constexpr int kQOff = kPOff + 2 * kPBytes;
   static constexpr int kSmallOff = kQOff + 2 * 2 * kBHalf;
-  // floats: qz [4][NR], -reference, row maximum, shift, rescale [NR] each, row limit [kSegs][NR], per
-  // warp [4][NR], token factors [4][128]
-  static constexpr int kSmallFloats = (4 + 4 + kSegs + 4) * NR + 4 * kTile;
+  // floats: qz [4][NR], -reference, row maximum, rescale [NR] each, row limit [kSegs][NR], per warp
+  // [4][NR], token factors [4][128]
+  static constexpr int kSmallFloats = (4 + 3 + kSegs + 4) * NR + 4 * kTile;
   static constexpr int kBarOff = kSmallOff + kSmallFloats * 4;
   static constexpr int kNumBars = 2 * kMaxSlots + 2 * 4 + kSegs + 2;
   static constexpr int kRecOff = (kBarOff + kNumBars * 8 + 127) & ~127;
@@ -338,8 +341,7 @@ __global__ void __launch_bounds__(blk::kThreads, 1) block_cache_kernel(BlockPara
   float* qz_s = reinterpret_cast<float*>(sm + S::kSmallOff);  // [4][NR]: page g's at g % 4
   float* nref_s = qz_s + 4 * NR;   // minus the row's reference
   float* max_s = nref_s + NR;      // the row's maximum when the reference was set (-inf: none yet)
-  float* shift_s = max_s + NR;     // old reference - new reference
-  float* alpha_s = shift_s + NR;   // rescale of l and O
+  float* alpha_s = max_s + NR;     // rescale of l and O
   int* lim_all = reinterpret_cast<int*>(alpha_s + NR);  // [kSegs][NR]: position from which a row's window sees
   float* warp_s = reinterpret_cast<float*>(lim_all + kSegs * NR);  // [4][NR]
   float* rt_s = warp_s + 4 * NR;  // [4][128]: the token factors of page g at g % 4
@@ -584,7 +586,7 @@ __global__ void __launch_bounds__(blk::kThreads, 1) block_cache_kernel(BlockPara
           float mx = -INFINITY;
 #pragma unroll
           for (int n = 0; n < NC; n += 2) mx = fmax3(mx, x[n], x[n + 1]);
-          if (!bar_any(sbar, 128, !moved && (unset || mx > kSlack))) break;
+          if (!bar_any(sbar, 128, !moved && (unset || mx > kHead + kSlack))) break;
           // Move the references to the rows' maxima, then take the logits again.  This runs once or
           // twice a segment, from a cold instruction cache that costs ~200 cycles for eight
           // instructions: short loops over eight rows here, and the code above for the rest.
@@ -610,9 +612,10 @@ __global__ void __launch_bounds__(blk::kThreads, 1) block_cache_kernel(BlockPara
             const float pm = fmaxf(fmaxf(warp_s[n], warp_s[NR + n]), fmaxf(warp_s[2 * NR + n], warp_s[3 * NR + n]));
             const float mn = fmaxf(old, pm);
             none = mn == -INFINITY;
+            const float nref = none ? 0.0f : kHead - mn;
+            alpha_s[n] = old == -INFINITY ? 0.0f : ex2_approx(nref - nref_s[n]);
             max_s[n] = mn;
-            nref_s[n] = none ? 0.0f : -mn;
-            alpha_s[n] = old == -INFINITY ? 0.0f : ex2_approx(old - mn);
+            nref_s[n] = nref;
           }
           unset = bar_any(sbar, 128, none);
           if (i > 0) {  // l and O of the pages before this one
@@ -687,7 +690,7 @@ __global__ void __launch_bounds__(blk::kThreads, 1) block_cache_kernel(BlockPara
       if (u < min(live, NC)) {
         const int n = c0 + u;
         float* d = dst + (int64_t)u * (D + 4);
-        d[0] = max_s[n];
+        d[0] = max_s[n] == -INFINITY ? -INFINITY : -nref_s[n];
         d[1] = (warp_s[n] + warp_s[NR + n]) + (warp_s[2 * NR + n] + warp_s[3 * NR + n]);
       }
       wait_pv(part, g - 1);
