@@ -70,6 +70,9 @@ constexpr int kFixUnits = 3, kMinUnits = 3;
 // maximum by kSlack: P is at most 2^15.  fp16 ends at 2^-24, so that what is lost of a weight lies
 // below 2^-32 of the row's largest (without the head 2^-25, which many tokens can add up to).
 constexpr float kHead = 7.0f, kSlack = 8.0f;
+// The raw tokens' reference follows the maximum from stage to stage: P is at most 2^12, what is lost of
+// a weight lies below 2^-37 of the row's largest, and the logits' own rounding has room up to 2^16.
+constexpr float kRawHead = 12.0f;
 constexpr int kSmemMax = 232448 - 1536;  // the rest is for the static part
 
 template <int D, int NR>
@@ -1119,8 +1122,8 @@ __global__ void __launch_bounds__(blk::kThreads, 1) block_cache_kernel(BlockPara
 // V rows stream through shared memory 64 tokens at a time (cp.async into swizzled fp16 rows, two
 // stages), the open tile's first, then the new tokens'.  mma.sync m16n8k16: A = the fp16 queries
 // (exact products; the scale applied to the fp32 sums) by ldmatrix, B = K rows by ldmatrix; online
-// softmax in the log2 domain; PV with the probabilities rounded once to fp16 (they move the output
-// like its own rounding).  A row that sees nothing leaves m = -inf, l = 0, o = 0.  The queries stay in
+// softmax in the log2 domain; PV with the probabilities, 2^12 at a row's maximum, rounded once to fp16
+// (they move the output like its own rounding).  A row that sees nothing leaves m = -inf, l = 0, o = 0.  The queries stay in
 // shared memory so that two CTAs (16 warps) fit an SM at head_dim 64 and 128: with them in registers,
 // one CTA an SM and fp16 hi + lo probabilities a 2 x 2048-token chunk took 482 us.  Masks are looked at
 // only in stages that some row of the warp does not see whole: that chunk 386 -> 332 us; latency
@@ -1303,8 +1306,8 @@ __global__ void __launch_bounds__(256, D <= 128 ? 2 : 1) block_raw_kernel(BlockP
       mxa = fmaxf(mxa, __shfl_xor_sync(0xffffffffu, mxa, 2));
       mxb = fmaxf(mxb, __shfl_xor_sync(0xffffffffu, mxb, 1));
       mxb = fmaxf(mxb, __shfl_xor_sync(0xffffffffu, mxb, 2));
-      // maxima in the log2 domain; qscale > 0
-      const float na = fmaxf(ma, mxa * p.qscale), nb = fmaxf(mb, mxb * p.qscale);
+      // references in the log2 domain, kRawHead below the maxima; qscale > 0
+      const float na = fmaxf(ma, fmaf(mxa, p.qscale, -blk::kRawHead)), nb = fmaxf(mb, fmaf(mxb, p.qscale, -blk::kRawHead));
       const float sa = na == -INFINITY ? 0.0f : -na, sb = nb == -INFINITY ? 0.0f : -nb;
       const float aa = ma == -INFINITY ? 0.0f : exp2f(ma - na);
       const float ab = mb == -INFINITY ? 0.0f : exp2f(mb - nb);

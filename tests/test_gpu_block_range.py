@@ -71,3 +71,24 @@ def test_small_weights_of_sealed_pages(kv, group, d0, preset):
     size = np.abs(ref).max(axis=1)
     assert size.min() > 0.005  # the small weights do carry the output
     print("G=%d d0=%d: output up to %.3f, max scaled error %.1e" % (group, d0, size.max(), B.close(got, ref, "sealed")))
+
+
+@pytest.mark.parametrize("group,d0", [(1, 128), (4, 64), (2, 256)])
+def test_small_weights_of_raw_tokens(kv, group, d0):
+    # a chunk without a cache whose first token leads for every row
+    n = 2048
+    g = torch.Generator().manual_seed(70 + d0)
+    q1, k, v = _rows(g, n, d0, LEAD, 1000.0)
+    desc = kv.desc_from_preset(d0, 1)
+    q = (q1 * (1.0 + 0.01 * torch.randn((1, n, group, 1), generator=g))).half()
+    out = torch.empty(q.shape, dtype=torch.float16, device="cuda")
+    pool, table = kv.alloc_pool(desc, 1), torch.zeros((1, 1), dtype=torch.int32, device="cuda")
+    kv.window_prefill_attention(desc, q.cuda(), k[None, :, None].contiguous().cuda(), v[None, :, None].contiguous().cuda(),
+                                pool, table, torch.zeros(1, dtype=torch.int32, device="cuda"), out,
+                                kv.alloc_window_prefill_workspace(desc, 1, group, n, 1, 1, 4096), 1, 4096)
+    got = out.cpu().double().numpy()[0]
+    on = np.tril(np.ones((n, n), dtype=bool))
+    kd, vd = k.double().numpy(), v.double().numpy()
+    ref = np.stack([B.attend(q[0, :, h].double().numpy(), kd, vd, on, B.scale_of(d0)) for h in range(group)], 1)
+    assert np.abs(ref[n // 2:]).max(axis=-1).min() > 0.01
+    print("G=%d d0=%d: max scaled error %.1e" % (group, d0, B.close(got, ref, "raw")))
