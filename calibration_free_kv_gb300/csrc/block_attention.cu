@@ -1461,7 +1461,8 @@ __global__ void __launch_bounds__(128) block_merge_kernel(BlockParams p) {
     }
 #pragma unroll
     for (int i = 0; i < kRows; ++i) {
-      if (ml[i].x == -INFINITY) continue;  // a partial that saw no token
+      // a partial that saw no token; one whose logits are NaN has no maximum either, but its sum is NaN
+      if (ml[i].x == -INFINITY && ml[i].y == 0.0f) continue;
       const float mn = fmaxf(M[i], ml[i].x);
       const float keep = M[i] == -INFINITY ? 0.0f : exp2f(M[i] - mn), w = exp2f(ml[i].x - mn);
       M[i] = mn;

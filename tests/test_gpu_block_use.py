@@ -187,3 +187,35 @@ def test_argument_checks(kv):
         kv.window_decode_attention(cache.desc, q[:, 0].contiguous(), cache.pool, table, cache.lens_t,
                                    torch.empty_like(q[:, 0]).contiguous(), ws, 0, 0, **cache.args)
     assert e.value.status == kv.KVARN_ERR_INVALID_ARG
+
+
+def test_a_nan_query_is_not_answered_with_zeros(kv):
+    # a query of NaN that sees sealed pages only gives NaN, as the decode call does, and its
+    # neighbours keep their outputs
+    cache = B.Cache(kv, [256, 1536], 1, 128, 52)
+    g = torch.Generator().manual_seed(53)
+    q, k, v = _half(g, 2, 5, 4, 128), _half(g, 2, 5, 1, 128), _half(g, 2, 5, 1, 128)
+    sees = np.zeros((2, 5, 5), dtype=bool)
+    sees[:, 0] = True
+    table = cache.table.cuda()
+    ws = kv.alloc_tree_workspace(cache.desc, 2, 4, 5, table.shape[1])
+
+    def run(q):
+        out = torch.empty_like(q)
+        kv.tree_attention(cache.desc, q, k, v, B.pack_mask(sees).cuda(), cache.pool, table, cache.lens_t, out, ws,
+                          **cache.args)
+        return out.cpu().double()
+
+    want = run(q)
+    bad = q.clone()
+    bad[0, 2, 1, 7] = float("nan")
+    bad[1, 3] = float("nan")
+    bad[1, 0, 0] = float("nan")  # sees raw tokens too
+    got = run(bad)
+    nan = torch.isnan(bad).any(-1).cpu()
+    assert torch.isnan(got[nan]).all()
+    B.close(got[~nan].numpy(), want[~nan].numpy(), "rows beside a NaN query")
+    step = torch.empty((2, 4, 128), dtype=torch.float16, device="cuda")
+    kv.decode_attention(cache.desc, bad[:, 3].contiguous(), cache.pool, table, cache.lens_t, step,
+                        kv.alloc_workspace(cache.desc, 2, 4, table.shape[1]), **cache.args)
+    assert torch.isnan(step[1]).all() and torch.isfinite(step[0]).all()
