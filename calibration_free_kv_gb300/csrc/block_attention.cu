@@ -21,21 +21,24 @@
 //      accumulator).  hi + lo because keys with outlier channels give logits in the hundreds, and
 //      one fp16 rounding of q~ s' (2^-11 relative) would move them by 0.1;
 //  PV  O[c][r] += sum_t A_V[c][t] P[t][r]; A_V = V~ rounded twice to fp16 (once per product),
-//      P = exp2 rounded once to fp16.  These roundings cost precision: against 64 bits the output is
-//      off by 3.3e-4 to 3.8e-4 (relative 2-norm), by 2.1e-4 where only it is rounded.  Without either
-//      V~'s second rounding or P's it would still be near 3e-4, and going without both takes fp32
-//      conversions and a second PV pass on the pipes that bound this kernel.
+//      P = exp2 rounded once to fp16.  These roundings cost precision, and kvarn.h tells the caller:
+//      against 64 bits the output is off by 3.1e-4 to 3.8e-4 (relative 2-norm), by 2.1e-4 where only it
+//      is rounded.  Without either V~'s second rounding or P's it would still be near 3e-4, and going
+//      without both takes fp32 conversions and a second PV pass on the pipes that bound this kernel.
 // Softmax: a thread owns a token and half the rows of the tile; each row's reference, 2^7 below a maximum
 // of the row, is kept from page to page and moved only when a logit passes that maximum by 2^8 (then O
 // and l are rescaled), so no maximum is exchanged on the usual page; P stays below 2^15 and l is fp32.
 // Warps: 0-7 softmax (two warpgroups, one per row half: also the rescale and the row tile's partial at
 // its end), 8-11 K codes, 12-15 q~ . z' (both groups: half of B each), 16-23 V, 24 page records (1-D
 // bulk copies into a ring), 25-26 QK and 27-28 PV (one warp per column part), 29-31 the walk and q~ of
-// the next segment.  Operand and score buffers are double; every wait on an mbarrier is bounded.
+// the next segment.  Operand and score buffers are double.  Every wait on an mbarrier is bounded; what
+// follows when one runs out is in role_waits.h: all roles go on to the same end, the copies and MMAs in
+// flight are waited for, and the call reports KVARN_DEV_WAIT_TIMEOUT.
 // What bounds it: the conversion of codes and the softmax on the ordinary pipes, not memory and not the
-// tensor cores.  With 64 rows, head_dim 128 and K4V2 a page takes about 1.27 us a SM (2500 cycles, 6650
+// tensor cores.  With 64 rows, head_dim 128 and K4V2 a page takes about 1.31 us a SM (2520 cycles, 6820
 // instructions; on 16 trees of 26 nodes issue slots 62 % used, shared memory's data pipe 52 %, tensor
-// pipe 31 %, DRAM 14 %), a segment about 10 us on top: 16 trees of 64 nodes over 16k 622 us, a 2 x 2048-token windowed chunk 693 us of this kernel.
+// pipe 30 %, DRAM 13 %), a segment about 10 us on top: 16 trees of 64 nodes over 16k 624 us, a 2 x 2048-token
+// windowed chunk 690 us of this kernel.
 #include "common.cuh"
 #include "decode_util.cuh"
 #include "params.cuh"
@@ -1123,7 +1126,8 @@ __global__ void __launch_bounds__(blk::kThreads, 1) block_cache_kernel(BlockPara
 // stages), the open tile's first, then the new tokens'.  mma.sync m16n8k16: A = the fp16 queries
 // (exact products; the scale applied to the fp32 sums) by ldmatrix, B = K rows by ldmatrix; online
 // softmax in the log2 domain; PV with the probabilities, 2^12 at a row's maximum, rounded once to fp16
-// (they move the output like its own rounding).  A row that sees nothing leaves m = -inf, l = 0, o = 0.  The queries stay in
+// (they move the output like its own rounding; as fp16 hi + lo the 2 x 2048-token chunk's call takes 1159
+// instead of 1076 us).  A row that sees nothing leaves m = -inf, l = 0, o = 0.  The queries stay in
 // shared memory so that two CTAs (16 warps) fit an SM at head_dim 64 and 128: with them in registers,
 // one CTA an SM and fp16 hi + lo probabilities a 2 x 2048-token chunk took 482 us.  Masks are looked at
 // only in stages that some row of the warp does not see whole: that chunk 386 -> 332 us; latency

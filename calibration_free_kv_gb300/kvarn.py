@@ -410,7 +410,8 @@ def window_prefill_attention(desc: KvarnDesc, q, chunk_k, chunk_v, pool, block_t
     """prefill_attention of queries that see the first `sink_tokens` tokens and the last `window`
     ones up to their own.  q, out: fp16 [batch, chunk, Hq, d0]; chunk_k/v: fp16 [batch, chunk, Hkv,
     d0]; chunk_lens: int32 [batch] or None, tokens of each sequence's chunk (rows of out past them
-    stay as they were).  Block-table entries of pages that no query sees are not read."""
+    stay as they were).  Block-table entries of pages that no query sees are not read.  Probabilities
+    and dequantised values are rounded to fp16: the output is off by up to 4e-4 of its 2-norm."""
     batch, chunk, hq, d0 = q.shape
     new, lens, cache = _block_args(desc, "chunk", q, chunk_k, chunk_v, chunk_lens, pool, block_table, cache_lens,
                                    partial_k, partial_v)
@@ -437,7 +438,8 @@ def tree_attention(desc: KvarnDesc, q, tree_k, tree_v, tree_mask, pool, block_ta
     """Drafted tokens of a tree over the cache: q, out fp16 [batch, nodes, Hq, d0]; tree_k/v fp16
     [batch, nodes, Hkv, d0]; tree_mask int32 (or uint32) [batch, nodes, ceil(nodes / 32)], bit j % 32
     of word j / 32 of row i set when node i sees node j, or None for a chain; tree_lens: int32
-    [batch] or None, nodes of each sequence (rows of out past them stay as they were)."""
+    [batch] or None, nodes of each sequence (rows of out past them stay as they were).  Probabilities
+    and dequantised values are rounded to fp16: the output is off by up to 4e-4 of its 2-norm."""
     batch, nodes, hq, d0 = q.shape
     new, lens, cache = _block_args(desc, "tree", q, tree_k, tree_v, tree_lens, pool, block_table, cache_lens,
                                    partial_k, partial_v)

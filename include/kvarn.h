@@ -243,7 +243,14 @@ int kvarn_prefill_attention(const kvarn_desc* desc, int batch, int num_q_heads, 
  * sink_tokens >= 0 and window >= 1 (else INVALID_ARG); either may exceed the sequence.
  * A page or a block of raw tokens that some query sees in part is read whole: the values in it have
  * to be finite, also those of tokens a query does not see (a weight of 0 times infinity is NaN).
- * max_pages up to 2^23 (else UNSUPPORTED). */
+ * max_pages up to 2^23 (else UNSUPPORTED).
+ *
+ * Precision.  kvarn_window_decode_attention computes as kvarn_decode_attention.
+ * kvarn_window_prefill_attention and kvarn_tree_attention round more than kvarn_prefill_attention,
+ * which keeps probabilities as two fp16 parts: here probabilities are rounded to fp16 once and the
+ * values of sealed pages twice (half a step, 2^-11, each; sums are 32 bits wide).  The output is off
+ * by 3e-4 to 4e-4 of its 2-norm, against 2e-4 from its own rounding alone.  A sealed token's value
+ * row is held in fp16 in the rotated basis: its 2-norm has to stay below 65504. */
 
 /* Workspace bytes of kvarn_window_decode_attention (host only; 0 if invalid).  It does not grow
  * with the sequences once they are longer than the window. */
