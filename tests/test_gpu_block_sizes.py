@@ -49,7 +49,7 @@ def _term_sizes(cache, b, d):
     return out
 
 
-class Judge:
+class RowCheck:
     def __init__(self):
         self.errors, self.share = [], 0.0  # per row: max error over max(1, max |out|); worst share of the bound
 
@@ -84,7 +84,7 @@ class Judge:
             self.share = max(self.share, float((err / tol).max()))
             self.errors.append(err.max(axis=1) / np.maximum(1.0, np.abs(o).max(axis=1)))
 
-    def verdict(self, what):
+    def finish(self, what):
         e = np.concatenate(self.errors)
         print("%s: %d rows, scaled error %.1e, at most %.1e, %.2f of the bound" % (what, e.size, np.median(e), e.max(),
                                                                                 self.share))
@@ -118,11 +118,11 @@ def _prefill(kv, lens, chunk, hkv, group, d0, sink, window, seed, preset="kvarn_
                                 sink, window, chunk_lens=torch.tensor(sizes, dtype=torch.int32, device="cuda"),
                                 status=status, **cache.args)
     assert int(status.item()) == 0
-    judge, out = Judge(), out.cpu().double().numpy()
+    check, out = RowCheck(), out.cpu().double().numpy()
     for b, m in enumerate(sizes):
-        judge.sequence(cache, b, out[b, :m], *(x[b, :m].double().numpy() for x in (q, k, v)), on[b][:, :lens[b] + m], group)
+        check.sequence(cache, b, out[b, :m], *(x[b, :m].double().numpy() for x in (q, k, v)), on[b][:, :lens[b] + m], group)
         assert (out[b, m:] == 7.0).all()
-    judge.verdict("window prefill %dx%d G=%d d0=%d %s" % (n, chunk, group, d0, preset))
+    check.finish("window prefill %dx%d G=%d d0=%d %s" % (n, chunk, group, d0, preset))
 
 
 @pytest.mark.parametrize("group,d0,preset", [(4, 128, "kvarn_k4v2_g128"), (8, 64, "kvarn_k2v2_g128"),
@@ -157,12 +157,12 @@ def test_tree_of_more_row_tiles_than_ctas(kv):
                       cache.lens_t, out, ws, tree_lens=torch.tensor(sizes, dtype=torch.int32, device="cuda"),
                       status=status, **cache.args)
     assert int(status.item()) == 0
-    judge, out = Judge(), out.cpu().double().numpy()
+    check, out = RowCheck(), out.cpu().double().numpy()
     for b, m in enumerate(sizes):
         on = np.concatenate([np.ones((m, lens[b]), dtype=bool), sees[b, :m, :m]], axis=1)
-        judge.sequence(cache, b, out[b, :m], *(x[b, :m].double().numpy() for x in (q, k, v)), on, group)
+        check.sequence(cache, b, out[b, :m], *(x[b, :m].double().numpy() for x in (q, k, v)), on, group)
         assert (out[b, m:] == 7.0).all()
-    judge.verdict("tree 4x300")
+    check.finish("tree 4x300")
 
 
 def test_window_decode_of_more_than_32_splits(kv):
