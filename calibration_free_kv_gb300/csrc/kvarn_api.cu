@@ -195,6 +195,8 @@ size_t kvarn_decode_workspace_bytes(const kvarn_desc* desc, int batch, int num_q
 
 namespace kvarn {
 
+int desc_check(const kvarn_desc* desc) { return check_desc(desc); }
+
 // Host-side checks of a decode call's arguments other than its workspace: a KVARN_ERR_* code,
 // KVARN_OK, or kDecodeNothingToDo for an empty batch (a valid call that launches nothing).
 int decode_args_check(const kvarn_desc* desc, int batch, int num_q_heads, const void* q,

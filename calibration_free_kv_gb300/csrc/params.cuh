@@ -125,6 +125,9 @@ struct DequantParams {
   float* err_out;
 };
 
+// Host-side check of a descriptor (kvarn_api.cu): KVARN_OK or a KVARN_ERR_* code.
+int desc_check(const kvarn_desc* desc);
+
 // decode_args_check: a valid decode call with nothing to launch (batch 0).
 constexpr int kDecodeNothingToDo = 1;
 // Host-side checks of a decode call's arguments other than its workspace (kvarn_api.cu):

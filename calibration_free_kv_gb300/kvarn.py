@@ -25,6 +25,9 @@ DEV_BAD_PAGE_ID = 1
 DEV_SEQ_TOO_LONG = 2
 DEV_WAIT_TIMEOUT = 4
 DEV_NO_PARTIAL = 8
+DEV_NO_PAGES = 16
+DEV_BAD_BEAM = 32
+DEV_BAD_LOGITS = 64
 
 EXPORTED_SYMBOLS = (
     "kvarn_desc_from_preset",
@@ -52,6 +55,11 @@ EXPORTED_SYMBOLS = (
     "kvarn_window_prefill_attention",
     "kvarn_tree_workspace_bytes",
     "kvarn_tree_attention",
+    "kvarn_plan_pages",
+    "kvarn_fp16_store",
+    "kvarn_beam_select_workspace_bytes",
+    "kvarn_beam_select",
+    "kvarn_beam_reorder",
 )
 
 # Size of the library's fixed decode scratch (KVARN_DECODE_NOALLOC_SCRATCH_BYTES in kvarn.h).
@@ -124,6 +132,13 @@ def _load():
         "kvarn_tree_workspace_bytes": (Z, [D, i32, i32, i32, i32]),
         "kvarn_tree_attention": (i32, [D, i32, i32, i32, P, P, P, P, P, P, i64, P, i32, P, P, P, F,
                                        P, P, Z, P, P]),
+    })
+    sig.update({
+        "kvarn_plan_pages": (i32, [i32, i32, P, P, P, i32, i64, i32, P, P, P, P]),
+        "kvarn_fp16_store": (i32, [i32, i32, i64, P, P, i64, i64, P, P, i64, P, P]),
+        "kvarn_beam_select_workspace_bytes": (Z, [i32, i32, i32, i32]),
+        "kvarn_beam_select": (i32, [i32, i32, i32, i32, P, i32, i64, P, P, i32, P, P, P, P, P, Z, P, P]),
+        "kvarn_beam_reorder": (i32, [D, i32, i32, i32, P, P, P, P, P, i32, P, P, P, P, P, P]),
     })
     for name, (res, args) in sig.items():
         fn = getattr(lib, name)
@@ -493,6 +508,111 @@ def fp16_decode_attention(num_kv_heads: int, q, pool, block_table, seq_lens, out
                                             float(softmax_scale), _ptr(out), _ptr(workspace),
                                             workspace.numel() * workspace.element_size(), _ptr(status),
                                             _stream(stream)), "kvarn_fp16_decode_attention")
+
+
+def plan_pages(seq_lens, block_table, num_pool_pages: int, seq_lens_out, new_lens=None, chunk_len: int = 1,
+               slot_map=None, open_tiles: bool = True, status=None, stream=None):
+    """Extend the block-table rows by the pages that the next tokens need, the lowest ids that no row names.
+    seq_lens, seq_lens_out: int32 [batch]; block_table: int32 [batch, max_pages], written in place; new_lens:
+    int32 [batch] or None (all chunk_len); slot_map: int64 [batch, chunk_len] or None, receives page * 128 +
+    row of every new token or -1.  open_tiles: only full tiles have a page (packed cache) or all (False, fp16
+    cache)."""
+    batch, width = block_table.shape
+    _ptr(seq_lens)
+    dev, i32, row = seq_lens.get_device(), torch.int32, (batch,)
+    _launch(_lib.kvarn_plan_pages, dev, stream, batch, chunk_len, _arg("seq_lens", seq_lens, dev, i32, row),
+            _opt("new_lens", new_lens, dev, i32, row), _arg("block_table", block_table, dev, i32, (batch, width)),
+            width, num_pool_pages, 1 if open_tiles else 0, _arg("seq_lens_out", seq_lens_out, dev, i32, row),
+            _opt("slot_map", slot_map, dev, torch.int64, (batch, chunk_len)), _status_arg(status, dev))
+
+
+def fp16_store(k, v, slot_map, pool, status=None, stream=None):
+    """Write tokens to their slots of the fp16 cache: k, v fp16 [tokens, Hkv, d] (token and head strides taken
+    from the tensors, equal in both); slot_map int64 with one entry a token (any shape); pool fp16 [pages, Hkv,
+    2, 128, d]."""
+    tokens, heads, d = k.shape
+    strides = k.stride()
+    if k.dtype is not torch.float16 or v.dtype is not torch.float16 or v.shape != k.shape or v.stride() != strides \
+            or strides[2] != 1:
+        raise ValueError("k and v must be fp16 [tokens, Hkv, d] with matching strides, channels contiguous")
+    _ptr(k), _ptr(v)
+    dev = k.get_device()
+    if v.get_device() != dev:
+        raise ValueError("v is on %s, k on cuda:%d" % (v.device, dev))
+    if slot_map.numel() != tokens:
+        raise ValueError("slot_map holds %d entries for %d tokens" % (slot_map.numel(), tokens))
+    _launch(_lib.kvarn_fp16_store, dev, stream, d, heads, tokens, k.data_ptr(), v.data_ptr(), strides[0], strides[1],
+            _arg("slot_map", slot_map, dev, torch.int64, slot_map.shape),
+            _arg("pool", pool, dev, torch.float16, (pool.shape[0], heads, 2, 128, d)), pool.shape[0],
+            _status_arg(status, dev))
+
+
+_LOGITS_TYPES = {torch.float16: 0, torch.bfloat16: 1, torch.float32: 2}
+
+
+def beam_select_workspace_bytes(batch: int, beams: int, vocab: int, count: int) -> int:
+    return int(_lib.kvarn_beam_select_workspace_bytes(batch, beams, vocab, count))
+
+
+def alloc_beam_select_workspace(batch: int, beams: int, vocab: int, count: int, device="cuda"):
+    return _alloc_bytes(beam_select_workspace_bytes(max(batch, 1), beams, vocab, count), "beam_select_workspace", device)
+
+
+def beam_select(logits, scores, out_scores, out_parents, out_tokens, workspace, done=None, end_token: int = -1,
+                out_done=None, status=None, stream=None):
+    """The best continuations of every group of beams.  logits: fp16, bf16 or fp32 [batch, beams, vocab], rows at
+    an even stride (a slice of a padded vocabulary is taken as it is); scores: fp32 [batch, beams]; done: bool (or
+    uint8) [batch, beams] or None; out_scores fp32, out_parents and out_tokens int32, out_done bool (or uint8) or
+    None: [batch, count], best first, -inf / -1 / -1 / False where a group has no more candidates."""
+    batch, beams, vocab = logits.shape
+    count = out_scores.shape[-1]
+    _ptr(logits)
+    dev, i32 = logits.get_device(), torch.int32
+    kind, strides = _LOGITS_TYPES.get(logits.dtype), logits.stride()
+    row_stride = strides[1] if beams > 1 else strides[0]
+    if kind is None or (strides[2] != 1 and vocab > 1) or (beams > 1 and batch > 1 and strides[0] != beams * row_stride):
+        raise ValueError("logits must be fp16, bf16 or fp32 [batch, beams, vocab] with tokens contiguous and rows at an "
+                         "even stride, got %s of strides %s" % (logits.dtype, list(strides)))
+    if batch * beams <= 1:
+        row_stride = max(row_stride, vocab)
+    rows, outs = (batch, beams), (batch, count)
+    flag = torch.uint8 if done is not None and done.dtype is torch.uint8 else torch.bool
+    out_flag = torch.uint8 if out_done is not None and out_done.dtype is torch.uint8 else torch.bool
+    _launch(_lib.kvarn_beam_select, dev, stream, batch, beams, vocab, count, logits.data_ptr(), kind, row_stride,
+            _arg("scores", scores, dev, torch.float32, rows), _opt("done", done, dev, flag, rows), end_token,
+            _arg("out_scores", out_scores, dev, torch.float32, outs), _arg("out_parents", out_parents, dev, i32, outs),
+            _arg("out_tokens", out_tokens, dev, i32, outs), _opt("out_done", out_done, dev, out_flag, outs),
+            *_workspace_arg(workspace, dev), _status_arg(status, dev))
+
+
+def beam_reorder(desc: KvarnDesc, parents, seq_lens, block_table, seq_lens_out, block_table_out, partial_k=None,
+                 partial_v=None, partial_k_out=None, partial_v_out=None, status=None, stream=None):
+    """Sequence b * beams + j takes over the state of sequence b * beams + parents[b, j] (-1: none, it becomes
+    empty).  parents: int32 [batch, beams]; seq_lens, seq_lens_out: int32 [batch * beams]; block_table(_out): int32
+    [batch * beams, max_pages]; partial_*: fp16 [batch * beams, Hkv, 128, d0], or one more dimension, layers, before
+    them (all four or none).  The table and the open tiles may be moved within their own buffers."""
+    batch, beams = parents.shape
+    _ptr(parents)
+    dev, i32, half, n = parents.get_device(), torch.int32, torch.float16, batch * beams
+    width = block_table.shape[-1]
+    layers = 0
+    tiles = (partial_k, partial_v, partial_k_out, partial_v_out)
+    if partial_k is not None:
+        shape = (n, desc.num_kv_heads, 128, desc.head_dim)
+        layers = 1
+        if partial_k.dim() == 5:
+            layers = partial_k.shape[0]
+            shape = (layers,) + shape
+        if partial_v is None or partial_k_out is None or partial_v_out is None:
+            raise ValueError("partial_k, partial_v, partial_k_out and partial_v_out go together")
+        tiles = [_arg(name, t, dev, half, shape) for name, t in
+                 zip(("partial_k", "partial_v", "partial_k_out", "partial_v_out"), tiles)]
+    elif any(t is not None for t in tiles):
+        raise ValueError("partial_k, partial_v, partial_k_out and partial_v_out go together")
+    _launch(_lib.kvarn_beam_reorder, dev, stream, ctypes.byref(desc), batch, beams, layers,
+            _arg("parents", parents, dev, i32, (batch, beams)), _arg("seq_lens", seq_lens, dev, i32, (n,)),
+            _arg("seq_lens_out", seq_lens_out, dev, i32, (n,)), _arg("block_table", block_table, dev, i32, (n, width)),
+            _arg("block_table_out", block_table_out, dev, i32, (n, width)), width, *tiles, _status_arg(status, dev))
 
 
 def selftest_wait_timeout(status, stream=None):

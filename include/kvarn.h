@@ -82,6 +82,9 @@ extern "C" {
 #define KVARN_DEV_SEQ_TOO_LONG 2     /* seq_len < 0, or its pages exceed the block table row  */
 #define KVARN_DEV_WAIT_TIMEOUT 4     /* a copy or matrix step was not done in ~2 s: wrong output */
 #define KVARN_DEV_NO_PARTIAL 8       /* a length has a remainder but partial_k/v were NULL   */
+#define KVARN_DEV_NO_PAGES 16        /* the pool has no pages left for some sequences        */
+#define KVARN_DEV_BAD_BEAM 32        /* a parent outside [-1, beams): the beam is empty      */
+#define KVARN_DEV_BAD_LOGITS 64      /* a beam with NaN or +inf (score or logit): left out   */
 
 /* Method constants of one cache.  Fill it with kvarn_desc_from_preset. */
 typedef struct kvarn_desc {
@@ -384,6 +387,95 @@ int kvarn_fp16_decode_attention(int head_dim, int num_kv_heads, int batch, int n
                                 const int32_t* block_table, int max_pages, const int32_t* seq_lens,
                                 float softmax_scale, void* out, void* workspace,
                                 size_t workspace_bytes, int32_t* dev_status, void* stream);
+
+/* ---- Pages planned on the GPU ----
+ * kvarn_plan_pages prepares the tables for the tokens that come next, without a word from the host:
+ * sequence b holds seq_lens[b] tokens, new_lens[b] more will be written.  It extends the sequences'
+ * block-table rows by the pages that they then need and tells every new token's place.
+ *  open_tiles   1: only full tiles have a page (the packed cache, whose open tiles lie outside the pool),
+ *               pages(L) = L / 128; 0: open tiles too (the fp16 cache), pages(L) = ceil(L / 128).
+ *  seq_lens     device int32 [batch]: tokens now; row b of the table names pages(seq_lens[b]) pages.
+ *  new_lens     device int32 [batch] or NULL (all chunk_len): tokens to come, 0..chunk_len (else clamped,
+ *               KVARN_DEV_SEQ_TOO_LONG).
+ *  block_table  device int32 [batch][max_pages]; entries pages(seq_lens[b]) up to the new length's pages are
+ *               written, no others are written or (past pages(seq_lens[b])) read.
+ * A page is free if no row of the call names it (rows may share pages; a row with 0 new tokens keeps its
+ * pages from being given away, one with length 0 gives them back).  Free pages go in ascending order to the
+ * sequences in order.  While the pool lasts: a sequence whose pages, with those wanted by the sequences
+ * before it, exceed the free ones gets none and keeps its length (KVARN_DEV_NO_PAGES); one that needs no
+ * page is always served.  A sequence of negative length, or whose pages would exceed max_pages, is left as
+ * it is (KVARN_DEV_SEQ_TOO_LONG); named pages outside the pool are passed over (KVARN_DEV_BAD_PAGE_ID).
+ *  seq_lens_out device int32 [batch], not seq_lens: seq_lens[b] + new_lens[b], or seq_lens[b] if not served.
+ *  slot_map     device int64 [batch][chunk_len] or NULL: page * 128 + row of token i of sequence b; -1 for
+ *               tokens past new_lens[b], of sequences not served, or of an open tile (open_tiles 1).
+ * The result depends on the arguments alone.  One launch; no workspace.
+ * UNSUPPORTED for batch over 16384, max_pages over 2^23, chunk_len over 2^30 or a pool over 2^23 pages. */
+int kvarn_plan_pages(int batch, int chunk_len, const int32_t* seq_lens, const int32_t* new_lens,
+                     int32_t* block_table, int max_pages, int64_t num_pool_pages, int open_tiles,
+                     int32_t* seq_lens_out, int64_t* slot_map, int32_t* dev_status, void* stream);
+
+/* Write new tokens into the fp16 cache that kvarn_fp16_decode_attention reads.
+ *  k, v       fp16; token t, kv head h, channel c at [t*tok_stride + h*head_stride + c].  Base 16-byte
+ *             aligned, strides multiples of 8 (elements): slices of a fused projection are taken as they are.
+ *  slot_map   device int64 [num_tokens]: page * 128 + row, as kvarn_plan_pages gives it with open_tiles 0;
+ *             negative: the token is not written; past the pool: not written, KVARN_DEV_BAD_PAGE_ID.  Two
+ *             tokens with one slot: which is kept, 16 bytes at a time, is open.
+ *  page_pool  16-byte aligned, [num_pool_pages][Hkv][2][128][head_dim]; only the tokens' rows are written.
+ * head_dim 64 or 128 (else UNSUPPORTED, as num_tokens or num_pool_pages over 2^31 - 1). */
+int kvarn_fp16_store(int head_dim, int num_kv_heads, int64_t num_tokens, const void* k, const void* v,
+                     int64_t tok_stride, int64_t head_stride, const int64_t* slot_map, void* page_pool,
+                     int64_t num_pool_pages, int32_t* dev_status, void* stream);
+
+/* ---- Beam search ----
+ * A group of `beams` sequences searches together; beam k of group b is sequence b*beams + k of the cache. */
+
+#define KVARN_LOGITS_F16 0
+#define KVARN_LOGITS_BF16 1
+#define KVARN_LOGITS_F32 2
+
+/* Workspace bytes of kvarn_beam_select (host only; 0 if invalid). */
+size_t kvarn_beam_select_workspace_bytes(int batch, int beams, int vocab, int count);
+
+/* The `count` best continuations of every group.  Candidate (k, v) of a group has the score
+ *   scores[k] + logits[k][v] - log sum_u exp(logits[k][u]);
+ * a finished beam (done[k] != 0) has one candidate, (k, end_token), with its score as it is; its logits are
+ * not read.  Candidates are ordered by score, equal ones by k, then v.  Sums of exponentials are made in 32
+ * bits a thread and joined in 64, scores are compared in 64: candidates of two beams that are nearer than
+ * about 1e-7 may change places, those of one beam are in the order of their logits exactly.
+ *  logits      fp16, bf16 or fp32 (KVARN_LOGITS_*): token v of row b*beams + k at [row*row_stride + v];
+ *              row_stride >= vocab, any alignment of the type (16-byte aligned rows are read fastest).
+ *              -inf: the token cannot be chosen.  A beam with NaN or +inf among its logits, or as its score,
+ *              has no candidates (KVARN_DEV_BAD_LOGITS); one with score -inf has none and is not read.
+ *  scores      device fp32 [batch][beams];  done: device bytes [batch][beams] or NULL (none is finished).
+ *  end_token   0..vocab-1, or -1 (no token ends a beam; only if done is NULL).
+ *  out_scores fp32, out_parents int32 (beam of the group), out_tokens int32, out_done bytes or NULL (1: the
+ *              parent was finished or the token is end_token): device [batch][count], best first.  Where a
+ *              group has fewer than `count` candidates the rest is -inf, -1, -1, 0.
+ *  workspace   device scratch of kvarn_beam_select_workspace_bytes (16-byte aligned).
+ * Equal arguments give equal results.  UNSUPPORTED for beams over 32, count over 64, vocab over 2^26 or
+ * batch over 2^20. */
+int kvarn_beam_select(int batch, int beams, int vocab, int count, const void* logits, int logits_type,
+                      int64_t row_stride, const float* scores, const uint8_t* done, int end_token,
+                      float* out_scores, int32_t* out_parents, int32_t* out_tokens, uint8_t* out_done,
+                      void* workspace, size_t workspace_bytes, int32_t* dev_status, void* stream);
+
+/* Move the cache's state to the beams that go on: sequence b*beams + j becomes a copy of sequence
+ * b*beams + parents[b][j].  Sealed pages are shared through the table; only table entries, lengths and the
+ * live rows of the open tiles move.
+ *  parents      device int32 [batch][beams]: a beam of the group, or -1: the sequence becomes empty (length 0;
+ *               outside [-1, beams): the same, KVARN_DEV_BAD_BEAM).
+ *  seq_lens, seq_lens_out        device int32 [batch*beams]; not the same buffer.
+ *  block_table, block_table_out  device int32 [batch*beams][max_pages]: entries up to seq_len/128 of the parent
+ *               are written, the others left as they were.
+ *  partial_k/v, partial_k/v_out  fp16 [layers][batch*beams][Hkv][128][d0], 16-byte aligned: rows up to
+ *               seq_len%128 of the parent are written, the others left as they were.  layers 0: not touched.
+ * block_table_out, partial_k_out and partial_v_out may each be the very buffer of their input (a beam that goes
+ * on from itself is then not moved); they must not overlap it otherwise.
+ * UNSUPPORTED for beams over 32, batch*beams over 2^24, layers over 16383. */
+int kvarn_beam_reorder(const kvarn_desc* desc, int batch, int beams, int layers, const int32_t* parents,
+                       const int32_t* seq_lens, int32_t* seq_lens_out, const int32_t* block_table,
+                       int32_t* block_table_out, int max_pages, const void* partial_k, const void* partial_v,
+                       void* partial_k_out, void* partial_v_out, int32_t* dev_status, void* stream);
 
 /* Self-test of the kernels' bounded waits: one thread waits on an mbarrier that nothing
  * completes; after ~2 s the wait gives up and KVARN_DEV_WAIT_TIMEOUT is OR-ed into
