@@ -18,16 +18,18 @@ constexpr int kMaxVocab = 1 << 26;     // beam * vocab + token stays within 31 b
 constexpr int kMergeEntries = 8192;    // candidates that the merge holds in shared memory
 
 // ---- selection: one pass over the logits ----------------------------------------------------
-// A row of logits (one beam) is cut into chunks, one CTA each.  A CTA streams its chunk in tiles held
-// in registers (64 bytes a thread), keeps per-thread sums of exp(x - ref) in 32 bits, and keeps the
-// chunk's `count` best logits in a short list: elements above the list's threshold are appended, the
-// list is cut back to `count` when it grows.  The merge joins the chunks' sums in 64 bits and takes
-// the best candidates off the sorted lists.
+// A row of logits (one beam) is cut into chunks, one CTA each.  A CTA streams its chunk through shared
+// memory; a thread keeps its sum of exp(x - ref) in 32 bits and notes the greatest of every 32 elements.
+// Then a bound is taken from these, below which none of the chunk's `count` best can be, and the few runs of
+// 32 whose greatest reaches it are read again: what reaches the bound goes into a short list, which is cut
+// to the `count` best.  The merge joins the chunks' sums and takes the best candidates off the lists.
 
 constexpr int kThreads = 256, kWarps = kThreads / 32;
+constexpr int kResident = 4;          // CTAs of the streaming kernel on an SM
 constexpr int kWords = 16;             // 32-bit words of a tile that a thread holds
+constexpr int kStages = 2;            // tiles on their way
 constexpr int kCap = 512;              // entries of the list
-constexpr int kPruneAt = 192;          // the list is cut back beyond this many
+constexpr float kFar = 65536.0f;       // references beyond it take the slower path
 constexpr float kStep = 40.0f;         // a thread's reference moves when a logit exceeds it by more
 
 enum DType { kF16 = 0, kBF16 = 1, kF32 = 2 };
@@ -59,6 +61,8 @@ struct F16 {
   static constexpr int kPerWord = 2;
   static constexpr uint32_t kNone = 0xfc00fc00u;  // -inf
   using Elem = uint16_t;
+  static __device__ __forceinline__ float one(Elem x) { return get(x).x; }
+  static __device__ __forceinline__ Elem bits(float x) { return __half_as_ushort(__float2half_rn(x)); }  // x is an element
   static __device__ __forceinline__ float2 get(uint32_t w) { return __half22float2(*reinterpret_cast<__half2*>(&w)); }
   static __device__ __forceinline__ uint32_t max(uint32_t a, uint32_t b) {
     const __half2 m = __hmax2_nan(*reinterpret_cast<__half2*>(&a), *reinterpret_cast<__half2*>(&b));
@@ -69,6 +73,8 @@ struct BF16 {
   static constexpr int kPerWord = 2;
   static constexpr uint32_t kNone = 0xff80ff80u;
   using Elem = uint16_t;
+  static __device__ __forceinline__ float one(Elem x) { return get(x).x; }
+  static __device__ __forceinline__ Elem bits(float x) { return (Elem)(__float_as_uint(x) >> 16); }
   static __device__ __forceinline__ float2 get(uint32_t w) {
     return make_float2(__uint_as_float(w << 16), __uint_as_float(w & 0xffff0000u));
   }
@@ -81,6 +87,8 @@ struct F32 {
   static constexpr int kPerWord = 1;
   static constexpr uint32_t kNone = 0xff800000u;
   using Elem = uint32_t;
+  static __device__ __forceinline__ float one(Elem x) { return __uint_as_float(x); }
+  static __device__ __forceinline__ Elem bits(float x) { return __float_as_uint(x); }
   static __device__ __forceinline__ uint32_t max(uint32_t a, uint32_t b) {
     return __float_as_uint(max_nan(__uint_as_float(a), __uint_as_float(b)));
   }
@@ -110,12 +118,14 @@ struct Tile {
   static constexpr int kLoads = 64 / kBytes;
   static constexpr int kElems = 64 / (int)sizeof(typename T::Elem);
   static constexpr int kSize = kThreads * kElems;
+  static constexpr int kRun = 32 / kElems;                            // tiles of a run of 32 elements
+  static constexpr int kRuns = T::kPerWord == 1 ? 10 : 20;            // runs of a thread that are noted at a time
   uint32_t w[kWords];
 
   // index within the tile of element e of this thread
   static __device__ __forceinline__ int index(int e) { return ((e / kPer) * kThreads + (int)threadIdx.x) * kPer + e % kPer; }
 
-  __device__ __forceinline__ void load(const typename T::Elem* row, int64_t at, int64_t end) {
+  __device__ __forceinline__ void load(const typename T::Elem* row, int at, int end) {
     if (at + kSize <= end) {
 #pragma unroll
       for (int l = 0; l < kLoads; ++l) {
@@ -133,31 +143,39 @@ struct Tile {
       }
       return;
     }
-    // the chunk's last tile: whole loads while they fit, then single elements
+    // The row's last tile: loads past the end are moved back into the row, all of them under way at once, and
+    // their elements replaced.
 #pragma unroll
     for (int l = 0; l < kLoads; ++l) {
-      const int64_t i = at + index(l * kPer);
-      const typename T::Elem* src = row + i;
+      const int i = at + index(l * kPer);
       if constexpr (kBytes == 16) {
         uint4 x = make_uint4(T::kNone, T::kNone, T::kNone, T::kNone);
         if (i + kPer <= end) {
-          x = __ldcs(reinterpret_cast<const uint4*>(src));
+          x = __ldcs(reinterpret_cast<const uint4*>(row + i));
         } else if (i < end) {
           uint32_t v[4] = {T::kNone, T::kNone, T::kNone, T::kNone};
+          typename T::Elem one[kPer];
+#pragma unroll
+          for (int e = 0; e < kPer; ++e) one[e] = row[::min(i + e, end - 1)];
 #pragma unroll
           for (int e = 0; e < kPer; ++e)
-            if (i + e < end) put(v[e / T::kPerWord], e % T::kPerWord, src[e]);
+            if (i + e < end) put(v[e / T::kPerWord], e % T::kPerWord, one[e]);
           x = make_uint4(v[0], v[1], v[2], v[3]);
         }
         w[4 * l] = x.x, w[4 * l + 1] = x.y, w[4 * l + 2] = x.z, w[4 * l + 3] = x.w;
-      } else if constexpr (kBytes == 4) {
-        w[l] = T::kNone;
-#pragma unroll
-        for (int e = 0; e < kPer; ++e)
-          if (i + e < end) put(w[l], e % T::kPerWord, src[e]);
-      } else {
-        if (l % 2 == 0) w[l / 2] = T::kNone;
-        if (i < end) put(w[l / 2], l % 2, *src);
+      } else if constexpr (kPer == 1) {
+        const typename T::Elem x = row[::min(i, end - 1)];
+        if constexpr (T::kPerWord == 1) {
+          w[l] = i < end ? x : T::kNone;
+        } else {
+          const uint32_t v = i < end ? x : T::kNone & 0xffffu;
+          if (l % 2 == 0) w[l / 2] = v;
+          else w[l / 2] |= v << 16;
+        }
+      } else {  // two halves a word
+        const uint32_t x = end >= 2 ? *reinterpret_cast<const uint32_t*>(row + ::min(i, (end & ~1) - 2)) : 0u;
+        w[l] = i + 2 <= end ? x : T::kNone;
+        if (i + 1 == end) put(w[l], 0, row[i]);
       }
     }
   }
@@ -183,20 +201,12 @@ struct Tile {
       return e % 2 == 0 ? f.x : f.y;
     }
   }
-  // sum of exp(x - ref)
-  __device__ __forceinline__ float sum(float ref) const {
-    float2 a = make_float2(0.0f, 0.0f);
-    const float2 r = make_float2(-ref, -ref), l = make_float2(kLog2e, kLog2e);
+  // sum of exp(x - ref) for a reference whose product with log2(e) may pass 32 bits' range
+  __device__ __forceinline__ float sum_far(float ref) const {
+    float a = 0.0f;
 #pragma unroll
-    for (int i = 0; i < kElems / 2; ++i) {
-      float2 x;
-      if constexpr (T::kPerWord == 1) x = make_float2(__uint_as_float(w[2 * i]), __uint_as_float(w[2 * i + 1]));
-      else x = T::get(w[i]);
-      // the difference first: it is exact near the reference, where the sum is made
-      x = mul2(add2(x, r), l);
-      a = add2(a, make_float2(exp2_fast(x.x), exp2_fast(x.y)));
-    }
-    return a.x + a.y;
+    for (int e = 0; e < kElems; ++e) a += exp2_fast((value(e) - ref) * kLog2e);
+    return a;
   }
 };
 
@@ -204,35 +214,140 @@ struct List {
   float2 e[kCap];  // logit, token
   int n;
   float threshold;  // `count` elements seen so far are at least as great; -inf while there are fewer
+  int far;          // a reference is beyond kFar
+};
+
+// Tiles on their way through shared memory: a thread reads the 64 bytes that it copied itself, so that it
+// waits for its own copies only.  Word i of a thread lies in slot[i / 4][thread], part i % 4.
+template <class T, int kBytes>
+struct Ring {
+  using Tl = Tile<T, kBytes>;
+  uint4 slot[kStages][4][kThreads];
+
+  __device__ __forceinline__ void issue(int stage, const typename T::Elem* row, int at, int end) {
+    if (at < end) {
+      const uint32_t to = smem_u32(&slot[stage][0][threadIdx.x]);
+      if (at + Tl::kSize <= end) {
+        const char* src = reinterpret_cast<const char*>(row + at) + threadIdx.x * kBytes;
+#pragma unroll
+        for (int l = 0; l < Tl::kLoads; ++l) {
+          const uint32_t dst = to + (kBytes == 16 ? l : l / 4) * kThreads * 16 + (kBytes == 16 ? 0 : l % 4 * 4);
+          if constexpr (kBytes == 16)
+            asm volatile("cp.async.cg.shared.global [%0], [%1], 16;" ::"r"(dst), "l"(src + l * kThreads * 16) : "memory");
+          else
+            asm volatile("cp.async.ca.shared.global [%0], [%1], 4;" ::"r"(dst), "l"(src + l * kThreads * 4) : "memory");
+        }
+      } else {
+        Tl tile;
+        tile.load(row, at, end);
+        put(stage, tile);
+      }
+    }
+    asm volatile("cp.async.commit_group;" ::: "memory");
+  }
+  __device__ __forceinline__ void put(int stage, const Tl& tile) {
+#pragma unroll
+    for (int i = 0; i < 4; ++i)
+      slot[stage][i][threadIdx.x] = make_uint4(tile.w[4 * i], tile.w[4 * i + 1], tile.w[4 * i + 2], tile.w[4 * i + 3]);
+  }
+  // the copies of all but the newest kStages - 1 tiles have arrived
+  __device__ __forceinline__ void wait() const { asm volatile("cp.async.wait_group %0;" ::"n"(kStages - 1) : "memory"); }
+
+  // element e of thread t
+  __device__ __forceinline__ float value(int stage, int t, int e) const {
+    const int i = e / T::kPerWord;
+    const uint32_t w = reinterpret_cast<const uint32_t*>(&slot[stage][i / 4][t])[i % 4];
+    if constexpr (T::kPerWord == 1) return __uint_as_float(w);
+    else {
+      const float2 f = T::get(w);
+      return e % 2 == 0 ? f.x : f.y;
+    }
+  }
+  __device__ __forceinline__ float top_of(uint32_t m) const {
+    if constexpr (T::kPerWord == 1) return __uint_as_float(m);
+    else {
+      const float2 f = T::get(m);
+      return max_nan(f.x, f.y);
+    }
+  }
+  // The thread's sum of 2^(x log2(e) - base), log2(e) and the argument rounded to 32 bits, and its greatest x
+  // (NaN if there is one).
+  __device__ __forceinline__ float sum(int stage, float base, float& top) const {
+    float2 a = make_float2(0.0f, 0.0f), b = a;
+    const float2 r = make_float2(-base, -base), l = make_float2(kLog2e, kLog2e);
+    const auto put = [&](float2& to, float2 x) {
+      x = fma2(x, l, r);
+      to = add2(to, make_float2(exp2_fast(x.x), exp2_fast(x.y)));
+    };
+    uint32_t m = T::kNone;
+#pragma unroll
+    for (int i = 0; i < 4; ++i) {
+      const uint4 v = slot[stage][i][threadIdx.x];
+      m = T::max(m, T::max(T::max(v.x, v.y), T::max(v.z, v.w)));
+      if constexpr (T::kPerWord == 1) {
+        put(a, make_float2(__uint_as_float(v.x), __uint_as_float(v.y)));
+        put(b, make_float2(__uint_as_float(v.z), __uint_as_float(v.w)));
+      } else {
+        put(a, T::get(v.x));
+        put(b, T::get(v.y));
+        put(a, T::get(v.z));
+        put(b, T::get(v.w));
+      }
+    }
+    top = top_of(m);
+    a = add2(a, b);
+    return a.x + a.y;
+  }
+};
+
+// Sum of exponentials of one thread: sum = sum of 2^(x log2(e) - base) with base = ref log2(e) rounded.
+struct Sum {
+  float ref, base, sum;
+  __device__ __forceinline__ void start() { ref = -CUDART_INF_F, base = 0.0f, sum = 0.0f; }
+  // Sum of exp(x - ref): what the rounding of base took, e^c with c = log(2) (base - ref log2(e)), is given back.
+  // |ref| <= kFar: |c| < 0.005, so 1 + c + c^2/2 is off by less than 2^-25.
+  __device__ __forceinline__ float of_ref() const {
+    const float c = 0.6931472f * fmaf(-ref, kLog2e, base);
+    return fmaf(sum, fmaf(0.5f * c, c, c), sum);
+  }
+  __device__ __forceinline__ void move(float to) {
+    if (ref > -CUDART_INF_F) sum = of_ref() * exp2_fast((ref - to) * kLog2e);
+    ref = to;
+    base = to * kLog2e;
+  }
 };
 
 __device__ __forceinline__ bool better(float xa, int ia, float xb, int ib) { return xa > xb || (xa == xb && ia < ib); }
 
+// Entries of the list that are better than one of them; a warp counts together.
+__device__ __forceinline__ int rank_of(const List& list, int n, float2 e) {
+  int r = 0;
+  for (int j = threadIdx.x & 31; j < n; j += 32) {
+    const float2 o = list.e[j];
+    r += better(o.x, __float_as_int(o.y), e.x, __float_as_int(e.y));
+  }
+  return __reduce_add_sync(~0u, r);
+}
 // Cuts the list's `n` entries (<= kCap, the same value in all threads) to the `count` best, in order.
 __device__ __forceinline__ void prune(List& list, int n, int count) {
-  constexpr int kMine = kCap / kThreads;
-  float2 mine[kMine];
-  int rank[kMine];
-#pragma unroll
-  for (int m = 0; m < kMine; ++m) {
-    const int i = threadIdx.x + m * kThreads;
-    rank[m] = kCap;
-    if (i >= n) continue;
-    mine[m] = list.e[i];
-    int r = 0;
-    for (int j = 0; j < n; ++j) {
-      const float2 o = list.e[j];
-      r += better(o.x, __float_as_int(o.y), mine[m].x, __float_as_int(mine[m].y));
-    }
-    rank[m] = r;
+  const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5;
+  static_assert(kCap <= 64 * kWarps, "a warp's entries, two a lane");
+  float2 first = {}, second = {};
+  int to_first = -1, to_second = -1, kept = 0;
+  for (int i = warp; i < n; i += kWarps, ++kept) {
+    const float2 e = list.e[i];
+    const int r = rank_of(list, n, e), to = r < count ? r : -1;
+    if (kept == lane) first = e, to_first = to;
+    if (kept == lane + 32) second = e, to_second = to;
   }
   __syncthreads();
-#pragma unroll
-  for (int m = 0; m < kMine; ++m)
-    if (rank[m] < count) {
-      list.e[rank[m]] = mine[m];
-      if (rank[m] == count - 1) list.threshold = mine[m].x;
-    }
+  const auto place = [&](float2 e, int to) {
+    if (to < 0) return;
+    list.e[to] = e;
+    if (to == count - 1) list.threshold = e.x;
+  };
+  place(first, to_first);
+  place(second, to_second);
   if (threadIdx.x == 0) {
     list.n = n < count ? n : count;
     if (n < count) list.threshold = -CUDART_INF_F;
@@ -252,7 +367,7 @@ __device__ __forceinline__ uint64_t entry_key(float x, int token) {
 // A tile with more candidates than the list holds (many equal logits, rising ones): the `count`-th
 // greatest of the list's first `have` entries and the tile, bit by bit, then what is not below it.
 template <class Tl>
-__device__ __noinline__ void select_exact(List& list, int have, int count, const Tl& tile, int64_t at, int* counters) {
+__device__ __forceinline__ void select_exact(List& list, int have, int count, const Tl& tile, int at, int* counters) {
   uint64_t cut = 0;
   if (threadIdx.x < 2) counters[threadIdx.x] = 0;
   __syncthreads();
@@ -261,15 +376,18 @@ __device__ __noinline__ void select_exact(List& list, int have, int count, const
     int n = 0;
     for (int i = threadIdx.x; i < have; i += kThreads)
       n += entry_key(list.e[i].x, __float_as_int(list.e[i].y)) >= trial;
+#pragma unroll
     for (int e = 0; e < Tl::kElems; ++e) {
       const float x = tile.value(e);
-      n += x > -CUDART_INF_F && entry_key(x, (int)at + Tl::index(e)) >= trial;
+      n += x > -CUDART_INF_F && entry_key(x, at + Tl::index(e)) >= trial;
     }
     n = __reduce_add_sync(~0u, n);
     int* c = counters + (bit & 1);
     if ((threadIdx.x & 31) == 0 && n > 0) atomicAdd(c, n);
     __syncthreads();
-    if (*c >= count) cut = trial;
+    const int found = *c;
+    if (found >= count) cut = trial;
+    if (found == count) break;
     if (threadIdx.x == 0) counters[(bit & 1) ^ 1] = 0;
     __syncthreads();
   }
@@ -288,12 +406,52 @@ __device__ __noinline__ void select_exact(List& list, int have, int count, const
 #pragma unroll
   for (int m = 0; m < kCap / kThreads; ++m)
     if (keep[m]) append(list, kept[m].x, __float_as_int(kept[m].y));
+#pragma unroll
   for (int e = 0; e < Tl::kElems; ++e) {
     const float x = tile.value(e);
-    const int token = (int)at + Tl::index(e);
+    const int token = at + Tl::index(e);
     if (x > -CUDART_INF_F && entry_key(x, token) >= cut) append(list, x, token);
   }
   __syncthreads();
+}
+
+// The rest of a chunk, from `at` on, where a group of tiles had more candidates than the list holds or a
+// logit beyond kFar.  sum.sum is the sum of exp(x - sum.ref) here.  Returns whether a logit was NaN.
+template <class Tl, class Elem>
+__device__ __noinline__ bool select_slow(List& list, int have, int count, const Elem* row, int at, int end,
+                                         Sum& sum, int* counters) {
+  bool nan = false;
+  if (threadIdx.x == 0) list.n = have;
+  __syncthreads();
+  for (; at < end; at += Tl::kSize) {
+    Tl tile;
+    tile.load(row, at, end);
+    const float top = tile.max(), least = list.threshold;
+    nan |= top != top;
+    if (top > least) {
+#pragma unroll
+      for (int e = 0; e < Tl::kElems; ++e)
+        if (tile.value(e) > least) append(list, tile.value(e), at + Tl::index(e));
+    }
+    if (top > sum.ref + kStep || (top > sum.ref && fabsf(top) > kFar)) {
+      sum.sum = sum.ref > -CUDART_INF_F ? sum.sum * exp2_fast((sum.ref - top) * kLog2e) : 0.0f;
+      sum.ref = top;
+    }
+    if (sum.ref > -CUDART_INF_F) sum.sum += tile.sum_far(sum.ref);
+    __syncthreads();
+    int n = list.n;
+    __syncthreads();
+    if (n > kCap) {
+      select_exact(list, have, count, tile, at, counters);
+      n = count;
+    }
+    if (n > have) {
+      prune(list, n, count);
+      n = n < count ? n : count;
+    }
+    have = n;
+  }
+  return nan;
 }
 
 // A beam that has candidates of its own logits: not finished, its score finite.
@@ -302,9 +460,14 @@ __device__ __forceinline__ bool beam_open(const SelectParams& p, int row) {
 }
 
 template <class T, int kBytes>
-__global__ void __launch_bounds__(kThreads) select_kernel(SelectParams p) {
+__global__ void __launch_bounds__(kThreads, kResident) select_kernel(SelectParams p) {
   using Tl = Tile<T, kBytes>;
+  extern __shared__ __align__(16) uint8_t dynamic_smem[];
+  Ring<T, kBytes>& ring = *reinterpret_cast<Ring<T, kBytes>*>(dynamic_smem);
+  __shared__ typename T::Elem noted[Tl::kRuns][kThreads];
   __shared__ List list;
+  __shared__ int runs[kCap];  // runs to read again: number x kThreads + thread
+  __shared__ int num_runs;
   __shared__ uint32_t warp_key[kWarps];
   __shared__ int counters[2];
   __shared__ float2 warp_sum[kWarps];
@@ -313,152 +476,264 @@ __global__ void __launch_bounds__(kThreads) select_kernel(SelectParams p) {
   if (tid == 0) {
     list.n = 0;
     list.threshold = -CUDART_INF_F;
+    list.far = 0;
+    num_runs = 0;
   }
   grid_dependency_wait();
-  if (!beam_open(p, row)) return;  // the merge does not look at its lists
+  const bool open = beam_open(p, row);
   const typename T::Elem* x = static_cast<const typename T::Elem*>(p.logits) + row * p.row_stride;
-  const int64_t begin = (int64_t)chunk * p.chunk_len;
-  const int64_t end = begin + p.chunk_len < p.vocab ? begin + p.chunk_len : p.vocab;
-  float ref = -CUDART_INF_F, sum = 0.0f;
+  const int begin = chunk * p.chunk_len;
+  const int end = min(begin + p.chunk_len, p.vocab);
+  Sum sum;
+  sum.start();
   int have = 0;
   bool nan = false;
-  Tl next;
-  next.load(x, begin, end);
-  for (int64_t at = begin; at < end; at += Tl::kSize) {
-    const Tl tile = next;
-    if (at + Tl::kSize < end) next.load(x, at + Tl::kSize, end);
-    const float top = tile.max();  // NaN if the tile holds one
-    nan |= top != top;
-    float least;
-    if (at == begin) {
-      // The m-th greatest of each warp's thread maxima, m = ceil(count / 8): the least of them over
-      // the 8 warps has `count` elements at or above it.
-      uint32_t key = order_key(top), mth = 0;
-      for (int m = (p.count + kWarps - 1) / kWarps; m > 0; --m) {
-        mth = __reduce_max_sync(~0u, key);
-        if (lane == __ffs(__ballot_sync(~0u, key == mth)) - 1) key = 0;
-      }
-      if (lane == 0) warp_key[warp] = mth;
-      __syncthreads();
-      mth = warp_key[0];
-      for (int w = 1; w < kWarps; ++w) mth = min(mth, warp_key[w]);
-      least = nextafterf(fmaxf(key_value(mth), -FLT_MAX), -CUDART_INF_F);
-    } else {
-      least = list.threshold;
-    }
-    bool pushed = false;
-    if (top > least) {
-#pragma unroll
-      for (int e = 0; e < Tl::kElems; ++e) {
-        const float v = tile.value(e);
-        if (v > least) append(list, v, (int)at + Tl::index(e));
-      }
-      pushed = true;
-    }
-    if (top > ref + kStep) {
-      sum *= exp2_fast((ref - top) * kLog2e);
-      ref = top;
-    }
-    if (ref > -CUDART_INF_F) sum += tile.sum(ref);
-    if (__syncthreads_or(pushed)) {
-      int n = list.n;
-      __syncthreads();
-      if (n > kCap) {
-        select_exact(list, have, p.count, tile, at, counters);
-        n = list.n;
-        __syncthreads();
-      }
-      if (at == begin || n > kPruneAt) {
-        prune(list, n, p.count);
-        n = n < p.count ? n : p.count;
-      }
-      have = n;
-    }
+  Tl next;  // rows aligned to 2 bytes: a tile in registers before it goes to the ring
+  if constexpr (kBytes == 2) {
+    next.load(x, begin, end);
+  } else {
+    for (int i = 0; i < kStages - 1; ++i) ring.issue(i, x, begin + i * Tl::kSize, end);
   }
-  if (have > 0) {
-    prune(list, have, p.count);
-    have = have < p.count ? have : p.count;
+  if (!open) {  // the merge does not look at its lists
+    asm volatile("cp.async.wait_all;" ::: "memory");
+    return;
   }
-  // threads' sums on one reference
-  float top = ref;
-  for (int d = 16; d > 0; d /= 2) top = fmaxf(top, __shfl_xor_sync(~0u, top, d));
-  if (lane == 0) warp_sum[warp].x = top;
-  __syncthreads();
-  top = warp_sum[0].x;
-  for (int w = 1; w < kWarps; ++w) top = fmaxf(top, warp_sum[w].x);
-  sum = nan ? CUDART_NAN_F : ref > -CUDART_INF_F ? sum * exp2f((ref - top) * kLog2e) : 0.0f;
-  for (int d = 16; d > 0; d /= 2) sum += __shfl_xor_sync(~0u, sum, d);
-  if (lane == 0) warp_sum[warp].y = sum;
-  __syncthreads();
-  if (tid == 0) {
-    for (int w = 1; w < kWarps; ++w) sum += warp_sum[w].y;
-    p.sums[blockIdx.x] = make_float2(top, sum);
-  }
+  // the warp's sums on the greatest of its references
+  const auto warp_total = [&](float ref, float total) {
+    const float top = key_value(__reduce_max_sync(~0u, order_key(ref)));
+    total = nan ? CUDART_NAN_F : ref > -CUDART_INF_F ? total * exp2f((ref - top) * kLog2e) : 0.0f;
+    for (int d = 16; d > 0; d /= 2) total += __shfl_xor_sync(~0u, total, d);
+    if (lane == 0) warp_sum[warp] = make_float2(top, total);
+  };
   float2* out = p.entries + (int64_t)blockIdx.x * p.count;
-  for (int i = tid; i < p.count; i += kThreads)
-    out[i] = i < have ? list.e[i] : make_float2(-CUDART_INF_F, __int_as_float(-1));
+  // the chunk's sum, and the rest of its list after the n best
+  const auto finish = [&](int n) {
+    for (int i = n + tid; i < p.count; i += kThreads) out[i] = make_float2(-CUDART_INF_F, __int_as_float(-1));
+    if (warp != 0) return;
+    const float2 v = lane < kWarps ? warp_sum[lane] : make_float2(-CUDART_INF_F, 0.0f);
+    const float top = key_value(__reduce_max_sync(~0u, order_key(v.x)));
+    float total = v.x > -CUDART_INF_F || v.y != v.y ? v.y * exp2f((v.x - top) * kLog2e) : 0.0f;
+    for (int d = kWarps / 2; d > 0; d /= 2) total += __shfl_xor_sync(~0u, total, d);
+    if (lane == 0) p.sums[blockIdx.x] = make_float2(top, total);
+  };
+  // One part for chunks of up to 20 x 8192 elements (fp32: 10 x 8192), which is nearly all of them.
+  int at = begin, stage = 0;
+  while (at < end) {
+    const int part = at, part_end = min(at + Tl::kRuns * Tl::kRun * Tl::kSize, end);
+    const Sum before = sum;
+    float most = -CUDART_INF_F, run_top = -CUDART_INF_F;
+    for (int t = 0; at < part_end; at += Tl::kSize, ++t, stage = stage == kStages - 1 ? 0 : stage + 1) {
+      if constexpr (kBytes == 2) {
+        ring.put(stage, next);
+        if (at + Tl::kSize < end) next.load(x, at + Tl::kSize, end);
+      } else {
+        ring.issue(stage == 0 ? kStages - 1 : stage - 1, x, at + (kStages - 1) * Tl::kSize, end);
+        ring.wait();
+      }
+      float top;
+      float part_sum = ring.sum(stage, sum.base, top);
+      if (top > sum.ref + kStep) {  // also a thread's first tile
+        sum.move(top);
+        part_sum = ring.sum(stage, sum.base, top);
+      }
+      sum.sum += part_sum;
+      nan |= top != top;
+      run_top = t % Tl::kRun == 0 ? top : fmaxf(run_top, top);
+      noted[t / Tl::kRun][tid] = T::bits(run_top);
+      most = fmaxf(most, top);
+    }
+    // Each warp whose lanes all hold elements takes the m-th greatest of its lanes' greatest ones: with
+    // m x warps >= count, `count` elements are at or above the least of these.
+    const int full = min(kWarps, (part_end - part) / (32 * Tl::kPer));
+    uint32_t key = order_key(most), mth = 0;
+    for (int m = full > 0 ? min(32, (p.count + full - 1) / full) : 0; m > 0; --m) {
+      mth = __reduce_max_sync(~0u, key);
+      if (lane == __ffs(__ballot_sync(~0u, key == mth)) - 1) key = 0;
+    }
+    if (lane == 0) warp_key[warp] = mth;
+    if (fabsf(sum.ref) > kFar && sum.ref > -CUDART_INF_F) list.far = 1;
+    if (part_end == end) warp_total(sum.ref, sum.ref > -CUDART_INF_F ? sum.of_ref() : 0.0f);
+    __syncthreads();
+    float least = list.threshold;
+    if (full * 32 >= p.count) {
+      mth = warp_key[0];
+      for (int w = 1; w < full; ++w) mth = min(mth, warp_key[w]);
+      least = fmaxf(least, nextafterf(fmaxf(key_value(mth), -FLT_MAX), -CUDART_INF_F));
+    }
+    const int tiles = (part_end - part + Tl::kSize - 1) / Tl::kSize;
+    if (most > least) {
+      for (int t = 0; t * Tl::kRun < tiles; ++t)
+        if (T::one(noted[t][tid]) > least) {
+          const int i = atomicAdd(&num_runs, 1);
+          if (i < kCap) runs[i] = t * kThreads + tid;
+        }
+    }
+    __syncthreads();
+    const int again = num_runs;
+    bool slow = again > kCap || list.far != 0;
+    if (!slow) {
+      for (int i = tid; i < again * 32; i += kThreads) {
+        const int r = runs[i / 32], thread = r % kThreads, e = i % Tl::kElems;
+        const int t = r / kThreads * Tl::kRun + i % 32 / Tl::kElems;
+        const int token = part + t * Tl::kSize + ((e / Tl::kPer) * kThreads + thread) * Tl::kPer + e % Tl::kPer;
+        if (token < part_end) {
+          const int back = tiles - t;  // the chunk's last tiles are still in the ring
+          const float v = part_end == end && back <= kStages
+                              ? ring.value(stage - back + (stage < back ? kStages : 0), thread, e)
+                              : T::one(x[token]);
+          if (v > least) append(list, v, token);
+        }
+      }
+    }
+    __syncthreads();
+    const int n = list.n;
+    slow = slow || n > kCap;
+    if (slow) {
+      __syncthreads();
+      sum = before;
+      at = part;
+      break;
+    }
+    if (part_end == end) {
+      grid_launch_dependents();
+      for (int i = warp; i < n; i += kWarps) {
+        const float2 e = list.e[i];
+        const int r = rank_of(list, n, e);
+        if (lane == 0 && r < p.count) out[r] = e;
+      }
+      finish(n);
+      return;
+    }
+    if (tid == 0) num_runs = 0;
+    __syncthreads();
+    prune(list, n, p.count);
+    have = n < p.count ? n : p.count;
+  }
+  // the slow path, for the rest of the chunk
+  asm volatile("cp.async.wait_all;" ::: "memory");
+  sum.sum = sum.ref > -CUDART_INF_F ? sum.of_ref() : 0.0f;
+  nan |= select_slow<Tl>(list, have, p.count, x, at, end, sum, counters);
+  grid_launch_dependents();
+  warp_total(sum.ref, sum.sum);
+  __syncthreads();
+  const int n = list.n;
+  for (int i = tid; i < n; i += kThreads) out[i] = list.e[i];
+  finish(n);
 }
+
+// ---- the merge --------------------------------------------------------------------------------
+// Scores are pairs of floats (hi + lo, |lo| at most half a step of hi: 48 bits): 64-bit arithmetic runs at
+// 1/64 of the 32-bit rate here and took two thirds of the merge's time.
+
+struct Pair {
+  float hi, lo;
+};
+// a + b without an error (Knuth)
+__device__ __forceinline__ Pair two_sum(float a, float b) {
+  const float s = a + b, t = s - a;
+  return {s, (a - (s - t)) + (b - t)};
+}
+__device__ __forceinline__ Pair add(Pair a, Pair b) {
+  Pair s = two_sum(a.hi, b.hi);
+  const Pair t = two_sum(a.lo, b.lo);
+  s = two_sum(s.hi, s.lo + t.hi);
+  return two_sum(s.hi, s.lo + t.lo);
+}
+__device__ __forceinline__ Pair mul(Pair a, Pair b) {
+  const float h = a.hi * b.hi;
+  return two_sum(h, fmaf(a.hi, b.hi, -h) + fmaf(a.hi, b.lo, a.lo * b.hi));
+}
+// exp(d) for -80 <= d.hi <= 80 to 2^-27: d = k log 2 + r, 1 + r exactly, r^2/2 + ... as Taylor's series to the ninth power in
+// 32 bits (at most 0.07, so its rounding is 2^-28 of the result).  log 2 = 2839/4096 + 3.19461849e-5: k times
+// the first part is exact.
+__device__ __forceinline__ Pair exp_pair(Pair d) {
+  const float k = rintf(d.hi * kLog2e);
+  const float r = fmaf(k, -2839.0f / 4096.0f, d.hi);
+  const Pair x = two_sum(r, fmaf(k, -3.194618494530941e-5f, d.lo));
+  float q = 1.0f / 362880.0f;
+  q = fmaf(q, x.hi, 1.0f / 40320.0f);
+  q = fmaf(q, x.hi, 1.0f / 5040.0f);
+  q = fmaf(q, x.hi, 1.0f / 720.0f);
+  q = fmaf(q, x.hi, 1.0f / 120.0f);
+  q = fmaf(q, x.hi, 1.0f / 24.0f);
+  q = fmaf(q, x.hi, 1.0f / 6.0f);
+  q = fmaf(q, x.hi, 0.5f);
+  const Pair s = two_sum(1.0f, x.hi);
+  const float rest = s.lo + fmaf(x.hi * x.hi, q, x.lo * s.hi);
+  const Pair e = two_sum(s.hi, rest);
+  const float scale = __int_as_float(((int)k + 127) << 23);
+  return {e.hi * scale, e.lo * scale};
+}
+// log(s) for 1 <= s <= e^80 to 2^-26: one Newton step from the 32-bit logarithm
+__device__ __forceinline__ Pair log_pair(Pair s) {
+  const float y = logf(s.hi);
+  const Pair t = mul(s, exp_pair({-y, 0.0f}));
+  return two_sum(y, (t.hi - 1.0f) + t.lo);
+}
+__device__ __forceinline__ uint64_t order_key(Pair x) { return ((uint64_t)order_key(x.hi) << 32) | order_key(x.lo); }
 
 constexpr int kMergeThreads = 256, kMergeWarps = kMergeThreads / 32;
 
-__device__ __forceinline__ uint64_t order_key(double x) {
-  const uint64_t b = (uint64_t)__double_as_longlong(x + 0.0);
-  return b >> 63 ? ~b : b | (1ull << 63);
-}
-__device__ __forceinline__ double key_value64(uint64_t k) {
-  return __longlong_as_double((long long)(k >> 63 ? k ^ (1ull << 63) : ~k));
-}
-
-// One CTA a group of beams: log-sum-exp of each beam in 64 bits, then `count` times the best head of
-// the sorted lists.
+// One CTA a group of beams: the log-sum-exp of each beam, the scores of all list entries, then `count`
+// times the best head of the lists, which are in order.  Bound by latency: a warp's rounds of one reduction,
+// one vote and one shared-memory read.
 __global__ void __launch_bounds__(kMergeThreads) select_merge_kernel(SelectParams p) {
-  extern __shared__ float2 entry[];  // [beams * chunks][count]
+  extern __shared__ uint64_t key[];  // [beams * chunks][count]: score, 0: no candidate
   // A candidate's score is offset + (logit - greatest): next to a logit of 1e38 a logarithm would be lost.
-  __shared__ double offset[kMaxBeams];  // score - log(sum exp(logit - greatest)), or a finished beam's score
+  __shared__ Pair offset[kMaxBeams];  // score - log(sum exp(logit - greatest)), or a finished beam's score
   __shared__ float greatest[kMaxBeams];
-  __shared__ int kind[kMaxBeams];       // 0: no candidates, 1: those of its lists, 2: finished
+  __shared__ int kind[kMaxBeams];  // 0: no candidates, 1: those of its lists, 2: finished
+  __shared__ uint32_t won_score[kMaxCount], won_at[kMaxCount];
   const int group = blockIdx.x, tid = threadIdx.x, lane = tid & 31, warp = tid >> 5;
-  const int lists = p.beams * p.chunks;
+  const int lists = p.beams * p.chunks, entries = lists * p.count, per_beam = p.chunks * p.count;
+  uint32_t* place = reinterpret_cast<uint32_t*>(key + entries);  // [beams * chunks][count]: beam * vocab + token
+  int* next = reinterpret_cast<int*>(place + entries);           // [beams * chunks]: entries taken, past 32 lists
   grid_dependency_wait();
-  const float2* src = p.entries + (int64_t)group * lists * p.count;
-  for (int i = tid; i < lists * p.count; i += kMergeThreads) {
-    const int row = group * p.beams + i / (p.count * p.chunks);
-    entry[i] = beam_open(p, row) ? src[i] : make_float2(-CUDART_INF_F, __int_as_float(-1));
-  }
+  const float2* src = p.entries + (int64_t)group * entries;
+  constexpr int kAhead = 4;
+  float2 ahead[kAhead];
+#pragma unroll
+  for (int j = 0; j < kAhead; ++j)
+    if (tid + j * kMergeThreads < entries) ahead[j] = __ldcg(src + tid + j * kMergeThreads);
   for (int k = warp; k < p.beams; k += kMergeWarps) {
     const int row = group * p.beams + k;
+    const float2* s = p.sums + (int64_t)row * p.chunks;
+    const float2 first = lane < p.chunks ? __ldcg(s + lane) : make_float2(-CUDART_INF_F, 0.0f);
     const float score = p.scores[row];
+    const bool finished = p.done != nullptr && p.done[row] != 0;
     int what = 0;
-    double off = 0.0;
+    Pair off = {score, 0.0f};
     float high = 0.0f;
     if (!(score < CUDART_INF_F)) {  // NaN, +inf
       if (lane == 0) flag_error(p.status, KVARN_DEV_BAD_LOGITS);
-    } else if (score > -CUDART_INF_F && p.done != nullptr && p.done[row] != 0) {
+    } else if (score > -CUDART_INF_F && finished) {
       what = 2;
-      off = score;
     } else if (score > -CUDART_INF_F) {
-      const float2* s = p.sums + (int64_t)row * p.chunks;
       float top = -CUDART_INF_F;
       bool bad = false;
       for (int c = lane; c < p.chunks; c += 32) {
-        const float2 v = s[c];
+        const float2 v = c == lane ? first : s[c];
         top = fmaxf(top, v.x);
         bad |= !(v.y < CUDART_INF_F);
       }
-      for (int d = 16; d > 0; d /= 2) top = fmaxf(top, __shfl_xor_sync(~0u, top, d));
+      const uint32_t highest = __reduce_max_sync(~0u, order_key(top));
+      top = key_value(highest);
       bad = __any_sync(~0u, bad);
       if (bad) {
         if (lane == 0) flag_error(p.status, KVARN_DEV_BAD_LOGITS);
       } else if (top > -CUDART_INF_F) {
-        double sum = 0.0;
+        Pair sum = {0.0f, 0.0f};
         for (int c = lane; c < p.chunks; c += 32) {
-          const float2 v = s[c];
-          if (v.x > -CUDART_INF_F) sum += v.x == top ? (double)v.y : (double)v.y * exp((double)v.x - (double)top);
+          const float2 v = c == lane ? first : s[c];
+          const Pair d = two_sum(v.x, -top);
+          if (d.hi > -80.0f) sum = add(sum, mul({v.y, 0.0f}, exp_pair(d)));
         }
-        for (int d = 16; d > 0; d /= 2) sum += __shfl_xor_sync(~0u, sum, d);
+        for (int d = 1; d < 32 && d < p.chunks; d *= 2)
+          sum = add(sum, {__shfl_xor_sync(~0u, sum.hi, d), __shfl_xor_sync(~0u, sum.lo, d)});
         what = 1;
-        off = (double)score - log(sum);
         high = top;
+        const Pair l = log_pair(sum);
+        off = add(off, {-l.hi, -l.lo});
       }
     }
     if (lane == 0) {
@@ -468,63 +743,84 @@ __global__ void __launch_bounds__(kMergeThreads) select_merge_kernel(SelectParam
     }
   }
   __syncthreads();
+  const auto enter = [&](int i, float2 e) {
+    const int k = i / per_beam;
+    uint64_t mine = 0;
+    int t = __float_as_int(e.y);
+    if (kind[k] == 1) {
+      const Pair score = add(offset[k], two_sum(e.x, -greatest[k]));
+      if (t >= 0 && fabsf(score.hi) < CUDART_INF_F) mine = order_key(score);
+    } else if (kind[k] == 2 && i == k * per_beam) {  // one candidate, first of the beam's first list
+      t = p.end_token;
+      mine = order_key(offset[k]);
+    }
+    key[i] = mine;
+    place[i] = (uint32_t)k * (uint32_t)p.vocab + (uint32_t)t;
+  };
+#pragma unroll
+  for (int j = 0; j < kAhead; ++j)
+    if (tid + j * kMergeThreads < entries) enter(tid + j * kMergeThreads, ahead[j]);
+  for (int i = tid + kAhead * kMergeThreads; i < entries; i += kMergeThreads) enter(i, __ldcg(src + i));
+  for (int i = tid; i < lists; i += kMergeThreads) next[i] = 0;
+  __syncthreads();
   if (warp != 0) return;
 
-  // Lane l keeps the heads of lists l, l + 32, ...: next[] counts what was taken of each.
-  extern __shared__ float2 dynamic[];
-  int* next = reinterpret_cast<int*>(dynamic + lists * p.count);
-  for (int i = lane; i < lists; i += 32) next[i] = 0;
-  __syncwarp();
+  // lane l looks after lists l, l + 32, ...: the best of their heads
   uint64_t best = 0;
-  uint32_t best_at = ~0u;  // beam * vocab + token
+  uint32_t best_at = ~0u;
+  int head = lane * p.count, last = lane < lists ? head + p.count : head;  // one list a lane
   int best_list = 0;
   const auto scan = [&]() {
     best = 0, best_at = ~0u;
+    if (lists <= 32) {
+      if (head < last) best = key[head], best_at = place[head];
+      return;
+    }
     for (int i = lane; i < lists; i += 32) {
-      const int k = i / p.chunks, n = next[i];
-      if (kind[k] == 0 || n >= p.count) continue;
-      uint64_t key;
-      uint32_t at;
-      if (kind[k] == 2) {
-        if (i != k * p.chunks || n > 0) continue;  // one candidate, in the first list
-        key = order_key(offset[k]);
-        at = (uint32_t)k * p.vocab + p.end_token;
-      } else {
-        const float2 e = entry[i * p.count + n];
-        if (__float_as_int(e.y) < 0) continue;
-        key = order_key(offset[k] + ((double)e.x - (double)greatest[k]));
-        at = (uint32_t)k * p.vocab + __float_as_int(e.y);
-      }
-      if (key > best || (key == best && at < best_at)) best = key, best_at = at, best_list = i;
+      const int n = next[i];
+      if (n >= p.count) continue;
+      const uint64_t k = key[i * p.count + n];
+      const uint32_t at = place[i * p.count + n];
+      if (k > best || (k == best && at < best_at)) best = k, best_at = at, best_list = i;
     }
   };
   scan();
-  for (int j = 0; j < p.count; ++j) {
+  int found = 0;
+  for (; found < p.count; ++found) {
     const uint32_t hi = __reduce_max_sync(~0u, (uint32_t)(best >> 32));
-    const bool in = (uint32_t)(best >> 32) == hi;
-    const uint32_t lo = __reduce_max_sync(~0u, in ? (uint32_t)best : 0u);
-    const uint32_t at = __reduce_min_sync(~0u, in && (uint32_t)best == lo ? best_at : ~0u);
-    const uint64_t key = ((uint64_t)hi << 32) | lo;
-    const int64_t o = (int64_t)group * p.count + j;
-    const bool found = at != ~0u;
-    if (lane == 0) {
-      const int k = found ? (int)(at / (uint32_t)p.vocab) : -1, token = found ? (int)(at - (uint32_t)k * p.vocab) : -1;
-      p.out_scores[o] = found ? (float)key_value64(key) : -CUDART_INF_F;
-      p.out_parents[o] = k;
-      p.out_tokens[o] = token;
-      if (p.out_done != nullptr) p.out_done[o] = found && (kind[k] == 2 || token == p.end_token);
+    if (hi == 0) break;
+    bool in = (uint32_t)(best >> 32) == hi;
+    uint32_t who = __ballot_sync(~0u, in);
+    if ((who & (who - 1)) != 0) {  // equal in 32 bits: the rest of the score, then the place
+      const uint32_t lo = __reduce_max_sync(~0u, in ? (uint32_t)best : 0u);
+      in = in && (uint32_t)best == lo;
+      const uint32_t at = __reduce_min_sync(~0u, in ? best_at : ~0u);
+      in = in && best_at == at;
     }
-    if (found && best_at == at) {
-      ++next[best_list];
+    if (in) {
+      won_score[found] = hi;
+      won_at[found] = best_at;
+      if (lists <= 32) ++head;
+      else ++next[best_list];
       scan();
     }
   }
+  __syncwarp();
+  for (int j = lane; j < p.count; j += 32) {
+    const int64_t o = (int64_t)group * p.count + j;
+    const bool on = j < found;
+    const int k = on ? (int)(won_at[j] / (uint32_t)p.vocab) : -1, t = on ? (int)(won_at[j] - (uint32_t)k * (uint32_t)p.vocab) : -1;
+    p.out_scores[o] = on ? key_value(won_score[j]) : -CUDART_INF_F;
+    p.out_parents[o] = k;
+    p.out_tokens[o] = t;
+    if (p.out_done != nullptr) p.out_done[o] = on && (kind[k] == 2 || t == p.end_token);
+  }
 }
 
-// Chunks of a row: enough CTAs to fill the GPU when the rows are few, each of some thousand logits at
-// least, and no more lists than the merge holds.
+// Chunks of a row: as many CTAs as run at a time (kResident an SM) when the rows are few, each of some thousand
+// logits at least, and no more lists than the merge holds.
 static int chunks_of(int64_t rows, int beams, int vocab, int count) {
-  int64_t c = (608 + rows - 1) / rows;
+  int64_t c = 152 * kResident / rows;
   const int64_t most = (vocab + 2047) / 2048, held = kMergeEntries / ((int64_t)beams * count);
   c = c < most ? c : most;
   c = c < held ? c : held;
@@ -569,8 +865,12 @@ static cudaLaunchConfig_t config(unsigned grid, unsigned block, size_t smem, cud
 
 template <class T, int kBytes>
 static int launch_select(const SelectParams& p, cudaStream_t stream) {
+  static PerDeviceOnce smem_once;
+  constexpr int kSmem = sizeof(Ring<T, kBytes>);
+  if (const int st = set_smem_limit(smem_once, reinterpret_cast<const void*>(select_kernel<T, kBytes>), kSmem); st != KVARN_OK)
+    return st;
   cudaLaunchAttribute attr;
-  const cudaLaunchConfig_t cfg = config((unsigned)(p.batch * p.beams * (int64_t)p.chunks), kThreads, 0, stream, &attr);
+  const cudaLaunchConfig_t cfg = config((unsigned)(p.batch * p.beams * (int64_t)p.chunks), kThreads, kSmem, stream, &attr);
   return cudaLaunchKernelEx(&cfg, select_kernel<T, kBytes>, p) == cudaSuccess ? KVARN_OK : KVARN_ERR_CUDA;
 }
 
@@ -729,11 +1029,11 @@ int kvarn_beam_select(int batch, int beams, int vocab, int count, const void* lo
   if (st != KVARN_OK) return st;
   const int lists = beams * L.chunks;
   static PerDeviceOnce smem_once;
-  const int most = kMergeEntries * (int)sizeof(float2) + kMergeEntries * 4;
+  const int most = kMergeEntries * 16;
   if (const int e = set_smem_limit(smem_once, reinterpret_cast<const void*>(select_merge_kernel), most); e != KVARN_OK) return e;
   cudaLaunchAttribute attr;
   const cudaLaunchConfig_t cfg =
-      config((unsigned)batch, kMergeThreads, (size_t)lists * count * sizeof(float2) + (size_t)lists * 4, s, &attr);
+      config((unsigned)batch, kMergeThreads, (size_t)lists * count * 12 + (size_t)lists * 4, s, &attr);
   return cudaLaunchKernelEx(&cfg, select_merge_kernel, p) == cudaSuccess ? KVARN_OK : KVARN_ERR_CUDA;
 }
 
