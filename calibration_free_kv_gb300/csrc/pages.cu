@@ -10,11 +10,17 @@ namespace kvarn {
 namespace pages {
 
 constexpr int kThreads = 1024, kWarps = kThreads / 32;
-constexpr int kMaxBatch = 16384;       // needs of all sequences are held in shared memory
-constexpr int kMaxShardLog = 20;       // pages of one CTA's bitmap: 128 KB of shared memory
-constexpr int kMaxCluster = 8;         // the portable cluster size
+constexpr int kMaxBatch = 16384;           // needs of all sequences are held in shared memory
+constexpr int kMaxPoolLog = 23;            // pages of a pool
+constexpr int kMaxBitsLog = 20;            // pages of a CTA's bitmap: 128 KB of shared memory
+constexpr int kCluster = 8;                // CTAs of a large plan: the portable cluster size
 constexpr uint32_t kManyPages = 1u << 30;  // needs are added up to here: no pool has as many pages
-constexpr int kSpan = 1024;            // table entries that a warp marks at a time
+constexpr int kAhead = 8;                  // table entries that a lane has under way
+constexpr int kSpan = 32 * kAhead;         // table entries that a warp marks at a time
+// Slots that the planning CTAs write themselves; more take a kernel of their own.
+constexpr int64_t kSlotsHere = 16384;
+// Up to these sizes one CTA plans.
+constexpr int64_t kSmallTable = 16384, kSmallPool = 65536, kSmallSlots = 4096;
 
 struct PlanParams {
   const int32_t* seq_lens;
@@ -23,24 +29,20 @@ struct PlanParams {
   int32_t* seq_lens_out;
   int64_t* slot_map;
   int32_t* status;
-  int64_t num_pool_pages;
+  int num_pool_pages;
   int batch, chunk, max_pages;
   int open_tiles;
-  int shard_log;  // CTA r of the cluster keeps the bitmap of pages [r << shard_log, (r + 1) << shard_log)
+  int ctas;   // 1, or kCluster
+  int whole;  // a CTA's bitmap is the whole pool's (its marks are joined with the others'), or its share of it
+  int share;  // words of the bitmap that a CTA counts and gives away
 };
 
-__device__ __forceinline__ uint32_t cluster_rank() {
-  uint32_t r;
-  asm volatile("mov.u32 %0, %%cluster_ctarank;" : "=r"(r));
-  return r;
-}
-__device__ __forceinline__ uint32_t cluster_size() {
-  uint32_t r;
-  asm volatile("mov.u32 %0, %%cluster_nctarank;" : "=r"(r));
-  return r;
-}
-// All threads of the cluster: what they wrote (shared and global memory) is seen after it.
-__device__ __forceinline__ void cluster_sync() {
+// All threads of the plan's CTAs: what they wrote (shared and global memory) is seen after it.
+__device__ __forceinline__ void plan_sync(int ctas) {
+  if (ctas == 1) {
+    __syncthreads();
+    return;
+  }
   __syncwarp();
   asm volatile("barrier.cluster.arrive.release.aligned;\n\tbarrier.cluster.wait.acquire.aligned;" ::: "memory");
 }
@@ -50,45 +52,47 @@ __device__ __forceinline__ uint32_t peer_smem(const void* p, uint32_t rank) {
   asm volatile("mapa.shared::cluster.u32 %0, %1, %2;" : "=r"(a) : "r"(smem_u32(p)), "r"(rank));
   return a;
 }
-__device__ __forceinline__ void peer_or(uint32_t addr, uint32_t bits) {
-  asm volatile("red.relaxed.cluster.shared::cluster.or.b32 [%0], %1;" ::"r"(addr), "r"(bits) : "memory");
+__device__ __forceinline__ uint32_t peer_load(uint32_t addr) {
+  uint32_t v;
+  asm volatile("ld.shared::cluster.u32 %0, [%1];" : "=r"(v) : "r"(addr) : "memory");
+  return v;
 }
 __device__ __forceinline__ void peer_store(uint32_t addr, uint32_t v) {
   asm volatile("st.shared::cluster.u32 [%0], %1;" ::"r"(addr), "r"(v) : "memory");
 }
 
-// Tokens and pages of one sequence: the length now, the tokens that come (0 where the sequence cannot
-// be served whatever the pool holds), the pages that its table row names and will name.
+// Pages of a length.
+__device__ __forceinline__ uint32_t pages_of(uint32_t len, int open_tiles) {
+  return (len + (open_tiles ? 0 : kTile - 1)) / kTile;
+}
+__device__ __forceinline__ int held_pages(const PlanParams& p, int len) {
+  return len < 0 ? 0 : (int)min(pages_of(len, p.open_tiles), (uint32_t)p.max_pages);
+}
+
+// One sequence: the tokens that come (-1 where it cannot be served whatever the pool holds), the pages that
+// its table row names and those that it wants.
 struct Request {
-  int64_t len, add;
-  int held, after;
-  int bad;  // KVARN_DEV_SEQ_TOO_LONG
+  int len, add, held, need, bad;
 };
 __device__ __forceinline__ Request request(const PlanParams& p, int b) {
   Request r;
   r.len = p.seq_lens[b];
   r.add = p.new_lens != nullptr ? p.new_lens[b] : p.chunk;
-  r.bad = 0;
-  if (r.add < 0 || r.add > p.chunk) {
-    r.add = r.add < 0 ? 0 : p.chunk;
+  r.bad = r.add < 0 || r.add > p.chunk ? KVARN_DEV_SEQ_TOO_LONG : 0;
+  r.add = min(max(r.add, 0), p.chunk);
+  r.held = held_pages(p, r.len);
+  const uint32_t after = pages_of((uint32_t)r.len + (uint32_t)r.add, p.open_tiles);  // below 2^32: both are below 2^31
+  if (r.len < 0 || after > (uint32_t)p.max_pages) {
     r.bad = KVARN_DEV_SEQ_TOO_LONG;
-  }
-  const int64_t up = p.open_tiles ? 0 : kTile - 1;
-  int64_t held = r.len < 0 ? 0 : (r.len + up) / kTile, after = r.len < 0 ? 0 : (r.len + r.add + up) / kTile;
-  if (r.len < 0 || after > p.max_pages) {
-    r.bad = KVARN_DEV_SEQ_TOO_LONG;
-    held = held < p.max_pages ? held : p.max_pages;
-    after = held;
     r.add = -1;
+    r.need = 0;
+  } else {
+    r.need = (int)after - r.held;
   }
-  r.held = (int)held;
-  r.after = (int)after;
   return r;
 }
 
-__device__ __forceinline__ uint32_t add_pages(uint32_t a, uint32_t b) {
-  return min(a + b, kManyPages);
-}
+__device__ __forceinline__ uint32_t add_pages(uint32_t a, uint32_t b) { return min(a + b, kManyPages); }
 
 // Sequence whose pages hold rank `r`: the first b with end[b] > r.
 __device__ __forceinline__ int owner_of(const uint32_t* end, int batch, uint32_t r) {
@@ -103,15 +107,16 @@ __device__ __forceinline__ int owner_of(const uint32_t* end, int batch, uint32_t
 
 // Slots of tokens first, first + stride, ... of the batch x chunk grid, once the lengths and the table
 // rows are written.
-__device__ __forceinline__ void write_slots(const PlanParams& p, int64_t first, int64_t stride) {
-  const int64_t total = (int64_t)p.batch * p.chunk;
-  for (int64_t t = first; t < total; t += stride) {
-    const int b = (int)(t / p.chunk);
-    const int64_t at = (int64_t)p.seq_lens[b] + (t - (int64_t)b * p.chunk);
-    const int64_t grown = __ldcg(p.seq_lens_out + b);
-    const int64_t page = at / kTile, pages = (grown + (p.open_tiles ? 0 : kTile - 1)) / kTile;
+template <class Index>
+__device__ __forceinline__ void write_slots(const PlanParams& p, Index first, Index stride) {
+  const Index total = (Index)p.batch * (Index)p.chunk;
+  for (Index t = first; t < total; t += stride) {
+    const int b = (int)(t / (Index)p.chunk);
+    const uint32_t at = (uint32_t)p.seq_lens[b] + (uint32_t)(t - (Index)b * (Index)p.chunk);
+    const int grown = __ldcg(p.seq_lens_out + b);
+    const uint32_t page = at / kTile;
     int64_t slot = -1;
-    if (at < grown && page < pages) {
+    if (grown >= 0 && at < (uint32_t)grown && page < pages_of(grown, p.open_tiles)) {
       const int32_t id = __ldcg(p.block_table + (int64_t)b * p.max_pages + page);
       if (id >= 0 && id < p.num_pool_pages) slot = (int64_t)id * kTile + at % kTile;
       else flag_error(p.status, KVARN_DEV_BAD_PAGE_ID);
@@ -120,108 +125,126 @@ __device__ __forceinline__ void write_slots(const PlanParams& p, int64_t first, 
   }
 }
 
-// One cluster plans the whole batch.  The pages that the table rows name are marked in a bitmap of the
-// pool that lies in the cluster's shared memory (a shard per CTA); its zero bits, in ascending order,
-// go to the sequences in order.
+// One CTA, or a cluster of them, plans the whole batch.  The pages that the table rows name are marked in a
+// bitmap of the pool in shared memory; its zero bits, in ascending order, go to the sequences in order.
+// Bound by latency: a chain of loads, marks, two counts and the writes, with a meeting of all threads
+// between them.
 __global__ void __launch_bounds__(kThreads) plan_kernel(PlanParams p) {
   extern __shared__ uint32_t smem[];
-  const uint32_t rank = cluster_rank(), ctas = cluster_size();
-  const int tid = threadIdx.x, lane = tid & 31, warp = tid >> 5;
-  const int words = 1 << (p.shard_log - 5);
+  __shared__ uint32_t warp_sum[kWarps], warp_free[kWarps];
+  __shared__ uint32_t cta_free[kCluster];
+  __shared__ uint32_t served_sum;
+  const int rank = blockIdx.x, tid = threadIdx.x, lane = tid & 31, warp = tid >> 5, warps = blockDim.x / 32;
+  const int words = p.whole ? (p.num_pool_pages + 31) / 32 : p.share;
+  const int first_word = p.whole ? 0 : rank * p.share;  // of the pool, at bitmap[0]
   uint32_t* bitmap = smem;
   uint32_t* end = smem + words;  // [batch] pages wanted by sequences 0..b
-  __shared__ uint32_t warp_sum[kWarps];
-  __shared__ uint32_t cta_free[kMaxCluster];
-  __shared__ uint32_t served_sum;
-
-  // pages past the pool's end count as used
-  const int64_t base = (int64_t)rank << p.shard_log;
-  for (int w = tid; w < words; w += kThreads) {
-    const int64_t left = p.num_pool_pages - base - 32 * (int64_t)w;
+  for (int w = tid; w < words; w += blockDim.x) {
+    // pages past the pool's end count as used
+    const int left = p.num_pool_pages - 32 * (first_word + w);
     bitmap[w] = left >= 32 ? 0u : left <= 0 ? ~0u : ~0u << left;
   }
+  if (tid == 0) served_sum = 0;
+  __syncthreads();
   grid_dependency_wait();
-  cluster_sync();
+  const int per = (p.batch + blockDim.x - 1) / blockDim.x;  // sequences of a thread, of every CTA
+  const Request mine = tid < p.batch ? request(p, tid) : Request{0, 0, 0, 0, 0};  // of thread tid where per is 1
 
-  // mark what the rows name
+  // mark what the rows name: a CTA's rows in a bitmap of the whole pool, or all rows in its share of it
   const int spans = (p.max_pages + kSpan - 1) / kSpan;
+  const int64_t items = (int64_t)p.batch * spans;
+  const int lines = p.whole ? p.ctas : 1;
   int flags = 0;
-  for (int64_t it = (int64_t)warp * ctas + rank; it < (int64_t)p.batch * spans; it += (int64_t)ctas * kWarps) {
-    const int b = (int)(it / spans);
-    const int from = (int)(it - (int64_t)b * spans) * kSpan;
-    const Request r = request(p, b);
-    const int to = min(r.held, from + kSpan);
+  for (int64_t it = (int64_t)warp * lines + (p.whole ? rank : 0); it < items; it += (int64_t)warps * lines) {
+    const int b = spans == 1 ? (int)it : (int)(it / spans);
+    const int from = (int)(it - (int64_t)b * spans) * kSpan + lane;
+    const int held = held_pages(p, p.seq_lens[b]);
     const int32_t* row = p.block_table + (int64_t)b * p.max_pages;
-    for (int i = from + lane; i < to; i += 32) {
-      const int32_t id = row[i];
-      if (id >= 0 && id < p.num_pool_pages)
-        peer_or(peer_smem(bitmap + ((id & ((1 << p.shard_log) - 1)) >> 5), (uint32_t)id >> p.shard_log), 1u << (id & 31));
-      else
+    int32_t id[kAhead];
+#pragma unroll
+    for (int j = 0; j < kAhead; ++j) id[j] = from + 32 * j < held ? row[from + 32 * j] : 0;
+#pragma unroll
+    for (int j = 0; j < kAhead; ++j) {
+      if (from + 32 * j >= held) continue;
+      if (id[j] < 0 || id[j] >= p.num_pool_pages) {
         flags |= KVARN_DEV_BAD_PAGE_ID;
+        continue;
+      }
+      const int w = id[j] / 32 - first_word;
+      if (w >= 0 && w < words) atomicOr(bitmap + w, 1u << (id[j] % 32));
     }
   }
 
   // pages wanted, added up over the sequences (every CTA by itself)
-  const int per = (p.batch + kThreads - 1) / kThreads;
-  uint32_t mine = 0;
+  uint32_t wanted = 0;
   for (int j = 0; j < per; ++j) {
     const int b = tid * per + j;
     if (b < p.batch) {
-      const Request r = request(p, b);
+      const Request r = per == 1 ? mine : request(p, b);
       flags |= r.bad;
-      mine = add_pages(mine, (uint32_t)(r.after - r.held));
-      end[b] = mine;
+      wanted = add_pages(wanted, (uint32_t)r.need);
+      end[b] = wanted;
     }
   }
-  uint32_t scan = mine;
+  uint32_t scan = wanted;
   for (int d = 1; d < 32; d *= 2) {
     const uint32_t o = __shfl_up_sync(~0u, scan, d);
     if (lane >= d) scan = add_pages(scan, o);
   }
   if (lane == 31) warp_sum[warp] = scan;
-  if (tid == 0) served_sum = 0;
   __syncthreads();
-  uint32_t before = 0;
-  for (int w = 0; w < warp; ++w) before = add_pages(before, warp_sum[w]);
-  const uint32_t up = __shfl_up_sync(~0u, scan, 1);
-  if (lane > 0) before = add_pages(before, up);
+  uint32_t before = __shfl_up_sync(~0u, scan, 1);
+  if (lane == 0) before = 0;
+  uint32_t others = lane < warp ? warp_sum[lane] : 0u;  // sums of the warps before this one
+  for (int d = 16; d > 0; d /= 2) others = add_pages(others, __shfl_xor_sync(~0u, others, d));
+  before = add_pages(before, others);
   for (int j = 0; j < per; ++j) {
     const int b = tid * per + j;
     if (b < p.batch) end[b] = add_pages(end[b], before);
   }
-  cluster_sync();
+  plan_sync(p.ctas);
 
-  // free pages of this CTA's shard: a run of words per warp
-  const int run = (words + kWarps - 1) / kWarps;
-  const int w0 = warp * run, w1 = min(words, w0 + run);
+  // Free pages of this CTA's share of the pool, by warps: a run of words each.
+  const int s0 = p.whole ? min(rank * p.share, words) : 0, s1 = min(s0 + p.share, words);
+  const int run = (s1 - s0 + warps - 1) / warps;
+  const int w0 = min(s0 + warp * run, s1), w1 = min(w0 + run, s1);
   uint32_t zeros = 0;
-  for (int w = w0 + lane; w < w1; w += 32) zeros += __popc(~bitmap[w]);
-  zeros = __reduce_add_sync(~0u, zeros);
-  __syncthreads();  // warp_sum is read above
-  if (lane == 0) warp_sum[warp] = zeros;
-  __syncthreads();
-  if (warp == 0) {
-    const uint32_t all = __reduce_add_sync(~0u, warp_sum[lane]);
-    if (lane < ctas) peer_store(peer_smem(cta_free + rank, lane), all);
+  for (int w = w0 + lane; w < w1; w += 32) {
+    uint32_t used = bitmap[w];
+    if (p.whole && p.ctas > 1) {
+      for (int c = 1; c < kCluster; ++c) used |= peer_load(peer_smem(bitmap + w, (rank + c) % kCluster));
+      bitmap[w] = used;  // no other CTA reads this CTA's share here
+    }
+    zeros += __popc(~used);
   }
-  cluster_sync();
-  uint32_t free_pages = 0, first = 0;
-  for (uint32_t c = 0; c < ctas; ++c) {
-    if (c == rank) first = free_pages;
-    free_pages += cta_free[c];
+  zeros = __reduce_add_sync(~0u, zeros);
+  if (lane == 0) warp_free[warp] = zeros;
+  __syncthreads();
+  const uint32_t counted = lane < warps ? warp_free[lane] : 0u;
+  const uint32_t in_cta = __reduce_add_sync(~0u, counted);
+  uint32_t free_pages = in_cta, first = __reduce_add_sync(~0u, lane < warp ? counted : 0u);
+  if (p.ctas > 1) {
+    if (tid < p.ctas) peer_store(peer_smem(cta_free + rank, tid), in_cta);
+    plan_sync(p.ctas);
+    const uint32_t of = lane < p.ctas ? cta_free[lane] : 0u;
+    free_pages = __reduce_add_sync(~0u, of);
+    first += __reduce_add_sync(~0u, lane < rank ? of : 0u);
   }
 
   // Sequences are served in order while their pages last; one that needs none always is.
   uint32_t most = 0;
-  for (int b = tid; b < p.batch; b += kThreads)
-    if (end[b] <= free_pages) most = max(most, end[b]);
-  most = __reduce_max_sync(~0u, most);
-  if (lane == 0 && most > 0) atomicMax(&served_sum, most);
-  __syncthreads();
-  const uint32_t taken = served_sum;
-  for (int w = 0; w < warp; ++w) first += warp_sum[w];
-  for (int w = w0; w < w1 && first < taken; w += 32) {
-    uint32_t z = w + lane < w1 ? ~bitmap[w + lane] : 0u;
+  if (end[p.batch - 1] <= free_pages) {
+    most = end[p.batch - 1];
+  } else {
+    for (int b = tid; b < p.batch; b += blockDim.x)
+      if (end[b] <= free_pages) most = max(most, end[b]);
+    most = __reduce_max_sync(~0u, most);
+    if (lane == 0 && most > 0) atomicMax(&served_sum, most);
+    __syncthreads();
+    most = served_sum;
+  }
+  for (int w = w0; w < w1 && first < most; w += 32) {
+    const uint32_t z = w + lane < w1 ? ~bitmap[w + lane] : 0u;
     const uint32_t n = __popc(z);
     uint32_t at = n;
     for (int d = 1; d < 32; d *= 2) {
@@ -229,26 +252,52 @@ __global__ void __launch_bounds__(kThreads) plan_kernel(PlanParams p) {
       if (lane >= d) at += o;
     }
     const uint32_t all = __shfl_sync(~0u, at, 31);
-    at += first - n;
-    for (; z != 0u && at < taken; z &= z - 1, ++at) {
-      const int b = owner_of(end, p.batch, at);
-      const uint32_t start = b > 0 ? end[b - 1] : 0u;
-      const Request r = request(p, b);
-      p.block_table[(int64_t)b * p.max_pages + r.held + (at - start)] =
-          (int32_t)(base + 32 * (int64_t)(w + lane) + (__ffs(z) - 1));
+    at -= n;
+    const uint32_t give = min(all, most - first);
+    for (uint32_t i0 = 0; i0 < give; i0 += 32) {
+      // zero bit i of the warp's 32 words: the last lane with `at` <= i has it, then its bit by halves
+      const uint32_t i = i0 + lane;
+      int of = 0;
+      for (int d = 16; d > 0; d /= 2)
+        if (__shfl_sync(~0u, at, of + d) <= i) of += d;
+      const uint32_t bits = __shfl_sync(~0u, z, of);
+      uint32_t k = i - __shfl_sync(~0u, at, of);
+      int bit = 0;
+      for (int d = 16; d > 0; d /= 2) {
+        const uint32_t low = __popc(bits >> bit & ((1u << d) - 1));
+        if (k >= low) k -= low, bit += d;
+      }
+      if (i < give) {
+        const int b = owner_of(end, p.batch, first + i);
+        const uint32_t start = b > 0 ? end[b - 1] : 0u;
+        p.block_table[(int64_t)b * p.max_pages + held_pages(p, p.seq_lens[b]) + (first + i - start)] =
+            32 * (first_word + w + of) + bit;
+      }
     }
     first += all;
   }
-  for (int b = (int)rank * kThreads + tid; b < p.batch; b += (int)ctas * kThreads) {
-    const Request r = request(p, b);
-    const bool served = r.after == r.held || end[b] <= free_pages;
-    if (!served) flags |= KVARN_DEV_NO_PAGES;
-    p.seq_lens_out[b] = (int32_t)(r.len + (served && r.add > 0 ? r.add : 0));
+  if (rank == 0) {
+    for (int j = 0; j < per; ++j) {
+      const int b = per == 1 ? tid : tid + j * blockDim.x;
+      if (b >= p.batch) continue;
+      const Request r = per == 1 ? mine : request(p, b);
+      const bool served = r.need == 0 || end[b] <= free_pages;
+      if (!served) flags |= KVARN_DEV_NO_PAGES;
+      p.seq_lens_out[b] = r.len + (served ? max(r.add, 0) : 0);
+    }
   }
   if (flags != 0) flag_error(p.status, flags);
-  if (p.slot_map == nullptr) return;
-  cluster_sync();
-  write_slots(p, (int64_t)rank * kThreads + tid, (int64_t)ctas * kThreads);
+  if (p.slot_map == nullptr || p.batch * (int64_t)p.chunk > kSlotsHere) return;
+  plan_sync(p.ctas);
+  write_slots<uint32_t>(p, rank * blockDim.x + tid, p.ctas * blockDim.x);
+}
+
+// The slots of a large plan, over the whole GPU.
+__global__ void __launch_bounds__(256) plan_slots_kernel(PlanParams p) {
+  grid_dependency_wait();
+  const uint64_t first = blockIdx.x * 256ull + threadIdx.x, stride = gridDim.x * 256ull;
+  if ((uint64_t)p.batch * p.chunk + stride < (1ull << 32)) write_slots<uint32_t>(p, (uint32_t)first, (uint32_t)stride);
+  else write_slots<uint64_t>(p, first, stride);
 }
 
 struct StoreParams {
@@ -311,7 +360,7 @@ int kvarn_plan_pages(int batch, int chunk_len, const int32_t* seq_lens, const in
                      int32_t* dev_status, void* stream) {
   if (batch < 0 || chunk_len < 1 || max_pages < 1 || num_pool_pages < 1) return KVARN_ERR_INVALID_ARG;
   if (batch > kMaxBatch || max_pages > (1 << 23) || chunk_len > (1 << 30) ||
-      num_pool_pages > ((int64_t)kMaxCluster << kMaxShardLog))
+      num_pool_pages > (1 << kMaxPoolLog))
     return KVARN_ERR_UNSUPPORTED;
   if (batch == 0) return KVARN_OK;
   if (seq_lens == nullptr || block_table == nullptr || seq_lens_out == nullptr || seq_lens_out == seq_lens)
@@ -323,32 +372,44 @@ int kvarn_plan_pages(int batch, int chunk_len, const int32_t* seq_lens, const in
   p.seq_lens_out = seq_lens_out;
   p.slot_map = slot_map;
   p.status = dev_status;
-  p.num_pool_pages = num_pool_pages;
+  p.num_pool_pages = (int)num_pool_pages;
   p.batch = batch;
   p.chunk = chunk_len;
   p.max_pages = max_pages;
   p.open_tiles = open_tiles != 0;
-  const int ctas = kMaxCluster;
-  p.shard_log = 5;
-  while (((int64_t)ctas << p.shard_log) < num_pool_pages) ++p.shard_log;
-  const int smem = (1 << (p.shard_log - 3)) + 4 * batch;
+  // One CTA where there is little to read, mark and write: the CTAs of a cluster meet three times.
+  const int64_t slots = slot_map != nullptr ? (int64_t)batch * chunk_len : 0;
+  const bool small = (int64_t)batch * max_pages <= kSmallTable && num_pool_pages <= kSmallPool &&
+                     (slots <= kSmallSlots || slots > kSlotsHere);
+  p.ctas = small ? 1 : kCluster;
+  p.whole = num_pool_pages <= (1 << kMaxBitsLog);
+  const int words = (int)((num_pool_pages + 31) / 32);
+  p.share = (words + p.ctas - 1) / p.ctas;
+  const int smem = 4 * ((p.whole ? words : p.share) + batch);
   static PerDeviceOnce smem_once;
   const void* fn = reinterpret_cast<const void*>(plan_kernel);
-  if (const int st = set_smem_limit(smem_once, fn, (1 << (kMaxShardLog - 3)) + 4 * kMaxBatch); st != KVARN_OK) return st;
+  if (const int st = set_smem_limit(smem_once, fn, (1 << (kMaxBitsLog - 3)) + 4 * kMaxBatch); st != KVARN_OK) return st;
   cudaLaunchAttribute attr[2];
   attr[0].id = cudaLaunchAttributeProgrammaticStreamSerialization;
   attr[0].val.programmaticStreamSerializationAllowed = 1;
   attr[1].id = cudaLaunchAttributeClusterDimension;
-  attr[1].val.clusterDim.x = ctas;
+  attr[1].val.clusterDim.x = p.ctas;
   attr[1].val.clusterDim.y = attr[1].val.clusterDim.z = 1;
   cudaLaunchConfig_t cfg = {};
-  cfg.gridDim = dim3(ctas);
+  cfg.gridDim = dim3(p.ctas);
   cfg.blockDim = dim3(kThreads);
   cfg.dynamicSmemBytes = smem;
   cfg.stream = static_cast<cudaStream_t>(stream);
   cfg.attrs = attr;
-  cfg.numAttrs = 2;
-  return cudaLaunchKernelEx(&cfg, plan_kernel, p) == cudaSuccess ? KVARN_OK : KVARN_ERR_CUDA;
+  cfg.numAttrs = p.ctas > 1 ? 2 : 1;
+  if (cudaLaunchKernelEx(&cfg, plan_kernel, p) != cudaSuccess) return KVARN_ERR_CUDA;
+  if (slots <= kSlotsHere) return KVARN_OK;
+  const int64_t grid = (slots + 1023) / 1024;
+  cfg.gridDim = dim3((unsigned)(grid < 152 * 8 ? grid : 152 * 8));
+  cfg.blockDim = dim3(256);
+  cfg.dynamicSmemBytes = 0;
+  cfg.numAttrs = 1;
+  return cudaLaunchKernelEx(&cfg, plan_slots_kernel, p) == cudaSuccess ? KVARN_OK : KVARN_ERR_CUDA;
 }
 
 int kvarn_fp16_store(int head_dim, int num_kv_heads, int64_t num_tokens, const void* k, const void* v,
