@@ -340,8 +340,13 @@ __global__ void __launch_bounds__(kStoreThreads) store_kernel(StoreParams p) {
       to[u] = ((((slot / kTile) * p.num_kv_heads + h) * 2 + kv) * kTile + slot % kTile) * p.dim + 8 * c;
     }
 #pragma unroll
-    for (int u = 0; u < kStoreUnroll; ++u)
-      if (to[u] >= 0) *reinterpret_cast<uint4*>(p.pool + to[u]) = x[u];
+    for (int u = 0; u < kStoreUnroll; ++u) {
+      if (to[u] < 0) continue;
+      uint4* dst = reinterpret_cast<uint4*>(p.pool + to[u]);
+      // prompts pass through the L2 cache (16384 tokens of 8 x 128: 19.0 -> 18.0 us), a step's tokens stay
+      if (p.per_cta > 1) __stcs(dst, x[u]);
+      else *dst = x[u];
+    }
   }
 }
 

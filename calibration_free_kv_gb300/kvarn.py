@@ -343,7 +343,7 @@ def _launch(fn, device, stream, *args):
     """Call fn(*args, stream) with CUDA device `device` current, on `stream` or the device's current
     stream."""
     raw = torch._C._cuda_getCurrentRawStream(device) if stream is None else stream.cuda_stream
-    if torch.cuda.current_device() == device:
+    if torch._C._cuda_getDevice() == device:
         status = fn(*args, raw)
     else:
         with torch.cuda.device(device):
@@ -530,21 +530,20 @@ def fp16_store(k, v, slot_map, pool, status=None, stream=None):
     """Write tokens to their slots of the fp16 cache: k, v fp16 [tokens, Hkv, d] (token and head strides taken
     from the tensors, equal in both); slot_map int64 with one entry a token (any shape); pool fp16 [pages, Hkv,
     2, 128, d]."""
-    tokens, heads, d = k.shape
-    strides = k.stride()
-    if k.dtype is not torch.float16 or v.dtype is not torch.float16 or v.shape != k.shape or v.stride() != strides \
-            or strides[2] != 1:
+    tokens, heads, d = shape = k.shape
+    strides, dev = k.stride(), k.get_device()
+    if not (k.dtype is torch.float16 and v.dtype is torch.float16 and v.shape == shape and v.stride() == strides
+            and strides[2] == 1):
         raise ValueError("k and v must be fp16 [tokens, Hkv, d] with matching strides, channels contiguous")
-    _ptr(k), _ptr(v)
-    dev = k.get_device()
-    if v.get_device() != dev:
+    if dev < 0 or v.get_device() != dev:
+        _ptr(k), _ptr(v)
         raise ValueError("v is on %s, k on cuda:%d" % (v.device, dev))
     if slot_map.numel() != tokens:
         raise ValueError("slot_map holds %d entries for %d tokens" % (slot_map.numel(), tokens))
+    pages = pool.shape[0]
     _launch(_lib.kvarn_fp16_store, dev, stream, d, heads, tokens, k.data_ptr(), v.data_ptr(), strides[0], strides[1],
             _arg("slot_map", slot_map, dev, torch.int64, slot_map.shape),
-            _arg("pool", pool, dev, torch.float16, (pool.shape[0], heads, 2, 128, d)), pool.shape[0],
-            _status_arg(status, dev))
+            _arg("pool", pool, dev, torch.float16, (pages, heads, 2, 128, d)), pages, _status_arg(status, dev))
 
 
 _LOGITS_TYPES = {torch.float16: 0, torch.bfloat16: 1, torch.float32: 2}
@@ -595,24 +594,22 @@ def beam_reorder(desc: KvarnDesc, parents, seq_lens, block_table, seq_lens_out, 
     _ptr(parents)
     dev, i32, half, n = parents.get_device(), torch.int32, torch.float16, batch * beams
     width = block_table.shape[-1]
-    layers = 0
-    tiles = (partial_k, partial_v, partial_k_out, partial_v_out)
-    if partial_k is not None:
+    layers, k, v, k_out, v_out = 0, partial_k, partial_v, partial_k_out, partial_v_out
+    if k is not None and v is not None and k_out is not None and v_out is not None:
         shape = (n, desc.num_kv_heads, 128, desc.head_dim)
         layers = 1
-        if partial_k.dim() == 5:
-            layers = partial_k.shape[0]
+        if k.dim() == 5:
+            layers = k.shape[0]
             shape = (layers,) + shape
-        if partial_v is None or partial_k_out is None or partial_v_out is None:
-            raise ValueError("partial_k, partial_v, partial_k_out and partial_v_out go together")
-        tiles = [_arg(name, t, dev, half, shape) for name, t in
-                 zip(("partial_k", "partial_v", "partial_k_out", "partial_v_out"), tiles)]
-    elif any(t is not None for t in tiles):
+        k, v = _arg("partial_k", k, dev, half, shape), _arg("partial_v", v, dev, half, shape)
+        k_out, v_out = _arg("partial_k_out", k_out, dev, half, shape), _arg("partial_v_out", v_out, dev, half, shape)
+    elif not (k is None and v is None and k_out is None and v_out is None):
         raise ValueError("partial_k, partial_v, partial_k_out and partial_v_out go together")
     _launch(_lib.kvarn_beam_reorder, dev, stream, ctypes.byref(desc), batch, beams, layers,
             _arg("parents", parents, dev, i32, (batch, beams)), _arg("seq_lens", seq_lens, dev, i32, (n,)),
             _arg("seq_lens_out", seq_lens_out, dev, i32, (n,)), _arg("block_table", block_table, dev, i32, (n, width)),
-            _arg("block_table_out", block_table_out, dev, i32, (n, width)), width, *tiles, _status_arg(status, dev))
+            _arg("block_table_out", block_table_out, dev, i32, (n, width)), width, k, v, k_out, v_out,
+            _status_arg(status, dev))
 
 
 def selftest_wait_timeout(status, stream=None):
