@@ -26,8 +26,8 @@ constexpr int kMergeEntries = 8192;    // candidates that the merge holds in sha
 
 constexpr int kThreads = 256, kWarps = kThreads / 32;
 constexpr int kResident = 4;          // CTAs of the streaming kernel on an SM
-constexpr int kWords = 16;             // 32-bit words of a tile that a thread holds
-constexpr int kStages = 2;            // tiles on their way
+constexpr int kWords = 8;              // 32-bit words of a tile that a thread holds
+constexpr int kStages = 3;            // tiles on their way
 constexpr int kCap = 512;              // entries of the list
 constexpr float kFar = 65536.0f;       // references beyond it take the slower path
 constexpr float kStep = 40.0f;         // a thread's reference moves when a logit exceeds it by more
@@ -115,8 +115,8 @@ __device__ __forceinline__ float key_value(uint32_t k) {
 template <class T, int kBytes>
 struct Tile {
   static constexpr int kPer = kBytes / (int)sizeof(typename T::Elem);         // elements of a load
-  static constexpr int kLoads = 64 / kBytes;
-  static constexpr int kElems = 64 / (int)sizeof(typename T::Elem);
+  static constexpr int kLoads = 4 * kWords / kBytes;
+  static constexpr int kElems = 4 * kWords / (int)sizeof(typename T::Elem);
   static constexpr int kSize = kThreads * kElems;
   static constexpr int kRun = 32 / kElems;                            // tiles of a run of 32 elements
   static constexpr int kRuns = T::kPerWord == 1 ? 10 : 20;            // runs of a thread that are noted at a time
@@ -217,12 +217,12 @@ struct List {
   int far;          // a reference is beyond kFar
 };
 
-// Tiles on their way through shared memory: a thread reads the 64 bytes that it copied itself, so that it
+// Tiles on their way through shared memory: a thread reads the words that it copied itself, so that it
 // waits for its own copies only.  Word i of a thread lies in slot[i / 4][thread], part i % 4.
 template <class T, int kBytes>
 struct Ring {
   using Tl = Tile<T, kBytes>;
-  uint4 slot[kStages][4][kThreads];
+  uint4 slot[kStages][kWords / 4][kThreads];
 
   __device__ __forceinline__ void issue(int stage, const typename T::Elem* row, int at, int end) {
     if (at < end) {
@@ -247,7 +247,7 @@ struct Ring {
   }
   __device__ __forceinline__ void put(int stage, const Tl& tile) {
 #pragma unroll
-    for (int i = 0; i < 4; ++i)
+    for (int i = 0; i < kWords / 4; ++i)
       slot[stage][i][threadIdx.x] = make_uint4(tile.w[4 * i], tile.w[4 * i + 1], tile.w[4 * i + 2], tile.w[4 * i + 3]);
   }
   // the copies of all but the newest kStages - 1 tiles have arrived
@@ -281,7 +281,7 @@ struct Ring {
     };
     uint32_t m = T::kNone;
 #pragma unroll
-    for (int i = 0; i < 4; ++i) {
+    for (int i = 0; i < kWords / 4; ++i) {
       const uint4 v = slot[stage][i][threadIdx.x];
       m = T::max(m, T::max(T::max(v.x, v.y), T::max(v.z, v.w)));
       if constexpr (T::kPerWord == 1) {
@@ -317,7 +317,10 @@ struct Sum {
   }
 };
 
-__device__ __forceinline__ bool better(float xa, int ia, float xb, int ib) { return xa > xb || (xa == xb && ia < ib); }
+// Without branches, as the ranks' loops want it.
+__device__ __forceinline__ bool better(float xa, int ia, float xb, int ib) {
+  return (xa > xb) | ((xa == xb) & (ia < ib));
+}
 
 // Entries of the list that are better than one of them; a warp counts together.
 __device__ __forceinline__ int rank_of(const List& list, int n, float2 e) {
@@ -454,6 +457,17 @@ __device__ __noinline__ bool select_slow(List& list, int have, int count, const 
   return nan;
 }
 
+// Keys that come before number i of them, whose value is `mine`.
+__device__ __forceinline__ int rank_of_key(const uint32_t* keys, int n, uint32_t mine, int i) {
+  int rank = 0;
+#pragma unroll 4
+  for (int j = 0; j < n; ++j) {
+    const uint32_t k = keys[j];
+    rank += (k > mine) | ((k == mine) & (j < i));
+  }
+  return rank;
+}
+
 // A beam that has candidates of its own logits: not finished, its score finite.
 __device__ __forceinline__ bool beam_open(const SelectParams& p, int row) {
   return !(p.done != nullptr && p.done[row] != 0) && fabsf(p.scores[row]) < CUDART_INF_F;
@@ -468,7 +482,7 @@ __global__ void __launch_bounds__(kThreads, kResident) select_kernel(SelectParam
   __shared__ List list;
   __shared__ int runs[kCap];  // runs to read again: number x kThreads + thread
   __shared__ int num_runs;
-  __shared__ uint32_t warp_key[kWarps];
+  __shared__ uint32_t keys[kThreads];
   __shared__ int counters[2];
   __shared__ float2 warp_sum[kWarps];
   const int row = blockIdx.x / p.chunks, chunk = blockIdx.x - row * p.chunks;
@@ -542,46 +556,75 @@ __global__ void __launch_bounds__(kThreads, kResident) select_kernel(SelectParam
       noted[t / Tl::kRun][tid] = T::bits(run_top);
       most = fmaxf(most, top);
     }
-    // Each warp whose lanes all hold elements takes the m-th greatest of its lanes' greatest ones: with
-    // m x warps >= count, `count` elements are at or above the least of these.
+    // The bound: the `take` greatest of the lanes' greatest ones of each warp (whose lanes all hold elements)
+    // are put together, and of these the count-th is taken.  At least `count` elements are not below it, and
+    // with twice as many taken as wanted it is most often the exact count-th of the threads' greatest.
     const int full = min(kWarps, (part_end - part) / (32 * Tl::kPer));
-    uint32_t key = order_key(most), mth = 0;
-    for (int m = full > 0 ? min(32, (p.count + full - 1) / full) : 0; m > 0; --m) {
-      mth = __reduce_max_sync(~0u, key);
-      if (lane == __ffs(__ballot_sync(~0u, key == mth)) - 1) key = 0;
+    const int take = full > 0 ? min(32, (2 * p.count + full - 1) / full) : 0, pool = full * take;
+    uint32_t key = order_key(most);
+    for (int m = 0; m < take; ++m) {
+      const uint32_t mth = __reduce_max_sync(~0u, key);
+      if (lane == __ffs(__ballot_sync(~0u, key == mth)) - 1) {
+        if (warp < full) keys[warp * take + m] = mth;
+        key = 0;
+      }
     }
-    if (lane == 0) warp_key[warp] = mth;
     if (fabsf(sum.ref) > kFar && sum.ref > -CUDART_INF_F) list.far = 1;
     if (part_end == end) warp_total(sum.ref, sum.ref > -CUDART_INF_F ? sum.of_ref() : 0.0f);
     __syncthreads();
     float least = list.threshold;
-    if (full * 32 >= p.count) {
-      mth = warp_key[0];
-      for (int w = 1; w < full; ++w) mth = min(mth, warp_key[w]);
-      least = fmaxf(least, nextafterf(fmaxf(key_value(mth), -FLT_MAX), -CUDART_INF_F));
+    if (pool >= p.count) {
+      uint32_t bound = 0;
+      for (int i = lane; i < pool; i += 32) {
+        const uint32_t mine = keys[i];
+        if (rank_of_key(keys, pool, mine, i) == p.count - 1) bound = mine;
+      }
+      bound = __reduce_max_sync(~0u, bound);
+      least = fmaxf(least, nextafterf(fmaxf(key_value(bound), -FLT_MAX), -CUDART_INF_F));
     }
-    const int tiles = (part_end - part + Tl::kSize - 1) / Tl::kSize;
-    if (most > least) {
-      for (int t = 0; t * Tl::kRun < tiles; ++t)
-        if (T::one(noted[t][tid]) > least) {
-          const int i = atomicAdd(&num_runs, 1);
-          if (i < kCap) runs[i] = t * kThreads + tid;
-        }
+    const int tiles = (part_end - part + Tl::kSize - 1) / Tl::kSize, num_noted = (tiles + Tl::kRun - 1) / Tl::kRun;
+    for (uint32_t lanes = __ballot_sync(~0u, most > least); lanes != 0; lanes &= lanes - 1) {
+      const int thread = warp * 32 + __ffs(lanes) - 1;
+      if (lane < num_noted && T::one(noted[lane][thread]) > least) {
+        const int i = atomicAdd(&num_runs, 1);
+        if (i < kCap) runs[i] = lane * kThreads + thread;
+      }
     }
     __syncthreads();
     const int again = num_runs;
     bool slow = again > kCap || list.far != 0;
     if (!slow) {
-      for (int i = tid; i < again * 32; i += kThreads) {
+      // element i of the runs: its token, where it is in the ring
+      struct Place {
+        int token, thread, tile, e;
+      };
+      const auto place = [&](int i) {
         const int r = runs[i / 32], thread = r % kThreads, e = i % Tl::kElems;
         const int t = r / kThreads * Tl::kRun + i % 32 / Tl::kElems;
-        const int token = part + t * Tl::kSize + ((e / Tl::kPer) * kThreads + thread) * Tl::kPer + e % Tl::kPer;
-        if (token < part_end) {
-          const int back = tiles - t;  // the chunk's last tiles are still in the ring
-          const float v = part_end == end && back <= kStages
-                              ? ring.value(stage - back + (stage < back ? kStages : 0), thread, e)
-                              : T::one(x[token]);
-          if (v > least) append(list, v, token);
+        return Place{part + t * Tl::kSize + ((e / Tl::kPer) * kThreads + thread) * Tl::kPer + e % Tl::kPer, thread, t, e};
+      };
+      if (part_end == end && tiles <= kStages) {  // the whole part is still in the ring
+        for (int i = tid; i < again * 32; i += kThreads) {
+          const Place at_i = place(i);
+          const int back = tiles - at_i.tile;
+          if (back <= 0) continue;
+          const float v = ring.value(stage - back + (stage < back ? kStages : 0), at_i.thread, at_i.e);
+          if (v > least) append(list, v, at_i.token);
+        }
+      } else {
+        constexpr int kAtOnce = 4;  // loads under way
+        for (int i0 = tid; i0 < again * 32; i0 += kAtOnce * kThreads) {
+          float v[kAtOnce];
+          int token[kAtOnce];
+#pragma unroll
+          for (int j = 0; j < kAtOnce; ++j) {
+            const int i = i0 + j * kThreads;
+            token[j] = i < again * 32 ? place(i).token : part_end;
+            v[j] = token[j] < part_end ? T::one(x[token[j]]) : -CUDART_INF_F;
+          }
+#pragma unroll
+          for (int j = 0; j < kAtOnce; ++j)
+            if (v[j] > least) append(list, v[j], token[j]);
         }
       }
     }
@@ -673,21 +716,35 @@ __device__ __forceinline__ Pair log_pair(Pair s) {
 __device__ __forceinline__ uint64_t order_key(Pair x) { return ((uint64_t)order_key(x.hi) << 32) | order_key(x.lo); }
 
 constexpr int kMergeThreads = 256, kMergeWarps = kMergeThreads / 32;
+constexpr int kGather = 256;  // candidates that count those before them
 
-// One CTA a group of beams: the log-sum-exp of each beam, the scores of all list entries, then `count`
-// times the best head of the lists, which are in order.  Bound by latency: a warp's rounds of one reduction,
-// one vote and one shared-memory read.
+// A candidate: its score's order, 0 for none, and beam * vocab + token.
+struct Candidate {
+  uint64_t key;
+  uint32_t place;
+};
+__device__ __forceinline__ bool before(const Candidate& a, const Candidate& b) {
+  return (a.key > b.key) | ((a.key == b.key) & (a.place < b.place));
+}
+
+// One CTA a group of beams: the log-sum-exp of each beam, the scores of all list entries, and the `count`
+// best of them.  As in a chunk, the greatest of each thread give a bound; what reaches it is gathered, and every
+// gathered candidate counts those before it, which is its place in the result.  Bound by latency.
 __global__ void __launch_bounds__(kMergeThreads) select_merge_kernel(SelectParams p) {
-  extern __shared__ uint64_t key[];  // [beams * chunks][count]: score, 0: no candidate
+  extern __shared__ uint64_t keys[];  // [beams * chunks][count]: score, 0: no candidate
   // A candidate's score is offset + (logit - greatest): next to a logit of 1e38 a logarithm would be lost.
   __shared__ Pair offset[kMaxBeams];  // score - log(sum exp(logit - greatest)), or a finished beam's score
   __shared__ float greatest[kMaxBeams];
   __shared__ int kind[kMaxBeams];  // 0: no candidates, 1: those of its lists, 2: finished
-  __shared__ uint32_t won_score[kMaxCount], won_at[kMaxCount];
+  __shared__ uint32_t pool[32 * kMergeWarps];
+  __shared__ int gathered, valid, counters[2];
   const int group = blockIdx.x, tid = threadIdx.x, lane = tid & 31, warp = tid >> 5;
   const int lists = p.beams * p.chunks, entries = lists * p.count, per_beam = p.chunks * p.count;
-  uint32_t* place = reinterpret_cast<uint32_t*>(key + entries);  // [beams * chunks][count]: beam * vocab + token
-  int* next = reinterpret_cast<int*>(place + entries);           // [beams * chunks]: entries taken, past 32 lists
+  uint32_t* places = reinterpret_cast<uint32_t*>(keys + entries);        // [beams * chunks][count]
+  uint16_t* gather = reinterpret_cast<uint16_t*>(places + entries);      // entries that are not behind the bound
+  if (tid == 0) {
+    gathered = valid = counters[0] = counters[1] = 0;
+  }
   grid_dependency_wait();
   const float2* src = p.entries + (int64_t)group * entries;
   constexpr int kAhead = 4;
@@ -709,24 +766,24 @@ __global__ void __launch_bounds__(kMergeThreads) select_merge_kernel(SelectParam
     } else if (score > -CUDART_INF_F && finished) {
       what = 2;
     } else if (score > -CUDART_INF_F) {
-      float top = -CUDART_INF_F;
-      bool bad = false;
-      for (int c = lane; c < p.chunks; c += 32) {
-        const float2 v = c == lane ? first : s[c];
+      float top = first.x;
+      bool bad = !(first.y < CUDART_INF_F);
+      for (int c = lane + 32; c < p.chunks; c += 32) {
+        const float2 v = s[c];
         top = fmaxf(top, v.x);
         bad |= !(v.y < CUDART_INF_F);
       }
-      const uint32_t highest = __reduce_max_sync(~0u, order_key(top));
-      top = key_value(highest);
+      top = key_value(__reduce_max_sync(~0u, order_key(top)));
       bad = __any_sync(~0u, bad);
       if (bad) {
         if (lane == 0) flag_error(p.status, KVARN_DEV_BAD_LOGITS);
       } else if (top > -CUDART_INF_F) {
         Pair sum = {0.0f, 0.0f};
-        for (int c = lane; c < p.chunks; c += 32) {
-          const float2 v = c == lane ? first : s[c];
-          const Pair d = two_sum(v.x, -top);
-          if (d.hi > -80.0f) sum = add(sum, mul({v.y, 0.0f}, exp_pair(d)));
+        if (first.x == top) sum.hi = first.y;
+        else if (first.x > -CUDART_INF_F) sum.hi = first.y * expf(first.x - top);
+        for (int c = lane + 32; c < p.chunks; c += 32) {
+          const float2 v = s[c];
+          if (v.x > -CUDART_INF_F) sum = add(sum, {v.x == top ? v.y : v.y * expf(v.x - top), 0.0f});
         }
         for (int d = 1; d < 32 && d < p.chunks; d *= 2)
           sum = add(sum, {__shfl_xor_sync(~0u, sum.hi, d), __shfl_xor_sync(~0u, sum.lo, d)});
@@ -743,77 +800,94 @@ __global__ void __launch_bounds__(kMergeThreads) select_merge_kernel(SelectParam
     }
   }
   __syncthreads();
-  const auto enter = [&](int i, float2 e) {
-    const int k = i / per_beam;
-    uint64_t mine = 0;
+  const float per_inverse = 1.0f / (float)per_beam;
+  int mine = 0;
+  uint32_t most = 0;  // the greatest score of the thread's entries, in 32 bits
+#pragma unroll 1
+  for (int i = tid, j = 0; i < entries; i += kMergeThreads, ++j) {
+    const float2 e = j == 0 ? ahead[0] : j == 1 ? ahead[1] : j == 2 ? ahead[2] : j == 3 ? ahead[3] : __ldcg(src + i);
+    const int k = (int)(((float)i + 0.5f) * per_inverse);  // i / per_beam: entries <= 8192
+    uint64_t key = 0;
     int t = __float_as_int(e.y);
     if (kind[k] == 1) {
       const Pair score = add(offset[k], two_sum(e.x, -greatest[k]));
-      if (t >= 0 && fabsf(score.hi) < CUDART_INF_F) mine = order_key(score);
+      if (t >= 0 && fabsf(score.hi) < CUDART_INF_F) key = order_key(score);
     } else if (kind[k] == 2 && i == k * per_beam) {  // one candidate, first of the beam's first list
       t = p.end_token;
-      mine = order_key(offset[k]);
+      key = order_key(offset[k]);
     }
-    key[i] = mine;
-    place[i] = (uint32_t)k * (uint32_t)p.vocab + (uint32_t)t;
-  };
-#pragma unroll
-  for (int j = 0; j < kAhead; ++j)
-    if (tid + j * kMergeThreads < entries) enter(tid + j * kMergeThreads, ahead[j]);
-  for (int i = tid + kAhead * kMergeThreads; i < entries; i += kMergeThreads) enter(i, __ldcg(src + i));
-  for (int i = tid; i < lists; i += kMergeThreads) next[i] = 0;
-  __syncthreads();
-  if (warp != 0) return;
-
-  // lane l looks after lists l, l + 32, ...: the best of their heads
-  uint64_t best = 0;
-  uint32_t best_at = ~0u;
-  int head = lane * p.count, last = lane < lists ? head + p.count : head;  // one list a lane
-  int best_list = 0;
-  const auto scan = [&]() {
-    best = 0, best_at = ~0u;
-    if (lists <= 32) {
-      if (head < last) best = key[head], best_at = place[head];
-      return;
-    }
-    for (int i = lane; i < lists; i += 32) {
-      const int n = next[i];
-      if (n >= p.count) continue;
-      const uint64_t k = key[i * p.count + n];
-      const uint32_t at = place[i * p.count + n];
-      if (k > best || (k == best && at < best_at)) best = k, best_at = at, best_list = i;
-    }
-  };
-  scan();
-  int found = 0;
-  for (; found < p.count; ++found) {
-    const uint32_t hi = __reduce_max_sync(~0u, (uint32_t)(best >> 32));
-    if (hi == 0) break;
-    bool in = (uint32_t)(best >> 32) == hi;
-    uint32_t who = __ballot_sync(~0u, in);
-    if ((who & (who - 1)) != 0) {  // equal in 32 bits: the rest of the score, then the place
-      const uint32_t lo = __reduce_max_sync(~0u, in ? (uint32_t)best : 0u);
-      in = in && (uint32_t)best == lo;
-      const uint32_t at = __reduce_min_sync(~0u, in ? best_at : ~0u);
-      in = in && best_at == at;
-    }
-    if (in) {
-      won_score[found] = hi;
-      won_at[found] = best_at;
-      if (lists <= 32) ++head;
-      else ++next[best_list];
-      scan();
+    keys[i] = key;
+    places[i] = (uint32_t)k * (uint32_t)p.vocab + (uint32_t)t;
+    mine += key != 0;
+    most = max(most, (uint32_t)(key >> 32));
+  }
+  mine = __reduce_add_sync(~0u, mine);
+  if (lane == 0 && mine > 0) atomicAdd(&valid, mine);
+  const int active = min(kMergeWarps, (entries + 31) / 32);  // warps that hold entries
+  const int take = min(32, (2 * p.count + active - 1) / active);
+  for (int m = 0; m < take; ++m) {
+    const uint32_t mth = __reduce_max_sync(~0u, most);
+    if (lane == __ffs(__ballot_sync(~0u, most == mth)) - 1) {
+      pool[warp * take + m] = mth;
+      most = 0;
     }
   }
-  __syncwarp();
-  for (int j = lane; j < p.count; j += 32) {
-    const int64_t o = (int64_t)group * p.count + j;
-    const bool on = j < found;
-    const int k = on ? (int)(won_at[j] / (uint32_t)p.vocab) : -1, t = on ? (int)(won_at[j] - (uint32_t)k * (uint32_t)p.vocab) : -1;
-    p.out_scores[o] = on ? key_value(won_score[j]) : -CUDART_INF_F;
+  __syncthreads();
+  const int want = min(p.count, valid);
+  uint32_t least = 0;
+  for (int i = lane; i < take * active; i += 32) {
+    const uint32_t k = pool[i];
+    if (rank_of_key(pool, take * active, k, i) == p.count - 1) least = k;
+  }
+  least = max(__reduce_max_sync(~0u, least), 1u);
+  for (int i = tid; i < entries; i += kMergeThreads)
+    if ((uint32_t)(keys[i] >> 32) >= least) gather[atomicAdd(&gathered, 1)] = (uint16_t)i;
+  __syncthreads();
+  int total = gathered;
+  if (total > kGather) {
+    // Many equal scores: the last of the `want` candidates, bit by bit (a lower place first), and those not
+    // behind it.
+    Candidate cut = {0, ~0u};
+    for (int bit = 95; bit >= 0; --bit) {
+      Candidate trial = cut;
+      if (bit >= 32) trial.key |= 1ull << (bit - 32);
+      else trial.place &= ~(1u << bit);
+      int n = 0;
+      for (int i = tid; i < entries; i += kMergeThreads)
+        n += (keys[i] != 0) & !before({trial.key, bit >= 32 ? ~0u : trial.place}, {keys[i], places[i]});
+      n = __reduce_add_sync(~0u, n);
+      if (lane == 0 && n > 0) atomicAdd(&counters[bit & 1], n);
+      __syncthreads();
+      if (counters[bit & 1] >= want) cut = trial;
+      if (tid == 0) counters[(bit & 1) ^ 1] = 0;
+      __syncthreads();
+    }
+    if (tid == 0) gathered = 0;
+    __syncthreads();
+    for (int i = tid; i < entries; i += kMergeThreads)
+      if (keys[i] != 0 && !before(cut, {keys[i], places[i]})) gather[atomicAdd(&gathered, 1)] = (uint16_t)i;
+    __syncthreads();
+    total = gathered;
+  }
+  for (int i = tid; i < total; i += kMergeThreads) {
+    const Candidate c = {keys[gather[i]], places[gather[i]]};
+    int rank = 0;
+#pragma unroll 4
+    for (int j = 0; j < total; ++j) rank += before({keys[gather[j]], places[gather[j]]}, c);
+    if (rank >= p.count) continue;
+    const int64_t o = (int64_t)group * p.count + rank;
+    const int k = (int)(c.place / (uint32_t)p.vocab), t = (int)(c.place - (uint32_t)k * (uint32_t)p.vocab);
+    p.out_scores[o] = key_value((uint32_t)(c.key >> 32));
     p.out_parents[o] = k;
     p.out_tokens[o] = t;
-    if (p.out_done != nullptr) p.out_done[o] = on && (kind[k] == 2 || t == p.end_token);
+    if (p.out_done != nullptr) p.out_done[o] = kind[k] == 2 || t == p.end_token;
+  }
+  for (int j = want + tid; j < p.count; j += kMergeThreads) {
+    const int64_t o = (int64_t)group * p.count + j;
+    p.out_scores[o] = -CUDART_INF_F;
+    p.out_parents[o] = -1;
+    p.out_tokens[o] = -1;
+    if (p.out_done != nullptr) p.out_done[o] = 0;
   }
 }
 
@@ -1033,7 +1107,7 @@ int kvarn_beam_select(int batch, int beams, int vocab, int count, const void* lo
   if (const int e = set_smem_limit(smem_once, reinterpret_cast<const void*>(select_merge_kernel), most); e != KVARN_OK) return e;
   cudaLaunchAttribute attr;
   const cudaLaunchConfig_t cfg =
-      config((unsigned)batch, kMergeThreads, (size_t)lists * count * 12 + (size_t)lists * 4, s, &attr);
+      config((unsigned)batch, kMergeThreads, (size_t)lists * count * 14, s, &attr);
   return cudaLaunchKernelEx(&cfg, select_merge_kernel, p) == cudaSuccess ? KVARN_OK : KVARN_ERR_CUDA;
 }
 
