@@ -468,11 +468,6 @@ __device__ __forceinline__ int rank_of_key(const uint32_t* keys, int n, uint32_t
   return rank;
 }
 
-// A beam that has candidates of its own logits: not finished, its score finite.
-__device__ __forceinline__ bool beam_open(const SelectParams& p, int row) {
-  return !(p.done != nullptr && p.done[row] != 0) && fabsf(p.scores[row]) < CUDART_INF_F;
-}
-
 template <class T, int kBytes>
 __global__ void __launch_bounds__(kThreads, kResident) select_kernel(SelectParams p) {
   using Tl = Tile<T, kBytes>;
@@ -482,7 +477,7 @@ __global__ void __launch_bounds__(kThreads, kResident) select_kernel(SelectParam
   __shared__ List list;
   __shared__ int runs[kCap];  // runs to read again: number x kThreads + thread
   __shared__ int num_runs;
-  __shared__ uint32_t keys[kThreads];
+  __shared__ uint32_t keys[kThreads], bound;
   __shared__ int counters[2];
   __shared__ float2 warp_sum[kWarps];
   const int row = blockIdx.x / p.chunks, chunk = blockIdx.x - row * p.chunks;
@@ -494,7 +489,8 @@ __global__ void __launch_bounds__(kThreads, kResident) select_kernel(SelectParam
     num_runs = 0;
   }
   grid_dependency_wait();
-  const bool open = beam_open(p, row);
+  const float score = p.scores[row];
+  const int finished = p.done != nullptr ? p.done[row] : 0;
   const typename T::Elem* x = static_cast<const typename T::Elem*>(p.logits) + row * p.row_stride;
   const int begin = chunk * p.chunk_len;
   const int end = min(begin + p.chunk_len, p.vocab);
@@ -508,7 +504,7 @@ __global__ void __launch_bounds__(kThreads, kResident) select_kernel(SelectParam
   } else {
     for (int i = 0; i < kStages - 1; ++i) ring.issue(i, x, begin + i * Tl::kSize, end);
   }
-  if (!open) {  // the merge does not look at its lists
+  if (finished != 0 || !(fabsf(score) < CUDART_INF_F)) {  // no candidates of its logits: the merge does not look here
     asm volatile("cp.async.wait_all;" ::: "memory");
     return;
   }
@@ -574,12 +570,8 @@ __global__ void __launch_bounds__(kThreads, kResident) select_kernel(SelectParam
     __syncthreads();
     float least = list.threshold;
     if (pool >= p.count) {
-      uint32_t bound = 0;
-      for (int i = lane; i < pool; i += 32) {
-        const uint32_t mine = keys[i];
-        if (rank_of_key(keys, pool, mine, i) == p.count - 1) bound = mine;
-      }
-      bound = __reduce_max_sync(~0u, bound);
+      if (tid < pool && rank_of_key(keys, pool, keys[tid], tid) == p.count - 1) bound = keys[tid];
+      __syncthreads();
       least = fmaxf(least, nextafterf(fmaxf(key_value(bound), -FLT_MAX), -CUDART_INF_F));
     }
     const int tiles = (part_end - part + Tl::kSize - 1) / Tl::kSize, num_noted = (tiles + Tl::kRun - 1) / Tl::kRun;
@@ -737,6 +729,7 @@ __global__ void __launch_bounds__(kMergeThreads) select_merge_kernel(SelectParam
   __shared__ float greatest[kMaxBeams];
   __shared__ int kind[kMaxBeams];  // 0: no candidates, 1: those of its lists, 2: finished
   __shared__ uint32_t pool[32 * kMergeWarps];
+  __shared__ uint32_t bound;
   __shared__ int gathered, valid, counters[2];
   const int group = blockIdx.x, tid = threadIdx.x, lane = tid & 31, warp = tid >> 5;
   const int lists = p.beams * p.chunks, entries = lists * p.count, per_beam = p.chunks * p.count;
@@ -744,6 +737,7 @@ __global__ void __launch_bounds__(kMergeThreads) select_merge_kernel(SelectParam
   uint16_t* gather = reinterpret_cast<uint16_t*>(places + entries);      // entries that are not behind the bound
   if (tid == 0) {
     gathered = valid = counters[0] = counters[1] = 0;
+    bound = 0;
   }
   grid_dependency_wait();
   const float2* src = p.entries + (int64_t)group * entries;
@@ -834,12 +828,9 @@ __global__ void __launch_bounds__(kMergeThreads) select_merge_kernel(SelectParam
   }
   __syncthreads();
   const int want = min(p.count, valid);
-  uint32_t least = 0;
-  for (int i = lane; i < take * active; i += 32) {
-    const uint32_t k = pool[i];
-    if (rank_of_key(pool, take * active, k, i) == p.count - 1) least = k;
-  }
-  least = max(__reduce_max_sync(~0u, least), 1u);
+  if (tid < take * active && rank_of_key(pool, take * active, pool[tid], tid) == p.count - 1) bound = pool[tid];
+  __syncthreads();
+  const uint32_t least = max(bound, 1u);
   for (int i = tid; i < entries; i += kMergeThreads)
     if ((uint32_t)(keys[i] >> 32) >= least) gather[atomicAdd(&gathered, 1)] = (uint16_t)i;
   __syncthreads();
