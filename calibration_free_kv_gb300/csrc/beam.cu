@@ -30,7 +30,9 @@ constexpr int kWords = 8;              // 32-bit words of a tile that a thread h
 constexpr int kStages = 3;            // tiles on their way
 constexpr int kCap = 512;              // entries of the list
 constexpr float kFar = 65536.0f;       // references beyond it take the slower path
-constexpr float kStep = 40.0f;         // a thread's reference moves when a logit exceeds it by more
+// A reference moves when a logit exceeds it by more: the greatest terms' arguments stay small, and with them
+// their rounding (with 40 the logarithm of a sum was off by 3.1e-7 in the mean square, with 1 by 1.3e-7).
+constexpr float kStep = 1.0f;
 
 enum DType { kF16 = 0, kBF16 = 1, kF32 = 2 };
 
@@ -100,6 +102,26 @@ __device__ __forceinline__ float exp2_fast(float x) {
   return y;
 }
 
+// Sums and scores are pairs of floats (hi + lo, |lo| at most half a step of hi: 48 bits): 64-bit arithmetic
+// runs at 1/64 of the 32-bit rate here and took two thirds of the merge's time.
+struct Pair {
+  float hi, lo;
+};
+// a + b without an error (Knuth)
+__device__ __forceinline__ Pair two_sum(float a, float b) {
+  const float s = a + b, t = s - a;
+  return {s, (a - (s - t)) + (b - t)};
+}
+__device__ __forceinline__ Pair add(Pair a, Pair b) {
+  Pair s = two_sum(a.hi, b.hi);
+  const Pair t = two_sum(a.lo, b.lo);
+  s = two_sum(s.hi, s.lo + t.hi);
+  return two_sum(s.hi, s.lo + t.lo);
+}
+__device__ __forceinline__ Pair mul(Pair a, Pair b) {
+  const float h = a.hi * b.hi;
+  return two_sum(h, fmaf(a.hi, b.hi, -h) + fmaf(a.hi, b.lo, a.lo * b.hi));
+}
 // Order of floats as unsigned integers; both zeros are one value.
 __device__ __forceinline__ uint32_t order_key(float x) {
   const uint32_t b = __float_as_uint(x + 0.0f);
@@ -300,18 +322,25 @@ struct Ring {
   }
 };
 
-// Sum of exponentials of one thread: sum = sum of 2^(x log2(e) - base) with base = ref log2(e) rounded.
+// Sum of exponentials of one thread: sum + rest = sum of 2^(x log2(e) - base) with base = ref log2(e) rounded.
+// The tiles' sums are added without an error, so that a rounding is a share of one tile only.
 struct Sum {
-  float ref, base, sum;
-  __device__ __forceinline__ void start() { ref = -CUDART_INF_F, base = 0.0f, sum = 0.0f; }
+  float ref, base, sum, rest;
+  __device__ __forceinline__ void start() { ref = -CUDART_INF_F, base = sum = rest = 0.0f; }
+  __device__ __forceinline__ void add(float part) {
+    const Pair s = two_sum(sum, part);
+    sum = s.hi;
+    rest += s.lo;
+  }
   // Sum of exp(x - ref): what the rounding of base took, e^c with c = log(2) (base - ref log2(e)), is given back.
   // |ref| <= kFar: |c| < 0.005, so 1 + c + c^2/2 is off by less than 2^-25.
   __device__ __forceinline__ float of_ref() const {
     const float c = 0.6931472f * fmaf(-ref, kLog2e, base);
-    return fmaf(sum, fmaf(0.5f * c, c, c), sum);
+    return sum + fmaf(sum, fmaf(0.5f * c, c, c), rest);
   }
   __device__ __forceinline__ void move(float to) {
     if (ref > -CUDART_INF_F) sum = of_ref() * exp2_fast((ref - to) * kLog2e);
+    rest = 0.0f;
     ref = to;
     base = to * kLog2e;
   }
@@ -522,9 +551,10 @@ __global__ void __launch_bounds__(kThreads, kResident) select_kernel(SelectParam
     if (warp != 0) return;
     const float2 v = lane < kWarps ? warp_sum[lane] : make_float2(-CUDART_INF_F, 0.0f);
     const float top = key_value(__reduce_max_sync(~0u, order_key(v.x)));
-    float total = v.x > -CUDART_INF_F || v.y != v.y ? v.y * exp2f((v.x - top) * kLog2e) : 0.0f;
-    for (int d = kWarps / 2; d > 0; d /= 2) total += __shfl_xor_sync(~0u, total, d);
-    if (lane == 0) p.sums[blockIdx.x] = make_float2(top, total);
+    Pair total = {v.x > -CUDART_INF_F || v.y != v.y ? v.x == top ? v.y : v.y * exp2f((v.x - top) * kLog2e) : 0.0f, 0.0f};
+    for (int d = kWarps / 2; d > 0; d /= 2)
+      total = add(total, {__shfl_xor_sync(~0u, total.hi, d), __shfl_xor_sync(~0u, total.lo, d)});
+    if (lane == 0) p.sums[blockIdx.x] = make_float2(top, total.hi);
   };
   // One part for chunks of up to 20 x 8192 elements (fp32: 10 x 8192), which is nearly all of them.
   int at = begin, stage = 0;
@@ -542,11 +572,11 @@ __global__ void __launch_bounds__(kThreads, kResident) select_kernel(SelectParam
       }
       float top;
       float part_sum = ring.sum(stage, sum.base, top);
-      if (top > sum.ref + kStep) {  // also a thread's first tile
-        sum.move(top);
+      if (__any_sync(~0u, top > sum.ref + kStep)) {  // also in the warp's first tile; its lanes have one reference
+        sum.move(key_value(__reduce_max_sync(~0u, order_key(top == top ? top : -CUDART_INF_F))));
         part_sum = ring.sum(stage, sum.base, top);
       }
-      sum.sum += part_sum;
+      sum.add(part_sum);
       nan |= top != top;
       run_top = t % Tl::kRun == 0 ? top : fmaxf(run_top, top);
       noted[t / Tl::kRun][tid] = T::bits(run_top);
@@ -647,6 +677,7 @@ __global__ void __launch_bounds__(kThreads, kResident) select_kernel(SelectParam
   // the slow path, for the rest of the chunk
   asm volatile("cp.async.wait_all;" ::: "memory");
   sum.sum = sum.ref > -CUDART_INF_F ? sum.of_ref() : 0.0f;
+  sum.rest = 0.0f;
   nan |= select_slow<Tl>(list, have, p.count, x, at, end, sum, counters);
   grid_launch_dependents();
   warp_total(sum.ref, sum.sum);
@@ -657,27 +688,6 @@ __global__ void __launch_bounds__(kThreads, kResident) select_kernel(SelectParam
 }
 
 // ---- the merge --------------------------------------------------------------------------------
-// Scores are pairs of floats (hi + lo, |lo| at most half a step of hi: 48 bits): 64-bit arithmetic runs at
-// 1/64 of the 32-bit rate here and took two thirds of the merge's time.
-
-struct Pair {
-  float hi, lo;
-};
-// a + b without an error (Knuth)
-__device__ __forceinline__ Pair two_sum(float a, float b) {
-  const float s = a + b, t = s - a;
-  return {s, (a - (s - t)) + (b - t)};
-}
-__device__ __forceinline__ Pair add(Pair a, Pair b) {
-  Pair s = two_sum(a.hi, b.hi);
-  const Pair t = two_sum(a.lo, b.lo);
-  s = two_sum(s.hi, s.lo + t.hi);
-  return two_sum(s.hi, s.lo + t.lo);
-}
-__device__ __forceinline__ Pair mul(Pair a, Pair b) {
-  const float h = a.hi * b.hi;
-  return two_sum(h, fmaf(a.hi, b.hi, -h) + fmaf(a.hi, b.lo, a.lo * b.hi));
-}
 // exp(d) for -80 <= d.hi <= 80 to 2^-27: d = k log 2 + r, 1 + r exactly, r^2/2 + ... as Taylor's series to the ninth power in
 // 32 bits (at most 0.07, so its rounding is 2^-28 of the result).  log 2 = 2839/4096 + 3.19461849e-5: k times
 // the first part is exact.

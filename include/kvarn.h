@@ -439,9 +439,10 @@ size_t kvarn_beam_select_workspace_bytes(int batch, int beams, int vocab, int co
 /* The `count` best continuations of every group.  Candidate (k, v) of a group has the score
  *   scores[k] + logits[k][v] - log sum_u exp(logits[k][u]);
  * a finished beam (done[k] != 0) has one candidate, (k, end_token), with its score as it is; its logits are
- * not read.  Candidates are ordered by score, equal ones by k, then v.  Sums of exponentials are made in 32
- * bits a thread and joined in 64, scores are compared in 64: candidates of two beams that are nearer than
- * about 1e-7 may change places, those of one beam are in the order of their logits exactly.
+ * not read.  Candidates are ordered by score, equal ones by k, then v.  Exponentials are summed in
+ * 32 bits (the logarithm of a sum was off by 8e-8 in the mean square and 4e-7 at most) and scores compared in 48:
+ * candidates of two beams that are nearer than 8e-7 may change places, those of one beam are in the order of their
+ * logits exactly.
  *  logits      fp16, bf16 or fp32 (KVARN_LOGITS_*): token v of row b*beams + k at [row*row_stride + v];
  *              row_stride >= vocab, any alignment of the type (16-byte aligned rows are read fastest).
  *              -inf: the token cannot be chosen.  A beam with NaN or +inf among its logits, or as its score,
@@ -451,9 +452,11 @@ size_t kvarn_beam_select_workspace_bytes(int batch, int beams, int vocab, int co
  *  out_scores fp32, out_parents int32 (beam of the group), out_tokens int32, out_done bytes or NULL (1: the
  *              parent was finished or the token is end_token): device [batch][count], best first.  Where a
  *              group has fewer than `count` candidates the rest is -inf, -1, -1, 0.
- *  workspace   device scratch of kvarn_beam_select_workspace_bytes (16-byte aligned).
- * Equal arguments give equal results.  UNSUPPORTED for beams over 32, count over 64, vocab over 2^26 or
- * batch over 2^20. */
+ *              With count == beams, out_scores and out_done may be scores and done themselves.
+ *  workspace   device scratch of kvarn_beam_select_workspace_bytes (16-byte aligned); calls that overlap on the
+ *              GPU need one each.
+ * A candidate whose score is not finite in 32 bits is none.  Equal arguments give equal results.
+ * UNSUPPORTED for beams over 32, count over 64, vocab over 2^26 or batch over 2^20. */
 int kvarn_beam_select(int batch, int beams, int vocab, int count, const void* logits, int logits_type,
                       int64_t row_stride, const float* scores, const uint8_t* done, int end_token,
                       float* out_scores, int32_t* out_parents, int32_t* out_tokens, uint8_t* out_done,

@@ -245,6 +245,84 @@ def test_select_again_captured_and_other_stream(kv):
     assert all(np.array_equal(a, b.cpu().numpy()) for a, b in zip(second, outs))
 
 
+@pytest.mark.parametrize("dtype,vocab", [("bf16", 700_003), ("fp32", 400_001)])
+@pytest.mark.parametrize("kind", ["random", "rising", "equal", "far", "late inf"])
+def test_select_long_chunks(kv, kind, dtype, vocab):
+    """Chunks of more elements than are noted at a time: 64 candidates of 32 beams leave four chunks a row."""
+    logits, scores = make(1, 32, vocab, dtype, 41)
+    if kind == "rising":
+        logits[0, 3] = torch.linspace(-20, 20, vocab, device="cuda").to(logits.dtype)
+    elif kind == "equal":
+        logits[0, 5:8] = 0.5
+    elif kind == "far":  # beyond what the fast path's references hold, late in a chunk
+        logits[0, 2, 173_000 if dtype == "bf16" else 98_000] = 3e5
+        logits[0, 9] -= 2e5
+    elif kind == "late inf":
+        logits[0, 4, -1] = math.inf
+        logits[0, 6, :600] = -math.inf
+    scores[0, 2:10] = -1.0
+    check(kv, logits, scores, 64, flags=kv.DEV_BAD_LOGITS if kind == "late inf" else 0)
+
+
+def test_select_in_place(kv):
+    """As many candidates as beams: the new scores and flags may take the place of the old ones."""
+    logits, scores = make(5, 4, 2003, "bf16", 51)
+    done = torch.zeros(5, 4, dtype=torch.bool, device="cuda")
+    done[1, 2] = done[3] = True
+    (s, p, t, d), _ = select(kv, logits, scores, 4, done=done, end=11)
+    parents, tokens = (torch.zeros(5, 4, dtype=torch.int32, device="cuda") for _ in range(2))
+    ws = kv.alloc_beam_select_workspace(5, 4, 2003, 4)
+    kv.beam_select(logits, scores, scores, parents, tokens, ws, done=done, end_token=11, out_done=done)
+    torch.cuda.synchronize()
+    for a, b in ((s, scores), (p, parents), (t, tokens), (d.astype(bool), done)):
+        assert np.array_equal(a, b.cpu().numpy())
+
+
+def test_select_two_calls_at_once(kv):
+    calls = []
+    for seed in (61, 62):
+        logits, scores = make(16, 5, 50_001, "fp16", seed, pad=seed % 2)
+        want, _ = select(kv, logits, scores, 10)
+        outs = [torch.zeros(16, 10, dtype=t, device="cuda") for t in (torch.float32, torch.int32, torch.int32)]
+        calls.append((logits, scores, want, outs, kv.alloc_beam_select_workspace(16, 5, 50_001, 10), torch.cuda.Stream()))
+    torch.cuda.synchronize()
+    for _ in range(10):
+        for logits, scores, _, outs, ws, stream in calls:
+            kv.beam_select(logits, scores, *outs, ws, stream=stream)
+    torch.cuda.synchronize()
+    for _, _, want, outs, _, _ in calls:
+        assert all(np.array_equal(a, b.cpu().numpy()) for a, b in zip(want, outs))
+
+
+def test_select_refuses(kv):
+    logits, scores = make(2, 3, 100, "fp16", 71)
+    f, i = torch.zeros(2, 6, device="cuda"), torch.zeros(2, 6, dtype=torch.int32, device="cuda")
+    ws = kv.alloc_beam_select_workspace(2, 3, 100, 6)
+    kv.beam_select(logits, scores, f, i, i.clone(), ws)
+    with pytest.raises(ValueError, match="out_tokens"):
+        kv.beam_select(logits, scores, f, i, i[:1], ws)
+    with pytest.raises(ValueError, match="scores"):
+        kv.beam_select(logits, scores.double(), f, i, i, ws)
+    with pytest.raises(ValueError, match="logits"):
+        kv.beam_select(logits.double(), scores, f, i, i, ws)
+    with pytest.raises(ValueError, match="logits"):
+        kv.beam_select(logits.transpose(0, 1).contiguous().transpose(0, 1), scores, f, i, i, ws)
+    with pytest.raises(kv.KvarnError):
+        kv.beam_select(logits, scores, f, i, i, ws[:4])
+    with pytest.raises(kv.KvarnError):  # one row for all beams
+        kv.beam_select(logits[:, :1].expand(2, 3, 100)[:1], scores[:1].clone(), f[:1], i[:1], i[:1], ws)
+    desc = kv.desc_from_preset(64, 1)
+    t = torch.zeros(6, 2, dtype=torch.int32, device="cuda")
+    n, p = torch.zeros(6, dtype=torch.int32, device="cuda"), torch.zeros(2, 3, dtype=torch.int32, device="cuda")
+    k = torch.zeros(6, 1, 128, 64, dtype=torch.float16, device="cuda")
+    with pytest.raises(ValueError, match="go together"):
+        kv.beam_reorder(desc, p, n, t, n.clone(), t.clone(), partial_k=k)
+    with pytest.raises(ValueError, match="block_table_out"):
+        kv.beam_reorder(desc, p, n, t, n.clone(), t[:, :1].contiguous())
+    with pytest.raises(kv.KvarnError):  # the lengths cannot be moved in place
+        kv.beam_reorder(desc, p, n, t, n, t.clone())
+
+
 def test_select_rows_past_32_bits(kv):
     # the last rows of the logits start past 2^31 elements
     batch, beams, vocab = 34, 32, 2_000_003
