@@ -969,30 +969,47 @@ struct ReorderParams {
 constexpr int kMoveThreads = 256;
 
 // Every 16-byte vector of the open tiles, and every table entry, is moved for all beams of a group by
-// one thread, which reads them all before it writes: the outputs may be the inputs' own buffers.
+// one thread, which reads them all before it writes: the outputs may be the inputs' own buffers.  The beams'
+// sources and live rows are worked out once a CTA (worked out for every move, the kernel ran 135 instructions a
+// move and was bound by them as much as by HBM).
 template <int kBeams>
 __global__ void __launch_bounds__(kMoveThreads) reorder_kernel(ReorderParams p) {
-  __shared__ int parent[kMaxBeams], length[kMaxBeams];
+  __shared__ int parent[kMaxBeams], pages[kMaxBeams], live[kMaxBeams];
+  __shared__ int64_t from[kMaxBeams];
+  __shared__ int most;
   const int tid = threadIdx.x;
   const int64_t unit = blockIdx.x;  // (group, kv head, slice)
   const int slice = (int)(unit % p.slices);
   const int head = (int)(unit / p.slices % p.num_kv_heads);
   const int group = (int)(unit / p.slices / p.num_kv_heads);
   const int rows0 = group * p.beams;
+  const int layer = ((int)blockIdx.y - 1) >> 1, kv = ((int)blockIdx.y - 1) & 1;
+  const int vecs = p.dim / 8;
+  const uint4* src = reinterpret_cast<const uint4*>(kv ? p.v : p.k);
+  uint4* dst = reinterpret_cast<uint4*>(kv ? p.v_out : p.k_out);
+  const int64_t seq = (int64_t)p.num_kv_heads * kTile * vecs;  // vectors of one sequence in one layer
   grid_dependency_wait();
-  if (tid < p.beams) {
-    int of = p.parents[rows0 + tid], n = 0, bad = 0;
-    if (of < -1 || of >= p.beams) bad = KVARN_DEV_BAD_BEAM, of = -1;
-    if (of >= 0) {
-      n = p.seq_lens[rows0 + of];
-      if (n < 0 || n / kTile > p.max_pages) bad = KVARN_DEV_SEQ_TOO_LONG;
+  if (tid < 32) {
+    int n = 0, rows = 0;
+    if (tid < p.beams) {
+      int of = p.parents[rows0 + tid], bad = 0;
+      if (of < -1 || of >= p.beams) bad = KVARN_DEV_BAD_BEAM, of = -1;
+      if (of >= 0) {
+        n = p.seq_lens[rows0 + of];
+        if (n < 0 || n / kTile > p.max_pages) bad = KVARN_DEV_SEQ_TOO_LONG;
+      }
+      rows = n > 0 && !(src == dst && of == tid) ? n % kTile : 0;
+      parent[tid] = of;
+      pages[tid] = max(n, 0) / kTile;
+      live[tid] = rows;
+      from[tid] = max(of, 0) * seq;
+      if (blockIdx.y == 0 && slice == 0 && head == 0) {
+        p.seq_lens_out[rows0 + tid] = n;
+        if (bad) flag_error(p.status, bad);
+      }
     }
-    parent[tid] = of;
-    length[tid] = n;
-    if (blockIdx.y == 0 && slice == 0 && head == 0) {
-      p.seq_lens_out[rows0 + tid] = n;
-      if (bad) flag_error(p.status, bad);
-    }
+    rows = __reduce_max_sync(~0u, rows);
+    if (tid == 0) most = rows;
   }
   __syncthreads();
   if (blockIdx.y == 0) {
@@ -1002,31 +1019,27 @@ __global__ void __launch_bounds__(kMoveThreads) reorder_kernel(ReorderParams p) 
       int32_t x[kBeams];
 #pragma unroll
       for (int b = 0; b < kBeams; ++b)
-        if (b < p.beams && i < length[b] / kTile) x[b] = p.table[(int64_t)(rows0 + parent[b]) * p.max_pages + i];
+        if (b < p.beams && i < pages[b]) x[b] = p.table[(int64_t)(rows0 + parent[b]) * p.max_pages + i];
 #pragma unroll
       for (int b = 0; b < kBeams; ++b)
-        if (b < p.beams && i < length[b] / kTile) p.table_out[(int64_t)(rows0 + b) * p.max_pages + i] = x[b];
+        if (b < p.beams && i < pages[b]) p.table_out[(int64_t)(rows0 + b) * p.max_pages + i] = x[b];
     }
     return;
   }
-  const int layer = (blockIdx.y - 1) >> 1, kv = (blockIdx.y - 1) & 1;
-  const int vecs = p.dim / 8;
-  const uint4* src = reinterpret_cast<const uint4*>(kv ? p.v : p.k);
-  uint4* dst = reinterpret_cast<uint4*>(kv ? p.v_out : p.k_out);
-  const int64_t seq = (int64_t)p.num_kv_heads * kTile * vecs;  // vectors of one sequence in one layer
   const int64_t first = (int64_t)layer * p.batch * p.beams * seq + (int64_t)rows0 * seq + (int64_t)head * kTile * vecs;
-  const bool in_place = src == dst;
-  for (int i = slice * kMoveThreads + tid; i < kTile * vecs; i += p.slices * kMoveThreads) {
-    const int row = i / vecs;
+  src += first;
+  dst += first;
+  const float per_row = 1.0f / (float)vecs;
+  for (int i = slice * kMoveThreads + tid; i < most * vecs; i += p.slices * kMoveThreads) {
+    const int row = (int)(((float)i + 0.5f) * per_row);  // i / vecs: i < 4096
     uint4 x[kBeams];
 #pragma unroll
     for (int b = 0; b < kBeams; ++b)
-      if (b < p.beams && length[b] > 0 && row < length[b] % kTile && !(in_place && parent[b] == b))
-        x[b] = src[first + parent[b] * seq + i];
+      if (b < p.beams && row < live[b]) x[b] = src[from[b] + i];
+    uint4* to = dst + i;
 #pragma unroll
-    for (int b = 0; b < kBeams; ++b)
-      if (b < p.beams && length[b] > 0 && row < length[b] % kTile && !(in_place && parent[b] == b))
-        dst[first + b * seq + i] = x[b];
+    for (int b = 0; b < kBeams; ++b, to += seq)
+      if (b < p.beams && row < live[b]) *to = x[b];
   }
 }
 
@@ -1145,8 +1158,9 @@ int kvarn_beam_reorder(const kvarn_desc* desc, int batch, int beams, int layers,
   p.layers = layers;
   p.num_kv_heads = desc->num_kv_heads;
   p.dim = desc->head_dim;
-  // Short rows of CTAs start late, long ones leave a small GPU share idle: 16 groups of 4 over 16 layers take 83 / 55 /
-  // 46 / 47 us in 8 / 4 / 2 / 1 slices, one group in one layer 2.6 / 2.6 / 3.2 / 4.3 us.
+  // Few units: CTAs to fill the GPU; many: long-lived ones.  16 groups of 4 over 16 layers take 52 / 45 / 45 / 46 us in
+  // 8 / 4 / 2 / 1 slices, 6 groups of 5 over 4 layers 5.3 / 4.1 / 3.8 / 4.2 us, one group in one layer 2.5 us in 4 or more,
+  // 3.2 in 2.
   p.slices = (int64_t)batch * p.num_kv_heads * (2 * layers + 1) <= 152 ? 4 : 2;
   if ((int64_t)batch * p.num_kv_heads * p.slices > 0x7fffffffLL) return KVARN_ERR_UNSUPPORTED;
   const cudaStream_t s = static_cast<cudaStream_t>(stream);

@@ -309,43 +309,49 @@ struct StoreParams {
   int64_t num_pool_pages;
   int64_t tokens;
   int num_kv_heads, dim, per_cta;
+  int streaming;  // many tokens
   int32_t* status;
 };
 
 constexpr int kStoreThreads = 256, kStoreUnroll = 4;
 
-// A CTA copies `per_cta` tokens, 16 bytes a thread and step.
+// A CTA copies `per_cta` tokens, 16 bytes a thread and step.  A thread keeps its place within a token (key or
+// value, head, channels), so that a copy costs a slot, two additions and the move: with the place worked out for
+// every copy the kernel was bound by its 150 instructions a copy.
 __global__ void __launch_bounds__(kStoreThreads) store_kernel(StoreParams p) {
   const int64_t t0 = (int64_t)blockIdx.x * p.per_cta;
   const int tokens = (int)min((int64_t)p.per_cta, p.tokens - t0);
   const int row = p.dim / 8, half = p.num_kv_heads * row, vecs = 2 * half;
+  const int groups = vecs < kStoreThreads ? kStoreThreads / vecs : 1;  // tokens that the CTA copies side by side
+  const int group = vecs < kStoreThreads ? (int)threadIdx.x / vecs : 0;
+  const int64_t limit = p.num_pool_pages * kTile, page = (int64_t)p.num_kv_heads * 2 * kTile * p.dim;
+  if (group >= groups) return;
   grid_dependency_wait();
-  for (int i0 = threadIdx.x; i0 < tokens * vecs; i0 += kStoreThreads * kStoreUnroll) {
-    uint4 x[kStoreUnroll];
-    int64_t to[kStoreUnroll];
+  for (int i = (int)threadIdx.x - group * vecs; i < vecs; i += kStoreThreads) {
+    const int kv = i >= half, hc = i - kv * half, h = hc / row, c = 8 * (hc - h * row);
+    const __half* src = (kv ? p.v : p.k) + h * p.head_stride + c;
+    __half* dst = p.pool + (int64_t)(2 * h + kv) * kTile * p.dim + c;
+    for (int t = group; t < tokens; t += kStoreUnroll * groups) {
+      uint4 x[kStoreUnroll];
+      int64_t slot[kStoreUnroll];
 #pragma unroll
-    for (int u = 0; u < kStoreUnroll; ++u) {
-      const int i = i0 + u * kStoreThreads;
-      to[u] = -1;
-      if (i >= tokens * vecs) continue;
-      const int t = i / vecs, r = i - t * vecs, kv = r >= half, hc = r - kv * half, h = hc / row, c = hc - h * row;
-      const int64_t slot = p.slots[t0 + t];
-      if (slot < 0) continue;
-      if (slot >= p.num_pool_pages * kTile) {
-        flag_error(p.status, KVARN_DEV_BAD_PAGE_ID);
-        continue;
+      for (int u = 0; u < kStoreUnroll; ++u) {
+        slot[u] = t + u * groups < tokens ? p.slots[t0 + t + u * groups] : -1;
+        if (slot[u] >= 0 && slot[u] < limit)
+          x[u] = __ldcs(reinterpret_cast<const uint4*>(src + (t0 + t + u * groups) * p.tok_stride));
       }
-      const __half* src = (kv ? p.v : p.k) + (t0 + t) * p.tok_stride + h * p.head_stride + 8 * c;
-      x[u] = __ldcs(reinterpret_cast<const uint4*>(src));
-      to[u] = ((((slot / kTile) * p.num_kv_heads + h) * 2 + kv) * kTile + slot % kTile) * p.dim + 8 * c;
-    }
 #pragma unroll
-    for (int u = 0; u < kStoreUnroll; ++u) {
-      if (to[u] < 0) continue;
-      uint4* dst = reinterpret_cast<uint4*>(p.pool + to[u]);
-      // prompts pass through the L2 cache (16384 tokens of 8 x 128: 19.0 -> 18.0 us), a step's tokens stay
-      if (p.per_cta > 1) __stcs(dst, x[u]);
-      else *dst = x[u];
+      for (int u = 0; u < kStoreUnroll; ++u) {
+        if (slot[u] < 0) continue;
+        if (slot[u] >= limit) {
+          flag_error(p.status, KVARN_DEV_BAD_PAGE_ID);
+          continue;
+        }
+        uint4* to = reinterpret_cast<uint4*>(dst + (slot[u] / kTile) * page + (slot[u] % kTile) * p.dim);
+        // prompts pass through the L2 cache, a step's tokens stay
+        if (p.streaming) __stcs(to, x[u]);
+        else *to = x[u];
+      }
     }
   }
 }
@@ -438,7 +444,10 @@ int kvarn_fp16_store(int head_dim, int num_kv_heads, int64_t num_tokens, const v
   p.tokens = num_tokens;
   p.num_kv_heads = num_kv_heads;
   p.dim = head_dim;
-  p.per_cta = num_tokens > 1024 ? 4 : 1;
+  // few tokens: as many CTAs as there are; many: enough copies a thread to keep their latency covered
+  const int vecs = 2 * num_kv_heads * (head_dim / 8), groups = vecs < kStoreThreads ? kStoreThreads / vecs : 1;
+  p.streaming = num_tokens > 1024;
+  p.per_cta = (p.streaming ? kStoreUnroll : 1) * groups;
   p.status = dev_status;
   cudaLaunchAttribute attr[1];
   attr[0].id = cudaLaunchAttributeProgrammaticStreamSerialization;
