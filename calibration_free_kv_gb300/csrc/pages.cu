@@ -17,10 +17,13 @@ constexpr int kCluster = 8;                // CTAs of a large plan: the portable
 constexpr uint32_t kManyPages = 1u << 30;  // needs are added up to here: no pool has as many pages
 constexpr int kAhead = 8;                  // table entries that a lane has under way
 constexpr int kSpan = 32 * kAhead;         // table entries that a warp marks at a time
-// Slots that the planning CTAs write themselves; more take a kernel of their own.
+// Slots that the planning CTAs write themselves; more take a kernel of their own (16384 slots: 7.8 against 8.7 us,
+// 65536: 11.4 against 9.1).
 constexpr int64_t kSlotsHere = 16384;
-// Up to these sizes one CTA plans.
-constexpr int64_t kSmallTable = 16384, kSmallPool = 65536, kSmallSlots = 4096;
+// Up to these sizes (table entries, pages of the pool, tokens that come) one CTA plans, beyond them a cluster.  One
+// CTA against a cluster: 1 row 4.3 / 5.8 us, 64 rows of 128 entries 5.3 / 5.9, 128 rows 6.8 / 6.2, 512 rows 15.7 / 7.6;
+// 64 rows and a pool of 200,000 pages 5.8 / 6.8; 8 rows of 128 / 512 / 1024 tokens 5.1 / 7.1, 7.2 / 7.1, 10.2 / 7.1.
+constexpr int64_t kSmallTable = 16384, kSmallPool = 262144, kSmallTokens = 4096;
 
 struct PlanParams {
   const int32_t* seq_lens;
@@ -128,7 +131,9 @@ __device__ __forceinline__ void write_slots(const PlanParams& p, Index first, In
 // One CTA, or a cluster of them, plans the whole batch.  The pages that the table rows name are marked in a
 // bitmap of the pool in shared memory; its zero bits, in ascending order, go to the sequences in order.
 // Bound by latency: a chain of loads, marks, two counts and the writes, with a meeting of all threads
-// between them.
+// between them (512 rows of 16k tokens: 8.5 us, of which the loads take two trips to memory and the cluster's three
+// meetings about 2 us).  A CTA of a cluster marks its rows in a bitmap of its own and reads the others' afterwards:
+// marks sent to the CTA that owns the page took 10 us of 17, for they pass one by one.
 __global__ void __launch_bounds__(kThreads) plan_kernel(PlanParams p) {
   extern __shared__ uint32_t smem[];
   __shared__ uint32_t warp_sum[kWarps], warp_free[kWarps];
@@ -391,7 +396,7 @@ int kvarn_plan_pages(int batch, int chunk_len, const int32_t* seq_lens, const in
   // One CTA where there is little to read, mark and write: the CTAs of a cluster meet three times.
   const int64_t slots = slot_map != nullptr ? (int64_t)batch * chunk_len : 0;
   const bool small = (int64_t)batch * max_pages <= kSmallTable && num_pool_pages <= kSmallPool &&
-                     (slots <= kSmallSlots || slots > kSlotsHere);
+                     (int64_t)batch * chunk_len <= kSmallTokens;
   p.ctas = small ? 1 : kCluster;
   p.whole = num_pool_pages <= (1 << kMaxBitsLog);
   const int words = (int)((num_pool_pages + 31) / 32);
