@@ -38,7 +38,8 @@ constexpr int kStages = 3;            // tiles on their way
 constexpr int kCap = 512;              // entries of the list
 constexpr float kFar = 65536.0f;       // references beyond it take the slower path
 // A reference moves when a logit exceeds it by more: the greatest terms' arguments stay small, and with them
-// their rounding (with 40 the logarithm of a sum was off by 3.1e-7 in the mean square, with 1 by 1.3e-7).
+// their rounding (with 40 the logarithm of a sum was off by 3.1e-7 in the mean square, with 1 by 1.3e-7, and by
+// 7.6e-8 since tiles are added without an error).
 constexpr float kStep = 1.0f;
 
 struct SelectParams {
@@ -452,8 +453,9 @@ __device__ __forceinline__ void select_exact(List& list, int have, int count, co
   __syncthreads();
 }
 
-// The rest of a chunk, from `at` on, where a group of tiles had more candidates than the list holds or a
-// logit beyond kFar.  sum.sum is the sum of exp(x - sum.ref) here.  Returns whether a logit was NaN.
+// The rest of a chunk, from `at` on, where more of it reached the bound than the list holds or a reference is beyond
+// kFar: tile by tile, references a thread's own.  sum.sum is the sum of exp(x - sum.ref) here.  Returns whether a logit
+// was NaN.
 template <class Tl, class Elem>
 __device__ __noinline__ bool select_slow(List& list, int have, int count, const Elem* row, int at, int end,
                                          Sum& sum, int* counters) {

@@ -195,6 +195,7 @@ def test_select_ties_and_order(kv, kind, dtype):
     scores = torch.tensor([[0.0, -1.0, -2.0], [-3.0, -3.0, -3.0]], device="cuda")
     check(kv, logits, scores, 16)
     check(kv, logits, scores, 1)
+    check(kv, logits, scores, 64)  # equal scores in all of the merge's lists
 
 
 def test_select_equal_beams_tie_exactly(kv):

@@ -45,7 +45,7 @@ def expected(table, lens, new, chunk, pool, open_tiles):
                 named.add(p)
             else:
                 status |= 1
-    free = [p for p in range(pool) if p not in named] if pool < 100000 else None
+    free = [p for p in range(pool) if p not in named] if pool < 50000 else None
     if free is None:
         mask = np.ones(pool, dtype=bool)
         mask[list(named)] = False
@@ -167,6 +167,18 @@ def test_plan_gives_back_pages_of_empty_sequences(kv):
     lens, new = [512, 0, 256], [0, 0, 256]  # the second sequence ended: its pages go to the third
     t, o, _, f = run(kv, table, lens, new, 256, 12, True)
     assert t.tolist() == [[0, 1, 2, 3], [4, 5, 6, 7], [8, 9, 4, 5]] and o.tolist() == [512, 0, 512] and f == 0
+
+
+@pytest.mark.parametrize("batch,pool", [(3, 1 << 20), (3, (1 << 20) + 1), (40, 3_000_001)])
+def test_plan_large_pools(kv, batch, pool):
+    # pools around and past what one CTA keeps a whole bitmap of; all pages but a few at the end are taken
+    rng = np.random.default_rng(batch)
+    lens = rng.integers(100, 3000, batch).tolist()
+    new = rng.integers(0, 700, batch).tolist()
+    table = make_table(lens, 32, 600, True, rng, shared=2)
+    table = np.where(table >= 0, pool - 1 - table, table).astype(np.int32)
+    check(kv, table, lens, new, 700, pool, True)
+    check(kv, table, lens, new, 700, pool, False)
 
 
 def test_plan_largest(kv):
