@@ -726,7 +726,7 @@ __device__ __forceinline__ Pair log_pair(Pair s) {
 __device__ __forceinline__ uint64_t order_key(Pair x) { return ((uint64_t)order_key(x.hi) << 32) | order_key(x.lo); }
 
 constexpr int kMergeThreads = 256, kMergeWarps = kMergeThreads / 32;
-constexpr int kGather = 256;  // candidates that count those before them
+constexpr int kGather = kMergeThreads;  // candidates that count those before them, one a thread
 
 // A candidate: its score's order, 0 for none, and beam * vocab + token.
 struct Candidate {
@@ -747,12 +747,14 @@ __global__ void __launch_bounds__(kMergeThreads) select_merge_kernel(SelectParam
   __shared__ float greatest[kMaxBeams];
   __shared__ int kind[kMaxBeams];  // 0: no candidates, 1: those of its lists, 2: finished
   __shared__ uint32_t pool[32 * kMergeWarps];
+  __shared__ uint64_t near_key[kGather];  // entries that are not behind the bound
+  __shared__ uint32_t near_place[kGather];
+  __shared__ int near_beam[kGather];
   __shared__ uint32_t bound;
   __shared__ int gathered, valid, counters[2];
   const int group = blockIdx.x, tid = threadIdx.x, lane = tid & 31, warp = tid >> 5;
   const int lists = p.beams * p.chunks, entries = lists * p.count, per_beam = p.chunks * p.count;
   uint32_t* places = reinterpret_cast<uint32_t*>(keys + entries);        // [beams * chunks][count]
-  uint16_t* gather = reinterpret_cast<uint16_t*>(places + entries);      // entries that are not behind the bound
   if (tid == 0) {
     gathered = valid = counters[0] = counters[1] = 0;
     bound = 0;
@@ -836,6 +838,7 @@ __global__ void __launch_bounds__(kMergeThreads) select_merge_kernel(SelectParam
   mine = __reduce_add_sync(~0u, mine);
   if (lane == 0 && mine > 0) atomicAdd(&valid, mine);
   const int active = min(kMergeWarps, (entries + 31) / 32);  // warps that hold entries
+  // twice as many as wanted: with a few more than wanted 64 candidates leave more than kGather (53 -> 75 us)
   const int take = min(32, (2 * p.count + active - 1) / active);
   for (int m = 0; m < take; ++m) {
     const uint32_t mth = __reduce_max_sync(~0u, most);
@@ -849,8 +852,15 @@ __global__ void __launch_bounds__(kMergeThreads) select_merge_kernel(SelectParam
   if (tid < take * active && rank_of_key(pool, take * active, pool[tid], tid) == p.count - 1) bound = pool[tid];
   __syncthreads();
   const uint32_t least = max(bound, 1u);
+  const auto gather = [&](int i) {
+    const int at = atomicAdd(&gathered, 1);
+    if (at >= kGather) return;
+    near_key[at] = keys[i];
+    near_place[at] = places[i];
+    near_beam[at] = (int)(((float)i + 0.5f) * per_inverse);
+  };
   for (int i = tid; i < entries; i += kMergeThreads)
-    if ((uint32_t)(keys[i] >> 32) >= least) gather[atomicAdd(&gathered, 1)] = (uint16_t)i;
+    if ((uint32_t)(keys[i] >> 32) >= least) gather(i);
   __syncthreads();
   int total = gathered;
   if (total > kGather) {
@@ -874,22 +884,23 @@ __global__ void __launch_bounds__(kMergeThreads) select_merge_kernel(SelectParam
     if (tid == 0) gathered = 0;
     __syncthreads();
     for (int i = tid; i < entries; i += kMergeThreads)
-      if (keys[i] != 0 && !before(cut, {keys[i], places[i]})) gather[atomicAdd(&gathered, 1)] = (uint16_t)i;
+      if (keys[i] != 0 && !before(cut, {keys[i], places[i]})) gather(i);
     __syncthreads();
     total = gathered;
   }
-  for (int i = tid; i < total; i += kMergeThreads) {
-    const Candidate c = {keys[gather[i]], places[gather[i]]};
+  if (tid < total) {
+    const Candidate c = {near_key[tid], near_place[tid]};
     int rank = 0;
 #pragma unroll 4
-    for (int j = 0; j < total; ++j) rank += before({keys[gather[j]], places[gather[j]]}, c);
-    if (rank >= p.count) continue;
-    const int64_t o = (int64_t)group * p.count + rank;
-    const int k = (int)(c.place / (uint32_t)p.vocab), t = (int)(c.place - (uint32_t)k * (uint32_t)p.vocab);
-    p.out_scores[o] = key_value((uint32_t)(c.key >> 32));
-    p.out_parents[o] = k;
-    p.out_tokens[o] = t;
-    if (p.out_done != nullptr) p.out_done[o] = kind[k] == 2 || t == p.end_token;
+    for (int j = 0; j < total; ++j) rank += before({near_key[j], near_place[j]}, c);
+    if (rank < p.count) {
+      const int64_t o = (int64_t)group * p.count + rank;
+      const int k = near_beam[tid], t = (int)(c.place - (uint32_t)k * (uint32_t)p.vocab);
+      p.out_scores[o] = key_value((uint32_t)(c.key >> 32));
+      p.out_parents[o] = k;
+      p.out_tokens[o] = t;
+      if (p.out_done != nullptr) p.out_done[o] = kind[k] == 2 || t == p.end_token;
+    }
   }
   for (int j = want + tid; j < p.count; j += kMergeThreads) {
     const int64_t o = (int64_t)group * p.count + j;
@@ -1130,7 +1141,7 @@ int kvarn_beam_select(int batch, int beams, int vocab, int count, const void* lo
   if (const int e = set_smem_limit(smem_once, reinterpret_cast<const void*>(select_merge_kernel), most); e != KVARN_OK) return e;
   cudaLaunchAttribute attr;
   const cudaLaunchConfig_t cfg =
-      config((unsigned)batch, kMergeThreads, (size_t)lists * count * 14, s, &attr);
+      config((unsigned)batch, kMergeThreads, (size_t)lists * count * 12, s, &attr);
   return cudaLaunchKernelEx(&cfg, select_merge_kernel, p) == cudaSuccess ? KVARN_OK : KVARN_ERR_CUDA;
 }
 
