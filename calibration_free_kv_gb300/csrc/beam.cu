@@ -15,7 +15,8 @@ namespace beam {
 
 constexpr int kMaxBeams = 32, kMaxCount = 64;
 constexpr int kMaxVocab = 1 << 26;     // beam * vocab + token stays within 31 bits
-constexpr int kMergeEntries = 8192;    // candidates that the merge holds in shared memory
+constexpr int kChunkEntries = 1024;    // candidates beyond which a group's rows are not divided further
+static_assert(kMaxBeams * kMaxCount * 12 + 16384 <= 49152, "the merge takes its lists without a raised limit");
 
 // ---- selection: one pass over the logits ----------------------------------------------------
 // A row of logits (one beam) is cut into chunks, one CTA each.  A CTA streams its chunk through shared
@@ -912,11 +913,13 @@ __global__ void __launch_bounds__(kMergeThreads) select_merge_kernel(SelectParam
 }
 
 // Chunks of a row: two CTAs an SM when the rows are few, each of some thousand logits at least, and no more lists than
-// the merge holds.  With 4 / 3 / 2 an SM 128 rows of 128000 take 15.8 / 15.7 / 15.2 us, 80 of 100000 14.0 / 12.7 / 12.8, 40 of
-// 50001 11.2 / 11.1 / 10.4: more chunks end more often and leave the merge more lists.
+// the one CTA that merges a group joins quickly.  With 4 / 3 / 2 an SM 128 rows of 128000 take 15.8 / 15.7 / 15.2 us, 80 of
+// 100000 14.0 / 12.7 / 12.8, 40 of 50001 11.2 / 11.1 / 10.4: more chunks end more often and leave the merge more lists.
+// One group of 8 rows of 151936 with 16 candidates takes 21.2 us with lists of up to 8192 candidates, 14.7 with 4096, 10.9
+// with 1024, 11.6 with 512, 12.8 with 256; one of 16 rows with 32 takes 48, 23, 19, 23 and 23 us.
 static int chunks_of(int64_t rows, int beams, int vocab, int count) {
   int64_t c = 152 * 2 / rows;
-  const int64_t most = (vocab + 2047) / 2048, held = kMergeEntries / ((int64_t)beams * count);
+  const int64_t most = (vocab + 2047) / 2048, held = kChunkEntries / ((int64_t)beams * count);
   c = c < most ? c : most;
   c = c < held ? c : held;
   return c < 1 ? 1 : (int)c;
@@ -1136,9 +1139,6 @@ int kvarn_beam_select(int batch, int beams, int vocab, int count, const void* lo
     st = both % 16 == 0 ? launch_select<F16, 16>(p, s) : both % 4 == 0 ? launch_select<F16, 4>(p, s) : launch_select<F16, 2>(p, s);
   if (st != KVARN_OK) return st;
   const int lists = beams * L.chunks;
-  static PerDeviceOnce smem_once;
-  const int most = kMergeEntries * 16;
-  if (const int e = set_smem_limit(smem_once, reinterpret_cast<const void*>(select_merge_kernel), most); e != KVARN_OK) return e;
   cudaLaunchAttribute attr;
   const cudaLaunchConfig_t cfg =
       config((unsigned)batch, kMergeThreads, (size_t)lists * count * 12, s, &attr);

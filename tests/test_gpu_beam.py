@@ -249,7 +249,7 @@ def test_select_again_captured_and_other_stream(kv):
 @pytest.mark.parametrize("dtype,vocab", [("bf16", 700_003), ("fp32", 400_001)])
 @pytest.mark.parametrize("kind", ["random", "rising", "equal", "far", "late inf"])
 def test_select_long_chunks(kv, kind, dtype, vocab):
-    """Chunks of more elements than are noted at a time: 64 candidates of 32 beams leave four chunks a row."""
+    """Chunks of more elements than are noted at a time: 64 candidates of 32 beams leave a row in one."""
     logits, scores = make(1, 32, vocab, dtype, 41)
     if kind == "rising":
         logits[0, 3] = torch.linspace(-20, 20, vocab, device="cuda").to(logits.dtype)
