@@ -37,7 +37,11 @@ constexpr int kResident = 4;          // CTAs of the streaming kernel on an SM
 constexpr int kWords = 8;              // 32-bit words of a tile that a thread holds
 constexpr int kStages = 3;            // tiles on their way
 constexpr int kCap = 512;              // entries of the list
-constexpr float kFar = 65536.0f;       // references beyond it take the slower path
+// References stay within it where sums are kept by their products with log2(e): farther out the rounding of the
+// product passes 0.004.  A warp whose logits are all below -kFar (a mask of finite values) keeps -kFar, against which
+// they count as next to nothing; with the mask's own value the product overflows.  A chunk that ends with a reference
+// of kFar or more, or of -kFar, takes the slower path.
+constexpr float kFar = 65536.0f;
 // A reference moves when a logit exceeds it by more: the greatest terms' arguments stay small, and with them
 // their rounding (with 40 the logarithm of a sum was off by 3.1e-7 in the mean square, with 1 by 1.3e-7, and by
 // 7.6e-8 since tiles are added without an error).
@@ -243,7 +247,7 @@ struct List {
   float2 e[kCap];  // logit, token
   int n;
   float threshold;  // `count` elements seen so far are at least as great; -inf while there are fewer
-  int far;          // a reference is beyond kFar
+  int far;          // a reference is kFar or more, or -kFar
 };
 
 // Tiles on their way through shared memory: a thread reads the words that it copied itself, so that it
@@ -582,7 +586,8 @@ __global__ void __launch_bounds__(kThreads, kResident) select_kernel(SelectParam
       float top;
       float part_sum = ring.sum(stage, sum.base, top);
       if (__any_sync(~0u, top > sum.ref + kStep)) {  // also in the warp's first tile; its lanes have one reference
-        sum.move(key_value(__reduce_max_sync(~0u, order_key(top == top ? top : -CUDART_INF_F))));
+        const float to = key_value(__reduce_max_sync(~0u, order_key(top == top ? top : -CUDART_INF_F)));
+        sum.move(fmaxf(to, -kFar));
         part_sum = ring.sum(stage, sum.base, top);
       }
       sum.add(part_sum);
@@ -604,7 +609,7 @@ __global__ void __launch_bounds__(kThreads, kResident) select_kernel(SelectParam
         key = 0;
       }
     }
-    if (fabsf(sum.ref) > kFar && sum.ref > -CUDART_INF_F) list.far = 1;
+    if (fabsf(sum.ref) >= kFar && sum.ref > -CUDART_INF_F) list.far = 1;
     if (part_end == end) warp_total(sum.ref, sum.ref > -CUDART_INF_F ? sum.of_ref() : 0.0f);
     __syncthreads();
     float least = list.threshold;
