@@ -118,10 +118,10 @@ __device__ __forceinline__ float exp2_fast(float x) {
 struct Pair {
   float hi, lo;
 };
-// a + b without an error (Knuth)
+// a + b without an error (Knuth); the intrinsics are never fused with a product before them
 __device__ __forceinline__ Pair two_sum(float a, float b) {
-  const float s = a + b, t = s - a;
-  return {s, (a - (s - t)) + (b - t)};
+  const float s = __fadd_rn(a, b), t = __fsub_rn(s, a);
+  return {s, __fadd_rn(__fsub_rn(a, __fsub_rn(s, t)), __fsub_rn(b, t))};
 }
 __device__ __forceinline__ Pair add(Pair a, Pair b) {
   Pair s = two_sum(a.hi, b.hi);
@@ -349,11 +349,19 @@ struct Sum {
     const float c = 0.6931472f * fmaf(-ref, kLog2e, base);
     return sum + fmaf(sum, fmaf(0.5f * c, c, c), rest);
   }
+  // What is carried stays a sum of 2^(x log2(e) - base): it is multiplied by 2^(old base - new base), the difference
+  // taken without an error, its whole part apart, the product kept with its rounding.
   __device__ __forceinline__ void move(float to) {
-    if (ref > -CUDART_INF_F) sum = of_ref() * exp2_fast((ref - to) * kLog2e);
-    rest = 0.0f;
+    const float next = __fmul_rn(to, kLog2e);
+    const Pair d = two_sum(base, -next);
+    const float n = rintf(d.hi);
+    const bool carried = ref > -CUDART_INF_F && n >= -126.0f;
+    const float by = carried ? expf(0.6931472f * ((d.hi - n) + d.lo)) * __int_as_float(((int)n + 127) << 23) : 0.0f;
+    const float s = carried ? sum * by : 0.0f;
+    rest = carried ? fmaf(rest, by, fmaf(sum, by, -s)) : 0.0f;
+    sum = s;
     ref = to;
-    base = to * kLog2e;
+    base = next;
   }
 };
 

@@ -1,0 +1,75 @@
+"""Precision of the selection's log-sum-exp (GPU).
+
+A row's score is chosen so that its best candidate ends next to zero: the result's own rounding is then lost beside
+the error of the logarithm, which is what it shows.
+
+Tolerance, in steps of 2^-24 of the sum.  A term is 2^y, y = (x - ref) log2(e) in one rounding: 2^-22 of the term (4)
+for the exponential, and d + 1 for the rounding of y and d / 4 for log2(e)'s own, d the distance from the row's greatest
+(a reference lies at most 1 below its warp's greatest logit).  A thread adds 16 (fp32: 8) terms of a tile in 5 (3)
+additions, the tiles without an error; 1 for the correction of the reference's product, 5 for a warp's threads, 5 for each
+of the two steps that join warps and chunks (an exponential, a product, an addition), 1 for the logarithm.  A reference moves by
+at least 1, so that a term is carried d times at most, each an exponential of 2 and a third of a step for its argument, 2.7.
+"""
+
+import pytest
+import torch
+from test_gpu_beam import TYPES, check, kv, make  # noqa: F401
+
+pytestmark = pytest.mark.gpu
+
+STEP = 2.0 ** -24
+
+
+def errors(kv, logits, count=1):  # noqa: F811
+    """Of every row: the error of the logarithm of its sum, and the tolerance above."""
+    rows, vocab = logits.shape
+    x = logits.double()
+    d = x.amax(1, keepdim=True) - x
+    total = torch.exp(-d).sum(1)
+    lse = torch.log(total)  # of the differences from the greatest
+    scores = lse.float().unsqueeze(1)
+    outs = [torch.zeros(rows, count, dtype=t, device="cuda") for t in (torch.float32, torch.int32, torch.int32)]
+    status = torch.zeros(1, dtype=torch.int32, device="cuda")
+    ws = kv.alloc_beam_select_workspace(rows, 1, vocab, count)
+    kv.beam_select(logits.unsqueeze(1), scores, *outs, ws, status=status)
+    torch.cuda.synchronize()
+    assert status.item() == 0
+    mean = (torch.nan_to_num(d, posinf=0.0) * torch.exp(-d)).sum(1) / total
+    tol = STEP * (4 + 1 + 5 + 1 + 5 + 10 + 1 + mean * (1 + 0.25 + 2.7))
+    return outs[0][:, 0].double() - (scores[:, 0].double() - lse), tol
+
+
+def rows_of(kind, rows, vocab, dtype, offset):
+    g = torch.Generator().manual_seed(rows + vocab)
+    x = torch.randn(rows, vocab, generator=g)
+    i = torch.arange(vocab)
+    x = {"random": 3.0 * x, "wide": 20.0 * x, "rising": x + 12.0 * i / vocab,
+         "steps": 2.0 * (i * 8 // vocab) - (2.0 * x).abs() - 8.0 * (i % 40 != 0)}[kind]
+    return (x + offset).to(TYPES[dtype]).cuda()
+
+
+@pytest.mark.parametrize("offset", [0.0, 30.0, -300.0, 3000.0, 60_000.0, -65_000.0])
+@pytest.mark.parametrize("kind", ["random", "wide", "rising", "steps"])
+@pytest.mark.parametrize("rows,vocab", [(320, 20_001), (3, 200_003)])  # one chunk a row, and many
+def test_offset(kv, rows, vocab, kind, offset):  # noqa: F811
+    """What is carried when a reference moves is not touched by the rounding of the new one's product."""
+    err, tol = errors(kv, rows_of(kind, rows, vocab, "fp32", offset))
+    assert (err.abs() <= tol).all(), (float(err.abs().max()), float(tol[err.abs().argmax()]))
+
+
+@pytest.mark.parametrize("dtype", ["fp16", "bf16"])
+@pytest.mark.parametrize("kind,offset", [("random", 0.0), ("wide", 0.0), ("steps", 0.0), ("random", 2000.0)])
+def test_offset_16_bits(kv, kind, offset, dtype):  # noqa: F811
+    err, tol = errors(kv, rows_of(kind, 320, 20_001, dtype, offset))
+    assert (err.abs() <= tol).all(), (float(err.abs().max()), float(tol[err.abs().argmax()]))
+
+
+@pytest.mark.parametrize("low", [-65_700.0, -65_540.0, -131_072.0, -3e38])
+def test_close_to_the_slower_path(kv, low):  # noqa: F811
+    # logits on both sides of -65536, where sums change their form, and behind a first tile of `low`
+    logits, scores = make(1, 32, 12289, "fp32", 7, scale=20.0)
+    logits -= 65_536.0
+    logits[:, 8:16] += 100.0
+    logits[:, 16:24] -= 100.0
+    logits[..., :2048] = low
+    check(kv, logits, scores, 64)
