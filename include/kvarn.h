@@ -440,9 +440,9 @@ size_t kvarn_beam_select_workspace_bytes(int batch, int beams, int vocab, int co
  *   scores[k] + logits[k][v] - log sum_u exp(logits[k][u]);
  * a finished beam (done[k] != 0) has one candidate, (k, end_token), with its score as it is; its logits are
  * not read.  Candidates are ordered by score, equal ones by k, then v.  Exponentials are summed in
- * 32 bits (the logarithm of a sum was off by 8e-8 in the mean square and 4e-7 at most) and scores compared in 48:
- * candidates of two beams that are nearer than 8e-7 may change places, those of one beam are in the order of their
- * logits exactly.
+ * 32 bits and scores compared in 48.  By its roundings the logarithm of a sum is off by 5e-6 at most (2^26 logits; 3.7e-6
+ * for 2^18), so that candidates of two beams that are nearer than 1e-5 may change places; over rows of random logits it
+ * is off by 8e-8 in the mean square.  Those of one beam are in the order of their logits exactly.
  *  logits      fp16, bf16 or fp32 (KVARN_LOGITS_*): token v of row b*beams + k at [row*row_stride + v];
  *              row_stride >= vocab, any alignment of the type (16-byte aligned rows are read fastest).
  *              -inf: the token cannot be chosen.  A beam with NaN or +inf among its logits, or as its score,

@@ -9,6 +9,8 @@ for the exponential, and d + 1 for the rounding of y and d / 4 for log2(e)'s own
 additions, the tiles without an error; 1 for the correction of the reference's product, 5 for a warp's threads, 5 for each
 of the two steps that join warps and chunks (an exponential, a product, an addition), 1 for the logarithm.  A reference moves by
 at least 1, so that a term is carried d times at most, each an exponential of 2 and a third of a step for its argument, 2.7.
+The mean of d over the terms is at most 9 for 2^18 logits and 14.4 for 2^26 (one peak above equal ones): 27 + 4 x 9 = 63 steps
+or 3.7e-6, 27 + 4 x 14.4 = 85 or 5e-6.
 """
 
 import pytest
@@ -73,3 +75,33 @@ def test_close_to_the_slower_path(kv, low):  # noqa: F811
     logits[:, 16:24] -= 100.0
     logits[..., :2048] = low
     check(kv, logits, scores, 64)
+
+
+@pytest.mark.parametrize("count", [1, 8])  # 8: all of the equal logits reach the bound, the slower path
+@pytest.mark.parametrize("rows,vocab", [(512, 151_936), (160, 1 << 20), (640, 9004)])
+def test_peak_over_equal_logits(kv, rows, vocab, count):  # noqa: F811
+    """A peak whose warp holds nothing else, over equal logits of which the other warps sum ones, exactly: the step
+    that joins the warps shows.
+
+    Of the sum the share w is of the equal logits: an exponential of 2 steps, a product, an addition.  The peak's share has the
+    exponential's 4, its argument's 1 and the correction's 1.  1 for the chunk's sum, 1 for the logarithm."""
+    i = torch.arange(vocab, device="cuda") % 1024 // 128  # the warp that loads it, 16 bytes a thread
+    at = torch.arange(rows, device="cuda") * 7919 % vocab
+    peak = 4.0 + 10.0 * torch.arange(rows, device="cuda") / rows
+    logits = torch.where(i == i[at].unsqueeze(1), -torch.inf, 0.0)
+    logits[torch.arange(rows, device="cuda"), at] = peak
+    err, _ = errors(kv, logits, count)
+    d = logits.amax(1).double()
+    w = 1.0 - 1.0 / (1.0 + (logits == 0).sum(1) * torch.exp(-d))
+    tol = STEP * (2 + 4 * w + 6 * (1 - w))
+    assert (err.abs() <= tol).all(), (float(err.abs().max()), float(tol[err.abs().argmax()]))
+
+
+@pytest.mark.parametrize("batch,beams,vocab,dtype", [(64, 8, 151_936, "bf16"), (32, 4, 128_000, "fp16"), (8, 5, 50_001, "fp32")])
+def test_random_rows(kv, batch, beams, vocab, dtype):  # noqa: F811
+    # the mean square that kvarn.h gives, 8e-8, within a factor of two for the sample and the shape
+    g = torch.Generator(device="cuda").manual_seed(3)
+    x = 2.0 * torch.randn(batch * beams, vocab, generator=g, device="cuda")
+    err, tol = errors(kv, x.to(TYPES[dtype]))
+    assert (err.abs() <= tol).all()
+    assert float(err.square().mean().sqrt()) <= 1.6e-7
