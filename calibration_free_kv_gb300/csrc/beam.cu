@@ -241,12 +241,12 @@ struct Tile {
       return e % 2 == 0 ? f.x : f.y;
     }
   }
-  // sum of exp(x - ref) for a reference whose product with log2(e) may pass 32 bits' range
-  __device__ __forceinline__ float sum_far(float ref) const {
-    float a = 0.0f;
+  // sum of exp(x - ref), in the order of the fast path's
+  __device__ __forceinline__ float sum_of(float ref) const {
+    float a[4] = {0.0f, 0.0f, 0.0f, 0.0f};
 #pragma unroll
-    for (int e = 0; e < kElems; ++e) a += exp2_fast((value(e) - ref) * kLog2e);
-    return a;
+    for (int e = 0; e < kElems; ++e) a[e % 4] += expf(value(e) - ref);
+    return (a[0] + a[2]) + (a[1] + a[3]);
   }
 };
 
@@ -364,11 +364,15 @@ struct Sum {
     const float n = rintf(d.hi);
     const bool carried = ref > -CUDART_INF_F && n >= -126.0f;
     const float by = carried ? expf(0.6931472f * ((d.hi - n) + d.lo)) * __int_as_float(((int)n + 127) << 23) : 0.0f;
-    const float s = carried ? sum * by : 0.0f;
-    rest = carried ? fmaf(rest, by, fmaf(sum, by, -s)) : 0.0f;
-    sum = s;
+    scale(by);
     ref = to;
     base = next;
+  }
+  // the product of 0 is 0: a sum against a reference within kFar is finite
+  __device__ __forceinline__ void scale(float by) {
+    const float s = sum * by;
+    rest = fmaf(rest, by, fmaf(sum, by, -s));
+    sum = s;
   }
 };
 
@@ -474,29 +478,30 @@ __device__ __forceinline__ void select_exact(List& list, int have, int count, co
 }
 
 // The rest of a chunk, from `at` on, where more of it reached the bound than the list holds or a reference is beyond
-// kFar: tile by tile, references a thread's own.  sum.sum is the sum of exp(x - sum.ref) here.  Returns whether a logit
-// was NaN.
+// kFar: tile by tile, references a thread's own.  sum.sum + sum.rest is the sum of exp(x - sum.ref) here, tiles added
+// without an error (with plain additions 2^20 logits 17 below 4096 others were off by 1e-5).  Returns whether a logit
+// was NaN or +inf.
 template <class Tl, class Elem>
 __device__ __noinline__ bool select_slow(List& list, int have, int count, const Elem* row, int at, int end,
                                          Sum& sum, int* counters) {
-  bool nan = false;
+  bool bad = false;
   if (threadIdx.x == 0) list.n = have;
   __syncthreads();
   for (; at < end; at += Tl::kSize) {
     Tl tile;
     tile.load(row, at, end);
     const float top = tile.max(), least = list.threshold;
-    nan |= top != top;
+    bad |= !(top < CUDART_INF_F);
     if (top > least) {
 #pragma unroll
       for (int e = 0; e < Tl::kElems; ++e)
         if (tile.value(e) > least) append(list, tile.value(e), at + Tl::index(e));
     }
-    if (top > sum.ref + kStep || (top > sum.ref && fabsf(top) > kFar)) {
-      sum.sum = sum.ref > -CUDART_INF_F ? sum.sum * exp2_fast((sum.ref - top) * kLog2e) : 0.0f;
+    if (top > sum.ref + kStep) {
+      sum.scale(exp_difference(sum.ref, top));
       sum.ref = top;
     }
-    if (sum.ref > -CUDART_INF_F) sum.sum += tile.sum_far(sum.ref);
+    if (sum.ref > -CUDART_INF_F) sum.add(tile.sum_of(sum.ref));
     __syncthreads();
     int n = list.n;
     __syncthreads();
@@ -510,7 +515,7 @@ __device__ __noinline__ bool select_slow(List& list, int have, int count, const 
     }
     have = n;
   }
-  return nan;
+  return bad;
 }
 
 // Keys that come before number i of them, whose value is `mine`.
@@ -709,7 +714,7 @@ __global__ void __launch_bounds__(kThreads, kResident) select_kernel(SelectParam
   sum.rest = 0.0f;
   nan |= select_slow<Tl>(list, have, p.count, x, at, end, sum, counters);
   grid_launch_dependents();
-  warp_total(sum.ref, sum.sum);
+  warp_total(sum.ref, sum.sum + sum.rest);
   __syncthreads();
   const int n = list.n;
   for (int i = tid; i < n; i += kThreads) out[i] = list.e[i];

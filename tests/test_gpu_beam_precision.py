@@ -105,3 +105,34 @@ def test_random_rows(kv, batch, beams, vocab, dtype):  # noqa: F811
     err, tol = errors(kv, x.to(TYPES[dtype]))
     assert (err.abs() <= tol).all()
     assert float(err.square().mean().sqrt()) <= 1.6e-7
+
+
+@pytest.mark.parametrize("count", [1, 8])
+@pytest.mark.parametrize("rows,vocab", [(512, 151_936), (3, 200_003)])
+def test_peak_among_equal_logits(kv, rows, vocab, count):  # noqa: F811
+    # the slower path: its terms have 2 + d steps (an exponential, the rounding of its argument), its sums those of the fast path
+    at = torch.arange(rows, device="cuda") * 7919 % vocab
+    logits = torch.zeros(rows, vocab, device="cuda")
+    logits[torch.arange(rows, device="cuda"), at] = 4.0 + 10.0 * torch.arange(rows, device="cuda") / rows
+    err, tol = errors(kv, logits, count)
+    assert (err.abs() <= tol).all(), (float(err.abs().max()), float(tol[err.abs().argmax()]))
+
+
+@pytest.mark.parametrize("dtype", ["bf16", "fp32"])
+@pytest.mark.parametrize("near", [4096, 1])  # whole tiles, the slower path, or one logit in 8
+def test_small_terms_are_not_lost(kv, near, dtype):  # noqa: F811
+    # each of the small logits' terms is less than half a step of the sum that it is added to
+    i = torch.arange(1 << 20, device="cuda")
+    high = i < near if near > 1 else (i < 2048) & (i % 8 == 0)
+    row = torch.where(high, 0.0, -17.0)
+    logits = row.to(TYPES[dtype]).expand(160, -1).contiguous()
+    err, tol = errors(kv, logits)
+    assert (err.abs() <= tol).all(), (float(err.abs().max()), float(tol[0]))
+
+
+def test_far_rows_that_rise(kv):  # noqa: F811
+    # references beyond 65536 that move often
+    x = torch.arange(30_000, device="cuda") / 2000 + 0.01 * torch.randn(160, 30_000, device="cuda")
+    for offset in (1e5, -1e5, 4e6):
+        err, tol = errors(kv, x + offset)
+        assert (err.abs() <= tol).all(), (offset, float(err.abs().max()), float(tol.max()))
