@@ -528,12 +528,12 @@ def plan_pages(seq_lens, block_table, num_pool_pages: int, seq_lens_out, new_len
 
 def fp16_store(k, v, slot_map, pool, status=None, stream=None):
     """Write tokens to their slots of the fp16 cache: k, v fp16 [tokens, Hkv, d] (token and head strides taken
-    from the tensors, equal in both); slot_map int64 with one entry a token (any shape); pool fp16 [pages, Hkv,
-    2, 128, d]."""
+    from the tensors, equal in both; those of a dimension of size 1 do not count); slot_map int64 with one entry a
+    token (any shape); pool fp16 [pages, Hkv, 2, 128, d]."""
     tokens, heads, d = shape = k.shape
-    strides, dev = k.stride(), k.get_device()
-    if not (k.dtype is torch.float16 and v.dtype is torch.float16 and v.shape == shape and v.stride() == strides
-            and strides[2] == 1):
+    (ts, hs, cs), vs, dev = k.stride(), v.stride(), k.get_device()
+    if not (k.dtype is torch.float16 and v.dtype is torch.float16 and v.shape == shape and (vs[0] == ts or tokens <= 1)
+            and (vs[1] == hs or heads == 1) and vs[2] == cs == 1):
         raise ValueError("k and v must be fp16 [tokens, Hkv, d] with matching strides, channels contiguous")
     if dev < 0 or v.get_device() != dev:
         _ptr(k), _ptr(v)
@@ -541,7 +541,8 @@ def fp16_store(k, v, slot_map, pool, status=None, stream=None):
     if slot_map.numel() != tokens:
         raise ValueError("slot_map holds %d entries for %d tokens" % (slot_map.numel(), tokens))
     pages = pool.shape[0]
-    _launch(_lib.kvarn_fp16_store, dev, stream, d, heads, tokens, k.data_ptr(), v.data_ptr(), strides[0], strides[1],
+    _launch(_lib.kvarn_fp16_store, dev, stream, d, heads, tokens, k.data_ptr(), v.data_ptr(), ts if tokens > 1 else 0,
+            hs if heads > 1 else 0,
             _arg("slot_map", slot_map, dev, torch.int64, slot_map.shape),
             _arg("pool", pool, dev, torch.float16, (pages, heads, 2, 128, d)), pages, _status_arg(status, dev))
 
