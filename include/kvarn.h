@@ -399,16 +399,16 @@ int kvarn_fp16_decode_attention(int head_dim, int num_kv_heads, int batch, int n
  *               KVARN_DEV_SEQ_TOO_LONG).
  *  block_table  device int32 [batch][max_pages]; entries pages(seq_lens[b]) up to the new length's pages are
  *               written, no others are written or (past pages(seq_lens[b])) read.
- * A page is free if no row of the call names it (rows may share pages; a row with 0 new tokens keeps its
- * pages from being given away, one with length 0 gives them back).  Free pages go in ascending order to the
- * sequences in order.  While the pool lasts: a sequence whose pages, with those wanted by the sequences
+ * A page is free if no row of the call names it (rows may share full pages, not one that new tokens go to: both
+ * would get its slots; a row with 0 new tokens keeps its pages from being given away, one with length 0 gives
+ * them back).  Free pages go in ascending order to the sequences in order.  While the pool lasts: a sequence whose pages, with those wanted by the sequences
  * before it, exceed the free ones gets none and keeps its length (KVARN_DEV_NO_PAGES); one that needs no
  * page is always served.  A sequence of negative length, or whose pages would exceed max_pages, is left as
  * it is (KVARN_DEV_SEQ_TOO_LONG); named pages outside the pool are passed over (KVARN_DEV_BAD_PAGE_ID).
  *  seq_lens_out device int32 [batch], not seq_lens: seq_lens[b] + new_lens[b], or seq_lens[b] if not served.
  *  slot_map     device int64 [batch][chunk_len] or NULL: page * 128 + row of token i of sequence b; -1 for
  *               tokens past new_lens[b], of sequences not served, or of an open tile (open_tiles 1).
- * The result depends on the arguments alone.  One launch; no workspace.
+ * The result depends on the arguments alone.  One launch, a second for more than 16384 slots; no workspace.
  * UNSUPPORTED for batch over 16384, max_pages over 2^23, chunk_len over 2^30 or a pool over 2^23 pages. */
 int kvarn_plan_pages(int batch, int chunk_len, const int32_t* seq_lens, const int32_t* new_lens,
                      int32_t* block_table, int max_pages, int64_t num_pool_pages, int open_tiles,
@@ -438,15 +438,16 @@ size_t kvarn_beam_select_workspace_bytes(int batch, int beams, int vocab, int co
 
 /* The `count` best continuations of every group.  Candidate (k, v) of a group has the score
  *   scores[k] + logits[k][v] - log sum_u exp(logits[k][u]);
- * a finished beam (done[k] != 0) has one candidate, (k, end_token), with its score as it is; its logits are
- * not read.  Candidates are ordered by score, equal ones by k, then v.  Exponentials are summed in
- * 32 bits and scores compared in 48.  By its roundings the logarithm of a sum is off by 5e-6 at most (2^26 logits; 3.7e-6
- * for 2^18), so that candidates of two beams that are nearer than 1e-5 may change places; over rows of random logits it
- * is off by 8e-8 in the mean square.  Those of one beam are in the order of their logits exactly.
+ * a finished beam (done[k] != 0) has one candidate, (k, end_token), with its score as it is, whatever its logits
+ * hold (they may be read: the rows have to be there).  Candidates are ordered by score, equal ones by k, then v.
+ * Exponentials are summed in 32 bits and scores compared in 48.  By its roundings the logarithm of a sum is off by 5e-6
+ * at most (2^26 logits; 3.7e-6 for 2^18), so that candidates of two beams that are nearer than 1e-5 may change places;
+ * over rows of random logits it is off by 8e-8 in the mean square.  Those of one beam are in the order of their logits
+ * where these differ by more than 2^-45 of the score.
  *  logits      fp16, bf16 or fp32 (KVARN_LOGITS_*): token v of row b*beams + k at [row*row_stride + v];
  *              row_stride >= vocab, any alignment of the type (16-byte aligned rows are read fastest).
  *              -inf: the token cannot be chosen.  A beam with NaN or +inf among its logits, or as its score,
- *              has no candidates (KVARN_DEV_BAD_LOGITS); one with score -inf has none and is not read.
+ *              has no candidates (KVARN_DEV_BAD_LOGITS); one with score -inf has none, whatever its logits hold.
  *  scores      device fp32 [batch][beams];  done: device bytes [batch][beams] or NULL (none is finished).
  *  end_token   0..vocab-1, or -1 (no token ends a beam; only if done is NULL).
  *  out_scores fp32, out_parents int32 (beam of the group), out_tokens int32, out_done bytes or NULL (1: the
@@ -464,7 +465,8 @@ int kvarn_beam_select(int batch, int beams, int vocab, int count, const void* lo
 
 /* Move the cache's state to the beams that go on: sequence b*beams + j becomes a copy of sequence
  * b*beams + parents[b][j].  Sealed pages are shared through the table; only table entries, lengths and the
- * live rows of the open tiles move.
+ * live rows of the open tiles move.  For the packed cache: an open tile of the fp16 cache lies in a page, which this
+ * call neither copies nor names.
  *  parents      device int32 [batch][beams]: a beam of the group, or -1: the sequence becomes empty (length 0;
  *               outside [-1, beams): the same, KVARN_DEV_BAD_BEAM).
  *  seq_lens, seq_lens_out        device int32 [batch*beams]; not the same buffer.

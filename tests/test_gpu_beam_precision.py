@@ -136,3 +136,35 @@ def test_far_rows_that_rise(kv):  # noqa: F811
     for offset in (1e5, -1e5, 4e6):
         err, tol = errors(kv, x + offset)
         assert (err.abs() <= tol).all(), (offset, float(err.abs().max()), float(tol.max()))
+
+
+@pytest.mark.parametrize("apart", [1e-11, 1e-9, 1e-6])
+def test_order_within_a_beam(kv, apart):  # noqa: F811
+    # logits of one beam more than 2^-45 of the score apart are in their order, the later token first here
+    logits = torch.full((1, 2, 5000), -50.0, device="cuda")
+    at = torch.arange(8, device="cuda") * 600
+    logits[0, :, at] = apart * torch.arange(8.0, device="cuda")
+    outs = [torch.zeros(1, 8, dtype=t, device="cuda") for t in (torch.float32, torch.int32, torch.int32)]
+    ws = kv.alloc_beam_select_workspace(1, 2, 5000, 8)
+    kv.beam_select(logits, torch.tensor([[-100.0, -30.0]], device="cuda"), *outs, ws)
+    assert apart > 2.0 ** -45 * 33
+    assert outs[1].tolist() == [[1] * 8] and outs[2].tolist() == [at.flip(0).tolist()]
+
+
+def test_finished_rows_hold_anything(kv):  # noqa: F811
+    # rows that do not count: no status, and the others' results to the bit
+    logits, scores = make(3, 4, 30_000, "bf16", 13)
+    done = torch.zeros(3, 4, dtype=torch.bool, device="cuda")
+    done[0, 1] = done[2] = True
+    scores[1, 2] = -torch.inf
+    results = []
+    for fill in (0.0, float("nan"), float("inf"), -3e38):
+        logits[0, 1] = logits[2] = logits[1, 2] = fill
+        outs = [torch.zeros(3, 8, dtype=t, device="cuda") for t in (torch.float32, torch.int32, torch.int32)]
+        status = torch.zeros(1, dtype=torch.int32, device="cuda")
+        ws = kv.alloc_beam_select_workspace(3, 4, 30_000, 8)
+        kv.beam_select(logits, scores, *outs, ws, done=done, end_token=9, status=status)
+        assert status.item() == 0
+        results.append(outs)
+    for outs in results[1:]:
+        assert all(torch.equal(a, b) for a, b in zip(outs, results[0]))
