@@ -313,7 +313,7 @@ def _arg(name, t, device, dtype, shape):
         return t.data_ptr()
     _ptr(t)
     if t.get_device() != device:
-        raise ValueError("%s is on %s, q on cuda:%d" % (name, t.device, device))
+        raise ValueError("%s is on %s, the call's first tensor on cuda:%d" % (name, t.device, device))
     raise ValueError("%s must be a contiguous %s tensor of shape %s, got %s of shape %s (strides %s)" %
                      (name, dtype, list(shape), t.dtype, list(t.shape), list(t.stride())))
 

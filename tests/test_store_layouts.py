@@ -54,3 +54,11 @@ def test_stored(kv, name):
     for t, s in enumerate(slots.tolist()):
         want[s // 128, :, 0, s % 128], want[s // 128, :, 1, s % 128] = k[t], v[t]
     assert torch.equal(pool, want)
+
+
+@pytest.mark.gpu
+def test_device_of_a_tensor_is_told(kv):
+    # as a call on the second GPU would find it
+    t = torch.zeros(2, 3, device="cuda")
+    with pytest.raises(ValueError, match="scores is on cuda:0, the call's first tensor on cuda:1"):
+        kv._arg("scores", t, 1, torch.float32, (2, 3))
