@@ -16,7 +16,7 @@ namespace beam {
 constexpr int kMaxBeams = 32, kMaxCount = 64;
 constexpr int kMaxVocab = 1 << 26;     // beam * vocab + token stays within 31 bits
 constexpr int kChunkEntries = 1024;    // candidates beyond which a group's rows are not divided further
-static_assert(kMaxBeams * kMaxCount * 12 + 16384 <= 49152, "the merge takes its lists without a raised limit");
+static_assert(kChunkEntries <= kMaxBeams * kMaxCount && kMaxBeams * kMaxCount * 12 + 16384 <= 49152, "the merge takes its lists without a raised limit");
 
 // ---- selection: one pass over the logits ----------------------------------------------------
 // A row of logits (one beam) is cut into chunks, one CTA each.  A CTA streams its chunk through shared
@@ -846,7 +846,7 @@ __global__ void __launch_bounds__(kMergeThreads) select_merge_kernel(SelectParam
 #pragma unroll 1
   for (int i = tid, j = 0; i < entries; i += kMergeThreads, ++j) {
     const float2 e = j == 0 ? ahead[0] : j == 1 ? ahead[1] : j == 2 ? ahead[2] : j == 3 ? ahead[3] : __ldcg(src + i);
-    const int k = (int)(((float)i + 0.5f) * per_inverse);  // i / per_beam: entries <= 8192
+    const int k = (int)(((float)i + 0.5f) * per_inverse);  // i / per_beam: entries <= 2048
     uint64_t key = 0;
     int t = __float_as_int(e.y);
     if (kind[k] == 1) {
