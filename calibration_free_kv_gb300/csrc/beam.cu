@@ -16,7 +16,8 @@ namespace beam {
 constexpr int kMaxBeams = 32, kMaxCount = 64;
 constexpr int kMaxVocab = 1 << 26;     // beam * vocab + token stays within 31 bits
 constexpr int kChunkEntries = 1024;    // candidates beyond which a group's rows are not divided further
-static_assert(kChunkEntries <= kMaxBeams * kMaxCount && kMaxBeams * kMaxCount * 12 + 16384 <= 49152, "the merge takes its lists without a raised limit");
+static_assert(kChunkEntries <= kMaxBeams * kMaxCount && kMaxBeams * kMaxCount * 12 + 16384 <= 49152,
+              "the merge takes its lists without a raised limit");
 
 // ---- selection: one pass over the logits ----------------------------------------------------
 // A row of logits (one beam) is cut into chunks, one CTA each.  A CTA streams its chunk through shared
@@ -43,8 +44,8 @@ constexpr int kCap = 512;              // entries of the list
 // of kFar or more, or of -kFar, takes the slower path.
 constexpr float kFar = 65536.0f;
 // A reference moves when a logit exceeds it by more: the greatest terms' arguments stay small, and with them
-// their rounding (with 40 the logarithm of a sum was off by 3.1e-7 in the mean square, with 1 by 1.3e-7, and by
-// 7.6e-8 since tiles are added without an error).
+// their rounding (with 40 the logarithm of a sum was off by 3.1e-7 in the mean square, with 1 by 1.3e-7, by 7.6e-8 since
+// tiles are added without an error, and by 7.5e-8 since a move is exact to a rounding of its factor).
 constexpr float kStep = 1.0f;
 
 struct SelectParams {
@@ -159,7 +160,9 @@ struct Tile {
   static constexpr int kElems = 4 * kWords / (int)sizeof(typename T::Elem);
   static constexpr int kSize = kThreads * kElems;
   static constexpr int kRun = 32 / kElems;                            // tiles of a run of 32 elements
-  static constexpr int kRuns = T::kPerWord == 1 ? 10 : 20;            // runs of a thread that are noted at a time
+  // Runs of a thread that are noted at a time, 10 KB; a chunk with more ends a part more than once: 512 rows of 163840
+  // 16-bit logits take 38.4 us, of 163848 45.0, of 200064 48.4; of 81920 32-bit ones 36.6, of 81928 40.0.
+  static constexpr int kRuns = T::kPerWord == 1 ? 10 : 20;
   uint32_t w[kWords];
 
   // index within the tile of element e of this thread
@@ -1205,7 +1208,8 @@ int kvarn_beam_reorder(const kvarn_desc* desc, int batch, int beams, int layers,
   p.dim = desc->head_dim;
   // Few units: CTAs to fill the GPU; many: long-lived ones.  16 groups of 4 over 16 layers take 52 / 45 / 45 / 46 us in
   // 8 / 4 / 2 / 1 slices, 6 groups of 5 over 4 layers 5.3 / 4.1 / 3.8 / 4.2 us, one group in one layer 2.5 us in 4 or more,
-  // 3.2 in 2.
+  // 3.2 in 2.  4 / 2 / 1 slices of 8 kv heads: 4 groups of 4 in one layer 2.9 / 3.6 / 3.8 us, 16 groups 4.8 / 4.2 / 4.9, 16 groups
+  // over 4 layers 14.8 / 15.1 / 15.3, 8 groups of 8 over 16 layers 91.0 / 92.8 / 95.6.
   p.slices = (int64_t)batch * p.num_kv_heads * (2 * layers + 1) <= 152 ? 4 : 2;
   if ((int64_t)batch * p.num_kv_heads * p.slices > 0x7fffffffLL) return KVARN_ERR_UNSUPPORTED;
   const cudaStream_t s = static_cast<cudaStream_t>(stream);

@@ -17,8 +17,8 @@ constexpr int kCluster = 8;                // CTAs of a large plan: the portable
 constexpr uint32_t kManyPages = 1u << 30;  // needs are added up to here: no pool has as many pages
 constexpr int kAhead = 8;                  // table entries that a lane has under way
 constexpr int kSpan = 32 * kAhead;         // table entries that a warp marks at a time
-// Slots that the planning CTAs write themselves; more take a kernel of their own (16384 slots: 7.8 against 8.7 us,
-// 65536: 11.4 against 9.1).
+// Slots that the planning CTAs write themselves; more take a kernel of their own (8192 slots: 7.6 against 9.2 us,
+// 16384: 8.9 against 9.8, 24576: 10.0 against 10.5, 32768: 11.2 against 11.1, 65536: 13.1 against 11.3).
 constexpr int64_t kSlotsHere = 16384;
 // Up to these sizes (table entries, pages of the pool, tokens that come) one CTA plans, beyond them a cluster.  One
 // CTA against a cluster: 1 row 4.3 / 5.8 us, 64 rows of 128 entries 5.3 / 5.9, 128 rows 6.8 / 6.2, 512 rows 15.7 / 7.6;
@@ -449,7 +449,9 @@ int kvarn_fp16_store(int head_dim, int num_kv_heads, int64_t num_tokens, const v
   p.tokens = num_tokens;
   p.num_kv_heads = num_kv_heads;
   p.dim = head_dim;
-  // few tokens: as many CTAs as there are; many: enough copies a thread to keep their latency covered
+  // Few tokens: as many CTAs as there are; many: enough copies a thread to keep their latency covered.  Few against many, 8
+  // kv heads, head_dim 128: 64 tokens 1.5 / 1.7 us, 512 2.1 / 1.8, 1024 3.0 / 2.1, 1536 3.9 / 2.5, 16384 41 / 21; 2 kv heads,
+  // head_dim 64: 1024 tokens 1.6 / 1.8, 4096 2.3 / 1.9.
   const int vecs = 2 * num_kv_heads * (head_dim / 8), groups = vecs < kStoreThreads ? kStoreThreads / vecs : 1;
   p.streaming = num_tokens > 1024;
   p.per_cta = (p.streaming ? kStoreUnroll : 1) * groups;

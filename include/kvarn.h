@@ -441,9 +441,9 @@ size_t kvarn_beam_select_workspace_bytes(int batch, int beams, int vocab, int co
  * a finished beam (done[k] != 0) has one candidate, (k, end_token), with its score as it is, whatever its logits
  * hold (they may be read: the rows have to be there).  Candidates are ordered by score, equal ones by k, then v.
  * Exponentials are summed in 32 bits and scores compared in 48.  By its roundings the logarithm of a sum is off by 5e-6
- * at most (2^26 logits; 3.7e-6 for 2^18), so that candidates of two beams that are nearer than 1e-5 may change places;
- * over rows of random logits it is off by 8e-8 in the mean square.  Those of one beam are in the order of their logits
- * where these differ by more than 2^-45 of the score.
+ * at most (2^26 logits; 3.7e-6 for 2^18), so that candidates of two beams that are nearer than 1e-5, or 2^-45 of the
+ * score, may change places; over rows of random logits it is off by 8e-8 in the mean square.  Those of one beam are in
+ * the order of their logits where these differ by more than 2^-45 of the score.
  *  logits      fp16, bf16 or fp32 (KVARN_LOGITS_*): token v of row b*beams + k at [row*row_stride + v];
  *              row_stride >= vocab, any alignment of the type (16-byte aligned rows are read fastest).
  *              -inf: the token cannot be chosen.  A beam with NaN or +inf among its logits, or as its score,
